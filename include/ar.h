@@ -593,6 +593,178 @@ int ar_comm_destroy(ar_comm* comm);
 int ar_allreduce_peer(ar_comm* comm, const void* input, void* out, size_t n, int dtype, int strategy,
                       ar_stream_t stream);
 
+/*
+ * ---------------------------------------------------------------------------
+ * The paged key-value cache: what a tensor-parallel decoder layer runs just
+ * before the row-parallel projection whose partials the calls above reduce.
+ * ar_kv_append rotates new queries and keys and writes new keys and values
+ * into the cache, ar_paged_attention attends from one new token of each
+ * sequence to its cached tokens, and ar_attention_join reduces R ranks'
+ * partial attentions (each rank holding a part of every sequence's cache)
+ * the way ar_sum reduces their partial activations.  No pages' counterpart:
+ * the pages begin at the projection.
+ * ---------------------------------------------------------------------------
+ */
+
+/* Element type of cached keys and values only: 8-bit floating point with 4
+ * exponent and 3 mantissa bits, largest value 448, no infinity.  Every other
+ * call refuses it (AR_ERR_UNSUPPORTED). */
+#define AR_FP8_E4M3 3
+
+/*
+ * ar_kv_cache -- a cache of fixed-size pages and the sequences that own them.
+ * Token j of sequence b and key-value head h lies at element
+ *     page_table[b * table_stride + j / page_size] * page_stride
+ *       + (j % page_size) * token_stride + h * head_stride
+ * of k and of v, head_dim elements side by side.  The strides give any order
+ * of pages, tokens and heads, and k and v may be halves of one buffer.
+ * A table entry outside [0, pages) stands for no page: nothing is written
+ * there, and attention leaves its tokens out.  Offsets are 64 bits wide.
+ * lengths[b] counts the tokens of sequence b, the new ones included; values
+ * outside [0, max_pages * page_size] are taken as the nearest bound by
+ * attention.  Entries of one sequence's table are read up to its length only.
+ */
+typedef struct {
+    void* k;                /* device: the pages of keys */
+    void* v;                /* device: the pages of values, with the same strides */
+    int dtype;              /* the calls' dtype, or AR_FP8_E4M3 beside AR_FP16 or AR_BF16 */
+    int pages;              /* pages in the buffers */
+    int page_size;          /* tokens of a page */
+    int kv_heads;           /* 1 .. 1024 */
+    int head_dim;           /* 1 .. 1024 (attention: see there) */
+    size_t page_stride;     /* elements from one page to the next */
+    size_t token_stride;    /* elements from one token of a page to the next */
+    size_t head_stride;     /* elements from one head of a token to the next */
+    float k_scale;          /* a cached key stands for its value times k_scale: finite, > 0 */
+    float v_scale;          /* the same for values; both apply to every cache dtype */
+    const int* page_table;  /* device [batch, max_pages], rows table_stride apart */
+    int batch;
+    int max_pages;
+    int table_stride;       /* >= max_pages */
+    const int* lengths;     /* device [batch] */
+} ar_kv_cache;
+
+/* The new tokens of ar_kv_append.  Strides are elements from one token to
+ * the next; the heads of a token and their elements lie side by side, so q, k
+ * and v may be parts of one projection's output. */
+typedef struct {
+    const void* q;          /* device [tokens, q_heads, head_dim], or NULL: no queries */
+    const void* k;          /* device [tokens, kv_heads, head_dim] */
+    const void* v;          /* device [tokens, kv_heads, head_dim] */
+    void* q_out;            /* device [tokens, q_heads, head_dim]; may be q with the same stride */
+    int tokens;
+    int q_heads;            /* 1 .. 1024 with q */
+    int dtype;              /* ar_dtype of q, k, v and q_out */
+    size_t q_stride, k_stride, v_stride, q_out_stride;
+    const int* seq_start;   /* device [batch + 1], ascending: rows seq_start[b] .. seq_start[b + 1] - 1
+                               are the last tokens of sequence b, in order.  NULL: tokens == batch
+                               and row b is the last token of sequence b */
+    const int* positions;   /* device [tokens]: the position a row is rotated by, or NULL: its index
+                               in its sequence */
+    const float* inv_freq;  /* device [rotary_dim / 2]: angle per position of each pair; NULL with
+                               rotary_dim == 0 */
+    int rotary_dim;         /* even, 0 .. head_dim: leading elements of a head that are rotated */
+    int interleaved;        /* 0: element j pairs with j + rotary_dim / 2; 1: 2j pairs with 2j + 1 */
+    float rotary_scale;     /* multiplies cosines and sines; finite */
+} ar_append_params;
+
+/*
+ * ar_kv_append -- appends new keys and values to a paged cache, with the
+ * position rotation applied on the way.  For the i-th of the n new rows of
+ * sequence b, at index p = lengths[b] - n + i of its sequence:
+ *     (x, y) -> rotary_scale * (x cos a - y sin a, y cos a + x sin a),
+ *     a = position * inv_freq[j]            for every pair j of q and k
+ *     cache k, v at token p  = rotated k / k_scale, v / v_scale
+ *     q_out row              = rotated q
+ * Arithmetic is fp32 with the angle reduced exactly from a 64-bit fixed-point
+ * product, so far positions lose nothing; each result is rounded once, to
+ * nearest even, and AR_FP8_E4M3 saturates at +-448 (a NaN stays one).
+ *   - Rows before seq_start[0] or from seq_start[batch] on are padding:
+ *     neither cached nor written to q_out.
+ *   - A row whose p lies outside [0, max_pages * page_size) (lengths[b] == 0
+ *     marks an idle sequence of a padded batch) or on a table entry that is
+ *     no page is not cached; its query is rotated all the same.
+ *   - Two rows that map to one cache element (sequences that share a page)
+ *     leave one row's value there, which one is not defined.
+ * Any stride and any element-aligned pointer is taken; 16-byte aligned pointers and strides
+ * (8-byte for AR_FP8_E4M3 caches), with head_dim and the rotated halves whole
+ * 16-byte vectors, take the vector path.  tokens == 0 launches nothing.
+ * Errors: AR_ERR_INVALID_ARG (NULL or not element-aligned pointer, a size or
+ *         stride that is too small, odd or oversized rotary_dim, scale not finite or <= 0,
+ *         tokens != batch without seq_start), AR_ERR_UNSUPPORTED (unknown
+ *         dtype or pair of dtypes, heads or head_dim over 1024), AR_ERR_CUDA.
+ */
+int ar_kv_append(const ar_kv_cache* cache, const ar_append_params* p, ar_stream_t stream);
+
+/* Bytes of device workspace that ar_paged_attention needs with this cache
+ * (its sizes and dtype are read, no pointer is) and q_heads query heads,
+ * whatever the lengths; a multiple of 256.  0 for arguments that the call
+ * refuses. */
+size_t ar_paged_attention_workspace_size(const ar_kv_cache* cache, int q_heads);
+
+/*
+ * ar_paged_attention -- attention of one new token of every sequence over
+ * the sequence's cached tokens (its own among them).  Query head i reads
+ * key-value head i / (q_heads / kv_heads).  With n = lengths[b]:
+ *     s_j    = scale * k_scale * q . k_j   (softcap > 0: softcap * tanh(s_j / softcap))
+ *     out    = v_scale * sum_j e^(s_j - m) v_j / sum_j e^(s_j - m),  m = max_j s_j
+ *     lse    = m + ln sum_j e^(s_j - m)
+ * over j < n, with window > 0 over n - window <= j < n, without the tokens of
+ * table entries that are no page.  With no token left, out is 0 and lse is
+ * -infinity.  Cached values that are left out are never read into a result,
+ * whatever they hold.
+ * One pass over the cache: sequences and heads are cut into tiles, the
+ * launch's blocks take equal runs of them whatever the lengths, and parts of
+ * one row's tokens that fell to several blocks are joined, in a fixed order,
+ * by a second kernel.  Statistics and sums are fp32.  Results repeat bit for
+ * bit for the same inputs; a sequence's rounding may depend on the other
+ * sequences' lengths.
+ *   lengths, page_table  read on the device: a captured graph follows them
+ *   q             device [batch, q_heads, head_dim], rows of a sequence
+ *                 q_stride elements apart
+ *   scale         finite; applied to the scores
+ *   window        >= 0, 0 for none
+ *   softcap       finite, >= 0, 0 for none
+ *   out           device [batch, q_heads, head_dim], dense
+ *   lse           device fp32 [batch, q_heads], or NULL
+ *   workspace     device, 16-byte aligned, of at least
+ *                 ar_paged_attention_workspace_size(cache, q_heads) bytes;
+ *                 its content does not matter.  Calls that may run at the
+ *                 same time (two graphs among them) need separate ones.
+ * head_dim <= 256; q, k, v and out 16-byte aligned and head_dim, q_stride and
+ * the cache's strides multiples of 16 bytes; q_heads <= 1024.  batch == 0
+ * launches nothing.
+ * Errors: AR_ERR_INVALID_ARG (NULL or not element-aligned pointer, bad size,
+ *         q_heads not a multiple of kv_heads, scale, window or softcap out of range),
+ *         AR_ERR_UNSUPPORTED (dtypes, alignment, head_dim over 256),
+ *         AR_ERR_WORKSPACE (missing, misaligned or too small), AR_ERR_CUDA.
+ */
+int ar_paged_attention(const ar_kv_cache* cache, const void* q, size_t q_stride, int q_heads, float scale,
+                       int window, float softcap, void* out, float* lse, void* workspace,
+                       size_t workspace_bytes, int dtype, ar_stream_t stream);
+
+/*
+ * ar_attention_join -- reduces R partial attentions of the same queries over
+ * disjoint parts of their keys (the R ranks' parts of the cache, each from
+ * ar_paged_attention) to the attention over all of them:
+ *     M = max_r lse_r,   out = sum_r e^(lse_r - M) partial_r / sum_r e^(lse_r - M),
+ *     lse_out = M + ln sum_r e^(lse_r - M)
+ * in fp32, in rank order.  A part with lse_r = -infinity counts nothing,
+ * whatever its row holds; where every part does, out is 0 and lse_out
+ * -infinity.
+ *   partials  host array of R device pointers, each [rows, head_dim], dense
+ *   lse       host array of R device pointers, each fp32 [rows]
+ *   out       device [rows, head_dim]; may be one of the partials
+ *   lse_out   device fp32 [rows], or NULL; not one of lse
+ * Any element-aligned pointer; 16-byte aligned ones with head_dim a multiple of 16 /
+ * element size take the packed path.  rows == 0 launches nothing.
+ * Errors: AR_ERR_INVALID_ARG (R out of range, rows < 0, head_dim < 1, NULL
+ *         or not element-aligned pointer, lse_out among lse), AR_ERR_UNSUPPORTED (unknown dtype),
+ *         AR_ERR_CUDA.
+ */
+int ar_attention_join(const void* const* partials, const float* const* lse, int R, int rows, int head_dim,
+                      void* out, float* lse_out, int dtype, ar_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -1,0 +1,346 @@
+// ar_append.cu -- appending keys and values to a paged cache with the position
+// rotation on the way, and the join of R ranks' partial attentions.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <climits>
+
+#include "ar_cache.h"
+#include "ar_kernels.cuh"
+#include "ar_launch_k.cuh"
+
+namespace ar {
+
+// ---------------------------------------------------------------------------
+// Angles.  One turn is 2^64: inv_freq / (2 pi) becomes a 64-bit fraction of a
+// turn, whose product with the position wraps around at whole turns by itself,
+// so the reduction is exact for any 32-bit position and costs one integer
+// multiply (a product in fp32 would be off by 0.06 rad at position 2^20, and
+// fp64 runs at 1/64 of the fp32 rate here).
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ uint64_t turn_fraction(float inv_freq)
+{
+    const uint32_t bits = __float_as_uint(inv_freq);
+    const int ex = static_cast<int>((bits >> 23) & 255u);
+    const uint64_t mant = (bits & 0x7fffffu) | (ex != 0 ? 0x800000u : 0u);
+    // inv_freq = mant * 2^(max(ex, 1) - 150); 2^64 / (2 pi) = 0x28be60db9391054a.
+    constexpr uint64_t kTurn = 0x28be60db9391054aull;
+    const uint64_t lo = mant * kTurn, hi = __umul64hi(mant, kTurn);
+    const int shift = 150 - (ex != 0 ? ex : 1);
+    uint64_t f;
+    if (shift >= 128)
+        f = 0;
+    else if (shift >= 64)
+        f = hi >> (shift - 64);
+    else if (shift > 0)
+        f = (lo >> shift) | (hi << (64 - shift));
+    else
+        f = -shift < 64 ? lo << -shift : 0;
+    return (bits >> 31) != 0 ? 0 - f : f;
+}
+
+__device__ __forceinline__ float2 cos_sin(uint64_t fraction, int position, float scale)
+{
+    const uint64_t turn = fraction * static_cast<uint64_t>(static_cast<int64_t>(position));
+    // The upper half as a signed number is the angle in half turns times 2^31, in [-1, 1).
+    const float half_turns = static_cast<float>(static_cast<int32_t>(turn >> 32)) * 0x1p-31f;
+    float s, c;
+    sincospif(half_turns, &s, &c);
+    return make_float2(c * scale, s * scale);
+}
+
+// ---------------------------------------------------------------------------
+// Units: VEC elements of T (a 16-byte vector, or one element) as fp32.
+// ---------------------------------------------------------------------------
+template <typename T, bool VEC>
+struct Part {
+    static constexpr int L = VEC ? Lanes<T>::V : 1;
+    __device__ static void load(const void* base, uint64_t e, float* f)
+    {
+        const T* p = static_cast<const T*>(base) + e;
+        if constexpr (VEC)
+            Lanes<T>::unpack(*reinterpret_cast<const uint4*>(p), f);
+        else
+            f[0] = Lanes<T>::to_f(*p);
+    }
+    __device__ static void store(void* base, uint64_t e, const float* f)
+    {
+        T* p = static_cast<T*>(base) + e;
+        if constexpr (VEC)
+            st16(p, Lanes<T>::pack(f));
+        else
+            *p = Lanes<T>::from_f(f[0]);
+    }
+};
+
+// Stores a unit of the cache: f / scale, rounded once.
+template <typename T, typename CT, bool VEC>
+__device__ __forceinline__ void store_cached(void* base, uint64_t e, float* f, float scale)
+{
+    constexpr int L = Part<T, VEC>::L;
+    if (scale != 1.0f) {
+#pragma unroll
+        for (int l = 0; l < L; ++l)
+            f[l] = __fdiv_rn(f[l], scale);
+    }
+    if constexpr (sizeof(CT) == 1) {
+        uint8_t* p = static_cast<uint8_t*>(base) + e;
+        if constexpr (VEC) {
+            uint32_t w[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(f[4 * i], f[4 * i + 1]), __NV_SATFINITE, __NV_E4M3);
+                const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(f[4 * i + 2], f[4 * i + 3]), __NV_SATFINITE, __NV_E4M3);
+                w[i] = lo | hi << 16;
+            }
+            *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+        } else {
+            *p = __nv_cvt_float_to_fp8(f[0], __NV_SATFINITE, __NV_E4M3);
+        }
+    } else {
+        Part<T, VEC>::store(base, e, f);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// The append.  A block takes up to kAppendMaxTokens rows: it finds their
+// sequences (one pass over seq_start, all threads at once: a binary search's
+// chain of loads would cost more than the row's copy), fills a table of their
+// cosines and sines in shared memory, which all heads of a row share, and then
+// walks the rows' units: pairs of vectors that rotate into each other, or
+// single vectors.  Bound by HBM for prompts and by its two dependent loads
+// (table, then nothing: rows are independent of it) for single tokens.
+// ---------------------------------------------------------------------------
+template <typename T, typename CT, bool VEC>
+__global__ void __launch_bounds__(kAppendThreads)
+k_kv_append(const AppendArgs a)
+{
+    extern __shared__ float2 s_turn[];  // [rows][half]
+    __shared__ int s_seq[kAppendMaxTokens];
+    __shared__ int s_pos[kAppendMaxTokens];
+    __shared__ int64_t s_dst[kAppendMaxTokens];  // element offset in the cache, -1: not cached
+    pdl_enter();
+    constexpr int L = Part<T, VEC>::L;
+    const int t0 = static_cast<int>(blockIdx.x) * a.block_tokens;
+    const int rows = min(a.block_tokens, a.tokens - t0);
+    const int tid = static_cast<int>(threadIdx.x);
+
+    int first = t0;  // sequence of row t0
+    if (a.seq_start != nullptr) {
+        first = 0;
+        for (int base = 0; base < a.batch; base += kAppendThreads)
+            first += __syncthreads_count(base + tid < a.batch && a.seq_start[base + tid + 1] <= t0);
+    }
+    if (tid < rows) {
+        const int t = t0 + tid;
+        int b = t, i = 0, n = 1;
+        if (a.seq_start != nullptr) {
+            b = first;
+            while (b < a.batch && a.seq_start[b + 1] <= t)
+                ++b;
+            if (b < a.batch) {
+                const int s = a.seq_start[b];
+                i = t - s;
+                n = a.seq_start[b + 1] - s;
+                if (i < 0)
+                    b = a.batch;  // before the first sequence
+            }
+        }
+        int64_t dst = -1, p = 0;
+        if (b < a.batch) {
+            p = static_cast<int64_t>(a.lengths[b]) - n + i;
+            if (p >= 0 && static_cast<uint64_t>(p) < a.capacity) {
+                const int column = static_cast<int>(p / a.page_size);
+                const int page = a.table[static_cast<uint64_t>(b) * a.table_stride + column];
+                if (page >= 0 && page < a.pages)
+                    dst = static_cast<int64_t>(static_cast<uint64_t>(page) * a.page_stride +
+                                               static_cast<uint64_t>(p % a.page_size) * a.token_stride);
+            }
+        }
+        s_seq[tid] = b < a.batch ? b : -1;
+        s_pos[tid] = a.positions != nullptr ? a.positions[t] : static_cast<int>(p);
+        s_dst[tid] = dst;
+    }
+    __syncthreads();
+    for (int x = tid; x < rows * a.half; x += kAppendThreads) {
+        const int row = x / a.half;
+        s_turn[x] = cos_sin(turn_fraction(a.inv_freq[x - row * a.half]), s_pos[row], a.rotary_scale);
+    }
+    __syncthreads();
+
+    const int q_units = a.q_heads * a.head_units;
+    const int k_units = q_units + a.kv_heads * a.head_units;
+    const int all = k_units + a.kv_heads * a.v_units;
+    const int pairs = a.half / L;  // units that are pairs (the vector path of interleaved pairs has none)
+    for (int x = tid; x < rows * all; x += kAppendThreads) {
+        const int row = (x >= all) + (x >= 2 * all) + (x >= 3 * all);
+        const int u = x - row * all;
+        const int64_t dst = s_dst[row];
+        const uint64_t t = static_cast<uint64_t>(t0 + row);
+        if (s_seq[row] < 0)
+            continue;
+        float f[L], g[L];
+        if (u >= k_units) {
+            if (dst < 0)
+                continue;
+            const uint32_t w = static_cast<uint32_t>(u - k_units);
+            const uint32_t head = static_cast<uint32_t>(w * a.v_magic >> 32);
+            const uint32_t d = (w - head * a.v_units) * L;
+            Part<T, VEC>::load(a.v, t * a.v_stride + head * a.head_dim + d, f);
+            store_cached<T, CT, VEC>(a.v_pages, dst + head * a.head_stride + d, f, a.v_scale);
+            continue;
+        }
+        const bool is_q = u < q_units;
+        if (!is_q && dst < 0)
+            continue;
+        const uint32_t w = static_cast<uint32_t>(is_q ? u : u - q_units);
+        const uint32_t head = static_cast<uint32_t>(w * a.head_magic >> 32);
+        const int c = static_cast<int>(w - head * a.head_units);
+        const void* src = is_q ? a.q : a.k;
+        const uint64_t from = t * (is_q ? a.q_stride : a.k_stride) + head * a.head_dim;
+        const uint64_t to = is_q ? t * a.q_out_stride + head * a.head_dim : dst + head * a.head_stride;
+        const float2* turn = s_turn + row * a.half;
+        const auto store = [&](int d, float* v) {
+            if (is_q)
+                Part<T, VEC>::store(a.q_out, to + d, v);
+            else
+                store_cached<T, CT, VEC>(a.k_pages, to + d, v, a.k_scale);
+        };
+        if (VEC && a.interleaved) {
+            const int d = c * L;
+            Part<T, VEC>::load(src, from + d, f);
+            if (d < 2 * a.half) {
+#pragma unroll
+                for (int l = 0; l + 1 < L; l += 2) {
+                    const float2 cs = turn[(d + l) / 2];
+                    const float x0 = f[l], y0 = f[l + 1];
+                    f[l] = x0 * cs.x - y0 * cs.y;
+                    f[l + 1] = y0 * cs.x + x0 * cs.y;
+                }
+            }
+            store(d, f);
+        } else if (c < pairs) {
+            const int d0 = a.interleaved ? 2 * c : c * L;
+            const int d1 = a.interleaved ? d0 + 1 : d0 + a.half;
+            Part<T, VEC>::load(src, from + d0, f);
+            Part<T, VEC>::load(src, from + d1, g);
+#pragma unroll
+            for (int l = 0; l < L; ++l) {
+                const float2 cs = turn[c * L + l];
+                const float x0 = f[l], y0 = g[l];
+                f[l] = x0 * cs.x - y0 * cs.y;
+                g[l] = y0 * cs.x + x0 * cs.y;
+            }
+            store(d0, f);
+            store(d1, g);
+        } else {
+            const int d = 2 * a.half + (c - pairs) * L;
+            Part<T, VEC>::load(src, from + d, f);
+            store(d, f);
+        }
+    }
+}
+
+template <typename T, typename CT>
+cudaError_t launch_append(const AppendArgs& args, bool vec, cudaStream_t s)
+{
+    AppendArgs a = args;
+    // Few rows: one a block, for latency; many: four, which share the search and the block's start.
+    a.block_tokens = a.tokens <= 1024 ? 1 : kAppendMaxTokens;
+    const unsigned grid = static_cast<unsigned>((a.tokens + a.block_tokens - 1) / a.block_tokens);
+    const size_t smem = static_cast<size_t>(a.block_tokens) * a.half * sizeof(float2);
+    return vec ? launch_k(k_kv_append<T, CT, true>, dim3(grid), dim3(kAppendThreads), smem, s, a)
+               : launch_k(k_kv_append<T, CT, false>, dim3(grid), dim3(kAppendThreads), smem, s, a);
+}
+
+template cudaError_t launch_append<float, float>(const AppendArgs&, bool, cudaStream_t);
+template cudaError_t launch_append<__half, __half>(const AppendArgs&, bool, cudaStream_t);
+template cudaError_t launch_append<__half, __nv_fp8_e4m3>(const AppendArgs&, bool, cudaStream_t);
+template cudaError_t launch_append<__nv_bfloat16, __nv_bfloat16>(const AppendArgs&, bool, cudaStream_t);
+template cudaError_t launch_append<__nv_bfloat16, __nv_fp8_e4m3>(const AppendArgs&, bool, cudaStream_t);
+
+// ---------------------------------------------------------------------------
+// The join of R partial attentions: a weighted R-way sum, bound by HBM like
+// k_sum.  A thread takes one unit of a row, forms the row's R weights itself
+// (R exponentials against R 16-byte loads: the threads of a row read the same
+// R words, one request a warp) and writes once.
+// ---------------------------------------------------------------------------
+template <typename T, bool PACKED, int R_CT>
+__global__ void __launch_bounds__(kFlatThreads)
+k_attention_join(const JoinArgs a)
+{
+    pdl_enter();
+    using U = Unit<T, PACKED>;
+    constexpr int L = U::L;
+    constexpr int N = R_CT > 0 ? R_CT : kMaxRanks;
+    const uint64_t i = static_cast<uint64_t>(blockIdx.x) * kFlatThreads + threadIdx.x;
+    if (i >= a.units)
+        return;
+    const uint64_t row = i / static_cast<uint32_t>(a.row_units);
+    typename U::raw v[R_CT > 0 ? R_CT : 1];
+    float w[N];
+#pragma unroll
+    for (int r = 0; r < N; ++r)
+        w[r] = r < a.R ? a.lse[r][row] : -INFINITY;
+    if constexpr (R_CT > 0) {
+#pragma unroll
+        for (int r = 0; r < R_CT; ++r)
+            v[r] = U::load(a.partials[r], i);
+    }
+    float top = -INFINITY;
+#pragma unroll
+    for (int r = 0; r < N; ++r)
+        top = fmaxf(top, w[r]);
+    const float base = top == -INFINITY ? 0.0f : top;
+    float total = 0.0f;
+    float acc[L];
+#pragma unroll
+    for (int l = 0; l < L; ++l)
+        acc[l] = 0.0f;
+#pragma unroll
+    for (int r = 0; r < N; ++r) {
+        if (w[r] == -INFINITY)
+            continue;  // counts nothing, whatever its row holds
+        const float e = expf(w[r] - base);
+        total += e;
+        float f[L];
+        if constexpr (R_CT > 0)
+            U::to_float(v[r], f);
+        else
+            U::to_float(U::load(a.partials[r], i), f);
+#pragma unroll
+        for (int l = 0; l < L; ++l)
+            acc[l] = fmaf(e, f[l], acc[l]);
+    }
+    const float inv = total == 0.0f ? 0.0f : 1.0f / total;
+#pragma unroll
+    for (int l = 0; l < L; ++l)
+        acc[l] *= inv;
+    U::store(a.out, i, acc);
+    if (a.lse_out != nullptr && i == row * static_cast<uint32_t>(a.row_units))
+        a.lse_out[row] = base + logf(total);
+}
+
+template <typename T>
+cudaError_t launch_join(const JoinArgs& a, bool packed, cudaStream_t s)
+{
+    const uint64_t blocks = (a.units + kFlatThreads - 1) / kFlatThreads;
+    if (blocks > static_cast<uint64_t>(INT_MAX))
+        return cudaErrorInvalidConfiguration;
+    const dim3 grid(static_cast<unsigned>(blocks)), block(kFlatThreads);
+    if (!packed)
+        return launch_k(k_attention_join<T, false, 0>, grid, block, 0, s, a);
+    switch (a.R) {
+    case 1: return launch_k(k_attention_join<T, true, 1>, grid, block, 0, s, a);
+    case 2: return launch_k(k_attention_join<T, true, 2>, grid, block, 0, s, a);
+    case 4: return launch_k(k_attention_join<T, true, 4>, grid, block, 0, s, a);
+    case 8: return launch_k(k_attention_join<T, true, 8>, grid, block, 0, s, a);
+    default: return launch_k(k_attention_join<T, true, 0>, grid, block, 0, s, a);
+    }
+}
+
+template cudaError_t launch_join<float>(const JoinArgs&, bool, cudaStream_t);
+template cudaError_t launch_join<__half>(const JoinArgs&, bool, cudaStream_t);
+template cudaError_t launch_join<__nv_bfloat16>(const JoinArgs&, bool, cudaStream_t);
+
+}  // namespace ar

@@ -1,0 +1,105 @@
+// ar_cache.h -- kernel argument blocks and launcher declarations of the paged
+// key-value cache calls, shared by their host side (ar_cache_api.cu) and the
+// kernel translation units.
+#pragma once
+
+#include <cuda_fp8.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "ar_internal.h"
+
+namespace ar {
+
+// Strides in elements.
+struct AppendArgs {
+    const void* q;  // nullable
+    const void* k;
+    const void* v;
+    void* q_out;
+    void* k_pages;
+    void* v_pages;
+    const int* table;
+    const int* lengths;
+    const int* seq_start;     // nullable: one row per sequence
+    const int* positions;     // nullable
+    const float* inv_freq;    // nullable with half == 0
+    uint64_t q_stride, k_stride, v_stride, q_out_stride;
+    uint64_t page_stride, token_stride, head_stride;
+    uint64_t capacity;        // max_pages * page_size
+    int pages, page_size, table_stride, batch;
+    int tokens, q_heads, kv_heads, head_dim;
+    int half;                 // rotated pairs of a head
+    int interleaved;
+    float rotary_scale, k_scale, v_scale;
+    int block_tokens;         // rows a block takes
+    int head_units, v_units;  // units of one q or k head, and of one v head
+    uint64_t head_magic, v_magic;  // ceil(2^32 / units): u / units == u * magic >> 32 for u * units < 2^32
+};
+
+// Rows a block of the append kernel may take, and its threads.
+constexpr int kAppendMaxTokens = 4;
+constexpr int kAppendThreads = 256;
+
+// One unit is a 16-byte vector of T (vec) or one element, a pair of them where the pair's halves lie apart.
+template <typename T, typename CT>
+cudaError_t launch_append(const AppendArgs& a, bool vec, cudaStream_t s);
+
+// Strides of the cache in bytes.
+struct AttnArgs {
+    const char* q;
+    const char* k;
+    const char* v;
+    char* out;
+    float* lse;               // nullable
+    float* part;              // partial results: two slots per block
+    const int* table;
+    const int* lengths;
+    uint64_t q_stride;        // bytes
+    uint64_t page_stride, token_stride, head_stride;
+    int table_stride, pages, page_size, batch;
+    int capacity;             // tokens a table row can hold
+    int kv_heads, group;      // group: query heads of one key-value head
+    int group_blocks;         // group cut into blocks of at most kAttnMaxHeads
+    int head_dim;
+    int window;
+    float scale;              // of the scores, k_scale included
+    float softcap;
+    float v_scale;
+    int slot_floats;          // floats of one partial slot
+};
+
+// Query heads of one key-value head that one block attends for at once.
+constexpr int kAttnMaxHeads = 16;
+// Blocks of the attention kernel, at most: two per SM of the 152.  The workspace holds two slots for each.
+constexpr int kAttnMaxBlocks = 304;
+constexpr int kAttnMaxDim = 256;
+
+// Cached tokens of one tile: what a block loads, and the work is cut into.
+__host__ __device__ constexpr int attn_tile(int) { return 32; }
+
+// A partial slot: [heads][head_dim] sums, [heads] maxima, [heads] sums of weights (heads = min(group, 16)).
+__host__ __device__ inline int attn_slot_floats(int group, int head_dim)
+{
+    const int heads = group < kAttnMaxHeads ? group : kAttnMaxHeads;
+    return (heads * (head_dim + 2) + 3) / 4 * 4;
+}
+
+// `blocks`: blocks of the attention kernel (the join kernel after it derives the same split from it).
+template <typename T, typename CT>
+cudaError_t launch_attention(const AttnArgs& a, int blocks, cudaStream_t s);
+
+struct JoinArgs {
+    const void* partials[kMaxRanks];
+    const float* lse[kMaxRanks];
+    void* out;
+    float* lse_out;           // nullable
+    int R;
+    int row_units;            // vectors (packed) or elements of a row
+    uint64_t units;           // rows * row_units
+};
+
+template <typename T>
+cudaError_t launch_join(const JoinArgs& a, bool packed, cudaStream_t s);
+
+}  // namespace ar

@@ -14,28 +14,10 @@
 
 #include "ar_kernels.cuh"
 #include "ar_lamport.cuh"
+#include "ar_launch_k.cuh"
 #include "ar_tma.cuh"
 
 namespace ar {
-
-// Launches `kernel` on `s` with the programmatic-stream-serialization
-// attribute (see pdl_enter in ar_kernels.cuh); returns the launch status.
-template <typename... KArgs, typename... Args>
-static cudaError_t launch_k(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t s,
-                            Args&&... args)
-{
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid;
-    cfg.blockDim = block;
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = pdl_enabled() ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
-}
 
 template <typename T, bool PACKED, int R_CT, int UNROLL>
 static cudaError_t run_sum(const SumArgs& a, int nslices, cudaStream_t s)
