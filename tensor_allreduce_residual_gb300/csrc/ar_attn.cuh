@@ -14,6 +14,9 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <climits>
+#include <type_traits>
+
 #include "ar_cache.h"
 #include "ar_kernels.cuh"
 #include "ar_launch_k.cuh"
@@ -45,14 +48,19 @@ struct Span {
 };
 
 template <int TILE>
-__device__ __forceinline__ Span span_of(const AttnArgs& a, int b)
+__device__ __forceinline__ Span span_of_length(const AttnArgs& a, int length)
 {
     Span s;
-    s.end = min(max(a.lengths[b], 0), a.capacity);
+    s.end = min(max(length, 0), a.capacity);
     s.start = a.window > 0 ? max(s.end - a.window, 0) : 0;
     s.tile0 = s.start / TILE;
     s.tiles = max((s.end + TILE - 1) / TILE - s.tile0, 1);
     return s;
+}
+template <int TILE>
+__device__ __forceinline__ Span span_of(const AttnArgs& a, int b)
+{
+    return span_of_length<TILE>(a, a.lengths[b]);
 }
 
 // The run of tiles of block `c` of `blocks`: the first total % blocks blocks take one more.
@@ -75,7 +83,9 @@ __device__ __forceinline__ int block_of(long long total, int blocks, long long x
 // Where a block is on the line.
 struct Cursor {
     int b, hb, tile;  // sequence, head and group block, tile of the item
+    int next_length;  // of sequence b + 1, loaded when b began
     Span s;
+    __device__ void fetch_next(const AttnArgs& a) { next_length = b + 1 < a.batch ? a.lengths[b + 1] : 0; }
     template <int TILE>
     __device__ void advance(const AttnArgs& a, int heads)
     {
@@ -85,8 +95,9 @@ struct Cursor {
         if (++hb < heads)
             return;
         hb = 0;
-        if (++b < a.batch)
-            s = span_of<TILE>(a, b);
+        ++b;
+        s = span_of_length<TILE>(a, next_length);
+        fetch_next(a);
     }
 };
 
@@ -149,6 +160,7 @@ __device__ Run find_run(const AttnArgs& a, int heads, Cursor& cur)
     const long long in = run.lo - s_before * heads;
     cur.hb = static_cast<int>(in / cur.s.tiles);
     cur.tile = static_cast<int>(in % cur.s.tiles);
+    cur.fetch_next(a);
     return run;
 }
 
@@ -160,30 +172,43 @@ struct TileInfo {
     int b, hb, flags, pad;
 };
 
-// Fills `info` for the cursor's tile, `t` of the run's `n`.  Threads of [0, TILE).
+// The description of the cursor's tile, `t` of the run's `n`, in two steps: the page's number is on its way between
+// them.  Thread `row` of [0, TILE) has token `row`.
+struct Described {
+    int page, slot, flags;
+    bool in;
+};
 template <int TILE>
-__device__ __forceinline__ void describe(const AttnArgs& a, const Cursor& cur, long long t, long long n, TileInfo<TILE>& info)
+__device__ __forceinline__ Described describe(const AttnArgs& a, const Cursor& cur, long long t, long long n, int row)
 {
-    const int tid = threadIdx.x;
-    if (tid < TILE) {
-        const int token = (cur.s.tile0 + cur.tile) * TILE + tid;
-        long long off = -1;
-        if (token >= cur.s.start && token < cur.s.end) {
-            const int column = token / a.page_size;
-            const int page = a.table[static_cast<uint64_t>(cur.b) * a.table_stride + column];
-            if (page >= 0 && page < a.pages)
-                off = static_cast<long long>(static_cast<uint64_t>(page) * a.page_stride +
-                                             static_cast<uint64_t>(token - column * a.page_size) * a.token_stride +
-                                             static_cast<uint64_t>(cur.hb / a.group_blocks) * a.head_stride);
-        }
-        info.offset[tid] = off;
+    Described d;
+    const int token = (cur.s.tile0 + cur.tile) * TILE + row;
+    d.in = row < TILE && token >= cur.s.start && token < cur.s.end;
+    d.page = -1;
+    d.slot = 0;
+    if (d.in) {
+        const int column = token / a.page_size;
+        d.slot = token - column * a.page_size;
+        d.page = a.table[static_cast<uint64_t>(cur.b) * a.table_stride + column];
     }
-    if (tid == 0) {
-        const bool begins = cur.tile == 0, ends = cur.tile + 1 == cur.s.tiles;
+    const bool begins = cur.tile == 0, ends = cur.tile + 1 == cur.s.tiles;
+    d.flags = (begins || t == 0 ? kTileFirst : 0) | (ends || t + 1 == n ? kTileLast : 0) |
+              (begins ? kTileBegins : 0) | (ends ? kTileEnds : 0);
+    return d;
+}
+template <int TILE>
+__device__ __forceinline__ void write_info(const AttnArgs& a, const Cursor& cur, const Described& d, int row, TileInfo<TILE>& info)
+{
+    if (row < TILE)
+        info.offset[row] = d.in && d.page >= 0 && d.page < a.pages
+                               ? static_cast<long long>(static_cast<uint64_t>(d.page) * a.page_stride +
+                                                        static_cast<uint64_t>(d.slot) * a.token_stride +
+                                                        static_cast<uint64_t>(cur.hb / a.group_blocks) * a.head_stride)
+                               : -1;
+    if (row == 0) {
         info.b = cur.b;
         info.hb = cur.hb;
-        info.flags = (begins || t == 0 ? kTileFirst : 0) | (ends || t + 1 == n ? kTileLast : 0) |
-                     (begins ? kTileBegins : 0) | (ends ? kTileEnds : 0);
+        info.flags = d.flags;
     }
 }
 
@@ -199,9 +224,9 @@ __device__ __forceinline__ int heads_of(const AttnArgs& a, int hb)
 }
 
 // A score in the exponent's base 2.
-__device__ __forceinline__ float score2(const AttnArgs& a, float dot)
+__device__ __forceinline__ float score2(const AttnArgs& a, float dot, float scale)
 {
-    const float s = dot * a.scale;
+    const float s = dot * scale;
     return (a.softcap > 0.0f ? a.softcap * tanhf(s / a.softcap) : s) * kLog2e;
 }
 __device__ __forceinline__ float lse_of(float top2, float total)
@@ -239,6 +264,7 @@ struct PlainShape {
     static constexpr int TILE_BYTES = TILE * PITCH;
     static constexpr int ITEM = STAGES * 2 * TILE_BYTES;
     static constexpr int SMEM = ITEM + HEADS * DIM * 4 + TILE * HEADS * 4;
+    static constexpr int BLOCKS = SMEM + 2048 + kSmemReservedPerBlock <= kSmemPerSM / 2 ? 2 : 1;
     // Threads over the head's elements, and over groups of heads where the elements leave some over.
     static constexpr int DT = DIM == 192 ? 96 : (DIM < 128 ? DIM : 128);
     static constexpr int HS = 128 / DT;
@@ -248,7 +274,7 @@ struct PlainShape {
 };
 
 template <typename T, typename CT, int DIM, int HEADS>
-__global__ void __launch_bounds__(kAttnThreads, 2)
+__global__ void __launch_bounds__(kAttnThreads, PlainShape<T, CT, DIM, HEADS>::BLOCKS)
 k_attn_plain(const AttnArgs a)
 {
     using P = PlainShape<T, CT, DIM, HEADS>;
@@ -271,7 +297,7 @@ k_attn_plain(const AttnArgs a)
     long long described = 0;
     const auto next_info = [&] {
         if (described < run.n) {
-            describe<TILE>(a, cur, described, run.n, s_info[described % RING]);
+            write_info<TILE>(a, cur, describe<TILE>(a, cur, described, run.n, tid), tid, s_info[described % RING]);
             cur.advance<TILE>(a, heads);
         }
         ++described;
@@ -359,7 +385,7 @@ k_attn_plain(const AttnArgs a)
             for (int i = 0; i < P::HPW; ++i) {
                 const int h = warp + i * kAttnWarps;
                 if (h < g) {
-                    const float x = in ? score2(a, dot[i]) : -INFINITY;
+                    const float x = in ? score2(a, dot[i], a.scale) : -INFINITY;
                     float top = x;
 #pragma unroll
                     for (int w = 16; w > 0; w >>= 1)
@@ -443,6 +469,463 @@ k_attn_plain(const AttnArgs a)
             __syncthreads();  // the next item's first tile writes s_top and s_total
         }
         next_info();
+    }
+}
+
+// ---------------------------------------------------------------------------
+// The matrix kernel, for 16-bit and 8-bit caches.  Scores are computed as
+// K Q^T and values as V^T P^T: tokens, and then the head's elements, are the
+// 16 rows of a matrix instruction and query heads its 8 columns, so that up to
+// 8 heads fill it where rows of queries would leave half of it empty, and both
+// operands from the cache come out of shared memory by ldmatrix as they lie
+// there.  Each warp takes a quarter of a tile's tokens with a maximum, a sum
+// and an accumulator of its own; the four meet once, at the end of the block's
+// part of an item.  Weights enter the second product as a pair of 16-bit
+// numbers, their rounding and what it leaves (17 bits and more together), which
+// costs an instruction that the memory's pace hides.  8-bit elements become
+// fp16 in registers, exactly; queries too large or small for fp16 are scaled
+// by a power of two per head first.
+// ---------------------------------------------------------------------------
+template <typename T, typename CT, int DIM, int NT>
+struct MmaShape {
+    static constexpr bool SMALL = sizeof(CT) == 1;
+    using MT = typename std::conditional<SMALL, __half, CT>::type;  // of the matrix instructions' operands
+    static constexpr int TILE = attn_tile(sizeof(CT));
+    static constexpr int KB = TILE / kAttnWarps / 16;  // 16-token blocks of a warp
+    static constexpr int CHUNKS = DIM * sizeof(CT) / 16;
+    static constexpr int QCHUNKS = DIM * sizeof(T) / 16;
+    // 16-byte chunks of a row: permuted within 128 bytes by the row, or padded to an odd number; either way the eight
+    // rows of an 8 x 8 matrix lie in different banks.
+    static constexpr int PITCH = CHUNKS % 8 == 0 ? CHUNKS : CHUNKS | 1;
+    static constexpr int QPITCH = QCHUNKS % 8 == 0 ? QCHUNKS : QCHUNKS | 1;
+    static constexpr int TILE_BYTES = TILE * PITCH * 16;
+    static constexpr int STAGE = 2 * TILE_BYTES + 8 * NT * QPITCH * 16;
+    static constexpr int INFO = TILE * 8 + 16;
+    static constexpr int OPITCH = DIM + 4;  // floats; the epilogue's rows, one per warp and head, lie in a used stage
+    static_assert(kAttnWarps * 8 * NT * OPITCH * 4 <= STAGE, "the epilogue fits a stage");
+    static constexpr int fits(int bytes)
+    {
+        const int n = (bytes - kSmemReservedPerBlock - 1024 - INFO) / (STAGE + INFO);
+        return n < 5 ? n : 5;
+    }
+    // Two blocks an SM where two stages of each fit, else one.
+    static constexpr int BLOCKS = fits(kSmemPerSM / 2) >= 2 ? 2 : 1;
+    static constexpr int STAGES = fits(kSmemPerSM / BLOCKS);
+    static constexpr int SMEM = STAGES * STAGE;
+    static __device__ __forceinline__ int chunk(int row, int c)
+    {
+        return CHUNKS % 8 == 0 ? row * PITCH + (c ^ (row & 7)) : row * PITCH + c;
+    }
+    static __device__ __forceinline__ int qchunk(int row, int c)
+    {
+        return QCHUNKS % 8 == 0 ? row * QPITCH + (c ^ (row & 7)) : row * QPITCH + c;
+    }
+};
+
+__device__ __forceinline__ void ldmatrix4(uint32_t addr, uint32_t* r)
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void ldmatrix4_trans(uint32_t addr, uint32_t* r)
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ uint32_t transposed(uint32_t x)
+{
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+template <typename MT>
+__device__ __forceinline__ void mma16816(float* c, const uint32_t* a, uint32_t b0, uint32_t b1)
+{
+    if constexpr (std::is_same<MT, __half>::value)
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+                     : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    else
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+                     : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// Two e4m3 values of the lower 16 bits as fp16, exactly.
+__device__ __forceinline__ uint32_t half2_of_e4m3(uint32_t x)
+{
+    uint32_t y;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(y) : "h"(static_cast<uint16_t>(x)));
+    return y;
+}
+__device__ __forceinline__ float exp2_fast(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+// Maximum or sum over the eight lanes that hold the same column.
+__device__ __forceinline__ float column_max(float x)
+{
+#pragma unroll
+    for (int w = 4; w < 32; w <<= 1)
+        x = fmaxf(x, __shfl_xor_sync(~0u, x, w));
+    return x;
+}
+__device__ __forceinline__ float column_sum(float x)
+{
+#pragma unroll
+    for (int w = 4; w < 32; w <<= 1)
+        x += __shfl_xor_sync(~0u, x, w);
+    return x;
+}
+
+template <typename T, typename CT, int DIM, int NT>
+__global__ void __launch_bounds__(kAttnThreads, MmaShape<T, CT, DIM, NT>::BLOCKS)
+k_attn_mma(const AttnArgs a)
+{
+    using P = MmaShape<T, CT, DIM, NT>;
+    using MT = typename P::MT;
+    constexpr int TILE = P::TILE, RING = P::STAGES + 1, KB = P::KB, MTILES = DIM / 16, KSTEPS = DIM / 16;
+    extern __shared__ __align__(128) char smem[];
+    __shared__ __align__(16) TileInfo<TILE> s_info[RING];
+    __shared__ float s_top[kAttnWarps][8 * NT], s_total[kAttnWarps][8 * NT];
+    pdl_enter();
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g8 = lane >> 2, t4 = lane & 3;
+    const int heads = a.kv_heads * a.group_blocks;
+    const int chunks = a.head_dim * static_cast<int>(sizeof(CT)) / 16;
+    const int qchunks = a.head_dim * static_cast<int>(sizeof(T)) / 16;
+
+    Cursor cur;
+    const Run run = find_run<TILE>(a, heads, cur);
+    if (run.n == 0)
+        return;
+    const int n = static_cast<int>(min(run.n, static_cast<long long>(INT_MAX)));
+
+    // Copies of tile `t` (in ring slot `slot` of the descriptions) into `stage`.  Chunks beyond the head's elements and
+    // tokens that are left out become zeros.
+    const auto issue = [&](int slot, int stage) {
+        const TileInfo<TILE>& info = s_info[slot];
+        const uint32_t base = smem_addr(smem + stage * P::STAGE);
+#pragma unroll
+        for (int i = 0; i < TILE * P::CHUNKS / kAttnThreads; ++i) {
+            const int x = tid + i * kAttnThreads;
+            const int row = x / P::CHUNKS, c = x - row * P::CHUNKS;
+            const long long off = info.offset[row];
+            const bool read = off >= 0 && c < chunks;
+            const long long at = read ? off + c * 16 : 0;
+            const uint32_t dst = base + P::chunk(row, c) * 16;
+            cp_async16(dst, a.k + at, read);
+            cp_async16(dst + P::TILE_BYTES, a.v + at, read);
+        }
+        if (info.flags & kTileFirst) {
+            const int g = heads_of(a, info.hb);
+            const char* q = a.q + info.b * a.q_stride + out_row(a, 0, info.hb, 0) * a.head_dim * sizeof(T);
+            for (int x = tid; x < 8 * NT * P::QCHUNKS; x += kAttnThreads) {
+                const int row = x / P::QCHUNKS, c = x - row * P::QCHUNKS;
+                const bool read = row < g && c < qchunks;
+                cp_async16(base + 2 * P::TILE_BYTES + P::qchunk(row, c) * 16,
+                           q + (read ? static_cast<size_t>(row) * a.head_dim * sizeof(T) + c * 16 : 0), read);
+            }
+        }
+    };
+
+    int described = 0, ring_w = 0;  // the next tile to describe, and its slot
+#pragma unroll 1
+    for (; described < P::STAGES; ++described) {
+        if (described < n) {
+            write_info<TILE>(a, cur, describe<TILE>(a, cur, described, n, tid), tid, s_info[ring_w]);
+            cur.advance<TILE>(a, heads);
+        }
+        ring_w = ring_w + 1 == RING ? 0 : ring_w + 1;
+    }
+    __syncthreads();
+#pragma unroll 1
+    for (int i = 0; i + 1 < P::STAGES; ++i) {
+        if (i < n)
+            issue(i, i);
+        cp_async_commit();
+    }
+
+    uint32_t qf[NT][KSTEPS][2];
+    float o[NT][MTILES][4], top[NT][2], total[NT][2], qscale[NT][2];
+    bool began = false;
+    int ring_r = 0, stage_r = 0, stage_w = P::STAGES - 1, ring_i = P::STAGES - 1;
+#pragma unroll 1
+    for (int t = 0; t < n; ++t) {
+        cp_async_wait<P::STAGES - 2>();
+        __syncthreads();
+        if (t + P::STAGES - 1 < n)
+            issue(ring_i, stage_w);
+        cp_async_commit();
+        Described next;
+        if (described < n)
+            next = describe<TILE>(a, cur, described, n, tid);
+        const TileInfo<TILE>& info = s_info[ring_r];
+        const int flags = info.flags;
+        char* stage = smem + stage_r * P::STAGE;
+        const uint32_t ks = smem_addr(stage), vs = ks + P::TILE_BYTES, qs = vs + P::TILE_BYTES;
+        if (flags & kTileFirst) {
+            began = flags & kTileBegins;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                if constexpr (!P::SMALL) {
+#pragma unroll
+                    for (int j = 0; j < KSTEPS; j += 2)
+                        ldmatrix4(qs + P::qchunk(nt * 8 + (lane & 7), 2 * j + (lane >> 3)) * 16, &qf[nt][j][0]);
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+                        qscale[nt][i] = a.scale;
+                } else {
+                    // Elements 4 t4 .. 4 t4 + 3 of each 16: the order in which the 8-bit keys' come.
+                    float most = 0.0f;
+#pragma unroll
+                    for (int j = 0; j < KSTEPS; ++j) {
+                        const uint2 w = *reinterpret_cast<const uint2*>(
+                            stage + 2 * P::TILE_BYTES + P::qchunk(nt * 8 + g8, 2 * j + (t4 >> 1)) * 16 + (t4 & 1) * 8);
+                        qf[nt][j][0] = w.x;
+                        qf[nt][j][1] = w.y;
+                        if constexpr (!std::is_same<T, __half>::value) {
+                            const float2 x = Lanes<T>::two(w.x), y = Lanes<T>::two(w.y);
+                            most = fmaxf(most, fmaxf(fmaxf(fabsf(x.x), fabsf(x.y)), fmaxf(fabsf(y.x), fabsf(y.y))));
+                        }
+                    }
+                    int e = 0;
+                    if constexpr (!std::is_same<T, __half>::value) {
+                        most = fmaxf(most, __shfl_xor_sync(~0u, most, 1));
+                        most = fmaxf(most, __shfl_xor_sync(~0u, most, 2));
+                        e = min(max(static_cast<int>(__float_as_uint(most) >> 23) - 127, -126), 126);
+                        const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+#pragma unroll
+                        for (int j = 0; j < KSTEPS; ++j)
+#pragma unroll
+                            for (int i = 0; i < 2; ++i) {
+                                const float2 x = Lanes<T>::two(qf[nt][j][i]);
+                                qf[nt][j][i] = Lanes<__half>::word(x.x * down, x.y * down);
+                            }
+                    }
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const int eh = __shfl_sync(~0u, e, (2 * t4 + i) * 4);
+                        // In two steps: the power of two alone may pass the range that its product with the scale keeps.
+                        qscale[nt][i] = ldexpf(a.scale, eh);
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    top[nt][i] = -INFINITY;
+                    total[nt][i] = 0.0f;
+                }
+#pragma unroll
+                for (int m = 0; m < MTILES; ++m)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        o[nt][m][i] = 0.0f;
+            }
+        }
+
+        // Scores of the warp's tokens: rows g8 and g8 + 8 of each block, heads 2 t4 and 2 t4 + 1 of each eight.
+        float s[KB][NT][4];
+#pragma unroll
+        for (int kb = 0; kb < KB; ++kb) {
+            const int row = (warp * KB + kb) * 16 + (lane & 15);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    s[kb][nt][i] = 0.0f;
+#pragma unroll
+            for (int j = 0; j < P::CHUNKS / 2; ++j) {
+                uint32_t r[4];
+                ldmatrix4(ks + P::chunk(row, 2 * j + (lane >> 4)) * 16, r);
+                if constexpr (!P::SMALL) {
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+                        mma16816<MT>(s[kb][nt], r, qf[nt][j][0], qf[nt][j][1]);
+                } else {
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        const uint32_t k[4] = {half2_of_e4m3(r[2 * c]), half2_of_e4m3(r[2 * c + 1]),
+                                               half2_of_e4m3(r[2 * c] >> 16), half2_of_e4m3(r[2 * c + 1] >> 16)};
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt)
+                            mma16816<MT>(s[kb][nt], k, qf[nt][2 * j + c][0], qf[nt][2 * j + c][1]);
+                    }
+                }
+            }
+            const int tok = (warp * KB + kb) * 16 + g8;
+            const bool in0 = info.offset[tok] >= 0, in1 = info.offset[tok + 8] >= 0;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    s[kb][nt][i] = (i < 2 ? in0 : in1) ? score2(a, s[kb][nt][i], qscale[nt][i & 1]) : -INFINITY;
+        }
+
+        // The running maximum and sum.
+        uint32_t hi[KB][NT][2], lo[KB][NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            float base[2];
+            bool moved = false;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                float x = fmaxf(s[0][nt][i], s[0][nt][i + 2]);
+#pragma unroll
+                for (int kb = 1; kb < KB; ++kb)
+                    x = fmaxf(x, fmaxf(s[kb][nt][i], s[kb][nt][i + 2]));
+                x = fmaxf(column_max(x), top[nt][i]);
+                moved = moved || x > top[nt][i];
+                base[i] = x;
+            }
+            if (__any_sync(~0u, moved)) {
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    // A maximum of minus infinity stands still here: 0 in its place keeps the difference defined.
+                    const float fix = exp2_fast(top[nt][i] - (base[i] == -INFINITY ? 0.0f : base[i]));
+                    top[nt][i] = base[i];
+                    total[nt][i] *= fix;
+#pragma unroll
+                    for (int m = 0; m < MTILES; ++m) {
+                        o[nt][m][i] *= fix;
+                        o[nt][m][i + 2] *= fix;
+                    }
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                base[i] = base[i] == -INFINITY ? 0.0f : base[i];
+#pragma unroll
+            for (int kb = 0; kb < KB; ++kb) {
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    const float p0 = exp2_fast(s[kb][nt][2 * r] - base[0]);
+                    const float p1 = exp2_fast(s[kb][nt][2 * r + 1] - base[1]);
+                    total[nt][0] += p0;
+                    total[nt][1] += p1;
+                    const uint32_t h = Lanes<MT>::word(p0, p1);
+                    const float2 back = Lanes<MT>::two(h);
+                    hi[kb][nt][r] = transposed(h);
+                    lo[kb][nt][r] = transposed(Lanes<MT>::word(p0 - back.x, p1 - back.y));
+                }
+            }
+        }
+
+        // Weighted values.  Rows of the result: elements g8 and g8 + 8 of each 16, or 2 g8 and 2 g8 + 1 (8-bit).
+#pragma unroll
+        for (int kb = 0; kb < KB; ++kb) {
+            const int row = (warp * KB + kb) * 16;
+            if constexpr (!P::SMALL) {
+#pragma unroll
+                for (int m = 0; m < MTILES; ++m) {
+                    uint32_t r[4];
+                    ldmatrix4_trans(vs + P::chunk(row + (lane & 7) + (lane >> 4) * 8, 2 * m + (lane >> 3 & 1)) * 16, r);
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        mma16816<MT>(o[nt][m], r, hi[kb][nt][0], hi[kb][nt][1]);
+                        mma16816<MT>(o[nt][m], r, lo[kb][nt][0], lo[kb][nt][1]);
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < P::CHUNKS / 2; ++j) {
+                    uint32_t r[4];
+                    ldmatrix4_trans(vs + P::chunk(row + (lane & 15), 2 * j + (lane >> 4)) * 16, r);
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        const uint32_t v[4] = {half2_of_e4m3(__byte_perm(r[2 * c], 0, 0x20)), half2_of_e4m3(__byte_perm(r[2 * c], 0, 0x31)),
+                                               half2_of_e4m3(__byte_perm(r[2 * c + 1], 0, 0x20)), half2_of_e4m3(__byte_perm(r[2 * c + 1], 0, 0x31))};
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) {
+                            mma16816<MT>(o[nt][2 * j + c], v, hi[kb][nt][0], hi[kb][nt][1]);
+                            mma16816<MT>(o[nt][2 * j + c], v, lo[kb][nt][0], lo[kb][nt][1]);
+                        }
+                    }
+                }
+            }
+        }
+
+        if (flags & kTileLast) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    total[nt][i] = column_sum(total[nt][i]);
+                    if (g8 == 0) {
+                        s_top[warp][nt * 8 + 2 * t4 + i] = top[nt][i];
+                        s_total[warp][nt * 8 + 2 * t4 + i] = total[nt][i];
+                    }
+                }
+            __syncthreads();  // and every warp is done with the stage
+            float* rows = reinterpret_cast<float*>(stage);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int head = nt * 8 + 2 * t4 + i;
+                    float best = s_top[0][head];
+#pragma unroll
+                    for (int w = 1; w < kAttnWarps; ++w)
+                        best = fmaxf(best, s_top[w][head]);
+                    const float fix = exp2_fast(top[nt][i] - (best == -INFINITY ? 0.0f : best));
+                    float* out = rows + (warp * 8 * NT + head) * P::OPITCH;
+#pragma unroll
+                    for (int m = 0; m < MTILES; ++m) {
+                        out[m * 16 + (P::SMALL ? 2 * g8 : g8)] = o[nt][m][i] * fix;
+                        out[m * 16 + (P::SMALL ? 2 * g8 + 1 : g8 + 8)] = o[nt][m][i + 2] * fix;
+                    }
+                }
+            __syncthreads();
+            const bool whole = began && (flags & kTileEnds);
+            const int g = heads_of(a, info.hb), fours = a.head_dim / 4;
+            const int slots = min(a.group, kAttnMaxHeads);
+            float* part = a.part + (2ull * blockIdx.x + (began ? 1 : 0)) * a.slot_floats;
+            for (int x = tid; x < g * fours; x += kAttnThreads) {
+                const int head = x / fours, d = (x - head * fours) * 4;
+                float best = s_top[0][head], sum = 0.0f;
+#pragma unroll
+                for (int w = 1; w < kAttnWarps; ++w)
+                    best = fmaxf(best, s_top[w][head]);
+                const float base = best == -INFINITY ? 0.0f : best;
+                float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+                for (int w = 0; w < kAttnWarps; ++w) {
+                    sum += s_total[w][head] * exp2_fast(s_top[w][head] - base);
+                    const float4 y = *reinterpret_cast<const float4*>(rows + (w * 8 * NT + head) * P::OPITCH + d);
+                    v.x += y.x;
+                    v.y += y.y;
+                    v.z += y.z;
+                    v.w += y.w;
+                }
+                if (whole) {
+                    const uint64_t row = out_row(a, info.b, info.hb, head);
+                    const float f = out_scale(a, sum);
+                    *reinterpret_cast<uint2*>(a.out + (row * a.head_dim + d) * sizeof(T)) =
+                        make_uint2(Lanes<T>::word(v.x * f, v.y * f), Lanes<T>::word(v.z * f, v.w * f));
+                    if (d == 0 && a.lse != nullptr)
+                        a.lse[row] = lse_of(best, sum);
+                } else {
+                    *reinterpret_cast<float4*>(part + head * a.head_dim + d) = v;
+                    if (d == 0) {
+                        part[slots * a.head_dim + head] = best;
+                        part[slots * (a.head_dim + 1) + head] = sum;
+                    }
+                }
+            }
+        }
+        if (described < n) {
+            write_info<TILE>(a, cur, next, tid, s_info[ring_w]);
+            cur.advance<TILE>(a, heads);
+            ++described;
+            ring_w = ring_w + 1 == RING ? 0 : ring_w + 1;
+        }
+        ring_r = ring_r + 1 == RING ? 0 : ring_r + 1;
+        ring_i = ring_i + 1 == RING ? 0 : ring_i + 1;
+        stage_r = stage_r + 1 == P::STAGES ? 0 : stage_r + 1;
+        stage_w = stage_w + 1 == P::STAGES ? 0 : stage_w + 1;
     }
 }
 
@@ -544,38 +1027,54 @@ k_attn_join(const AttnArgs a, const int blocks)
         a.lse[row] = lse_of(best, sum);
 }
 
-template <typename Kernel>
-cudaError_t launch_tiles(Kernel kernel, const AttnArgs& a, int blocks, size_t smem, cudaStream_t s)
+// Launches `kernel`, `per_sm` blocks of which fit an SM, and then the join.
+template <typename T, int TILE, typename Kernel>
+cudaError_t launch_tiles(Kernel kernel, const AttnArgs& a, int most, int sms, int per_sm, size_t smem, cudaStream_t s)
 {
-    const cudaError_t e =
-        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-    return e != cudaSuccess ? e : launch_k(kernel, dim3(blocks), dim3(kAttnThreads), smem, s, a);
+    const uint64_t joins = static_cast<uint64_t>(a.batch) * a.kv_heads * a.group_blocks * (a.group < kAttnMaxHeads ? a.group : kAttnMaxHeads);
+    if (joins > static_cast<uint64_t>(INT_MAX))
+        return cudaErrorInvalidConfiguration;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    if (e != cudaSuccess)
+        return e;
+    const int blocks = most < sms * per_sm ? most : sms * per_sm;
+    e = launch_k(kernel, dim3(blocks), dim3(kAttnThreads), smem, s, a);
+    if (e != cudaSuccess)
+        return e;
+    return launch_k(k_attn_join<T, TILE>, dim3(static_cast<unsigned>(joins)), dim3(kAttnThreads), 0, s, a, blocks);
+}
+
+template <typename T, typename CT, int DIM, int HEADS>
+cudaError_t launch_heads(const AttnArgs& a, int most, int sms, cudaStream_t s)
+{
+    constexpr int TILE = attn_tile(sizeof(CT));
+    if constexpr (sizeof(CT) == 4) {
+        using P = PlainShape<T, CT, DIM, HEADS>;
+        return launch_tiles<T, TILE>(k_attn_plain<T, CT, DIM, HEADS>, a, most, sms, P::BLOCKS, P::SMEM, s);
+    } else {
+        using P = MmaShape<T, CT, DIM, HEADS / 8>;
+        return launch_tiles<T, TILE>(k_attn_mma<T, CT, DIM, HEADS / 8>, a, most, sms, P::BLOCKS, P::SMEM, s);
+    }
 }
 
 template <typename T, typename CT, int DIM>
-cudaError_t launch_plain(const AttnArgs& a, int blocks, cudaStream_t s)
+cudaError_t launch_dim(const AttnArgs& a, int most, int sms, cudaStream_t s)
 {
-    if (a.group <= 2)
-        return launch_tiles(k_attn_plain<T, CT, DIM, 2>, a, blocks, PlainShape<T, CT, DIM, 2>::SMEM, s);
-    if (a.group <= 8)
-        return launch_tiles(k_attn_plain<T, CT, DIM, 8>, a, blocks, PlainShape<T, CT, DIM, 8>::SMEM, s);
-    return launch_tiles(k_attn_plain<T, CT, DIM, 16>, a, blocks, PlainShape<T, CT, DIM, 16>::SMEM, s);
+    if constexpr (sizeof(CT) == 4) {
+        if (a.group <= 2)
+            return launch_heads<T, CT, DIM, 2>(a, most, sms, s);
+    }
+    return a.group <= 8 ? launch_heads<T, CT, DIM, 8>(a, most, sms, s) : launch_heads<T, CT, DIM, 16>(a, most, sms, s);
 }
 
 template <typename T, typename CT>
-cudaError_t launch_attention(const AttnArgs& a, int blocks, cudaStream_t s)
+cudaError_t launch_attention(const AttnArgs& a, int most, int sms, cudaStream_t s)
 {
-    const uint64_t joins = static_cast<uint64_t>(a.batch) * a.kv_heads * a.group_blocks * (a.group < kAttnMaxHeads ? a.group : kAttnMaxHeads);
-    if (joins > 0x7fffffffull)
-        return cudaErrorInvalidConfiguration;
-    cudaError_t e = a.head_dim <= 64    ? launch_plain<T, CT, 64>(a, blocks, s)
-                    : a.head_dim <= 96  ? launch_plain<T, CT, 96>(a, blocks, s)
-                    : a.head_dim <= 128 ? launch_plain<T, CT, 128>(a, blocks, s)
-                    : a.head_dim <= 192 ? launch_plain<T, CT, 192>(a, blocks, s)
-                                        : launch_plain<T, CT, 256>(a, blocks, s);
-    if (e != cudaSuccess)
-        return e;
-    return launch_k(k_attn_join<T, 32>, dim3(static_cast<unsigned>(joins)), dim3(kAttnThreads), 0, s, a, blocks);
+    return a.head_dim <= 64    ? launch_dim<T, CT, 64>(a, most, sms, s)
+           : a.head_dim <= 96  ? launch_dim<T, CT, 96>(a, most, sms, s)
+           : a.head_dim <= 128 ? launch_dim<T, CT, 128>(a, most, sms, s)
+           : a.head_dim <= 192 ? launch_dim<T, CT, 192>(a, most, sms, s)
+                               : launch_dim<T, CT, 256>(a, most, sms, s);
 }
 
 }  // namespace ar

@@ -4,7 +4,7 @@
 
 namespace ar {
 
-template cudaError_t launch_attention<__nv_bfloat16, __nv_bfloat16>(const AttnArgs&, int, cudaStream_t);
-template cudaError_t launch_attention<__nv_bfloat16, __nv_fp8_e4m3>(const AttnArgs&, int, cudaStream_t);
+template cudaError_t launch_attention<__nv_bfloat16, __nv_bfloat16>(const AttnArgs&, int, int, cudaStream_t);
+template cudaError_t launch_attention<__nv_bfloat16, __nv_fp8_e4m3>(const AttnArgs&, int, int, cudaStream_t);
 
 }  // namespace ar

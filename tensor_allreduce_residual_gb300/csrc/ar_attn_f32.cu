@@ -4,6 +4,6 @@
 
 namespace ar {
 
-template cudaError_t launch_attention<float, float>(const AttnArgs&, int, cudaStream_t);
+template cudaError_t launch_attention<float, float>(const AttnArgs&, int, int, cudaStream_t);
 
 }  // namespace ar

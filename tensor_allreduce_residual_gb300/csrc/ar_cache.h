@@ -76,7 +76,7 @@ constexpr int kAttnMaxBlocks = 304;
 constexpr int kAttnMaxDim = 256;
 
 // Cached tokens of one tile: what a block loads, and the work is cut into.
-__host__ __device__ constexpr int attn_tile(int) { return 32; }
+__host__ __device__ constexpr int attn_tile(int cache_esize) { return 128 / cache_esize; }
 
 // A partial slot: [heads][head_dim] sums, [heads] maxima, [heads] sums of weights (heads = min(group, 16)).
 __host__ __device__ inline int attn_slot_floats(int group, int head_dim)
@@ -85,9 +85,9 @@ __host__ __device__ inline int attn_slot_floats(int group, int head_dim)
     return (heads * (head_dim + 2) + 3) / 4 * 4;
 }
 
-// `blocks`: blocks of the attention kernel (the join kernel after it derives the same split from it).
+// At most `most` blocks of the attention kernel, and no more than `sms` SMs hold at once; then the join kernel.
 template <typename T, typename CT>
-cudaError_t launch_attention(const AttnArgs& a, int blocks, cudaStream_t s);
+cudaError_t launch_attention(const AttnArgs& a, int most, int sms, cudaStream_t s);
 
 struct JoinArgs {
     const void* partials[kMaxRanks];

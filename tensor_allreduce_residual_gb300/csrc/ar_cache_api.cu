@@ -96,15 +96,15 @@ int check_attention(const ar_kv_cache* c, int q_heads)
     return AR_OK;
 }
 
-// Blocks of the attention kernel: as many as the SMs hold at once, and no more than there can be tiles.
-int attention_blocks(const ar_kv_cache* c, int q_heads, int resident)
+// Blocks of the attention kernel, at most: no more than there can be tiles.
+int attention_blocks(const ar_kv_cache* c, int q_heads)
 {
     const long long cap = static_cast<long long>(c->max_pages) * c->page_size;
     const long long tile = ar::attn_tile(cache_esize_of(c->dtype));
     const long long group_blocks = (q_heads / c->kv_heads + ar::kAttnMaxHeads - 1) / ar::kAttnMaxHeads;
     const long long items = static_cast<long long>(c->batch) * c->kv_heads * group_blocks;
     const long long tiles = (cap < INT_MAX ? cap : INT_MAX) / tile + 2;
-    const long long most = resident < ar::kAttnMaxBlocks ? resident : ar::kAttnMaxBlocks;
+    const long long most = ar::kAttnMaxBlocks;
     return static_cast<int>(items >= most || items * tiles >= most ? most : items * tiles);
 }
 
@@ -200,7 +200,7 @@ size_t ar_paged_attention_workspace_size(const ar_kv_cache* cache, int q_heads)
     const ar_kv_cache* const c = &own;
     if (check_attention(c, q_heads) != AR_OK)
         return 0;
-    const size_t blocks = static_cast<size_t>(attention_blocks(c, q_heads, ar::kAttnMaxBlocks));
+    const size_t blocks = static_cast<size_t>(attention_blocks(c, q_heads));
     const size_t slot = static_cast<size_t>(ar::attn_slot_floats(q_heads / c->kv_heads, c->head_dim)) * sizeof(float);
     return (2 * blocks * slot + 255) / 256 * 256;
 }
@@ -265,10 +265,10 @@ int ar_paged_attention(const ar_kv_cache* cache, const void* q, size_t q_stride,
     if (cudaGetDevice(&dev) != cudaSuccess ||
         cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
         return AR_ERR_CUDA;
-    const int blocks = attention_blocks(c, q_heads, 2 * sms);
+    const int most = attention_blocks(c, q_heads);
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     return status_of(by_dtypes(dtype, c->dtype, [&](auto t, auto ct) {
-        return ar::launch_attention<decltype(t), decltype(ct)>(a, blocks, s);
+        return ar::launch_attention<decltype(t), decltype(ct)>(a, most, sms, s);
     }));
 }
 
