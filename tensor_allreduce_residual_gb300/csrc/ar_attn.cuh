@@ -172,43 +172,30 @@ struct TileInfo {
     int b, hb, flags, pad;
 };
 
-// The description of the cursor's tile, `t` of the run's `n`, in two steps: the page's number is on its way between
-// them.  Thread `row` of [0, TILE) has token `row`.
-struct Described {
-    int page, slot, flags;
-    bool in;
-};
+// Fills `info` for the cursor's tile, `t` of the run's `n`.
 template <int TILE>
-__device__ __forceinline__ Described describe(const AttnArgs& a, const Cursor& cur, long long t, long long n, int row)
+__device__ __forceinline__ void describe(const AttnArgs& a, const Cursor& cur, long long t, long long n, TileInfo<TILE>& info)
 {
-    Described d;
-    const int token = (cur.s.tile0 + cur.tile) * TILE + row;
-    d.in = row < TILE && token >= cur.s.start && token < cur.s.end;
-    d.page = -1;
-    d.slot = 0;
-    if (d.in) {
-        const int column = token / a.page_size;
-        d.slot = token - column * a.page_size;
-        d.page = a.table[static_cast<uint64_t>(cur.b) * a.table_stride + column];
+    const int tid = threadIdx.x;
+    if (tid < TILE) {
+        const int token = (cur.s.tile0 + cur.tile) * TILE + tid;
+        long long off = -1;
+        if (token >= cur.s.start && token < cur.s.end) {
+            const uint32_t column = static_cast<uint32_t>(static_cast<uint64_t>(token) * a.page_magic >> a.page_shift);
+            const int page = a.table[static_cast<uint64_t>(cur.b) * a.table_stride + column];
+            if (page >= 0 && page < a.pages)
+                off = static_cast<long long>(static_cast<uint64_t>(page) * a.page_stride +
+                                             static_cast<uint64_t>(token - static_cast<int>(column) * a.page_size) * a.token_stride +
+                                             static_cast<uint64_t>(cur.hb / a.group_blocks) * a.head_stride);
+        }
+        info.offset[tid] = off;
     }
-    const bool begins = cur.tile == 0, ends = cur.tile + 1 == cur.s.tiles;
-    d.flags = (begins || t == 0 ? kTileFirst : 0) | (ends || t + 1 == n ? kTileLast : 0) |
-              (begins ? kTileBegins : 0) | (ends ? kTileEnds : 0);
-    return d;
-}
-template <int TILE>
-__device__ __forceinline__ void write_info(const AttnArgs& a, const Cursor& cur, const Described& d, int row, TileInfo<TILE>& info)
-{
-    if (row < TILE)
-        info.offset[row] = d.in && d.page >= 0 && d.page < a.pages
-                               ? static_cast<long long>(static_cast<uint64_t>(d.page) * a.page_stride +
-                                                        static_cast<uint64_t>(d.slot) * a.token_stride +
-                                                        static_cast<uint64_t>(cur.hb / a.group_blocks) * a.head_stride)
-                               : -1;
-    if (row == 0) {
+    if (tid == 0) {
+        const bool begins = cur.tile == 0, ends = cur.tile + 1 == cur.s.tiles;
         info.b = cur.b;
         info.hb = cur.hb;
-        info.flags = d.flags;
+        info.flags = (begins || t == 0 ? kTileFirst : 0) | (ends || t + 1 == n ? kTileLast : 0) |
+                     (begins ? kTileBegins : 0) | (ends ? kTileEnds : 0);
     }
 }
 
@@ -223,11 +210,10 @@ __device__ __forceinline__ int heads_of(const AttnArgs& a, int hb)
     return min(a.group - (hb % a.group_blocks) * kAttnMaxHeads, kAttnMaxHeads);
 }
 
-// A score in the exponent's base 2.
-__device__ __forceinline__ float score2(const AttnArgs& a, float dot, float scale)
+// A score in the exponent's base 2, of a dot product times scale2.
+__device__ __forceinline__ float score2(const AttnArgs& a, float s)
 {
-    const float s = dot * scale;
-    return (a.softcap > 0.0f ? a.softcap * tanhf(s / a.softcap) : s) * kLog2e;
+    return a.softcap > 0.0f ? a.softcap2 * tanhf(s) : s;
 }
 __device__ __forceinline__ float lse_of(float top2, float total)
 {
@@ -297,7 +283,7 @@ k_attn_plain(const AttnArgs a)
     long long described = 0;
     const auto next_info = [&] {
         if (described < run.n) {
-            write_info<TILE>(a, cur, describe<TILE>(a, cur, described, run.n, tid), tid, s_info[described % RING]);
+            describe<TILE>(a, cur, described, run.n, s_info[described % RING]);
             cur.advance<TILE>(a, heads);
         }
         ++described;
@@ -385,7 +371,7 @@ k_attn_plain(const AttnArgs a)
             for (int i = 0; i < P::HPW; ++i) {
                 const int h = warp + i * kAttnWarps;
                 if (h < g) {
-                    const float x = in ? score2(a, dot[i], a.scale) : -INFINITY;
+                    const float x = in ? score2(a, dot[i] * a.scale2) : -INFINITY;
                     float top = x;
 #pragma unroll
                     for (int w = 16; w > 0; w >>= 1)
@@ -478,9 +464,10 @@ k_attn_plain(const AttnArgs a)
 // 16 rows of a matrix instruction and query heads its 8 columns, so that up to
 // 8 heads fill it where rows of queries would leave half of it empty, and both
 // operands from the cache come out of shared memory by ldmatrix as they lie
-// there.  Each warp takes a quarter of a tile's tokens with a maximum, a sum
-// and an accumulator of its own; the four meet once, at the end of the block's
-// part of an item.  Weights enter the second product as a pair of 16-bit
+// there.  Each warp takes a quarter of a tile's tokens, through a ring of its
+// own, with a maximum, a sum and an accumulator of its own: the four meet at the
+// ends of the block's part of an item only, and between them no warp waits for
+// another.  Weights enter the second product as a pair of 16-bit
 // numbers, their rounding and what it leaves (17 bits and more together), which
 // costs an instruction that the memory's pace hides.  8-bit elements become
 // fp16 in registers, exactly; queries too large or small for fp16 are scaled
@@ -491,16 +478,18 @@ struct MmaShape {
     static constexpr bool SMALL = sizeof(CT) == 1;
     using MT = typename std::conditional<SMALL, __half, CT>::type;  // of the matrix instructions' operands
     static constexpr int TILE = attn_tile(sizeof(CT));
-    static constexpr int KB = TILE / kAttnWarps / 16;  // 16-token blocks of a warp
+    static constexpr int TOKENS = TILE / kAttnWarps;  // a warp's tokens of a tile
+    static constexpr int KB = TOKENS / 16;            // and their blocks of 16
     static constexpr int CHUNKS = DIM * sizeof(CT) / 16;
     static constexpr int QCHUNKS = DIM * sizeof(T) / 16;
     // 16-byte chunks of a row: permuted within 128 bytes by the row, or padded to an odd number; either way the eight
     // rows of an 8 x 8 matrix lie in different banks.
     static constexpr int PITCH = CHUNKS % 8 == 0 ? CHUNKS : CHUNKS | 1;
     static constexpr int QPITCH = QCHUNKS % 8 == 0 ? QCHUNKS : QCHUNKS | 1;
-    static constexpr int TILE_BYTES = TILE * PITCH * 16;
-    static constexpr int STAGE = 2 * TILE_BYTES + 8 * NT * QPITCH * 16;
-    static constexpr int INFO = TILE * 8 + 16;
+    static constexpr int HALF = TOKENS * PITCH * 16;  // a warp's keys of a stage, and its values
+    static constexpr int QROWS = kAttnWarps * 2 * HALF;  // where a stage's queries begin
+    static constexpr int STAGE = QROWS + 8 * NT * QPITCH * 16;
+    static constexpr int INFO = kAttnWarps * (TOKENS * 8 + 16);
     static constexpr int OPITCH = DIM + 4;  // floats; the epilogue's rows, one per warp and head, lie in a used stage
     static_assert(kAttnWarps * 8 * NT * OPITCH * 4 <= STAGE, "the epilogue fits a stage");
     static constexpr int fits(int bytes)
@@ -508,8 +497,12 @@ struct MmaShape {
         const int n = (bytes - kSmemReservedPerBlock - 1024 - INFO) / (STAGE + INFO);
         return n < 5 ? n : 5;
     }
-    // Two blocks an SM where two stages of each fit, else one.
-    static constexpr int BLOCKS = fits(kSmemPerSM / 2) >= 2 ? 2 : 1;
+    // Blocks of an SM.  A tile of few bytes takes a warp longer than they take to come, so that more warps help: four
+    // blocks of heads up to 64 elements (31.8 against 34.3 us with two on 93 MB of fp16 cache), three of 8-bit ones up to
+    // 128 (93.5 against 98.6 us on 533 MB).  For 128 16-bit elements two blocks' deeper rings do better (93 against 98 us
+    // on 511 MB).  Long heads leave room for two stages in one block only.
+    static constexpr int WANT = NT == 1 && DIM <= 64 ? 4 : NT == 1 && DIM <= 128 && SMALL ? 3 : 2;
+    static constexpr int BLOCKS = fits(kSmemPerSM / WANT) >= 2 ? WANT : 1;
     static constexpr int STAGES = fits(kSmemPerSM / BLOCKS);
     static constexpr int SMEM = STAGES * STAGE;
     static __device__ __forceinline__ int chunk(int row, int c)
@@ -520,6 +513,14 @@ struct MmaShape {
     {
         return QCHUNKS % 8 == 0 ? row * QPITCH + (c ^ (row & 7)) : row * QPITCH + c;
     }
+};
+
+// A warp's part of one tile in flight: whose it is, its tokens' offsets in the cache, and which of them count.
+template <int TOKENS>
+struct WarpTile {
+    long long offset[TOKENS];
+    int b, hb, flags;
+    uint32_t in;
 };
 
 __device__ __forceinline__ void ldmatrix4(uint32_t addr, uint32_t* r)
@@ -589,9 +590,9 @@ k_attn_mma(const AttnArgs a)
 {
     using P = MmaShape<T, CT, DIM, NT>;
     using MT = typename P::MT;
-    constexpr int TILE = P::TILE, RING = P::STAGES + 1, KB = P::KB, MTILES = DIM / 16, KSTEPS = DIM / 16;
+    constexpr int TILE = P::TILE, TOKENS = P::TOKENS, RING = P::STAGES + 1, KB = P::KB, MTILES = DIM / 16, KSTEPS = DIM / 16;
     extern __shared__ __align__(128) char smem[];
-    __shared__ __align__(16) TileInfo<TILE> s_info[RING];
+    __shared__ __align__(16) WarpTile<TOKENS> s_tiles[kAttnWarps][RING];
     __shared__ float s_top[kAttnWarps][8 * NT], s_total[kAttnWarps][8 * NT];
     pdl_enter();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g8 = lane >> 2, t4 = lane & 3;
@@ -605,69 +606,103 @@ k_attn_mma(const AttnArgs a)
         return;
     const int n = static_cast<int>(min(run.n, static_cast<long long>(INT_MAX)));
 
-    // Copies of tile `t` (in ring slot `slot` of the descriptions) into `stage`.  Chunks beyond the head's elements and
-    // tokens that are left out become zeros.
-    const auto issue = [&](int slot, int stage) {
-        const TileInfo<TILE>& info = s_info[slot];
-        const uint32_t base = smem_addr(smem + stage * P::STAGE);
-#pragma unroll
-        for (int i = 0; i < TILE * P::CHUNKS / kAttnThreads; ++i) {
-            const int x = tid + i * kAttnThreads;
-            const int row = x / P::CHUNKS, c = x - row * P::CHUNKS;
-            const long long off = info.offset[row];
-            const bool read = off >= 0 && c < chunks;
-            const long long at = read ? off + c * 16 : 0;
-            const uint32_t dst = base + P::chunk(row, c) * 16;
-            cp_async16(dst, a.k + at, read);
-            cp_async16(dst + P::TILE_BYTES, a.v + at, read);
+    // The description of the cursor's tile, `t` of the run, in two steps: its pages' numbers are on their way between them.
+    WarpTile<TOKENS>* const tiles = s_tiles[warp];
+    int page = -1, slot = 0;
+    const auto look_up = [&] {
+        const int token = (cur.s.tile0 + cur.tile) * TILE + warp * TOKENS + lane;
+        page = -1;
+        if (lane < TOKENS && token >= cur.s.start && token < cur.s.end) {
+            const uint32_t column = static_cast<uint32_t>(static_cast<uint64_t>(token) * a.page_magic >> a.page_shift);
+            slot = token - static_cast<int>(column) * a.page_size;
+            page = a.table[static_cast<uint64_t>(cur.b) * a.table_stride + column];
         }
-        if (info.flags & kTileFirst) {
-            const int g = heads_of(a, info.hb);
-            const char* q = a.q + info.b * a.q_stride + out_row(a, 0, info.hb, 0) * a.head_dim * sizeof(T);
+    };
+    const auto describe_tile = [&](int t, WarpTile<TOKENS>& tile) {
+        const bool in = page >= 0 && page < a.pages;
+        const uint32_t mask = __ballot_sync(~0u, in);
+        if (lane < TOKENS)
+            tile.offset[lane] = in ? static_cast<long long>(static_cast<uint64_t>(page) * a.page_stride +
+                                                            static_cast<uint64_t>(slot) * a.token_stride +
+                                                            static_cast<uint64_t>(cur.hb / a.group_blocks) * a.head_stride)
+                                   : 0;
+        if (lane == 0) {
+            const bool begins = cur.tile == 0, ends = cur.tile + 1 == cur.s.tiles;
+            tile.b = cur.b;
+            tile.hb = cur.hb;
+            tile.flags = (begins || t == 0 ? kTileFirst : 0) | (ends || t + 1 == n ? kTileLast : 0) |
+                         (begins ? kTileBegins : 0) | (ends ? kTileEnds : 0);
+            tile.in = mask;
+        }
+        cur.advance<TILE>(a, heads);
+    };
+    // The warp's copies of a described tile.  Chunks beyond the head's elements and tokens that are left out become zeros.
+    const auto issue = [&](const WarpTile<TOKENS>& tile, int stage) {
+        const uint32_t base = smem_addr(smem + stage * P::STAGE);
+        const uint32_t ks = base + warp * 2 * P::HALF;
+        const uint32_t in = tile.in;
+#pragma unroll
+        for (int i = 0; i < TOKENS * P::CHUNKS / 32; ++i) {
+            int row, c;
+            if constexpr (32 % P::CHUNKS == 0) {
+                row = i * (32 / P::CHUNKS) + lane / P::CHUNKS;
+                c = lane % P::CHUNKS;
+            } else {
+                row = (lane + i * 32) / P::CHUNKS;
+                c = lane + i * 32 - row * P::CHUNKS;
+            }
+            const bool read = (in >> row & 1) != 0 && c < chunks;
+            const long long at = tile.offset[row] + (c < chunks ? c * 16 : 0);
+            const uint32_t dst = ks + P::chunk(row, c) * 16;
+            cp_async16(dst, a.k + at, read);
+            cp_async16(dst + P::HALF, a.v + at, read);
+        }
+        if (tile.flags & kTileFirst) {
+            const int g = heads_of(a, tile.hb);
+            const char* q = a.q + tile.b * a.q_stride + out_row(a, 0, tile.hb, 0) * a.head_dim * sizeof(T);
             for (int x = tid; x < 8 * NT * P::QCHUNKS; x += kAttnThreads) {
                 const int row = x / P::QCHUNKS, c = x - row * P::QCHUNKS;
                 const bool read = row < g && c < qchunks;
-                cp_async16(base + 2 * P::TILE_BYTES + P::qchunk(row, c) * 16,
+                cp_async16(base + P::QROWS + P::qchunk(row, c) * 16,
                            q + (read ? static_cast<size_t>(row) * a.head_dim * sizeof(T) + c * 16 : 0), read);
             }
         }
     };
 
-    int described = 0, ring_w = 0;  // the next tile to describe, and its slot
+    int described = 0, ring_w = 0;  // the next tile to describe, and its slot of the ring
 #pragma unroll 1
-    for (; described < P::STAGES; ++described) {
-        if (described < n) {
-            write_info<TILE>(a, cur, describe<TILE>(a, cur, described, n, tid), tid, s_info[ring_w]);
-            cur.advance<TILE>(a, heads);
-        }
-        ring_w = ring_w + 1 == RING ? 0 : ring_w + 1;
+    for (; described < P::STAGES && described < n; ++described) {
+        look_up();
+        describe_tile(described, tiles[ring_w]);
+        ++ring_w;
     }
-    __syncthreads();
+    __syncwarp();
 #pragma unroll 1
     for (int i = 0; i + 1 < P::STAGES; ++i) {
         if (i < n)
-            issue(i, i);
+            issue(tiles[i], i);
         cp_async_commit();
     }
 
     uint32_t qf[NT][KSTEPS][2];
     float o[NT][MTILES][4], top[NT][2], total[NT][2], qscale[NT][2];
     bool began = false;
-    int ring_r = 0, stage_r = 0, stage_w = P::STAGES - 1, ring_i = P::STAGES - 1;
+    int ring_r = 0, ring_i = P::STAGES - 1, stage_r = 0, stage_w = P::STAGES - 1;
 #pragma unroll 1
     for (int t = 0; t < n; ++t) {
         cp_async_wait<P::STAGES - 2>();
-        __syncthreads();
+        __syncwarp();
         if (t + P::STAGES - 1 < n)
-            issue(ring_i, stage_w);
+            issue(tiles[ring_i], stage_w);
         cp_async_commit();
-        Described next;
         if (described < n)
-            next = describe<TILE>(a, cur, described, n, tid);
-        const TileInfo<TILE>& info = s_info[ring_r];
-        const int flags = info.flags;
+            look_up();
+        const WarpTile<TOKENS>& tile = tiles[ring_r];
+        const int flags = tile.flags;
         char* stage = smem + stage_r * P::STAGE;
-        const uint32_t ks = smem_addr(stage), vs = ks + P::TILE_BYTES, qs = vs + P::TILE_BYTES;
+        const uint32_t ks = smem_addr(stage) + warp * 2 * P::HALF, vs = ks + P::HALF, qs = smem_addr(stage) + P::QROWS;
+        if (flags & kTileFirst)
+            __syncthreads();  // the queries are the block's
         if (flags & kTileFirst) {
             began = flags & kTileBegins;
 #pragma unroll
@@ -678,14 +713,14 @@ k_attn_mma(const AttnArgs a)
                         ldmatrix4(qs + P::qchunk(nt * 8 + (lane & 7), 2 * j + (lane >> 3)) * 16, &qf[nt][j][0]);
 #pragma unroll
                     for (int i = 0; i < 2; ++i)
-                        qscale[nt][i] = a.scale;
+                        qscale[nt][i] = a.scale2;
                 } else {
                     // Elements 4 t4 .. 4 t4 + 3 of each 16: the order in which the 8-bit keys' come.
                     float most = 0.0f;
 #pragma unroll
                     for (int j = 0; j < KSTEPS; ++j) {
                         const uint2 w = *reinterpret_cast<const uint2*>(
-                            stage + 2 * P::TILE_BYTES + P::qchunk(nt * 8 + g8, 2 * j + (t4 >> 1)) * 16 + (t4 & 1) * 8);
+                            stage + P::QROWS + P::qchunk(nt * 8 + g8, 2 * j + (t4 >> 1)) * 16 + (t4 & 1) * 8);
                         qf[nt][j][0] = w.x;
                         qf[nt][j][1] = w.y;
                         if constexpr (!std::is_same<T, __half>::value) {
@@ -710,8 +745,7 @@ k_attn_mma(const AttnArgs a)
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
                         const int eh = __shfl_sync(~0u, e, (2 * t4 + i) * 4);
-                        // In two steps: the power of two alone may pass the range that its product with the scale keeps.
-                        qscale[nt][i] = ldexpf(a.scale, eh);
+                        qscale[nt][i] = ldexpf(a.scale2, eh);
                     }
                 }
 #pragma unroll
@@ -725,18 +759,21 @@ k_attn_mma(const AttnArgs a)
                     for (int i = 0; i < 4; ++i)
                         o[nt][m][i] = 0.0f;
             }
+            __syncthreads();  // a warp ahead may bring the next queries here
         }
 
-        // Scores of the warp's tokens: rows g8 and g8 + 8 of each block, heads 2 t4 and 2 t4 + 1 of each eight.
+        // Scores of the warp's tokens: rows g8 and g8 + 8 of each block, heads 2 t4 and 2 t4 + 1 of each eight.  Two sums
+        // each, of even and odd steps, so that an instruction need not wait for the one before.
         float s[KB][NT][4];
 #pragma unroll
         for (int kb = 0; kb < KB; ++kb) {
-            const int row = (warp * KB + kb) * 16 + (lane & 15);
+            const int row = kb * 16 + (lane & 15);
+            float odd[NT][4];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    s[kb][nt][i] = 0.0f;
+                    s[kb][nt][i] = odd[nt][i] = 0.0f;
 #pragma unroll
             for (int j = 0; j < P::CHUNKS / 2; ++j) {
                 uint32_t r[4];
@@ -744,7 +781,7 @@ k_attn_mma(const AttnArgs a)
                 if constexpr (!P::SMALL) {
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
-                        mma16816<MT>(s[kb][nt], r, qf[nt][j][0], qf[nt][j][1]);
+                        mma16816<MT>(j % 2 == 0 ? s[kb][nt] : odd[nt], r, qf[nt][j][0], qf[nt][j][1]);
                 } else {
 #pragma unroll
                     for (int c = 0; c < 2; ++c) {
@@ -752,17 +789,34 @@ k_attn_mma(const AttnArgs a)
                                                half2_of_e4m3(r[2 * c] >> 16), half2_of_e4m3(r[2 * c + 1] >> 16)};
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt)
-                            mma16816<MT>(s[kb][nt], k, qf[nt][2 * j + c][0], qf[nt][2 * j + c][1]);
+                            mma16816<MT>(c == 0 ? s[kb][nt] : odd[nt], k, qf[nt][2 * j + c][0], qf[nt][2 * j + c][1]);
                     }
                 }
             }
-            const int tok = (warp * KB + kb) * 16 + g8;
-            const bool in0 = info.offset[tok] >= 0, in1 = info.offset[tok + 8] >= 0;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    s[kb][nt][i] = (i < 2 ? in0 : in1) ? score2(a, s[kb][nt][i], qscale[nt][i & 1]) : -INFINITY;
+                    s[kb][nt][i] = (s[kb][nt][i] + odd[nt][i]) * qscale[nt][i & 1];
+        }
+        if (a.softcap > 0.0f) {
+#pragma unroll
+            for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        s[kb][nt][i] = a.softcap2 * tanhf(s[kb][nt][i]);
+        }
+        if (tile.in != (TOKENS == 32 ? ~0u : 0xffffu)) {
+            const uint32_t in = tile.in >> g8;
+#pragma unroll
+            for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        s[kb][nt][i] = (in >> (kb * 16 + (i < 2 ? 0 : 8)) & 1) != 0 ? s[kb][nt][i] : -INFINITY;
         }
 
         // The running maximum and sum.
@@ -817,7 +871,7 @@ k_attn_mma(const AttnArgs a)
         // Weighted values.  Rows of the result: elements g8 and g8 + 8 of each 16, or 2 g8 and 2 g8 + 1 (8-bit).
 #pragma unroll
         for (int kb = 0; kb < KB; ++kb) {
-            const int row = (warp * KB + kb) * 16;
+            const int row = kb * 16;
             if constexpr (!P::SMALL) {
 #pragma unroll
                 for (int m = 0; m < MTILES; ++m) {
@@ -880,7 +934,7 @@ k_attn_mma(const AttnArgs a)
                 }
             __syncthreads();
             const bool whole = began && (flags & kTileEnds);
-            const int g = heads_of(a, info.hb), fours = a.head_dim / 4;
+            const int g = heads_of(a, tile.hb), fours = a.head_dim / 4;
             const int slots = min(a.group, kAttnMaxHeads);
             float* part = a.part + (2ull * blockIdx.x + (began ? 1 : 0)) * a.slot_floats;
             for (int x = tid; x < g * fours; x += kAttnThreads) {
@@ -901,7 +955,7 @@ k_attn_mma(const AttnArgs a)
                     v.w += y.w;
                 }
                 if (whole) {
-                    const uint64_t row = out_row(a, info.b, info.hb, head);
+                    const uint64_t row = out_row(a, tile.b, tile.hb, head);
                     const float f = out_scale(a, sum);
                     *reinterpret_cast<uint2*>(a.out + (row * a.head_dim + d) * sizeof(T)) =
                         make_uint2(Lanes<T>::word(v.x * f, v.y * f), Lanes<T>::word(v.z * f, v.w * f));
@@ -915,10 +969,10 @@ k_attn_mma(const AttnArgs a)
                     }
                 }
             }
+            __syncthreads();  // the next copies go to this stage
         }
         if (described < n) {
-            write_info<TILE>(a, cur, next, tid, s_info[ring_w]);
-            cur.advance<TILE>(a, heads);
+            describe_tile(described, tiles[ring_w]);
             ++described;
             ring_w = ring_w + 1 == RING ? 0 : ring_w + 1;
         }
@@ -930,118 +984,153 @@ k_attn_mma(const AttnArgs a)
 }
 
 // ---------------------------------------------------------------------------
-// The join of an item's parts: one block per item and head.  It derives the
-// blocks that hold parts from the same lengths and the same split; an item
-// that one block had whole is written already.  Warps take every fourth part,
-// lanes the row's elements; the warps' sums are added in order.
+// The join of an item's parts.  It derives the blocks that hold parts from the
+// same lengths and the same split; an item that one block had whole is written
+// already.  A block takes `columns` (a power of two) of an item's groups of
+// four elements, heads after each other; its threads take a column over every
+// (threads / columns)-th part with a maximum and a sum of their own, all loads
+// of eight parts at once, and meet in a fixed tree in shared memory.
 // ---------------------------------------------------------------------------
+constexpr int kJoinThreads = 256;
+
 template <typename T, int TILE>
-__global__ void __launch_bounds__(kAttnThreads)
-k_attn_join(const AttnArgs a, const int blocks)
+__global__ void __launch_bounds__(kJoinThreads)
+k_attn_join(const AttnArgs a, const int blocks, const int columns)
 {
-    __shared__ long long s_sum[2][kAttnWarps];
-    __shared__ float s_top[kAttnWarps], s_total[kAttnWarps];
-    __shared__ float s_o[kAttnWarps][kAttnMaxDim];
+    constexpr int WARPS = kJoinThreads / 32, AHEAD = 8;
+    __shared__ long long s_sum[2][WARPS];
+    __shared__ float4 s_o[kJoinThreads];
+    __shared__ float2 s_w[kJoinThreads];  // maximum and sum
     pdl_enter();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int heads = a.kv_heads * a.group_blocks;
-    const int slots = min(a.group, kAttnMaxHeads);
-    const int i = blockIdx.x % slots;
-    const int item = blockIdx.x / slots;
+    const int slots = min(a.group, kAttnMaxHeads), fours = a.head_dim / 4;
+    const int cuts = (slots * fours + columns - 1) / columns;
+    const int item = blockIdx.x / cuts;
     const int b = item / heads, hb = item - b * heads;
 
     long long before = 0, all = 0;
-    for (int s = tid; s < a.batch; s += kAttnThreads) {
+    for (int s = tid; s < a.batch; s += kJoinThreads) {
         const int n = span_of<TILE>(a, s).tiles;
         all += n;
         before += s < b ? n : 0;
     }
-#pragma unroll
-    for (int w = 16; w > 0; w >>= 1) {
-        all += __shfl_xor_sync(~0u, all, w);
-        before += __shfl_xor_sync(~0u, before, w);
-    }
-    if (lane == 0) {
-        s_sum[0][warp] = all;
-        s_sum[1][warp] = before;
-    }
-    __syncthreads();
-    all = before = 0;
-    for (int w = 0; w < kAttnWarps; ++w) {
-        all += s_sum[0][w];
-        before += s_sum[1][w];
-    }
     const int tiles = span_of<TILE>(a, b).tiles;
+    if (a.batch > 1) {
+#pragma unroll
+        for (int w = 16; w > 0; w >>= 1) {
+            all += __shfl_xor_sync(~0u, all, w);
+            before += __shfl_xor_sync(~0u, before, w);
+        }
+        if (lane == 0) {
+            s_sum[0][warp] = all;
+            s_sum[1][warp] = before;
+        }
+        __syncthreads();
+        all = before = 0;
+#pragma unroll
+        for (int w = 0; w < WARPS; ++w) {
+            all += s_sum[0][w];
+            before += s_sum[1][w];
+        }
+    } else {
+        all = tiles;
+    }
     const long long lo = before * heads + static_cast<long long>(hb) * tiles;
     const int c0 = block_of(all * heads, blocks, lo), c1 = block_of(all * heads, blocks, lo + tiles - 1);
-    if (c0 == c1 || i >= heads_of(a, hb))
+    if (c0 == c1)
         return;
-
-    constexpr int DPL = kAttnMaxDim / 32;
-    float o[DPL], top = -INFINITY, total = 0.0f;
+    const int parts = c1 - c0 + 1, groups = kJoinThreads / columns, group = tid / columns;
+    const int x = (blockIdx.x - item * cuts) * columns + tid % columns;
+    const int h = x / fours, e = (x - h * fours) * 4;
+    const bool mine = h < heads_of(a, hb);
+    float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    float top = -INFINITY, total = 0.0f;
+    for (int p0 = group; p0 < parts && mine; p0 += AHEAD * groups) {
+        float4 v[AHEAD];
+        float m[AHEAD], n[AHEAD];
 #pragma unroll
-    for (int d = 0; d < DPL; ++d)
-        o[d] = 0.0f;
-    for (int c = c0 + warp; c <= c1; c += kAttnWarps) {
-        const float* part = a.part + (2ull * c + (c == c0 ? 1 : 0)) * a.slot_floats;
-        const float m = part[slots * a.head_dim + i], n = part[slots * (a.head_dim + 1) + i];
-        const float next = fmaxf(top, m), base = next == -INFINITY ? 0.0f : next;
-        const float fix = exp2f(top - base), f = exp2f(m - base);
-        total = total * fix + n * f;
-        top = next;
+        for (int i = 0; i < AHEAD; ++i) {
+            const int p = p0 + i * groups;
+            m[i] = -INFINITY;
+            n[i] = 0.0f;
+            v[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            if (p < parts) {
+                // Part 0 lies in its block's slot 1 (it begins the item), the others in their blocks' slots 0.
+                const float* part = a.part + (2ull * (c0 + p) + (p == 0 ? 1 : 0)) * a.slot_floats;
+                m[i] = part[slots * a.head_dim + h];
+                n[i] = part[slots * (a.head_dim + 1) + h];
+                v[i] = *reinterpret_cast<const float4*>(part + h * a.head_dim + e);
+            }
+        }
+        float best = top;
 #pragma unroll
-        for (int d = 0; d < DPL; ++d) {
-            const int e = lane + 32 * d;
-            if (e < a.head_dim)
-                o[d] = o[d] * fix + part[i * a.head_dim + e] * f;
+        for (int i = 0; i < AHEAD; ++i)
+            best = fmaxf(best, m[i]);
+        const float base = best == -INFINITY ? 0.0f : best;
+        float f = exp2f(top - base);
+        top = best;
+        total *= f;
+        o = make_float4(o.x * f, o.y * f, o.z * f, o.w * f);
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) {
+            f = exp2f(m[i] - base);
+            total = fmaf(n[i], f, total);
+            o = make_float4(fmaf(v[i].x, f, o.x), fmaf(v[i].y, f, o.y), fmaf(v[i].z, f, o.z), fmaf(v[i].w, f, o.w));
         }
     }
-#pragma unroll
-    for (int d = 0; d < DPL; ++d)
-        s_o[warp][lane + 32 * d] = o[d];
-    if (lane == 0) {
-        s_top[warp] = top;
-        s_total[warp] = total;
+    for (int w = groups / 2; w > 0; w >>= 1) {
+        if (group < 2 * w) {
+            s_o[tid] = o;
+            s_w[tid] = make_float2(top, total);
+        }
+        __syncthreads();
+        if (group < w) {
+            const float4 v = s_o[tid + w * columns];
+            const float2 y = s_w[tid + w * columns];
+            const float best = fmaxf(top, y.x), base = best == -INFINITY ? 0.0f : best;
+            const float f = exp2f(top - base), g = exp2f(y.x - base);
+            top = best;
+            total = total * f + y.y * g;
+            o = make_float4(o.x * f + v.x * g, o.y * f + v.y * g, o.z * f + v.z * g, o.w * f + v.w * g);
+        }
+        __syncthreads();
     }
-    __syncthreads();
-    float best = -INFINITY;
-    for (int w = 0; w < kAttnWarps; ++w)
-        best = fmaxf(best, s_top[w]);
-    const float base = best == -INFINITY ? 0.0f : best;
-    float f[kAttnWarps], sum = 0.0f;
-#pragma unroll
-    for (int w = 0; w < kAttnWarps; ++w) {
-        f[w] = exp2f(s_top[w] - base);
-        sum += s_total[w] * f[w];
+    if (group == 0 && mine) {
+        const uint64_t row = out_row(a, b, hb, h);
+        const float f = out_scale(a, total);
+        T* out = reinterpret_cast<T*>(a.out) + row * a.head_dim + e;
+        if constexpr (sizeof(T) == 4)
+            *reinterpret_cast<float4*>(out) = make_float4(o.x * f, o.y * f, o.z * f, o.w * f);
+        else
+            *reinterpret_cast<uint2*>(out) = make_uint2(Lanes<T>::word(o.x * f, o.y * f), Lanes<T>::word(o.z * f, o.w * f));
+        if (e == 0 && a.lse != nullptr)
+            a.lse[row] = lse_of(top, total);
     }
-    const uint64_t row = out_row(a, b, hb, i);
-    const float scale = out_scale(a, sum);
-    for (int e = tid; e < a.head_dim; e += kAttnThreads) {
-        float v = 0.0f;
-#pragma unroll
-        for (int w = 0; w < kAttnWarps; ++w)
-            v += s_o[w][e] * f[w];
-        reinterpret_cast<T*>(a.out)[row * a.head_dim + e] = Lanes<T>::from_f(v * scale);
-    }
-    if (tid == 0 && a.lse != nullptr)
-        a.lse[row] = lse_of(best, sum);
 }
 
 // Launches `kernel`, `per_sm` blocks of which fit an SM, and then the join.
 template <typename T, int TILE, typename Kernel>
 cudaError_t launch_tiles(Kernel kernel, const AttnArgs& a, int most, int sms, int per_sm, size_t smem, cudaStream_t s)
 {
-    const uint64_t joins = static_cast<uint64_t>(a.batch) * a.kv_heads * a.group_blocks * (a.group < kAttnMaxHeads ? a.group : kAttnMaxHeads);
+    // The join's threads of a column: a quarter of the parts an item has if all are alike, four at least (one sequence
+    // may be much longer than the others), 32 at most.
+    const int blocks = most < sms * per_sm ? most : sms * per_sm;
+    const uint64_t items = static_cast<uint64_t>(a.batch) * a.kv_heads * a.group_blocks;
+    int groups = 4;
+    while (groups < 32 && 8ull * groups * items <= static_cast<uint64_t>(blocks))
+        groups *= 2;
+    const int columns = kJoinThreads / groups, slots = a.group < kAttnMaxHeads ? a.group : kAttnMaxHeads;
+    const uint64_t joins = items * ((slots * (a.head_dim / 4) + columns - 1) / columns);
     if (joins > static_cast<uint64_t>(INT_MAX))
         return cudaErrorInvalidConfiguration;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (e != cudaSuccess)
         return e;
-    const int blocks = most < sms * per_sm ? most : sms * per_sm;
     e = launch_k(kernel, dim3(blocks), dim3(kAttnThreads), smem, s, a);
     if (e != cudaSuccess)
         return e;
-    return launch_k(k_attn_join<T, TILE>, dim3(static_cast<unsigned>(joins)), dim3(kAttnThreads), 0, s, a, blocks);
+    return launch_k(k_attn_join<T, TILE>, dim3(static_cast<unsigned>(joins)), dim3(kJoinThreads), 0, s, a, blocks, columns);
 }
 
 template <typename T, typename CT, int DIM, int HEADS>

@@ -58,21 +58,24 @@ struct AttnArgs {
     uint64_t q_stride;        // bytes
     uint64_t page_stride, token_stride, head_stride;
     int table_stride, pages, page_size, batch;
+    uint64_t page_magic;      // token / page_size == token * page_magic >> page_shift for token < 2^31
+    int page_shift;
     int capacity;             // tokens a table row can hold
     int kv_heads, group;      // group: query heads of one key-value head
     int group_blocks;         // group cut into blocks of at most kAttnMaxHeads
     int head_dim;
     int window;
-    float scale;              // of the scores, k_scale included
+    float scale2;             // of the scores, k_scale included, in base 2; with softcap over softcap instead
     float softcap;
+    float softcap2;           // softcap in base 2
     float v_scale;
     int slot_floats;          // floats of one partial slot
 };
 
 // Query heads of one key-value head that one block attends for at once.
 constexpr int kAttnMaxHeads = 16;
-// Blocks of the attention kernel, at most: two per SM of the 152.  The workspace holds two slots for each.
-constexpr int kAttnMaxBlocks = 304;
+// Blocks of the attention kernel, at most: four per SM of the 152.  The workspace holds two slots for each.
+constexpr int kAttnMaxBlocks = 608;
 constexpr int kAttnMaxDim = 256;
 
 // Cached tokens of one tile: what a block loads, and the work is cut into.

@@ -250,14 +250,21 @@ int ar_paged_attention(const ar_kv_cache* cache, const void* q, size_t q_stride,
     a.pages = c->pages;
     a.page_size = c->page_size;
     a.batch = c->batch;
+    // m = ceil(2^(31 + l) / d) with 2^l >= d is at most 2^l / 2^(31 + l) too large: n m >> (31 + l) is exact below 2^31.
+    while ((1ll << a.page_shift) < c->page_size)
+        ++a.page_shift;
+    a.page_shift += 31;
+    a.page_magic = ((1ull << a.page_shift) + c->page_size - 1) / c->page_size;
     a.capacity = static_cast<int>(cap < INT_MAX - 64 ? cap : INT_MAX - 64);  // a tile's end stays an int
     a.kv_heads = c->kv_heads;
     a.group = q_heads / c->kv_heads;
     a.group_blocks = (a.group + ar::kAttnMaxHeads - 1) / ar::kAttnMaxHeads;
     a.head_dim = c->head_dim;
     a.window = window;
-    a.scale = scale * c->k_scale;
+    constexpr float kLog2e = 1.4426950408889634f;
+    a.scale2 = softcap > 0.0f ? scale * c->k_scale / softcap : scale * c->k_scale * kLog2e;
     a.softcap = softcap;
+    a.softcap2 = softcap * kLog2e;
     a.v_scale = c->v_scale;
     a.slot_floats = ar::attn_slot_floats(a.group, c->head_dim);
 
