@@ -129,6 +129,7 @@ KERNEL_NAMES = {1: "k_fused_oneshot", 2: "k_fused_oneshot", 3: "k_fused_oneshot_
                 4: "k_fused_oneshot_tma", 5: "k_twoshot_phase1+k_twoshot_phase2", 6: "k_fused_oneshot_cluster"}
 
 _lib: Optional[ctypes.CDLL] = None
+_calls = None   # the extension module _binding, once bound to the library
 _lib_path = LIB_PATH
 
 
@@ -558,69 +559,19 @@ def ar_residual_rmsnorm_lamport(partials: Sequence[torch.Tensor], residual: torc
 
 
 # ------------------------------------------------------------------ the paged key-value cache
+#
+# These calls are marshalled by the extension module _binding (csrc/ar_binding.cpp): a decode step's kernels are shorter
+# than the marshalling of their many sizes and strides by ctypes would be.
 
-_CACHE_TO_AR = {**_TORCH_TO_AR, torch.float8_e4m3fn: AR_FP8_E4M3}
-_LAYOUTS = {"NHD": (1, 2), "HND": (2, 1)}   # dimensions of a page's tokens and of its heads
-
-
-def _empty(shape, dtype, device, stream) -> torch.Tensor:
-    """A new tensor for a call on ``stream``: made on that stream, so that the allocator hands out no memory
-    that work queued elsewhere still uses."""
-    if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    if isinstance(stream, int):
-        stream = torch.cuda.ExternalStream(stream, device=device)
-    with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
-
-
-def _ints(t: Optional[torch.Tensor], what: str, shape, dev: int) -> Optional[int]:
-    """Pointer of a dense int32 tensor of that shape."""
-    if t is None:
-        return None
-    if t.dtype != torch.int32 or t.shape != shape or t.get_device() != dev or not t.is_contiguous():
-        raise ValueError(f"{what} must be a contiguous int32 tensor of shape {tuple(shape)} on cuda:{dev}")
-    return t.data_ptr()
-
-
-def _heads(t: torch.Tensor, what: str, rows: int, heads: Optional[int], dim: int, dtype, dev: int):
-    """(pointer, elements between rows) of a [rows, heads, dim] tensor whose rows are dense."""
-    s = t.stride()
-    if (t.dim() != 3 or t.shape[0] != rows or t.shape[2] != dim or (heads is not None and t.shape[1] != heads)
-            or t.dtype != dtype or t.get_device() != dev or (s[2] != 1 and dim > 1) or (s[1] != dim and t.shape[1] > 1)):
-        want = "heads" if heads is None else heads
-        raise ValueError(f"{what} must be a [{rows}, {want}, {dim}] {dtype} tensor with dense rows on cuda:{dev}")
-    return t.data_ptr(), s[0]
-
-
-def _kv_cache(k_pages, v_pages, page_table, lengths, layout, k_scale, v_scale):
-    """(ArKVCache, device index) of a cache's tensors, each checked."""
-    try:
-        token_dim, head_dim = _LAYOUTS[layout]
-    except KeyError:
-        raise ValueError("layout must be 'NHD' ([pages, page_size, kv_heads, head_dim]) or 'HND' "
-                         "([pages, kv_heads, page_size, head_dim])") from None
-    dev = k_pages.get_device()
-    if dev < 0 or (_get_device is not None and dev != _get_device()):
-        raise ValueError("k_pages must be a CUDA tensor of the current device")
-    shape, strides = k_pages.shape, k_pages.stride()
-    if (len(shape) != 4 or (strides[3] != 1 and shape[3] > 1) or v_pages.shape != shape or v_pages.stride() != strides
-            or v_pages.dtype != k_pages.dtype or v_pages.get_device() != dev):
-        raise ValueError("k_pages and v_pages must be 4-d tensors of one shape, dtype, device and set of strides, "
-                         "with dense heads")
-    code = _CACHE_TO_AR.get(k_pages.dtype)
-    if code is None:
-        raise ValueError(f"unsupported cache dtype {k_pages.dtype}; expected float32, float16, bfloat16 or float8_e4m3fn")
-    if (page_table.dim() != 2 or page_table.dtype != torch.int32 or page_table.get_device() != dev
-            or (page_table.stride(1) != 1 and page_table.shape[1] > 1)):
-        raise ValueError(f"page_table must be an int32 [batch, pages of a sequence] tensor with dense rows on cuda:{dev}")
-    batch, columns = page_table.shape
-    stride = page_table.stride(0) if batch > 1 else columns
-    if stride < columns:
-        raise ValueError("page_table's rows must not overlap")
-    return ArKVCache(k_pages.data_ptr(), v_pages.data_ptr(), code, shape[0], shape[token_dim], shape[head_dim], shape[3],
-                     strides[0], strides[token_dim], strides[head_dim], k_scale, v_scale, page_table.data_ptr(), batch,
-                     columns, stride, _ints(lengths, "lengths", (batch,), dev)), dev
+def _bound_calls():
+    """The extension module, bound to the loaded library."""
+    global _calls
+    L = lib()
+    from . import _binding
+    _binding.bind(ARError, *(ctypes.cast(f, ctypes.c_void_p).value for f in (
+        L.ar_kv_append, L.ar_paged_attention_workspace_size, L.ar_paged_attention, L.ar_attention_join)))
+    _calls = _binding
+    return _calls
 
 
 def ar_kv_append(k_pages: torch.Tensor, v_pages: torch.Tensor, page_table: torch.Tensor, lengths: torch.Tensor,
@@ -635,39 +586,15 @@ def ar_kv_append(k_pages: torch.Tensor, v_pages: torch.Tensor, page_table: torch
     sequence b's newest; without seq_start row b is sequence b's one new token.  ``inv_freq`` (float32) holds the
     rotation's angle per position for each pair of elements; None rotates nothing.  q_out may be q.
     """
-    cache, dev = _kv_cache(k_pages, v_pages, page_table, lengths, layout, k_scale, v_scale)
-    tokens, heads, dim = k.shape[0], cache.kv_heads, cache.head_dim
-    code = dtype_code(k.dtype)
-    p_k, k_stride = _heads(k, "k", tokens, heads, dim, k.dtype, dev)
-    p_v, v_stride = _heads(v, "v", tokens, heads, dim, k.dtype, dev)
-    p_q = p_out = None
-    q_heads = q_stride = out_stride = 0
-    if q is not None:
-        p_q, q_stride = _heads(q, "q", tokens, None, dim, k.dtype, dev)
-        q_heads = q.shape[1]
-        if q_out is None:
-            q_out = _empty((tokens, q_heads, dim), k.dtype, q.device, stream)
-        p_out, out_stride = _heads(q_out, "q_out", tokens, q_heads, dim, k.dtype, dev)
-    elif q_out is not None:
-        raise ValueError("q_out is given without q")
-    rotary = 0
-    if inv_freq is not None:
-        rotary = 2 * inv_freq.numel()
-        if inv_freq.dtype != torch.float32 or inv_freq.get_device() != dev or not inv_freq.is_contiguous():
-            raise ValueError(f"inv_freq must be a contiguous float32 tensor on cuda:{dev}")
-    params = ArAppendParams(p_q, p_k, p_v, p_out, tokens, q_heads, code, q_stride, k_stride, v_stride, out_stride,
-                            _ints(seq_start, "seq_start", (cache.batch + 1,), dev),
-                            _ints(positions, "positions", (tokens,), dev),
-                            None if rotary == 0 else inv_freq.data_ptr(), rotary, interleaved, rotary_scale)
-    _check("ar_kv_append", lib().ar_kv_append(cache, params, _stream_handle(stream)))
-    return q_out
+    return (_calls or _bound_calls()).kv_append(
+        k_pages, v_pages, page_table, lengths, k, v, q, q_out, seq_start, positions, inv_freq, interleaved, rotary_scale, layout,
+        k_scale, v_scale, None if stream is None else _stream_handle(stream))
 
 
 def ar_paged_attention_workspace_size(k_pages: torch.Tensor, v_pages: torch.Tensor, page_table: torch.Tensor,
                                       lengths: torch.Tensor, q_heads: int, layout: str = "NHD") -> int:
     """Bytes of workspace ar_paged_attention needs with this cache (0 where it refuses it)."""
-    cache, _ = _kv_cache(k_pages, v_pages, page_table, lengths, layout, 1.0, 1.0)
-    return int(lib().ar_paged_attention_workspace_size(cache, q_heads))
+    return (_calls or _bound_calls()).paged_attention_workspace_size(k_pages, v_pages, page_table, lengths, q_heads, layout)
 
 
 def ar_paged_attention(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, page_table: torch.Tensor,
@@ -681,33 +608,9 @@ def ar_paged_attention(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Te
     ``workspace`` is any CUDA tensor of at least ar_paged_attention_workspace_size(...) bytes; when it is None one is
     allocated with torch.
     """
-    cache, dev = _kv_cache(k_pages, v_pages, page_table, lengths, layout, k_scale, v_scale)
-    batch, dim, dtype = cache.batch, cache.head_dim, q.dtype
-    code = dtype_code(dtype)
-    p_q, q_stride = _heads(q, "q", batch, None, dim, dtype, dev)
-    q_heads, device = q.shape[1], q.device
-    if out is None:
-        out = _empty((batch, q_heads, dim), dtype, device, stream)
-    elif out.shape != q.shape or out.dtype != dtype or out.get_device() != dev or not out.is_contiguous():
-        raise ValueError(f"out must be a contiguous tensor of q's shape and dtype on cuda:{dev}")
-    if lse is None:
-        if return_lse:
-            lse = _empty((batch, q_heads), torch.float32, device, stream)
-    elif lse.shape != (batch, q_heads) or lse.dtype != torch.float32 or lse.get_device() != dev or not lse.is_contiguous():
-        raise ValueError(f"lse must be a contiguous float32 tensor of shape {(batch, q_heads)} on cuda:{dev}")
-    L = lib()
-    if workspace is None:
-        nbytes = L.ar_paged_attention_workspace_size(cache, q_heads)
-        workspace = _empty((nbytes,), torch.uint8, device, stream)
-    elif workspace.get_device() != dev or not workspace.is_contiguous():
-        raise ValueError(f"workspace must be a contiguous tensor on cuda:{dev}")
-    else:
-        nbytes = workspace.numel() * workspace.element_size()
-    _check("ar_paged_attention",
-           L.ar_paged_attention(cache, p_q, q_stride, q_heads, dim ** -0.5 if scale is None else scale, window, softcap,
-                                out.data_ptr(), None if lse is None else lse.data_ptr(), workspace.data_ptr(), nbytes,
-                                code, _stream_handle(stream)))
-    return out if lse is None else (out, lse)
+    return (_calls or _bound_calls()).paged_attention(
+        q, k_pages, v_pages, page_table, lengths, scale, window, softcap, layout, k_scale, v_scale, out, lse, return_lse, workspace,
+        None if stream is None else _stream_handle(stream))
 
 
 def ar_attention_join(partials: Sequence[torch.Tensor], lse: Sequence[torch.Tensor], out: Optional[torch.Tensor] = None,
@@ -716,31 +619,8 @@ def ar_attention_join(partials: Sequence[torch.Tensor], lse: Sequence[torch.Tens
 
     Returns out, or (out, lse_out) when ``lse_out`` is given or ``return_lse``.  out may be one of the partials.
     """
-    if len(partials) == 0 or len(lse) != len(partials):
-        raise ValueError("ar_attention_join needs at least one partial, and one lse for each")
-    p0 = partials[0]
-    shape, dtype, dev = p0.shape, p0.dtype, p0.get_device()
-    code = dtype_code(dtype)
-    if dev < 0 or (_get_device is not None and dev != _get_device()) or len(shape) < 1:
-        raise ValueError("partials must be [..., head_dim] CUDA tensors of the current device")
-    rows = shape[:-1]
-
-    def pointer(t, what, want, kind):
-        if t.shape != want or t.dtype != kind or t.get_device() != dev or not t.is_contiguous():
-            raise ValueError(f"{what} must be a contiguous {kind} tensor of shape {tuple(want)} on cuda:{dev}")
-        return t.data_ptr()
-
-    ptrs = _ptr_array([pointer(p, f"partials[{r}]", shape, dtype) for r, p in enumerate(partials)])
-    lses = _ptr_array([pointer(x, f"lse[{r}]", rows, torch.float32) for r, x in enumerate(lse)])
-    if out is None:
-        out = _empty(shape, dtype, p0.device, stream)
-    if lse_out is None and return_lse:
-        lse_out = _empty(rows, torch.float32, p0.device, stream)
-    p_out = pointer(out, "out", shape, dtype)
-    p_lse = None if lse_out is None else pointer(lse_out, "lse_out", rows, torch.float32)
-    _check("ar_attention_join", lib().ar_attention_join(ptrs, lses, len(partials), rows.numel(), shape[-1], p_out, p_lse,
-                                                        code, _stream_handle(stream)))
-    return out if lse_out is None else (out, lse_out)
+    return (_calls or _bound_calls()).attention_join(partials, lse, out, lse_out, return_lse,
+                                                None if stream is None else _stream_handle(stream))
 
 
 # ------------------------------------------------------------ the all-reduce across GPUs (one process per GPU)

@@ -9,6 +9,10 @@ of the bounded-wait tests and the programmatic-launch switch, each read from
 the environment, and a communicator over local buffers for the peer
 barrier's timeout test).  Only ar_api.cu and ar_peer.cu differ, so only
 they are compiled twice.
+_binding.so is the CPython extension that marshals the paged key-value cache
+calls from torch tensors (host code only, compiled by g++ against torch's
+headers).
+
 The tests of forced launch shapes and of bounded waits, and the shape sweeps
 that build the AUTO table, load it; everything else loads libar.so, which
 reads no environment variable.
@@ -19,6 +23,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -27,6 +32,8 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libar.so")
 TEST_LIB = os.path.join(PKG, "libar_test.so")
+BINDING = os.path.join(PKG, "_binding.so")
+BINDING_SOURCE = os.path.join(CSRC, "ar_binding.cpp")
 
 SOURCES = ["ar_api.cu", "ar_kern_f32.cu", "ar_kern_f16.cu", "ar_kern_bf16.cu", "ar_noalloc.cu", "ar_host.cu",
            "ar_peer.cu", "ar_cache_api.cu", "ar_append.cu", "ar_attn_f32.cu", "ar_attn_f16.cu", "ar_attn_bf16.cu"]
@@ -46,15 +53,28 @@ def nvcc() -> str:
 
 
 def _stale() -> bool:
-    if not (os.path.exists(LIB) and os.path.exists(TEST_LIB)):
+    if not all(os.path.exists(f) for f in (LIB, TEST_LIB, BINDING)):
         return True
-    t = min(os.path.getmtime(LIB), os.path.getmtime(TEST_LIB))
-    deps = [os.path.join(CSRC, f) for f in SOURCES + HEADERS] + [os.path.join(INCLUDE, "ar.h"), __file__]
+    t = min(os.path.getmtime(f) for f in (LIB, TEST_LIB, BINDING))
+    deps = [os.path.join(CSRC, f) for f in SOURCES + HEADERS] + [os.path.join(INCLUDE, "ar.h"), BINDING_SOURCE, __file__]
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def _binding_command(out: str) -> list:
+    """The g++ command of the extension module: torch's own headers and libraries, and CUDA's for its stream type."""
+    import torch
+    root = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+    includes = [INCLUDE, os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
+                os.path.join(cuda, "include"), sysconfig.get_path("include")]
+    lib_dir = os.path.join(root, "lib")
+    return [shutil.which("g++") or "c++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *(f"-I{i}" for i in includes), BINDING_SOURCE,
+            "-o", out, f"-L{lib_dir}", f"-Wl,-rpath,{lib_dir}", "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10_cuda", "-lc10"]
+
+
 def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:
-    """Compile and link libar.so and libar_test.so if any source is newer; returns libar.so's path."""
+    """Compile and link libar.so, libar_test.so and _binding.so if any source is newer; returns libar.so's path."""
     if not force and not _stale():
         return LIB
     os.makedirs(BUILD, exist_ok=True)
@@ -72,6 +92,11 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
             print(" ".join(cmd), file=sys.stderr)
         procs.append((src, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)))
         objs.append(obj)
+    binding = f"{BINDING}.{os.getpid()}.tmp"
+    cmd = _binding_command(binding)
+    if verbose:
+        print(" ".join(cmd), file=sys.stderr)
+    procs.append(("ar_binding.cpp", subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)))
     failed = []
     for src, p in procs:
         out, _ = p.communicate()
@@ -80,7 +105,8 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
         if p.returncode != 0:
             failed.append(src)
     if failed:
-        raise RuntimeError(f"nvcc failed on {failed}")
+        raise RuntimeError(f"the compiler failed on {failed}")
+    os.replace(binding, BINDING)
     product = objs[:len(SOURCES)]
     swap = {os.path.join(BUILD, "ar_api.o"): objs[-2], os.path.join(BUILD, "ar_peer.o"): objs[-1]}
     test = [swap.get(o, o) for o in product]
