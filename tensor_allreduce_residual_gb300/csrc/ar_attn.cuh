@@ -109,6 +109,15 @@ __device__ Run find_run(const AttnArgs& a, int heads, Cursor& cur)
     __shared__ int s_b;
     __shared__ long long s_before;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    if (a.batch == 1) {
+        cur.b = 0;
+        cur.s = span_of<TILE>(a, 0);
+        const Run run = run_of(static_cast<long long>(cur.s.tiles) * heads, gridDim.x, blockIdx.x);
+        cur.hb = static_cast<int>(run.lo / cur.s.tiles);
+        cur.tile = static_cast<int>(run.lo % cur.s.tiles);
+        cur.next_length = 0;
+        return run;
+    }
     // Tiles of the sequences [base, base + kAttnThreads), scanned: this thread's own are [before, before + mine).
     int mine = 0, before = 0, chunk = 0;
     const auto scan = [&](int base) {
@@ -164,41 +173,6 @@ __device__ Run find_run(const AttnArgs& a, int heads, Cursor& cur)
     return run;
 }
 
-// One tile in flight: who it belongs to, and each token's offset in the cache (-1: left out).
-enum { kTileFirst = 1, kTileLast = 2, kTileBegins = 4, kTileEnds = 8 };  // of the block's part; of the item
-template <int TILE>
-struct TileInfo {
-    long long offset[TILE];
-    int b, hb, flags, pad;
-};
-
-// Fills `info` for the cursor's tile, `t` of the run's `n`.
-template <int TILE>
-__device__ __forceinline__ void describe(const AttnArgs& a, const Cursor& cur, long long t, long long n, TileInfo<TILE>& info)
-{
-    const int tid = threadIdx.x;
-    if (tid < TILE) {
-        const int token = (cur.s.tile0 + cur.tile) * TILE + tid;
-        long long off = -1;
-        if (token >= cur.s.start && token < cur.s.end) {
-            const uint32_t column = static_cast<uint32_t>(static_cast<uint64_t>(token) * a.page_magic >> a.page_shift);
-            const int page = a.table[static_cast<uint64_t>(cur.b) * a.table_stride + column];
-            if (page >= 0 && page < a.pages)
-                off = static_cast<long long>(static_cast<uint64_t>(page) * a.page_stride +
-                                             static_cast<uint64_t>(token - static_cast<int>(column) * a.page_size) * a.token_stride +
-                                             static_cast<uint64_t>(cur.hb / a.group_blocks) * a.head_stride);
-        }
-        info.offset[tid] = off;
-    }
-    if (tid == 0) {
-        const bool begins = cur.tile == 0, ends = cur.tile + 1 == cur.s.tiles;
-        info.b = cur.b;
-        info.hb = cur.hb;
-        info.flags = (begins || t == 0 ? kTileFirst : 0) | (ends || t + 1 == n ? kTileLast : 0) |
-                     (begins ? kTileBegins : 0) | (ends ? kTileEnds : 0);
-    }
-}
-
 // Row of the output of head `i` of the item's group block, and how many heads the block has.
 __device__ __forceinline__ uint64_t out_row(const AttnArgs& a, int b, int hb, int i)
 {
@@ -210,11 +184,6 @@ __device__ __forceinline__ int heads_of(const AttnArgs& a, int hb)
     return min(a.group - (hb % a.group_blocks) * kAttnMaxHeads, kAttnMaxHeads);
 }
 
-// A score in the exponent's base 2, of a dot product times scale2.
-__device__ __forceinline__ float score2(const AttnArgs& a, float s)
-{
-    return a.softcap > 0.0f ? a.softcap2 * tanhf(s) : s;
-}
 __device__ __forceinline__ float lse_of(float top2, float total)
 {
     return total == 0.0f ? -INFINITY : (top2 + log2f(total)) * kLn2;
@@ -225,286 +194,71 @@ __device__ __forceinline__ float out_scale(const AttnArgs& a, float total)
     return total == 0.0f ? 0.0f : a.v_scale / total;
 }
 
-template <typename CT>
-__device__ __forceinline__ float cached_to_f(CT v)
+__device__ __forceinline__ float exp2_fast(float x)
 {
-    if constexpr (sizeof(CT) == 1)
-        return static_cast<float>(v);
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+// What a maximum is subtracted as: minus infinity stands for no token yet, and 0 in its place keeps differences defined.
+__device__ __forceinline__ float base_of(float top) { return top == -INFINITY ? 0.0f : top; }
+
+// Four elements of a row of the output.
+template <typename T>
+__device__ __forceinline__ void store_four(T* out, float4 v, float f)
+{
+    if constexpr (sizeof(T) == 4)
+        *reinterpret_cast<float4*>(out) = make_float4(v.x * f, v.y * f, v.z * f, v.w * f);
     else
-        return Lanes<CT>::to_f(v);
+        *reinterpret_cast<uint2*>(out) = make_uint2(Lanes<T>::word(v.x * f, v.y * f), Lanes<T>::word(v.z * f, v.w * f));
 }
 
 // ---------------------------------------------------------------------------
-// The plain-arithmetic kernel: fp32 multiply-adds.  Tiles come through a ring
-// of asynchronous copies; a warp's lanes take one token each and the warps
-// share the heads for the scores, the threads take one element of the head
-// each for the weighted values, so no sum ever crosses a thread.
+// Shape of an attention kernel: query type, cache type, head elements (those
+// of a shorter head are followed by zeros) and query heads of a block.
+//
+// Each warp takes a quarter of a tile's tokens, through a ring of stages of its
+// own filled by asynchronous 16-byte copies, with a maximum, a sum and an
+// accumulator of its own.  The four warps meet at the ends of the block's part
+// of an item only; between them no warp waits for another.
 // ---------------------------------------------------------------------------
-template <typename T, typename CT, int DIM, int HEADS>
-struct PlainShape {
-    static constexpr int TILE = 32;
-    static constexpr int STAGES = 3;
-    static constexpr int VE = 16 / sizeof(CT);
-    static constexpr int CHUNKS = DIM / VE;
-    static constexpr int PITCH = DIM * sizeof(CT) + 16;  // an odd number of 16-byte words: lanes meet no bank twice
-    static constexpr int TILE_BYTES = TILE * PITCH;
-    static constexpr int ITEM = STAGES * 2 * TILE_BYTES;
-    static constexpr int SMEM = ITEM + HEADS * DIM * 4 + TILE * HEADS * 4;
-    static constexpr int BLOCKS = SMEM + 2048 + kSmemReservedPerBlock <= kSmemPerSM / 2 ? 2 : 1;
-    // Threads over the head's elements, and over groups of heads where the elements leave some over.
-    static constexpr int DT = DIM == 192 ? 96 : (DIM < 128 ? DIM : 128);
-    static constexpr int HS = 128 / DT;
-    static constexpr int DPT = DIM / DT;
-    static constexpr int NH = (HEADS + HS - 1) / HS;
-    static constexpr int HPW = (HEADS + kAttnWarps - 1) / kAttnWarps;
-};
-
-template <typename T, typename CT, int DIM, int HEADS>
-__global__ void __launch_bounds__(kAttnThreads, PlainShape<T, CT, DIM, HEADS>::BLOCKS)
-k_attn_plain(const AttnArgs a)
-{
-    using P = PlainShape<T, CT, DIM, HEADS>;
-    constexpr int TILE = P::TILE, RING = P::STAGES + 1;
-    extern __shared__ __align__(16) char smem[];
-    __shared__ TileInfo<TILE> s_info[RING];
-    __shared__ float s_top[HEADS], s_total[HEADS], s_fix[HEADS];
-    float* s_q = reinterpret_cast<float*>(smem + P::ITEM);  // [HEADS][DIM]
-    float* s_p = s_q + HEADS * DIM;                         // [TILE][HEADS]
-    pdl_enter();
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int heads = a.kv_heads * a.group_blocks;
-    const int chunks = a.head_dim / P::VE;
-
-    Cursor cur;
-    const Run run = find_run<TILE>(a, heads, cur);
-    if (run.n == 0)
-        return;
-
-    long long described = 0;
-    const auto next_info = [&] {
-        if (described < run.n) {
-            describe<TILE>(a, cur, described, run.n, s_info[described % RING]);
-            cur.advance<TILE>(a, heads);
-        }
-        ++described;
-    };
-    const auto issue = [&](long long t) {
-        if (t < run.n) {
-            const TileInfo<TILE>& info = s_info[t % RING];
-            char* stage = smem + (t % P::STAGES) * 2 * P::TILE_BYTES;
-            for (int x = tid; x < TILE * P::CHUNKS; x += kAttnThreads) {
-                const int row = x / P::CHUNKS, c = x - row * P::CHUNKS;
-                if (c < chunks) {
-                    const long long off = info.offset[row];
-                    const uint32_t dst = smem_addr(stage + row * P::PITCH + c * 16);
-                    const long long at = (off < 0 ? 0 : off) + c * 16;
-                    cp_async16(dst, a.k + at, off >= 0);
-                    cp_async16(dst + P::TILE_BYTES, a.v + at, off >= 0);
-                }
-            }
-        }
-        cp_async_commit();
-    };
-    for (int i = 0; i < P::STAGES; ++i)
-        next_info();
-    __syncthreads();
-    for (int i = 0; i + 1 < P::STAGES; ++i)
-        issue(i);
-
-    const int d0 = tid % P::DT, hs = tid / P::DT;
-    float o[P::NH][P::DPT];
-    bool began = false;  // the block's part of the item holds its first tile
-    for (long long t = 0; t < run.n; ++t) {
-        cp_async_wait<P::STAGES - 2>();
-        __syncthreads();
-        issue(t + P::STAGES - 1);
-        const TileInfo<TILE>& info = s_info[t % RING];
-        const char* ks = smem + (t % P::STAGES) * 2 * P::TILE_BYTES;
-        const char* vs = ks + P::TILE_BYTES;
-        const int g = heads_of(a, info.hb);
-        if (info.flags & kTileFirst) {
-            began = info.flags & kTileBegins;
-            const T* q = reinterpret_cast<const T*>(a.q + info.b * a.q_stride) +
-                         (out_row(a, 0, info.hb, 0)) * a.head_dim;
-            for (int x = tid; x < g * a.head_dim; x += kAttnThreads) {
-                const int h = x / a.head_dim;
-                s_q[h * DIM + x - h * a.head_dim] = Lanes<T>::to_f(q[x]);
-            }
-            if (tid < HEADS) {
-                s_top[tid] = -INFINITY;
-                s_total[tid] = 0.0f;
-            }
-#pragma unroll
-            for (int h = 0; h < P::NH; ++h)
-#pragma unroll
-                for (int d = 0; d < P::DPT; ++d)
-                    o[h][d] = 0.0f;
-            __syncthreads();
-        }
-        // Scores: lane = token, heads over warps.
-        {
-            float dot[P::HPW];
-#pragma unroll
-            for (int i = 0; i < P::HPW; ++i)
-                dot[i] = 0.0f;
-            for (int c = 0; c < chunks; ++c) {
-                const CT* kc = reinterpret_cast<const CT*>(ks + lane * P::PITCH + c * 16);
-                float k[P::VE];
-                const uint4 raw = *reinterpret_cast<const uint4*>(kc);
-                const CT* e = reinterpret_cast<const CT*>(&raw);
-#pragma unroll
-                for (int l = 0; l < P::VE; ++l)
-                    k[l] = cached_to_f(e[l]);
-#pragma unroll
-                for (int i = 0; i < P::HPW; ++i) {
-                    const int h = warp + i * kAttnWarps;
-                    if (h < g) {
-                        const float* q = s_q + h * DIM + c * P::VE;
-#pragma unroll
-                        for (int l = 0; l < P::VE; ++l)
-                            dot[i] = fmaf(q[l], k[l], dot[i]);
-                    }
-                }
-            }
-            const bool in = info.offset[lane] >= 0;
-#pragma unroll
-            for (int i = 0; i < P::HPW; ++i) {
-                const int h = warp + i * kAttnWarps;
-                if (h < g) {
-                    const float x = in ? score2(a, dot[i] * a.scale2) : -INFINITY;
-                    float top = x;
-#pragma unroll
-                    for (int w = 16; w > 0; w >>= 1)
-                        top = fmaxf(top, __shfl_xor_sync(~0u, top, w));
-                    const float old = s_top[h];
-                    top = fmaxf(top, old);
-                    const float base = top == -INFINITY ? 0.0f : top;
-                    const float p = exp2f(x - base);
-                    float sum = p;
-#pragma unroll
-                    for (int w = 16; w > 0; w >>= 1)
-                        sum += __shfl_xor_sync(~0u, sum, w);
-                    s_p[lane * HEADS + h] = p;
-                    __syncwarp();
-                    if (lane == 0) {
-                        const float fix = exp2f(old - base);
-                        s_fix[h] = fix;
-                        s_total[h] = s_total[h] * fix + sum;
-                        s_top[h] = top;
-                    }
-                }
-            }
-        }
-        __syncthreads();
-        // Weighted values: thread = element of the head.
-        if (hs < P::HS) {
-#pragma unroll
-            for (int h = 0; h < P::NH; ++h) {
-                const float fix = s_fix[min(hs * P::NH + h, HEADS - 1)];
-#pragma unroll
-                for (int d = 0; d < P::DPT; ++d)
-                    o[h][d] = hs * P::NH + h < g ? o[h][d] * fix : 0.0f;
-            }
-#pragma unroll 4
-            for (int j = 0; j < TILE; ++j) {
-                float v[P::DPT];
-#pragma unroll
-                for (int d = 0; d < P::DPT; ++d)
-                    v[d] = cached_to_f(reinterpret_cast<const CT*>(vs + j * P::PITCH)[d0 + d * P::DT]);
-#pragma unroll
-                for (int h = 0; h < P::NH; ++h) {
-                    if (hs * P::NH + h < g) {
-                        const float p = s_p[j * HEADS + hs * P::NH + h];
-#pragma unroll
-                        for (int d = 0; d < P::DPT; ++d)
-                            o[h][d] = fmaf(p, v[d], o[h][d]);
-                    }
-                }
-            }
-        }
-        if (info.flags & kTileLast) {
-            const bool whole = began && (info.flags & kTileEnds);
-            const int slots = min(a.group, kAttnMaxHeads);
-            float* part = a.part + (2ull * blockIdx.x + (began ? 1 : 0)) * a.slot_floats;
-#pragma unroll
-            for (int h = 0; h < P::NH; ++h) {
-                const int head = hs * P::NH + h;
-                if (hs < P::HS && head < g) {
-                    const uint64_t row = out_row(a, info.b, info.hb, head);
-                    const float f = out_scale(a, s_total[head]);
-#pragma unroll
-                    for (int d = 0; d < P::DPT; ++d) {
-                        const int e = d0 + d * P::DT;
-                        if (e < a.head_dim) {
-                            if (whole)
-                                reinterpret_cast<T*>(a.out)[row * a.head_dim + e] = Lanes<T>::from_f(o[h][d] * f);
-                            else
-                                part[head * a.head_dim + e] = o[h][d];
-                        }
-                    }
-                }
-            }
-            if (tid < g) {
-                if (!whole) {
-                    part[slots * a.head_dim + tid] = s_top[tid];
-                    part[slots * (a.head_dim + 1) + tid] = s_total[tid];
-                } else if (a.lse != nullptr) {
-                    a.lse[out_row(a, info.b, info.hb, tid)] = lse_of(s_top[tid], s_total[tid]);
-                }
-            }
-            __syncthreads();  // the next item's first tile writes s_top and s_total
-        }
-        next_info();
-    }
-}
-
-// ---------------------------------------------------------------------------
-// The matrix kernel, for 16-bit and 8-bit caches.  Scores are computed as
-// K Q^T and values as V^T P^T: tokens, and then the head's elements, are the
-// 16 rows of a matrix instruction and query heads its 8 columns, so that up to
-// 8 heads fill it where rows of queries would leave half of it empty, and both
-// operands from the cache come out of shared memory by ldmatrix as they lie
-// there.  Each warp takes a quarter of a tile's tokens, through a ring of its
-// own, with a maximum, a sum and an accumulator of its own: the four meet at the
-// ends of the block's part of an item only, and between them no warp waits for
-// another.  Weights enter the second product as a pair of 16-bit
-// numbers, their rounding and what it leaves (17 bits and more together), which
-// costs an instruction that the memory's pace hides.  8-bit elements become
-// fp16 in registers, exactly; queries too large or small for fp16 are scaled
-// by a power of two per head first.
-// ---------------------------------------------------------------------------
-template <typename T, typename CT, int DIM, int NT>
-struct MmaShape {
-    static constexpr bool SMALL = sizeof(CT) == 1;
-    using MT = typename std::conditional<SMALL, __half, CT>::type;  // of the matrix instructions' operands
+template <typename T_, typename CT_, int DIM_, int HEADS_>
+struct AttnShape {
+    using T = T_;
+    using CT = CT_;
+    static constexpr int DIM = DIM_, HEADS = HEADS_;
+    static constexpr bool SMALL = sizeof(CT) == 1, WIDE = sizeof(CT) == 4;
     static constexpr int TILE = attn_tile(sizeof(CT));
     static constexpr int TOKENS = TILE / kAttnWarps;  // a warp's tokens of a tile
-    static constexpr int KB = TOKENS / 16;            // and their blocks of 16
     static constexpr int CHUNKS = DIM * sizeof(CT) / 16;
     static constexpr int QCHUNKS = DIM * sizeof(T) / 16;
     // 16-byte chunks of a row: permuted within 128 bytes by the row, or padded to an odd number; either way the eight
     // rows of an 8 x 8 matrix lie in different banks.
     static constexpr int PITCH = CHUNKS % 8 == 0 ? CHUNKS : CHUNKS | 1;
     static constexpr int QPITCH = QCHUNKS % 8 == 0 ? QCHUNKS : QCHUNKS | 1;
-    static constexpr int HALF = TOKENS * PITCH * 16;  // a warp's keys of a stage, and its values
+    static constexpr int HALF = TOKENS * PITCH * 16;     // a warp's keys of a stage, and its values
     static constexpr int QROWS = kAttnWarps * 2 * HALF;  // where a stage's queries begin
-    static constexpr int STAGE = QROWS + 8 * NT * QPITCH * 16;
+    static constexpr int STAGE = QROWS + HEADS * QPITCH * 16;
     static constexpr int INFO = kAttnWarps * (TOKENS * 8 + 16);
+    // Shared memory of a block that is no stage's (the fp32 kernel's: queries, and weights of a tile).
+    static constexpr int OTHER = WIDE ? HEADS * DIM * 4 + TILE * HEADS * 4 + kAttnWarps * HEADS * 4 : 0;
     static constexpr int OPITCH = DIM + 4;  // floats; the epilogue's rows, one per warp and head, lie in a used stage
-    static_assert(kAttnWarps * 8 * NT * OPITCH * 4 <= STAGE, "the epilogue fits a stage");
+    static_assert(kAttnWarps * HEADS * OPITCH * 4 <= STAGE, "the epilogue fits a stage");
     static constexpr int fits(int bytes)
     {
-        const int n = (bytes - kSmemReservedPerBlock - 1024 - INFO) / (STAGE + INFO);
+        const int n = (bytes - kSmemReservedPerBlock - 1024 - INFO - OTHER) / (STAGE + INFO);
         return n < 5 ? n : 5;
     }
     // Blocks of an SM.  A tile of few bytes takes a warp longer than they take to come, so that more warps help: four
     // blocks of heads up to 64 elements (31.8 against 34.3 us with two on 93 MB of fp16 cache), three of 8-bit ones up to
-    // 128 (93.5 against 98.6 us on 533 MB).  For 128 16-bit elements two blocks' deeper rings do better (93 against 98 us
-    // on 511 MB).  Long heads leave room for two stages in one block only.
-    static constexpr int WANT = NT == 1 && DIM <= 64 ? 4 : NT == 1 && DIM <= 128 && SMALL ? 3 : 2;
+    // 128 (93.5 against 98.6 us on 533 MB) and of fp32 ones with two query heads (40.0 against 41.6 us on 194 MB).  For 128
+    // 16-bit elements two blocks' deeper rings do better (93 against 98 us on 511 MB).  Long heads leave room for two
+    // stages in one block only.
+    static constexpr int WANT = HEADS == 8 && DIM <= 64 && !WIDE ? 4 : (HEADS == 8 && DIM <= 128 && SMALL) || HEADS == 2 ? 3 : 2;
     static constexpr int BLOCKS = fits(kSmemPerSM / WANT) >= 2 ? WANT : 1;
     static constexpr int STAGES = fits(kSmemPerSM / BLOCKS);
-    static constexpr int SMEM = STAGES * STAGE;
+    static constexpr int RING = STAGES + 1;  // descriptions of tiles: one more is written than copies are under way
+    static constexpr int SMEM = STAGES * STAGE + OTHER;
     static __device__ __forceinline__ int chunk(int row, int c)
     {
         return CHUNKS % 8 == 0 ? row * PITCH + (c ^ (row & 7)) : row * PITCH + c;
@@ -516,6 +270,7 @@ struct MmaShape {
 };
 
 // A warp's part of one tile in flight: whose it is, its tokens' offsets in the cache, and which of them count.
+enum { kTileFirst = 1, kTileLast = 2, kTileBegins = 4, kTileEnds = 8 };  // of the block's part; of the item
 template <int TOKENS>
 struct WarpTile {
     long long offset[TOKENS];
@@ -523,6 +278,392 @@ struct WarpTile {
     uint32_t in;
 };
 
+// A warp's ring: describes the tiles of the block's run one after the other, and issues the copies of described ones.
+template <typename P>
+struct Feed {
+    using Tile = WarpTile<P::TOKENS>;
+    const AttnArgs& a;
+    Tile* tiles;  // [RING]
+    char* smem;
+    int heads, n, warp, lane, chunks, qchunks;
+    Cursor cur;
+    int page = -1, slot = 0;
+    int described = 0, ring_w = 0, ring_i = P::STAGES - 1, ring_r = 0, stage_w = P::STAGES - 1, stage_r = 0;
+
+    __device__ Feed(const AttnArgs& a_, Tile* tiles_, char* smem_, int n_, const Cursor& c)
+        : a(a_), tiles(tiles_), smem(smem_), heads(a_.kv_heads * a_.group_blocks), n(n_), warp(threadIdx.x >> 5), lane(threadIdx.x & 31),
+          chunks(a_.head_dim * static_cast<int>(sizeof(typename P::CT)) / 16), qchunks(a_.head_dim * static_cast<int>(sizeof(typename P::T)) / 16),
+          cur(c)
+    {
+    }
+
+    // The next tile's description, in two steps: its pages' numbers are on their way between them.
+    __device__ __forceinline__ void look_up()
+    {
+        if (described >= n)
+            return;
+        const int token = (cur.s.tile0 + cur.tile) * P::TILE + warp * P::TOKENS + lane;
+        page = -1;
+        if (lane < P::TOKENS && token >= cur.s.start && token < cur.s.end) {
+            const uint32_t column = static_cast<uint32_t>(static_cast<uint64_t>(token) * a.page_magic >> a.page_shift);
+            slot = token - static_cast<int>(column) * a.page_size;
+            page = a.table[static_cast<uint64_t>(cur.b) * a.table_stride + column];
+        }
+    }
+    __device__ __forceinline__ void describe()
+    {
+        if (described >= n)
+            return;
+        Tile& tile = tiles[ring_w];
+        const bool in = page >= 0 && page < a.pages;
+        const uint32_t mask = __ballot_sync(~0u, in);
+        if (lane < P::TOKENS)
+            tile.offset[lane] = in ? static_cast<long long>(static_cast<uint64_t>(page) * a.page_stride +
+                                                            static_cast<uint64_t>(slot) * a.token_stride +
+                                                            static_cast<uint64_t>(cur.hb / a.group_blocks) * a.head_stride)
+                                   : 0;
+        if (lane == 0) {
+            const bool begins = cur.tile == 0, ends = cur.tile + 1 == cur.s.tiles;
+            tile.b = cur.b;
+            tile.hb = cur.hb;
+            tile.flags = (begins || described == 0 ? kTileFirst : 0) | (ends || described + 1 == n ? kTileLast : 0) |
+                         (begins ? kTileBegins : 0) | (ends ? kTileEnds : 0);
+            tile.in = mask;
+        }
+        cur.advance<P::TILE>(a, heads);
+        ++described;
+        ring_w = ring_w + 1 == P::RING ? 0 : ring_w + 1;
+    }
+    // The warp's copies of a described tile, and its share of a new item's queries.  Chunks beyond the head's elements
+    // and tokens that are left out become zeros.
+    __device__ __forceinline__ void issue(const Tile& tile, int stage)
+    {
+        const uint32_t base = smem_addr(smem + stage * P::STAGE);
+        const uint32_t ks = base + warp * 2 * P::HALF;
+        const uint32_t in = tile.in;
+#pragma unroll
+        for (int i = 0; i < P::TOKENS * P::CHUNKS / 32; ++i) {
+            int row, c;
+            if constexpr (32 % P::CHUNKS == 0) {
+                row = i * (32 / P::CHUNKS) + lane / P::CHUNKS;
+                c = lane % P::CHUNKS;
+            } else {
+                row = (lane + i * 32) / P::CHUNKS;
+                c = lane + i * 32 - row * P::CHUNKS;
+            }
+            const bool read = (in >> row & 1) != 0 && c < chunks;
+            const long long at = tile.offset[row] + (c < chunks ? c * 16 : 0);
+            const uint32_t dst = ks + P::chunk(row, c) * 16;
+            cp_async16(dst, a.k + at, read);
+            cp_async16(dst + P::HALF, a.v + at, read);
+        }
+        if (tile.flags & kTileFirst) {
+            const int g = heads_of(a, tile.hb);
+            const char* q = a.q + tile.b * a.q_stride + out_row(a, 0, tile.hb, 0) * a.head_dim * sizeof(typename P::T);
+            for (int x = threadIdx.x; x < P::HEADS * P::QCHUNKS; x += kAttnThreads) {
+                const int row = x / P::QCHUNKS, c = x - row * P::QCHUNKS;
+                const bool read = row < g && c < qchunks;
+                cp_async16(base + P::QROWS + P::qchunk(row, c) * 16,
+                           q + (read ? static_cast<size_t>(row) * a.head_dim * sizeof(typename P::T) + c * 16 : 0), read);
+            }
+        }
+    }
+    // Fills the ring before the first tile.
+    __device__ __forceinline__ void start()
+    {
+#pragma unroll 1
+        while (described < P::STAGES && described < n) {
+            look_up();
+            describe();
+        }
+        __syncwarp();
+#pragma unroll 1
+        for (int i = 0; i + 1 < P::STAGES; ++i) {
+            if (i < n)
+                issue(tiles[i], i);
+            cp_async_commit();
+        }
+    }
+    // Waits for tile t's copies and sends the next ones on their way.
+    __device__ __forceinline__ void turn(int t)
+    {
+        cp_async_wait<P::STAGES - 2>();
+        __syncwarp();
+        if (t + P::STAGES - 1 < n)
+            issue(tiles[ring_i], stage_w);
+        cp_async_commit();
+        look_up();
+    }
+    __device__ __forceinline__ void next()
+    {
+        describe();
+        ring_r = ring_r + 1 == P::RING ? 0 : ring_r + 1;
+        ring_i = ring_i + 1 == P::RING ? 0 : ring_i + 1;
+        stage_r = stage_r + 1 == P::STAGES ? 0 : stage_r + 1;
+        stage_w = stage_w + 1 == P::STAGES ? 0 : stage_w + 1;
+    }
+};
+
+// The end of the block's part of an item, after every warp has left its maxima, sums (s_top, s_total) and accumulators,
+// the latter scaled to the block's maximum, in `rows`: adds the warps' up and writes the result or the part.
+template <typename P>
+__device__ __forceinline__ void write_part(const AttnArgs& a, const WarpTile<P::TOKENS>& tile, bool began, const float* rows,
+                                           const float (*s_top)[P::HEADS], const float (*s_total)[P::HEADS])
+{
+    using T = typename P::T;
+    const bool whole = began && (tile.flags & kTileEnds);
+    const int g = heads_of(a, tile.hb), fours = a.head_dim / 4, slots = min(a.group, kAttnMaxHeads);
+    float* part = a.part + (2ull * blockIdx.x + (began ? 1 : 0)) * a.slot_floats;
+    for (int x = threadIdx.x; x < g * fours; x += kAttnThreads) {
+        const int head = x / fours, d = (x - head * fours) * 4;
+        float best = s_top[0][head], sum = 0.0f;
+#pragma unroll
+        for (int w = 1; w < kAttnWarps; ++w)
+            best = fmaxf(best, s_top[w][head]);
+        const float base = base_of(best);
+        float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+        for (int w = 0; w < kAttnWarps; ++w) {
+            sum += s_total[w][head] * exp2_fast(s_top[w][head] - base);
+            const float4 y = *reinterpret_cast<const float4*>(rows + (w * P::HEADS + head) * P::OPITCH + d);
+            v.x += y.x;
+            v.y += y.y;
+            v.z += y.z;
+            v.w += y.w;
+        }
+        if (whole) {
+            const uint64_t row = out_row(a, tile.b, tile.hb, head);
+            store_four(reinterpret_cast<T*>(a.out) + row * a.head_dim + d, v, out_scale(a, sum));
+            if (d == 0 && a.lse != nullptr)
+                a.lse[row] = lse_of(best, sum);
+        } else {
+            *reinterpret_cast<float4*>(part + head * a.head_dim + d) = v;
+            if (d == 0) {
+                part[slots * a.head_dim + head] = best;
+                part[slots * (a.head_dim + 1) + head] = sum;
+            }
+        }
+    }
+}
+
+// Maximum or sum over the eight lanes that differ in the lane's upper three bits.
+__device__ __forceinline__ float column_max(float x)
+{
+#pragma unroll
+    for (int w = 4; w < 32; w <<= 1)
+        x = fmaxf(x, __shfl_xor_sync(~0u, x, w));
+    return x;
+}
+__device__ __forceinline__ float column_sum(float x)
+{
+#pragma unroll
+    for (int w = 4; w < 32; w <<= 1)
+        x += __shfl_xor_sync(~0u, x, w);
+    return x;
+}
+
+// ---------------------------------------------------------------------------
+// The fp32 kernel: multiply-adds, as no matrix instruction keeps 24 bits.
+// Scores: a warp's eight tokens take four lanes each, which share the head's
+// chunks and then exchange halves of their heads' sums, so that each ends with
+// the sums of a quarter of the heads.  Weighted values: a lane takes four
+// elements of the head (half of the tokens where those are fewer than lanes)
+// and every head's weights from shared memory.
+// ---------------------------------------------------------------------------
+template <typename P>
+__global__ void __launch_bounds__(kAttnThreads, P::BLOCKS)
+k_attn_fma(const AttnArgs a)
+{
+    constexpr int HEADS = P::HEADS, DIM = P::DIM, COLS = DIM / 4, CPL = (COLS + 31) / 32, HALVES = COLS <= 16 ? 2 : 1;
+    constexpr int HL = HEADS >= 4 ? HEADS / 4 : 1;  // heads whose sums a lane ends with
+    static_assert(P::TOKENS == 8 && P::CHUNKS % 8 == 0, "four lanes a token");
+    extern __shared__ __align__(128) char smem[];
+    __shared__ __align__(16) WarpTile<P::TOKENS> s_tiles[kAttnWarps][P::RING];
+    __shared__ float s_top[kAttnWarps][HEADS], s_total[kAttnWarps][HEADS];
+    float* const s_q = reinterpret_cast<float*>(smem + P::STAGES * P::STAGE);  // [HEADS][DIM]
+    pdl_enter();
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    float* const s_p = s_q + HEADS * DIM + warp * (P::TOKENS + 1) * HEADS;  // [TOKENS][HEADS], then [HEADS] factors
+    float* const s_fix = s_p + P::TOKENS * HEADS;
+
+    Cursor cur;
+    const Run run = find_run<P::TILE>(a, a.kv_heads * a.group_blocks, cur);
+    if (run.n == 0)
+        return;
+    Feed<P> feed(a, s_tiles[warp], smem, static_cast<int>(min(run.n, static_cast<long long>(INT_MAX))), cur);
+    feed.start();
+
+    // Lanes of a token differ in bits 0 and 1; tokens r and r + 4 lie beside each other, so that the eight lanes of one
+    // 128-byte read meet no bank twice.
+    const int quarter = lane & 3, token = lane >> 3 | (lane & 4);
+    const int head0 = HEADS >= 4 ? (quarter & 2 ? HEADS / 2 : 0) + (quarter & 1 ? HEADS / 4 : 0) : quarter >> 1;
+    const int col = HALVES == 2 ? lane & 15 : lane;
+    float4 o[HEADS][CPL];
+    float top[HL], total[HL];
+    bool began = false;
+#pragma unroll 1
+    for (int t = 0; t < feed.n; ++t) {
+        feed.turn(t);
+        const WarpTile<P::TOKENS>& tile = feed.tiles[feed.ring_r];
+        const int flags = tile.flags;
+        char* const stage = smem + feed.stage_r * P::STAGE;
+        const char* const ks = stage + warp * 2 * P::HALF;
+        const char* const vs = ks + P::HALF;
+        if (flags & kTileFirst) {
+            began = flags & kTileBegins;
+            __syncthreads();  // the queries are the block's
+            for (int x = tid; x < HEADS * P::QCHUNKS; x += kAttnThreads) {
+                const int row = x / P::QCHUNKS, c = x - row * P::QCHUNKS;
+                *reinterpret_cast<float4*>(s_q + row * DIM + c * 4) =
+                    *reinterpret_cast<const float4*>(stage + P::QROWS + P::qchunk(row, c) * 16);
+            }
+#pragma unroll
+            for (int i = 0; i < HL; ++i) {
+                top[i] = -INFINITY;
+                total[i] = 0.0f;
+            }
+#pragma unroll
+            for (int h = 0; h < HEADS; ++h)
+#pragma unroll
+                for (int c = 0; c < CPL; ++c)
+                    o[h][c] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            __syncthreads();
+        }
+
+        float dot[HEADS];
+#pragma unroll
+        for (int h = 0; h < HEADS; ++h)
+            dot[h] = 0.0f;
+#pragma unroll 4
+        for (int i = 0; i < P::CHUNKS / 4; ++i) {
+            const int c = 4 * i + quarter;
+            const float4 k = *reinterpret_cast<const float4*>(ks + P::chunk(token, c) * 16);
+#pragma unroll
+            for (int h = 0; h < HEADS; ++h) {
+                const float4 q = *reinterpret_cast<const float4*>(s_q + h * DIM + c * 4);
+                dot[h] = fmaf(q.x, k.x, fmaf(q.y, k.y, fmaf(q.z, k.z, fmaf(q.w, k.w, dot[h]))));
+            }
+        }
+        float s[HL];
+        if constexpr (HEADS >= 4) {
+            float two[HEADS / 2];
+#pragma unroll
+            for (int i = 0; i < HEADS / 2; ++i) {
+                const float keep = quarter & 2 ? dot[i + HEADS / 2] : dot[i], send = quarter & 2 ? dot[i] : dot[i + HEADS / 2];
+                two[i] = keep + __shfl_xor_sync(~0u, send, 2);
+            }
+#pragma unroll
+            for (int i = 0; i < HL; ++i) {
+                const float keep = quarter & 1 ? two[i + HL] : two[i], send = quarter & 1 ? two[i] : two[i + HL];
+                s[i] = keep + __shfl_xor_sync(~0u, send, 1);
+            }
+        } else {
+            const float keep = quarter & 2 ? dot[HEADS - 1] : dot[0], send = quarter & 2 ? dot[0] : dot[HEADS - 1];
+            s[0] = keep + __shfl_xor_sync(~0u, send, 2);
+            s[0] += __shfl_xor_sync(~0u, s[0], 1);
+        }
+        const bool in = (tile.in >> token & 1) != 0;
+        bool moved = false;
+        float fix[HL];
+#pragma unroll
+        for (int i = 0; i < HL; ++i) {
+            float x = s[i] * a.scale2;
+            if (a.softcap > 0.0f)
+                x = a.softcap2 * tanhf(x);
+            x = in ? x : -INFINITY;
+            const float best = fmaxf(column_max(x), top[i]);
+            moved = moved || best > top[i];
+            fix[i] = exp2f(top[i] - base_of(best));
+            const float p = exp2f(x - base_of(best));
+            total[i] = total[i] * fix[i] + p;
+            top[i] = best;
+            if (HEADS >= 4 || (quarter & 1) == 0)
+                s_p[token * HEADS + head0 + i] = p;
+        }
+        if (__any_sync(~0u, moved)) {
+            if (token == 0 && (HEADS >= 4 || (quarter & 1) == 0)) {
+#pragma unroll
+                for (int i = 0; i < HL; ++i)
+                    s_fix[head0 + i] = fix[i];
+            }
+            __syncwarp();
+#pragma unroll
+            for (int h = 0; h < HEADS; ++h) {
+                const float f = s_fix[h];
+#pragma unroll
+                for (int c = 0; c < CPL; ++c)
+                    o[h][c] = make_float4(o[h][c].x * f, o[h][c].y * f, o[h][c].z * f, o[h][c].w * f);
+            }
+        }
+        __syncwarp();
+#pragma unroll
+        for (int j = 0; j < P::TOKENS / HALVES; ++j) {
+            const int row = HALVES == 2 ? j + (lane >> 4) * (P::TOKENS / 2) : j;
+#pragma unroll
+            for (int c = 0; c < CPL; ++c) {
+                if (COLS % 32 == 0 || HALVES == 2 || col + 32 * c < COLS) {
+                    const float4 v = *reinterpret_cast<const float4*>(vs + P::chunk(row, col + 32 * c) * 16);
+#pragma unroll
+                    for (int h = 0; h < HEADS; ++h) {
+                        const float p = s_p[row * HEADS + h];
+                        o[h][c] = make_float4(fmaf(p, v.x, o[h][c].x), fmaf(p, v.y, o[h][c].y), fmaf(p, v.z, o[h][c].z), fmaf(p, v.w, o[h][c].w));
+                    }
+                }
+            }
+        }
+
+        if (flags & kTileLast) {
+#pragma unroll
+            for (int i = 0; i < HL; ++i) {
+                const float sum = column_sum(total[i]);
+                if (token == 0 && (HEADS >= 4 || (quarter & 1) == 0)) {
+                    s_top[warp][head0 + i] = top[i];
+                    s_total[warp][head0 + i] = sum;
+                }
+            }
+            __syncthreads();  // and every warp is done with the stage
+            float* const rows = reinterpret_cast<float*>(stage);
+#pragma unroll
+            for (int h = 0; h < HEADS; ++h) {
+                float best = s_top[0][h];
+#pragma unroll
+                for (int w = 1; w < kAttnWarps; ++w)
+                    best = fmaxf(best, s_top[w][h]);
+                const float f = exp2_fast(s_top[warp][h] - base_of(best));
+#pragma unroll
+                for (int c = 0; c < CPL; ++c) {
+                    float4 v = o[h][c];
+                    if constexpr (HALVES == 2) {
+                        v.x += __shfl_xor_sync(~0u, v.x, 16);
+                        v.y += __shfl_xor_sync(~0u, v.y, 16);
+                        v.z += __shfl_xor_sync(~0u, v.z, 16);
+                        v.w += __shfl_xor_sync(~0u, v.w, 16);
+                    }
+                    if (COLS % 32 == 0 || (HALVES == 2 ? lane < 16 : col + 32 * c < COLS))
+                        *reinterpret_cast<float4*>(rows + (warp * HEADS + h) * P::OPITCH + (col + 32 * c) * 4) =
+                            make_float4(v.x * f, v.y * f, v.z * f, v.w * f);
+                }
+            }
+            __syncthreads();
+            write_part<P>(a, tile, began, rows, s_top, s_total);
+            __syncthreads();  // the next copies go to this stage
+        }
+        feed.next();
+    }
+}
+
+// ---------------------------------------------------------------------------
+// The matrix kernel, for 16-bit and 8-bit caches.  Scores are computed as
+// K Q^T and values as V^T P^T: tokens, and then the head's elements, are the
+// 16 rows of a matrix instruction and query heads its 8 columns, so that up to
+// 8 heads fill it where rows of queries would leave half of it empty, and both
+// operands from the cache come out of shared memory by ldmatrix as they lie
+// there.  Weights enter the second product as a pair of 16-bit numbers, their
+// rounding and what it leaves (17 bits and more together), which costs an
+// instruction that the memory's pace hides.  8-bit elements become fp16 in
+// registers, exactly; queries too large or small for fp16 are scaled by a
+// power of two per head first.
+// ---------------------------------------------------------------------------
 __device__ __forceinline__ void ldmatrix4(uint32_t addr, uint32_t* r)
 {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
@@ -562,144 +703,35 @@ __device__ __forceinline__ uint32_t half2_of_e4m3(uint32_t x)
     asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(y) : "h"(static_cast<uint16_t>(x)));
     return y;
 }
-__device__ __forceinline__ float exp2_fast(float x)
-{
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-// Maximum or sum over the eight lanes that hold the same column.
-__device__ __forceinline__ float column_max(float x)
-{
-#pragma unroll
-    for (int w = 4; w < 32; w <<= 1)
-        x = fmaxf(x, __shfl_xor_sync(~0u, x, w));
-    return x;
-}
-__device__ __forceinline__ float column_sum(float x)
-{
-#pragma unroll
-    for (int w = 4; w < 32; w <<= 1)
-        x += __shfl_xor_sync(~0u, x, w);
-    return x;
-}
-
-template <typename T, typename CT, int DIM, int NT>
-__global__ void __launch_bounds__(kAttnThreads, MmaShape<T, CT, DIM, NT>::BLOCKS)
+template <typename P>
+__global__ void __launch_bounds__(kAttnThreads, P::BLOCKS)
 k_attn_mma(const AttnArgs a)
 {
-    using P = MmaShape<T, CT, DIM, NT>;
-    using MT = typename P::MT;
-    constexpr int TILE = P::TILE, TOKENS = P::TOKENS, RING = P::STAGES + 1, KB = P::KB, MTILES = DIM / 16, KSTEPS = DIM / 16;
+    using T = typename P::T;
+    using MT = typename std::conditional<P::SMALL, __half, typename P::CT>::type;  // of the instructions' operands
+    constexpr int TOKENS = P::TOKENS, KB = TOKENS / 16, NT = P::HEADS / 8, MTILES = P::DIM / 16, KSTEPS = P::DIM / 16;
     extern __shared__ __align__(128) char smem[];
-    __shared__ __align__(16) WarpTile<TOKENS> s_tiles[kAttnWarps][RING];
-    __shared__ float s_top[kAttnWarps][8 * NT], s_total[kAttnWarps][8 * NT];
+    __shared__ __align__(16) WarpTile<TOKENS> s_tiles[kAttnWarps][P::RING];
+    __shared__ float s_top[kAttnWarps][P::HEADS], s_total[kAttnWarps][P::HEADS];
     pdl_enter();
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g8 = lane >> 2, t4 = lane & 3;
-    const int heads = a.kv_heads * a.group_blocks;
-    const int chunks = a.head_dim * static_cast<int>(sizeof(CT)) / 16;
-    const int qchunks = a.head_dim * static_cast<int>(sizeof(T)) / 16;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g8 = lane >> 2, t4 = lane & 3;
 
     Cursor cur;
-    const Run run = find_run<TILE>(a, heads, cur);
+    const Run run = find_run<P::TILE>(a, a.kv_heads * a.group_blocks, cur);
     if (run.n == 0)
         return;
-    const int n = static_cast<int>(min(run.n, static_cast<long long>(INT_MAX)));
-
-    // The description of the cursor's tile, `t` of the run, in two steps: its pages' numbers are on their way between them.
-    WarpTile<TOKENS>* const tiles = s_tiles[warp];
-    int page = -1, slot = 0;
-    const auto look_up = [&] {
-        const int token = (cur.s.tile0 + cur.tile) * TILE + warp * TOKENS + lane;
-        page = -1;
-        if (lane < TOKENS && token >= cur.s.start && token < cur.s.end) {
-            const uint32_t column = static_cast<uint32_t>(static_cast<uint64_t>(token) * a.page_magic >> a.page_shift);
-            slot = token - static_cast<int>(column) * a.page_size;
-            page = a.table[static_cast<uint64_t>(cur.b) * a.table_stride + column];
-        }
-    };
-    const auto describe_tile = [&](int t, WarpTile<TOKENS>& tile) {
-        const bool in = page >= 0 && page < a.pages;
-        const uint32_t mask = __ballot_sync(~0u, in);
-        if (lane < TOKENS)
-            tile.offset[lane] = in ? static_cast<long long>(static_cast<uint64_t>(page) * a.page_stride +
-                                                            static_cast<uint64_t>(slot) * a.token_stride +
-                                                            static_cast<uint64_t>(cur.hb / a.group_blocks) * a.head_stride)
-                                   : 0;
-        if (lane == 0) {
-            const bool begins = cur.tile == 0, ends = cur.tile + 1 == cur.s.tiles;
-            tile.b = cur.b;
-            tile.hb = cur.hb;
-            tile.flags = (begins || t == 0 ? kTileFirst : 0) | (ends || t + 1 == n ? kTileLast : 0) |
-                         (begins ? kTileBegins : 0) | (ends ? kTileEnds : 0);
-            tile.in = mask;
-        }
-        cur.advance<TILE>(a, heads);
-    };
-    // The warp's copies of a described tile.  Chunks beyond the head's elements and tokens that are left out become zeros.
-    const auto issue = [&](const WarpTile<TOKENS>& tile, int stage) {
-        const uint32_t base = smem_addr(smem + stage * P::STAGE);
-        const uint32_t ks = base + warp * 2 * P::HALF;
-        const uint32_t in = tile.in;
-#pragma unroll
-        for (int i = 0; i < TOKENS * P::CHUNKS / 32; ++i) {
-            int row, c;
-            if constexpr (32 % P::CHUNKS == 0) {
-                row = i * (32 / P::CHUNKS) + lane / P::CHUNKS;
-                c = lane % P::CHUNKS;
-            } else {
-                row = (lane + i * 32) / P::CHUNKS;
-                c = lane + i * 32 - row * P::CHUNKS;
-            }
-            const bool read = (in >> row & 1) != 0 && c < chunks;
-            const long long at = tile.offset[row] + (c < chunks ? c * 16 : 0);
-            const uint32_t dst = ks + P::chunk(row, c) * 16;
-            cp_async16(dst, a.k + at, read);
-            cp_async16(dst + P::HALF, a.v + at, read);
-        }
-        if (tile.flags & kTileFirst) {
-            const int g = heads_of(a, tile.hb);
-            const char* q = a.q + tile.b * a.q_stride + out_row(a, 0, tile.hb, 0) * a.head_dim * sizeof(T);
-            for (int x = tid; x < 8 * NT * P::QCHUNKS; x += kAttnThreads) {
-                const int row = x / P::QCHUNKS, c = x - row * P::QCHUNKS;
-                const bool read = row < g && c < qchunks;
-                cp_async16(base + P::QROWS + P::qchunk(row, c) * 16,
-                           q + (read ? static_cast<size_t>(row) * a.head_dim * sizeof(T) + c * 16 : 0), read);
-            }
-        }
-    };
-
-    int described = 0, ring_w = 0;  // the next tile to describe, and its slot of the ring
-#pragma unroll 1
-    for (; described < P::STAGES && described < n; ++described) {
-        look_up();
-        describe_tile(described, tiles[ring_w]);
-        ++ring_w;
-    }
-    __syncwarp();
-#pragma unroll 1
-    for (int i = 0; i + 1 < P::STAGES; ++i) {
-        if (i < n)
-            issue(tiles[i], i);
-        cp_async_commit();
-    }
+    Feed<P> feed(a, s_tiles[warp], smem, static_cast<int>(min(run.n, static_cast<long long>(INT_MAX))), cur);
+    feed.start();
 
     uint32_t qf[NT][KSTEPS][2];
     float o[NT][MTILES][4], top[NT][2], total[NT][2], qscale[NT][2];
     bool began = false;
-    int ring_r = 0, ring_i = P::STAGES - 1, stage_r = 0, stage_w = P::STAGES - 1;
 #pragma unroll 1
-    for (int t = 0; t < n; ++t) {
-        cp_async_wait<P::STAGES - 2>();
-        __syncwarp();
-        if (t + P::STAGES - 1 < n)
-            issue(tiles[ring_i], stage_w);
-        cp_async_commit();
-        if (described < n)
-            look_up();
-        const WarpTile<TOKENS>& tile = tiles[ring_r];
+    for (int t = 0; t < feed.n; ++t) {
+        feed.turn(t);
+        const WarpTile<TOKENS>& tile = feed.tiles[feed.ring_r];
         const int flags = tile.flags;
-        char* stage = smem + stage_r * P::STAGE;
+        char* stage = smem + feed.stage_r * P::STAGE;
         const uint32_t ks = smem_addr(stage) + warp * 2 * P::HALF, vs = ks + P::HALF, qs = smem_addr(stage) + P::QROWS;
         if (flags & kTileFirst)
             __syncthreads();  // the queries are the block's
@@ -838,8 +870,7 @@ k_attn_mma(const AttnArgs a)
             if (__any_sync(~0u, moved)) {
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    // A maximum of minus infinity stands still here: 0 in its place keeps the difference defined.
-                    const float fix = exp2_fast(top[nt][i] - (base[i] == -INFINITY ? 0.0f : base[i]));
+                    const float fix = exp2_fast(top[nt][i] - base_of(base[i]));
                     top[nt][i] = base[i];
                     total[nt][i] *= fix;
 #pragma unroll
@@ -851,7 +882,7 @@ k_attn_mma(const AttnArgs a)
             }
 #pragma unroll
             for (int i = 0; i < 2; ++i)
-                base[i] = base[i] == -INFINITY ? 0.0f : base[i];
+                base[i] = base_of(base[i]);
 #pragma unroll
             for (int kb = 0; kb < KB; ++kb) {
 #pragma unroll
@@ -924,8 +955,8 @@ k_attn_mma(const AttnArgs a)
 #pragma unroll
                     for (int w = 1; w < kAttnWarps; ++w)
                         best = fmaxf(best, s_top[w][head]);
-                    const float fix = exp2_fast(top[nt][i] - (best == -INFINITY ? 0.0f : best));
-                    float* out = rows + (warp * 8 * NT + head) * P::OPITCH;
+                    const float fix = exp2_fast(top[nt][i] - base_of(best));
+                    float* out = rows + (warp * P::HEADS + head) * P::OPITCH;
 #pragma unroll
                     for (int m = 0; m < MTILES; ++m) {
                         out[m * 16 + (P::SMALL ? 2 * g8 : g8)] = o[nt][m][i] * fix;
@@ -933,53 +964,10 @@ k_attn_mma(const AttnArgs a)
                     }
                 }
             __syncthreads();
-            const bool whole = began && (flags & kTileEnds);
-            const int g = heads_of(a, tile.hb), fours = a.head_dim / 4;
-            const int slots = min(a.group, kAttnMaxHeads);
-            float* part = a.part + (2ull * blockIdx.x + (began ? 1 : 0)) * a.slot_floats;
-            for (int x = tid; x < g * fours; x += kAttnThreads) {
-                const int head = x / fours, d = (x - head * fours) * 4;
-                float best = s_top[0][head], sum = 0.0f;
-#pragma unroll
-                for (int w = 1; w < kAttnWarps; ++w)
-                    best = fmaxf(best, s_top[w][head]);
-                const float base = best == -INFINITY ? 0.0f : best;
-                float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll
-                for (int w = 0; w < kAttnWarps; ++w) {
-                    sum += s_total[w][head] * exp2_fast(s_top[w][head] - base);
-                    const float4 y = *reinterpret_cast<const float4*>(rows + (w * 8 * NT + head) * P::OPITCH + d);
-                    v.x += y.x;
-                    v.y += y.y;
-                    v.z += y.z;
-                    v.w += y.w;
-                }
-                if (whole) {
-                    const uint64_t row = out_row(a, tile.b, tile.hb, head);
-                    const float f = out_scale(a, sum);
-                    *reinterpret_cast<uint2*>(a.out + (row * a.head_dim + d) * sizeof(T)) =
-                        make_uint2(Lanes<T>::word(v.x * f, v.y * f), Lanes<T>::word(v.z * f, v.w * f));
-                    if (d == 0 && a.lse != nullptr)
-                        a.lse[row] = lse_of(best, sum);
-                } else {
-                    *reinterpret_cast<float4*>(part + head * a.head_dim + d) = v;
-                    if (d == 0) {
-                        part[slots * a.head_dim + head] = best;
-                        part[slots * (a.head_dim + 1) + head] = sum;
-                    }
-                }
-            }
+            write_part<P>(a, tile, began, rows, s_top, s_total);
             __syncthreads();  // the next copies go to this stage
         }
-        if (described < n) {
-            describe_tile(described, tiles[ring_w]);
-            ++described;
-            ring_w = ring_w + 1 == RING ? 0 : ring_w + 1;
-        }
-        ring_r = ring_r + 1 == RING ? 0 : ring_r + 1;
-        ring_i = ring_i + 1 == RING ? 0 : ring_i + 1;
-        stage_r = stage_r + 1 == P::STAGES ? 0 : stage_r + 1;
-        stage_w = stage_w + 1 == P::STAGES ? 0 : stage_w + 1;
+        feed.next();
     }
 }
 
@@ -1098,12 +1086,7 @@ k_attn_join(const AttnArgs a, const int blocks, const int columns)
     }
     if (group == 0 && mine) {
         const uint64_t row = out_row(a, b, hb, h);
-        const float f = out_scale(a, total);
-        T* out = reinterpret_cast<T*>(a.out) + row * a.head_dim + e;
-        if constexpr (sizeof(T) == 4)
-            *reinterpret_cast<float4*>(out) = make_float4(o.x * f, o.y * f, o.z * f, o.w * f);
-        else
-            *reinterpret_cast<uint2*>(out) = make_uint2(Lanes<T>::word(o.x * f, o.y * f), Lanes<T>::word(o.z * f, o.w * f));
+        store_four(reinterpret_cast<T*>(a.out) + row * a.head_dim + e, o, out_scale(a, total));
         if (e == 0 && a.lse != nullptr)
             a.lse[row] = lse_of(top, total);
     }
@@ -1136,14 +1119,11 @@ cudaError_t launch_tiles(Kernel kernel, const AttnArgs& a, int most, int sms, in
 template <typename T, typename CT, int DIM, int HEADS>
 cudaError_t launch_heads(const AttnArgs& a, int most, int sms, cudaStream_t s)
 {
-    constexpr int TILE = attn_tile(sizeof(CT));
-    if constexpr (sizeof(CT) == 4) {
-        using P = PlainShape<T, CT, DIM, HEADS>;
-        return launch_tiles<T, TILE>(k_attn_plain<T, CT, DIM, HEADS>, a, most, sms, P::BLOCKS, P::SMEM, s);
-    } else {
-        using P = MmaShape<T, CT, DIM, HEADS / 8>;
-        return launch_tiles<T, TILE>(k_attn_mma<T, CT, DIM, HEADS / 8>, a, most, sms, P::BLOCKS, P::SMEM, s);
-    }
+    using P = AttnShape<T, CT, DIM, HEADS>;
+    if constexpr (P::WIDE)
+        return launch_tiles<T, P::TILE>(k_attn_fma<P>, a, most, sms, P::BLOCKS, P::SMEM, s);
+    else
+        return launch_tiles<T, P::TILE>(k_attn_mma<P>, a, most, sms, P::BLOCKS, P::SMEM, s);
 }
 
 template <typename T, typename CT, int DIM>
