@@ -33,6 +33,10 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool r
 {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(read ? 16 : 0) : "memory");
 }
+__device__ __forceinline__ void cp_async16_all(uint32_t dst, const void* src)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void cp_async_wait()
@@ -65,13 +69,14 @@ __device__ __forceinline__ Span span_of(const AttnArgs& a, int b)
 
 // The run of tiles of block `c` of `blocks`: the first total % blocks blocks take one more.
 struct Run {
+    long long total;  // tiles of the line
     long long lo;
     long long n;
 };
 __device__ __forceinline__ Run run_of(long long total, int blocks, int c)
 {
     const long long q = total / blocks, r = total % blocks;
-    return {c * q + min(static_cast<long long>(c), r), q + (c < r)};
+    return {total, c * q + min(static_cast<long long>(c), r), q + (c < r)};
 }
 // The block whose run has tile x.
 __device__ __forceinline__ int block_of(long long total, int blocks, long long x)
@@ -85,6 +90,13 @@ struct Cursor {
     int b, hb, tile;  // sequence, head and group block, tile of the item
     int next_length;  // of sequence b + 1, loaded when b began
     Span s;
+    uint64_t head_offset;  // of the item's key-value head in a token
+    const int* table;      // the sequence's row of the page table
+    __device__ void place(const AttnArgs& a)
+    {
+        head_offset = static_cast<uint64_t>(hb / a.group_blocks) * a.head_stride;
+        table = a.table + static_cast<uint64_t>(b) * a.table_stride;
+    }
     __device__ void fetch_next(const AttnArgs& a) { next_length = b + 1 < a.batch ? a.lengths[b + 1] : 0; }
     template <int TILE>
     __device__ void advance(const AttnArgs& a, int heads)
@@ -92,12 +104,13 @@ struct Cursor {
         if (++tile < s.tiles)
             return;
         tile = 0;
-        if (++hb < heads)
-            return;
-        hb = 0;
-        ++b;
-        s = span_of_length<TILE>(a, next_length);
-        fetch_next(a);
+        if (++hb == heads) {
+            hb = 0;
+            ++b;
+            s = span_of_length<TILE>(a, next_length);
+            fetch_next(a);
+        }
+        place(a);
     }
 };
 
@@ -116,6 +129,7 @@ __device__ Run find_run(const AttnArgs& a, int heads, Cursor& cur)
         cur.hb = static_cast<int>(run.lo / cur.s.tiles);
         cur.tile = static_cast<int>(run.lo % cur.s.tiles);
         cur.next_length = 0;
+        cur.place(a);
         return run;
     }
     // Tiles of the sequences [base, base + kAttnThreads), scanned: this thread's own are [before, before + mine).
@@ -170,6 +184,7 @@ __device__ Run find_run(const AttnArgs& a, int heads, Cursor& cur)
     cur.hb = static_cast<int>(in / cur.s.tiles);
     cur.tile = static_cast<int>(in % cur.s.tiles);
     cur.fetch_next(a);
+    cur.place(a);
     return run;
 }
 
@@ -199,6 +214,12 @@ __device__ __forceinline__ float exp2_fast(float x)
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+// tanh(x) of 2 x in base 2, off by 2^-22 at the most: (e - 1) / (e + 1) with e = e^(2 x).
+__device__ __forceinline__ float tanh_fast(float two_x)
+{
+    const float e = exp2_fast(fminf(two_x, 64.0f));
+    return __fdividef(e - 1.0f, e + 1.0f);
 }
 // What a maximum is subtracted as: minus infinity stands for no token yet, and 0 in its place keeps differences defined.
 __device__ __forceinline__ float base_of(float top) { return top == -INFINITY ? 0.0f : top; }
@@ -305,9 +326,9 @@ struct Feed {
         const int token = (cur.s.tile0 + cur.tile) * P::TILE + warp * P::TOKENS + lane;
         page = -1;
         if (lane < P::TOKENS && token >= cur.s.start && token < cur.s.end) {
-            const uint32_t column = static_cast<uint32_t>(static_cast<uint64_t>(token) * a.page_magic >> a.page_shift);
+            const uint32_t column = __umulhi(2u * token, a.page_magic) >> a.page_shift;
             slot = token - static_cast<int>(column) * a.page_size;
-            page = a.table[static_cast<uint64_t>(cur.b) * a.table_stride + column];
+            page = cur.table[column];
         }
     }
     __device__ __forceinline__ void describe()
@@ -318,9 +339,8 @@ struct Feed {
         const bool in = page >= 0 && page < a.pages;
         const uint32_t mask = __ballot_sync(~0u, in);
         if (lane < P::TOKENS)
-            tile.offset[lane] = in ? static_cast<long long>(static_cast<uint64_t>(page) * a.page_stride +
-                                                            static_cast<uint64_t>(slot) * a.token_stride +
-                                                            static_cast<uint64_t>(cur.hb / a.group_blocks) * a.head_stride)
+            tile.offset[lane] = in ? static_cast<long long>(static_cast<uint32_t>(page) * a.page_stride +
+                                                            static_cast<uint32_t>(slot) * a.token_stride + cur.head_offset)
                                    : 0;
         if (lane == 0) {
             const bool begins = cur.tile == 0, ends = cur.tile + 1 == cur.s.tiles;
@@ -341,21 +361,33 @@ struct Feed {
         const uint32_t base = smem_addr(smem + stage * P::STAGE);
         const uint32_t ks = base + warp * 2 * P::HALF;
         const uint32_t in = tile.in;
+        constexpr uint32_t ALL = P::TOKENS == 32 ? ~0u : (1u << P::TOKENS) - 1;
+        if (32 % P::CHUNKS == 0 && in == ALL && chunks == P::CHUNKS) {
+            // A lane keeps its chunk and takes every (32 / CHUNKS)-th row.  The rows' permutation flips address bits 4 to 6
+            // only, and those of its step are constants.
+            constexpr int STEP = 32 % P::CHUNKS == 0 ? 32 / P::CHUNKS : 1;
+            const int row0 = lane / P::CHUNKS, c = lane % P::CHUNKS;
+            const char* const k = a.k + c * 16;
+            const char* const v = a.v + c * 16;
+            const uint32_t first = ks + P::chunk(row0, c) * 16;
 #pragma unroll
-        for (int i = 0; i < P::TOKENS * P::CHUNKS / 32; ++i) {
-            int row, c;
-            if constexpr (32 % P::CHUNKS == 0) {
-                row = i * (32 / P::CHUNKS) + lane / P::CHUNKS;
-                c = lane % P::CHUNKS;
-            } else {
-                row = (lane + i * 32) / P::CHUNKS;
-                c = lane + i * 32 - row * P::CHUNKS;
+            for (int i = 0; i < P::TOKENS / STEP; ++i) {
+                const long long at = tile.offset[row0 + i * STEP];
+                const uint32_t flip = P::CHUNKS % 8 == 0 ? (i * STEP & 7) << 4 : 0;
+                const uint32_t dst = (first ^ flip) + i * STEP * P::PITCH * 16;
+                cp_async16_all(dst, k + at);
+                cp_async16_all(dst + P::HALF, v + at);
             }
-            const bool read = (in >> row & 1) != 0 && c < chunks;
-            const long long at = tile.offset[row] + (c < chunks ? c * 16 : 0);
-            const uint32_t dst = ks + P::chunk(row, c) * 16;
-            cp_async16(dst, a.k + at, read);
-            cp_async16(dst + P::HALF, a.v + at, read);
+        } else {
+#pragma unroll 4
+            for (int i = 0; i < P::TOKENS * P::CHUNKS / 32; ++i) {
+                const int row = (lane + i * 32) / P::CHUNKS, c = lane + i * 32 - row * P::CHUNKS;
+                const bool read = (in >> row & 1) != 0 && c < chunks;
+                const long long at = tile.offset[row] + (c < chunks ? c * 16 : 0);
+                const uint32_t dst = ks + P::chunk(row, c) * 16;
+                cp_async16(dst, a.k + at, read);
+                cp_async16(dst + P::HALF, a.v + at, read);
+            }
         }
         if (tile.flags & kTileFirst) {
             const int g = heads_of(a, tile.hb);
@@ -405,15 +437,23 @@ struct Feed {
 };
 
 // The end of the block's part of an item, after every warp has left its maxima, sums (s_top, s_total) and accumulators,
-// the latter scaled to the block's maximum, in `rows`: adds the warps' up and writes the result or the part.
+// the latter scaled to the block's maximum, in `rows`: adds the warps' up and writes the result or the part.  `first`: the
+// run's tile that this part began with.
 template <typename P>
-__device__ __forceinline__ void write_part(const AttnArgs& a, const WarpTile<P::TOKENS>& tile, bool began, const float* rows,
-                                           const float (*s_top)[P::HEADS], const float (*s_total)[P::HEADS])
+__device__ __forceinline__ void write_part(const AttnArgs& a, const WarpTile<P::TOKENS>& tile, const Run& run, int first, bool began,
+                                           const float* rows, const float (*s_top)[P::HEADS], const float (*s_total)[P::HEADS])
 {
     using T = typename P::T;
     const bool whole = began && (tile.flags & kTileEnds);
     const int g = heads_of(a, tile.hb), fours = a.head_dim / 4, slots = min(a.group, kAttnMaxHeads);
     float* part = a.part + (2ull * blockIdx.x + (began ? 1 : 0)) * a.slot_floats;
+    if (began && threadIdx.x == 0) {  // tells the join which blocks have the item's parts
+        int last = static_cast<int>(blockIdx.x);
+        if (!whole) {
+            last = block_of(run.total, static_cast<int>(gridDim.x), run.lo + first + span_of<P::TILE>(a, tile.b).tiles - 1);
+        }
+        a.blocks_of[static_cast<uint64_t>(tile.b) * (a.kv_heads * a.group_blocks) + tile.hb] = make_int2(static_cast<int>(blockIdx.x), last);
+    }
     for (int x = threadIdx.x; x < g * fours; x += kAttnThreads) {
         const int head = x / fours, d = (x - head * fours) * 4;
         float best = s_top[0][head], sum = 0.0f;
@@ -500,7 +540,8 @@ k_attn_fma(const AttnArgs a)
     const int col = HALVES == 2 ? lane & 15 : lane;
     float4 o[HEADS][CPL];
     float top[HL], total[HL];
-    bool began = false;
+    bool began = false;  // whether the block's part of the item begins it
+    int first = 0;       // the part's first tile
 #pragma unroll 1
     for (int t = 0; t < feed.n; ++t) {
         feed.turn(t);
@@ -511,6 +552,7 @@ k_attn_fma(const AttnArgs a)
         const char* const vs = ks + P::HALF;
         if (flags & kTileFirst) {
             began = flags & kTileBegins;
+            first = t;
             __syncthreads();  // the queries are the block's
             for (int x = tid; x < HEADS * P::QCHUNKS; x += kAttnThreads) {
                 const int row = x / P::QCHUNKS, c = x - row * P::QCHUNKS;
@@ -569,7 +611,7 @@ k_attn_fma(const AttnArgs a)
         for (int i = 0; i < HL; ++i) {
             float x = s[i] * a.scale2;
             if (a.softcap > 0.0f)
-                x = a.softcap2 * tanhf(x);
+                x = a.softcap2 * tanhf(x * (0.5f * kLn2));
             x = in ? x : -INFINITY;
             const float best = fmaxf(column_max(x), top[i]);
             moved = moved || best > top[i];
@@ -645,7 +687,7 @@ k_attn_fma(const AttnArgs a)
                 }
             }
             __syncthreads();
-            write_part<P>(a, tile, began, rows, s_top, s_total);
+            write_part<P>(a, tile, run, first, began, rows, s_top, s_total);
             __syncthreads();  // the next copies go to this stage
         }
         feed.next();
@@ -725,7 +767,8 @@ k_attn_mma(const AttnArgs a)
 
     uint32_t qf[NT][KSTEPS][2];
     float o[NT][MTILES][4], top[NT][2], total[NT][2], qscale[NT][2];
-    bool began = false;
+    bool began = false;  // whether the block's part of the item begins it
+    int first = 0;       // the part's first tile
 #pragma unroll 1
     for (int t = 0; t < feed.n; ++t) {
         feed.turn(t);
@@ -737,6 +780,7 @@ k_attn_mma(const AttnArgs a)
             __syncthreads();  // the queries are the block's
         if (flags & kTileFirst) {
             began = flags & kTileBegins;
+            first = t;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
                 if constexpr (!P::SMALL) {
@@ -838,7 +882,7 @@ k_attn_mma(const AttnArgs a)
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
-                        s[kb][nt][i] = a.softcap2 * tanhf(s[kb][nt][i]);
+                        s[kb][nt][i] = a.softcap2 * tanh_fast(s[kb][nt][i]);
         }
         if (tile.in != (TOKENS == 32 ? ~0u : 0xffffu)) {
             const uint32_t in = tile.in >> g8;
@@ -964,7 +1008,7 @@ k_attn_mma(const AttnArgs a)
                     }
                 }
             __syncthreads();
-            write_part<P>(a, tile, began, rows, s_top, s_total);
+            write_part<P>(a, tile, run, first, began, rows, s_top, s_total);
             __syncthreads();  // the next copies go to this stage
         }
         feed.next();
@@ -972,8 +1016,8 @@ k_attn_mma(const AttnArgs a)
 }
 
 // ---------------------------------------------------------------------------
-// The join of an item's parts.  It derives the blocks that hold parts from the
-// same lengths and the same split; an item that one block had whole is written
+// The join of an item's parts, which lie in the slots of the blocks that the
+// item's first block names; an item that one block had whole is written
 // already.  A block takes `columns` (a power of two) of an item's groups of
 // four elements, heads after each other; its threads take a column over every
 // (threads / columns)-th part with a maximum and a sum of their own, all loads
@@ -981,53 +1025,24 @@ k_attn_mma(const AttnArgs a)
 // ---------------------------------------------------------------------------
 constexpr int kJoinThreads = 256;
 
-template <typename T, int TILE>
+template <typename T>
 __global__ void __launch_bounds__(kJoinThreads)
-k_attn_join(const AttnArgs a, const int blocks, const int columns)
+k_attn_join(const AttnArgs a, const int columns)
 {
-    constexpr int WARPS = kJoinThreads / 32, AHEAD = 8;
-    __shared__ long long s_sum[2][WARPS];
+    constexpr int AHEAD = 8;
     __shared__ float4 s_o[kJoinThreads];
     __shared__ float2 s_w[kJoinThreads];  // maximum and sum
     pdl_enter();
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int tid = threadIdx.x;
     const int heads = a.kv_heads * a.group_blocks;
     const int slots = min(a.group, kAttnMaxHeads), fours = a.head_dim / 4;
     const int cuts = (slots * fours + columns - 1) / columns;
     const int item = blockIdx.x / cuts;
-    const int b = item / heads, hb = item - b * heads;
-
-    long long before = 0, all = 0;
-    for (int s = tid; s < a.batch; s += kJoinThreads) {
-        const int n = span_of<TILE>(a, s).tiles;
-        all += n;
-        before += s < b ? n : 0;
-    }
-    const int tiles = span_of<TILE>(a, b).tiles;
-    if (a.batch > 1) {
-#pragma unroll
-        for (int w = 16; w > 0; w >>= 1) {
-            all += __shfl_xor_sync(~0u, all, w);
-            before += __shfl_xor_sync(~0u, before, w);
-        }
-        if (lane == 0) {
-            s_sum[0][warp] = all;
-            s_sum[1][warp] = before;
-        }
-        __syncthreads();
-        all = before = 0;
-#pragma unroll
-        for (int w = 0; w < WARPS; ++w) {
-            all += s_sum[0][w];
-            before += s_sum[1][w];
-        }
-    } else {
-        all = tiles;
-    }
-    const long long lo = before * heads + static_cast<long long>(hb) * tiles;
-    const int c0 = block_of(all * heads, blocks, lo), c1 = block_of(all * heads, blocks, lo + tiles - 1);
+    const int2 blocks = a.blocks_of[item];
+    const int c0 = blocks.x, c1 = blocks.y;
     if (c0 == c1)
         return;
+    const int b = item / heads, hb = item - b * heads;
     const int parts = c1 - c0 + 1, groups = kJoinThreads / columns, group = tid / columns;
     const int x = (blockIdx.x - item * cuts) * columns + tid % columns;
     const int h = x / fours, e = (x - h * fours) * 4;
@@ -1093,14 +1108,14 @@ k_attn_join(const AttnArgs a, const int blocks, const int columns)
 }
 
 // Launches `kernel`, `per_sm` blocks of which fit an SM, and then the join.
-template <typename T, int TILE, typename Kernel>
+template <typename T, typename Kernel>
 cudaError_t launch_tiles(Kernel kernel, const AttnArgs& a, int most, int sms, int per_sm, size_t smem, cudaStream_t s)
 {
-    // The join's threads of a column: a quarter of the parts an item has if all are alike, four at least (one sequence
-    // may be much longer than the others), 32 at most.
+    // The join's threads of a column: a quarter of the parts an item has if all are alike, 32 at most, and two at least,
+    // for one sequence may be much longer than the others (four cost 2 us more on 511 MB of bf16 cache in 256 rows).
     const int blocks = most < sms * per_sm ? most : sms * per_sm;
     const uint64_t items = static_cast<uint64_t>(a.batch) * a.kv_heads * a.group_blocks;
-    int groups = 4;
+    int groups = 2;
     while (groups < 32 && 8ull * groups * items <= static_cast<uint64_t>(blocks))
         groups *= 2;
     const int columns = kJoinThreads / groups, slots = a.group < kAttnMaxHeads ? a.group : kAttnMaxHeads;
@@ -1113,7 +1128,7 @@ cudaError_t launch_tiles(Kernel kernel, const AttnArgs& a, int most, int sms, in
     e = launch_k(kernel, dim3(blocks), dim3(kAttnThreads), smem, s, a);
     if (e != cudaSuccess)
         return e;
-    return launch_k(k_attn_join<T, TILE>, dim3(static_cast<unsigned>(joins)), dim3(kJoinThreads), 0, s, a, blocks, columns);
+    return launch_k(k_attn_join<T>, dim3(static_cast<unsigned>(joins)), dim3(kJoinThreads), 0, s, a, columns);
 }
 
 template <typename T, typename CT, int DIM, int HEADS>
@@ -1121,9 +1136,9 @@ cudaError_t launch_heads(const AttnArgs& a, int most, int sms, cudaStream_t s)
 {
     using P = AttnShape<T, CT, DIM, HEADS>;
     if constexpr (P::WIDE)
-        return launch_tiles<T, P::TILE>(k_attn_fma<P>, a, most, sms, P::BLOCKS, P::SMEM, s);
+        return launch_tiles<T>(k_attn_fma<P>, a, most, sms, P::BLOCKS, P::SMEM, s);
     else
-        return launch_tiles<T, P::TILE>(k_attn_mma<P>, a, most, sms, P::BLOCKS, P::SMEM, s);
+        return launch_tiles<T>(k_attn_mma<P>, a, most, sms, P::BLOCKS, P::SMEM, s);
 }
 
 template <typename T, typename CT, int DIM>

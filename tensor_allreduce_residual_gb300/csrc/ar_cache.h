@@ -52,20 +52,21 @@ struct AttnArgs {
     const char* v;
     char* out;
     float* lse;               // nullable
+    int2* blocks_of;          // the first and last block of each item
     float* part;              // partial results: two slots per block
     const int* table;
     const int* lengths;
     uint64_t q_stride;        // bytes
     uint64_t page_stride, token_stride, head_stride;
     int table_stride, pages, page_size, batch;
-    uint64_t page_magic;      // token / page_size == token * page_magic >> page_shift for token < 2^31
+    uint32_t page_magic;      // token / page_size == (2 token * page_magic >> 32) >> page_shift for token < 2^31
     int page_shift;
     int capacity;             // tokens a table row can hold
     int kv_heads, group;      // group: query heads of one key-value head
     int group_blocks;         // group cut into blocks of at most kAttnMaxHeads
     int head_dim;
     int window;
-    float scale2;             // of the scores, k_scale included, in base 2; with softcap over softcap instead
+    float scale2;             // of the scores, k_scale included, in base 2; with softcap twice that over softcap
     float softcap;
     float softcap2;           // softcap in base 2
     float v_scale;

@@ -96,13 +96,19 @@ int check_attention(const ar_kv_cache* c, int q_heads)
     return AR_OK;
 }
 
+// Sequences times key-value heads times blocks of query heads.
+size_t attention_items(const ar_kv_cache* c, int q_heads)
+{
+    const int group_blocks = (q_heads / c->kv_heads + ar::kAttnMaxHeads - 1) / ar::kAttnMaxHeads;
+    return static_cast<size_t>(c->batch) * c->kv_heads * group_blocks;
+}
+
 // Blocks of the attention kernel, at most: no more than there can be tiles.
 int attention_blocks(const ar_kv_cache* c, int q_heads)
 {
     const long long cap = static_cast<long long>(c->max_pages) * c->page_size;
     const long long tile = ar::attn_tile(cache_esize_of(c->dtype));
-    const long long group_blocks = (q_heads / c->kv_heads + ar::kAttnMaxHeads - 1) / ar::kAttnMaxHeads;
-    const long long items = static_cast<long long>(c->batch) * c->kv_heads * group_blocks;
+    const long long items = static_cast<long long>(attention_items(c, q_heads));
     const long long tiles = (cap < INT_MAX ? cap : INT_MAX) / tile + 2;
     const long long most = ar::kAttnMaxBlocks;
     return static_cast<int>(items >= most || items * tiles >= most ? most : items * tiles);
@@ -202,7 +208,7 @@ size_t ar_paged_attention_workspace_size(const ar_kv_cache* cache, int q_heads)
         return 0;
     const size_t blocks = static_cast<size_t>(attention_blocks(c, q_heads));
     const size_t slot = static_cast<size_t>(ar::attn_slot_floats(q_heads / c->kv_heads, c->head_dim)) * sizeof(float);
-    return (2 * blocks * slot + 255) / 256 * 256;
+    return (attention_items(c, q_heads) * sizeof(int2) + 255) / 256 * 256 + (2 * blocks * slot + 255) / 256 * 256;
 }
 
 int ar_paged_attention(const ar_kv_cache* cache, const void* q, size_t q_stride, int q_heads, float scale, int window,
@@ -239,7 +245,8 @@ int ar_paged_attention(const ar_kv_cache* cache, const void* q, size_t q_stride,
     a.v = static_cast<const char*>(c->v);
     a.out = static_cast<char*>(out);
     a.lse = lse;
-    a.part = static_cast<float*>(workspace);
+    a.blocks_of = static_cast<int2*>(workspace);
+    a.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + (attention_items(c, q_heads) * sizeof(int2) + 255) / 256 * 256);
     a.table = c->page_table;
     a.lengths = c->lengths;
     a.q_stride = c->batch > 1 ? q_stride * e : 0;
@@ -250,11 +257,10 @@ int ar_paged_attention(const ar_kv_cache* cache, const void* q, size_t q_stride,
     a.pages = c->pages;
     a.page_size = c->page_size;
     a.batch = c->batch;
-    // m = ceil(2^(31 + l) / d) with 2^l >= d is at most 2^l / 2^(31 + l) too large: n m >> (31 + l) is exact below 2^31.
+    // m = ceil(2^(31 + l) / d) with 2^l the power of two from d on is below 2^32, and n m >> (31 + l) = n / d below 2^31.
     while ((1ll << a.page_shift) < c->page_size)
         ++a.page_shift;
-    a.page_shift += 31;
-    a.page_magic = ((1ull << a.page_shift) + c->page_size - 1) / c->page_size;
+    a.page_magic = static_cast<uint32_t>(((1ull << (31 + a.page_shift)) + c->page_size - 1) / c->page_size);
     a.capacity = static_cast<int>(cap < INT_MAX - 64 ? cap : INT_MAX - 64);  // a tile's end stays an int
     a.kv_heads = c->kv_heads;
     a.group = q_heads / c->kv_heads;
@@ -262,7 +268,7 @@ int ar_paged_attention(const ar_kv_cache* cache, const void* q, size_t q_stride,
     a.head_dim = c->head_dim;
     a.window = window;
     constexpr float kLog2e = 1.4426950408889634f;
-    a.scale2 = softcap > 0.0f ? scale * c->k_scale / softcap : scale * c->k_scale * kLog2e;
+    a.scale2 = scale * c->k_scale * kLog2e * (softcap > 0.0f ? 2.0f / softcap : 1.0f);
     a.softcap = softcap;
     a.softcap2 = softcap * kLog2e;
     a.v_scale = c->v_scale;
