@@ -70,7 +70,8 @@ def _binding_command(out: str) -> list:
     lib_dir = os.path.join(root, "lib")
     return [shutil.which("g++") or "c++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
             f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *(f"-I{i}" for i in includes), BINDING_SOURCE,
-            "-o", out, f"-L{lib_dir}", f"-Wl,-rpath,{lib_dir}", "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10_cuda", "-lc10"]
+            "-o", out, f"-L{lib_dir}", f"-Wl,-rpath,{lib_dir}", "-ltorch_python", "-ltorch", "-ltorch_cpu",
+            "-ltorch_cuda", "-lc10_cuda", "-lc10"]
 
 
 def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:

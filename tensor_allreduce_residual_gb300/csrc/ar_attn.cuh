@@ -73,15 +73,20 @@ struct Run {
     long long lo;
     long long n;
 };
+// a / b of a >= 0, b > 0: a 64-bit division takes five times as long as a 32-bit one, and is hardly ever needed.
+__device__ __forceinline__ long long divide(long long a, int b)
+{
+    return a <= 0xffffffffll ? static_cast<uint32_t>(a) / static_cast<uint32_t>(b) : a / b;
+}
 __device__ __forceinline__ Run run_of(long long total, int blocks, int c)
 {
-    const long long q = total / blocks, r = total % blocks;
+    const long long q = divide(total, blocks), r = total - q * blocks;
     return {total, c * q + min(static_cast<long long>(c), r), q + (c < r)};
 }
 // The block whose run has tile x.
 __device__ __forceinline__ int block_of(long long total, int blocks, long long x)
 {
-    const long long q = total / blocks, r = total % blocks, edge = r * (q + 1);
+    const long long q = divide(total, blocks), r = total - q * blocks, edge = r * (q + 1);
     return static_cast<int>(x < edge ? x / (q + 1) : r + (x - edge) / q);
 }
 
@@ -126,8 +131,8 @@ __device__ Run find_run(const AttnArgs& a, int heads, Cursor& cur)
         cur.b = 0;
         cur.s = span_of<TILE>(a, 0);
         const Run run = run_of(static_cast<long long>(cur.s.tiles) * heads, gridDim.x, blockIdx.x);
-        cur.hb = static_cast<int>(run.lo / cur.s.tiles);
-        cur.tile = static_cast<int>(run.lo % cur.s.tiles);
+        cur.hb = static_cast<int>(divide(run.lo, cur.s.tiles));
+        cur.tile = static_cast<int>(run.lo - static_cast<long long>(cur.hb) * cur.s.tiles);
         cur.next_length = 0;
         cur.place(a);
         return run;
@@ -162,7 +167,7 @@ __device__ Run find_run(const AttnArgs& a, int heads, Cursor& cur)
     const Run run = run_of(tiles * heads, gridDim.x, blockIdx.x);
     if (run.n == 0)
         return run;
-    const long long x = run.lo / heads;  // sequence b takes [heads * P, heads * (P + tiles of b)) of the line
+    const long long x = divide(run.lo, heads);  // sequence b takes [heads * P, heads * (P + tiles of b)) of the line
     long long passed = 0;
     for (int base = 0; base < a.batch; base += kAttnThreads) {
         if (a.batch > kAttnThreads)
@@ -181,8 +186,8 @@ __device__ Run find_run(const AttnArgs& a, int heads, Cursor& cur)
     cur.b = s_b;
     cur.s = span_of<TILE>(a, cur.b);
     const long long in = run.lo - s_before * heads;
-    cur.hb = static_cast<int>(in / cur.s.tiles);
-    cur.tile = static_cast<int>(in % cur.s.tiles);
+    cur.hb = static_cast<int>(divide(in, cur.s.tiles));
+    cur.tile = static_cast<int>(in - static_cast<long long>(cur.hb) * cur.s.tiles);
     cur.fetch_next(a);
     cur.place(a);
     return run;
@@ -1021,18 +1026,20 @@ k_attn_mma(const AttnArgs a)
 // already.  A block takes `columns` (a power of two) of an item's groups of
 // four elements, heads after each other; its threads take a column over every
 // (threads / columns)-th part with a maximum and a sum of their own, all loads
-// of eight parts at once, and meet in a fixed tree in shared memory.
+// of four parts at once, and meet in a fixed tree in shared memory.
 // ---------------------------------------------------------------------------
 constexpr int kJoinThreads = 256;
 
 template <typename T>
-__global__ void __launch_bounds__(kJoinThreads)
+__global__ void __launch_bounds__(kJoinThreads, 4)  // 64 registers: a join fits beside attention blocks
 k_attn_join(const AttnArgs a, const int columns)
 {
-    constexpr int AHEAD = 8;
+    constexpr int AHEAD = 4;
     __shared__ float4 s_o[kJoinThreads];
     __shared__ float2 s_w[kJoinThreads];  // maximum and sum
-    pdl_enter();
+    // The next kernel is not let in early here: blocks of the next attention that then filled the SMs beside waiting joins
+    // lay unevenly, and the last of them ran as a second wave (93 MB of fp16 cache: 24.0 against 29 us a call).
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     const int tid = threadIdx.x;
     const int heads = a.kv_heads * a.group_blocks;
     const int slots = min(a.group, kAttnMaxHeads), fours = a.head_dim / 4;
@@ -1111,8 +1118,8 @@ k_attn_join(const AttnArgs a, const int columns)
 template <typename T, typename Kernel>
 cudaError_t launch_tiles(Kernel kernel, const AttnArgs& a, int most, int sms, int per_sm, size_t smem, cudaStream_t s)
 {
-    // The join's threads of a column: a quarter of the parts an item has if all are alike, 32 at most, and two at least,
-    // for one sequence may be much longer than the others (four cost 2 us more on 511 MB of bf16 cache in 256 rows).
+    // The join's threads of a column: an eighth of the parts an item has if all are alike at least, 32 at most, and two
+    // at least, for one sequence may be much longer than the others (four cost 2 us more on 511 MB of bf16 cache in 256 rows).
     const int blocks = most < sms * per_sm ? most : sms * per_sm;
     const uint64_t items = static_cast<uint64_t>(a.batch) * a.kv_heads * a.group_blocks;
     int groups = 2;

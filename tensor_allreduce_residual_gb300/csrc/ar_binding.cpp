@@ -7,6 +7,8 @@
 #include <Python.h>
 
 #include <ATen/ATen.h>
+#include <ATen/cuda/EmptyTensor.h>
+#include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
@@ -134,10 +136,24 @@ struct Stream {
     }
 };
 
+// As torch.empty, without the way through the dispatcher.
 Tensor empty(at::IntArrayRef shape, at::ScalarType type, const Tensor& like)
 {
-    return at::empty(shape, at::TensorOptions().dtype(type).device(like.device()));
+    return Tensor(at::detail::empty_cuda(shape, type, like.device(), std::nullopt));
 }
+
+// Memory of the current stream's pool for one call: no tensor, and given back to that stream when the call is queued.
+struct Scratch {
+    void* p = nullptr;
+    Scratch() = default;
+    Scratch(const Scratch&) = delete;
+    void make(size_t bytes) { p = c10::cuda::CUDACachingAllocator::raw_alloc(bytes); }
+    ~Scratch()
+    {
+        if (p != nullptr)
+            c10::cuda::CUDACachingAllocator::raw_delete(p);
+    }
+};
 
 // A dense tensor of exactly this shape and type.
 void dense(const Tensor& t, const char* what, at::IntArrayRef shape, at::ScalarType type, int dev)
@@ -295,7 +311,8 @@ PyObject* paged_attention(PyObject* const* a)
     const int window = int32(a[6], "window");
     const float softcap = static_cast<float>(number(a[7]));
     Stream s(a[15], dev);
-    Tensor out, lse, work;
+    Tensor out, lse;
+    Scratch scratch;
     if (given(a[11])) {
         out = tensor(a[11], "out");
         dense(out, "out", {batch, q_heads, dim}, type, dev);
@@ -308,19 +325,23 @@ PyObject* paged_attention(PyObject* const* a)
     } else if (PyObject_IsTrue(a[13])) {
         lse = empty({batch, q_heads}, at::kFloat, q);
     }
+    void* workspace;
     size_t bytes;
     if (given(a[14])) {
-        work = tensor(a[14], "workspace");
+        const Tensor& work = tensor(a[14], "workspace");
         if (cuda_index(work) != dev || !work.is_contiguous())
             bad("workspace must be a contiguous tensor" + on(dev));
         bytes = static_cast<size_t>(work.numel()) * work.element_size();
+        workspace = work.data_ptr();
     } else {
         bytes = g_workspace_size(&cache, q_heads);
-        work = empty({static_cast<int64_t>(bytes)}, at::kByte, q);
+        if (bytes != 0)
+            scratch.make(bytes);
+        workspace = scratch.p;
     }
     check("ar_paged_attention",
           g_attention(&cache, q.data_ptr(), q_stride, q_heads, scale, window, softcap, out.data_ptr(),
-                      lse.defined() ? static_cast<float*>(lse.data_ptr()) : nullptr, work.data_ptr(), bytes, code, s.handle));
+                      lse.defined() ? static_cast<float*>(lse.data_ptr()) : nullptr, workspace, bytes, code, s.handle));
     if (!lse.defined())
         return THPVariable_Wrap(std::move(out));
     PyObject* x = THPVariable_Wrap(std::move(out));

@@ -38,7 +38,7 @@ struct AppendArgs {
 };
 
 // Rows a block of the append kernel may take, and its threads.
-constexpr int kAppendMaxTokens = 4;
+constexpr int kAppendMaxTokens = 2;
 constexpr int kAppendThreads = 256;
 
 // One unit is a 16-byte vector of T (vec) or one element, a pair of them where the pair's halves lie apart.
