@@ -28,14 +28,19 @@ constexpr int kAttnWarps = kAttnThreads / 32;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
-// 16-byte asynchronous copy into shared memory; `read` == false writes zeros.
+// 16-byte asynchronous copies into shared memory; `read` == false writes zeros.  `policy`: how long L2 keeps the line.
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool read)
 {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(read ? 16 : 0) : "memory");
 }
-__device__ __forceinline__ void cp_async16_all(uint32_t dst, const void* src)
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool read, uint64_t policy)
 {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+    asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2, %3;" ::"r"(dst), "l"(src), "r"(read ? 16 : 0), "l"(policy)
+                 : "memory");
+}
+__device__ __forceinline__ void cp_async16_all(uint32_t dst, const void* src, uint64_t policy)
+{
+    asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "l"(policy) : "memory");
 }
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -278,8 +283,8 @@ struct AttnShape {
     // Blocks of an SM.  A tile of few bytes takes a warp longer than they take to come, so that more warps help: four
     // blocks of heads up to 64 elements (31.8 against 34.3 us with two on 93 MB of fp16 cache), three of 8-bit ones up to
     // 128 (93.5 against 98.6 us on 533 MB) and of fp32 ones with two query heads (40.0 against 41.6 us on 194 MB).  For 128
-    // 16-bit elements two blocks' deeper rings do better (93 against 98 us on 511 MB).  Long heads leave room for two
-    // stages in one block only.
+    // 16-bit elements two blocks with deeper rings are as good (511 MB in 256 rows: 87.1 against 85.5 us with three; 67 MB
+    // in one: 18.0 against 18.3 to 20 us).  Long heads leave room for two stages in one block only.
     static constexpr int WANT = HEADS == 8 && DIM <= 64 && !WIDE ? 4 : (HEADS == 8 && DIM <= 128 && SMALL) || HEADS == 2 ? 3 : 2;
     static constexpr int BLOCKS = fits(kSmemPerSM / WANT) >= 2 ? WANT : 1;
     static constexpr int STAGES = fits(kSmemPerSM / BLOCKS);
@@ -313,6 +318,7 @@ struct Feed {
     char* smem;
     int heads, n, warp, lane, chunks, qchunks;
     Cursor cur;
+    uint64_t policy;
     int page = -1, slot = 0;
     int described = 0, ring_w = 0, ring_i = P::STAGES - 1, ring_r = 0, stage_w = P::STAGES - 1, stage_r = 0;
 
@@ -321,6 +327,12 @@ struct Feed {
           chunks(a_.head_dim * static_cast<int>(sizeof(typename P::CT)) / 16), qchunks(a_.head_dim * static_cast<int>(sizeof(typename P::T)) / 16),
           cur(c)
     {
+        // The cache streams through L2 and leaves it to others, unless more query heads are to read the same tiles.
+        // (511 MB of bf16 cache: 87.1 against 89.8 us; 67 MB: 18.0 against 19.0.)
+        if (a.group_blocks == 1)
+            asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(policy));
+        else
+            asm("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(policy));
     }
 
     // The next tile's description, in two steps: its pages' numbers are on their way between them.
@@ -367,21 +379,26 @@ struct Feed {
         const uint32_t ks = base + warp * 2 * P::HALF;
         const uint32_t in = tile.in;
         constexpr uint32_t ALL = P::TOKENS == 32 ? ~0u : (1u << P::TOKENS) - 1;
-        if (32 % P::CHUNKS == 0 && in == ALL && chunks == P::CHUNKS) {
-            // A lane keeps its chunk and takes every (32 / CHUNKS)-th row.  The rows' permutation flips address bits 4 to 6
-            // only, and those of its step are constants.
-            constexpr int STEP = 32 % P::CHUNKS == 0 ? 32 / P::CHUNKS : 1;
-            const int row0 = lane / P::CHUNKS, c = lane % P::CHUNKS;
-            const char* const k = a.k + c * 16;
-            const char* const v = a.v + c * 16;
-            const uint32_t first = ks + P::chunk(row0, c) * 16;
+        if (in == ALL && chunks == P::CHUNKS) {
+            // 32 lanes cover PER * 32 chunks, ROWS whole rows, in PER steps; then everything repeats ROWS rows further, where
+            // the rows' permutation flips address bits 4 to 6 by a constant.
+            constexpr int ROWS = P::CHUNKS % 32 == 0 ? 1 : P::CHUNKS % 16 == 0 ? 2 : P::CHUNKS % 8 == 0 ? 4 : P::CHUNKS % 4 == 0 ? 8 : 16;
+            constexpr int PER = ROWS * P::CHUNKS / 32;
+            static_assert(PER * 32 == ROWS * P::CHUNKS && P::TOKENS % ROWS == 0, "whole rows, whole tiles");
 #pragma unroll
-            for (int i = 0; i < P::TOKENS / STEP; ++i) {
-                const long long at = tile.offset[row0 + i * STEP];
-                const uint32_t flip = P::CHUNKS % 8 == 0 ? (i * STEP & 7) << 4 : 0;
-                const uint32_t dst = (first ^ flip) + i * STEP * P::PITCH * 16;
-                cp_async16_all(dst, k + at);
-                cp_async16_all(dst + P::HALF, v + at);
+            for (int j = 0; j < PER; ++j) {
+                const int row0 = (lane + 32 * j) / P::CHUNKS, c = lane + 32 * j - row0 * P::CHUNKS;
+                const char* const k = a.k + c * 16;
+                const char* const v = a.v + c * 16;
+                const uint32_t first = ks + P::chunk(row0, c) * 16;
+#pragma unroll
+                for (int i = 0; i < P::TOKENS; i += ROWS) {
+                    const long long at = tile.offset[row0 + i];
+                    const uint32_t flip = P::CHUNKS % 8 == 0 ? (i & 7) << 4 : 0;
+                    const uint32_t dst = (first ^ flip) + i * P::PITCH * 16;
+                    cp_async16_all(dst, k + at, policy);
+                    cp_async16_all(dst + P::HALF, v + at, policy);
+                }
             }
         } else {
 #pragma unroll 4
@@ -390,8 +407,8 @@ struct Feed {
                 const bool read = (in >> row & 1) != 0 && c < chunks;
                 const long long at = tile.offset[row] + (c < chunks ? c * 16 : 0);
                 const uint32_t dst = ks + P::chunk(row, c) * 16;
-                cp_async16(dst, a.k + at, read);
-                cp_async16(dst + P::HALF, a.v + at, read);
+                cp_async16(dst, a.k + at, read, policy);
+                cp_async16(dst + P::HALF, a.v + at, read, policy);
             }
         }
         if (tile.flags & kTileFirst) {
