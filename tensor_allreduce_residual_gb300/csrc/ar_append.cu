@@ -108,11 +108,15 @@ __device__ __forceinline__ void store_cached(void* base, uint64_t e, float* f, f
 // chain of loads would cost more than the row's copy), fills a table of their
 // cosines and sines in shared memory, which all heads of a row share, and then
 // walks the rows' units: pairs of vectors that rotate into each other, or
-// single vectors.  Bound by HBM for prompts and by its two dependent loads
-// (table, then nothing: rows are independent of it) for single tokens.
+// single vectors.  Bound by HBM for prompts (365 MB in 63 us, 5.8 TB/s) and for
+// single tokens by the chain of loads length, page, store (3.0 us for 8 rows).
+// What hides the loads is the number of threads: forms that kept several units
+// a thread in flight, or a head's cosines and sines in registers, ran fewer of
+// them and took 69 to 94 us for the same prompts; hence one unit at a time and
+// eight blocks an SM.
 // ---------------------------------------------------------------------------
 template <typename T, typename CT, bool VEC>
-__global__ void __launch_bounds__(kAppendThreads)
+__global__ void __launch_bounds__(kAppendThreads, 8)
 k_kv_append(const AppendArgs a)
 {
     extern __shared__ float2 s_turn[];  // [rows][half]
