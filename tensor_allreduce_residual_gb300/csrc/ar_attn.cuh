@@ -95,30 +95,41 @@ __device__ __forceinline__ int block_of(long long total, int blocks, long long x
     return static_cast<int>(x < edge ? x / (q + 1) : r + (x - edge) / q);
 }
 
-// Where a block is on the line.
+// Where a warp is on the line.  All lanes hold the same, but for `lengths`, of which each has one of 32 sequences'.
 struct Cursor {
     int b, hb, tile;  // sequence, head and group block, tile of the item
-    int next_length;  // of sequence b + 1, loaded when b began
     Span s;
     uint64_t head_offset;  // of the item's key-value head in a token
     const int* table;      // the sequence's row of the page table
-    __device__ void place(const AttnArgs& a)
+    int lengths, first;    // of sequences first .. first + 31
+    __device__ __forceinline__ void load(const AttnArgs& a, int from)
     {
-        head_offset = static_cast<uint64_t>(hb / a.group_blocks) * a.head_stride;
+        const int lane = threadIdx.x & 31;
+        first = from;
+        lengths = from + lane < a.batch ? a.lengths[from + lane] : 0;
+    }
+    template <int TILE>
+    __device__ __forceinline__ void enter(const AttnArgs& a, int sequence)
+    {
+        b = sequence;
+        if (b - first >= 32)
+            load(a, b);
+        s = span_of_length<TILE>(a, __shfl_sync(~0u, lengths, b - first));
         table = a.table + static_cast<uint64_t>(b) * a.table_stride;
     }
-    __device__ void fetch_next(const AttnArgs& a) { next_length = b + 1 < a.batch ? a.lengths[b + 1] : 0; }
+    __device__ __forceinline__ void place(const AttnArgs& a)
+    {
+        head_offset = static_cast<uint64_t>(a.group_blocks == 1 ? hb : hb / a.group_blocks) * a.head_stride;
+    }
     template <int TILE>
-    __device__ void advance(const AttnArgs& a, int heads)
+    __device__ __forceinline__ void advance(const AttnArgs& a, int heads)
     {
         if (++tile < s.tiles)
             return;
         tile = 0;
         if (++hb == heads) {
             hb = 0;
-            ++b;
-            s = span_of_length<TILE>(a, next_length);
-            fetch_next(a);
+            enter<TILE>(a, b + 1);
         }
         place(a);
     }
@@ -133,12 +144,11 @@ __device__ Run find_run(const AttnArgs& a, int heads, Cursor& cur)
     __shared__ long long s_before;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     if (a.batch == 1) {
-        cur.b = 0;
-        cur.s = span_of<TILE>(a, 0);
+        cur.load(a, 0);
+        cur.enter<TILE>(a, 0);
         const Run run = run_of(static_cast<long long>(cur.s.tiles) * heads, gridDim.x, blockIdx.x);
         cur.hb = static_cast<int>(divide(run.lo, cur.s.tiles));
         cur.tile = static_cast<int>(run.lo - static_cast<long long>(cur.hb) * cur.s.tiles);
-        cur.next_length = 0;
         cur.place(a);
         return run;
     }
@@ -188,12 +198,11 @@ __device__ Run find_run(const AttnArgs& a, int heads, Cursor& cur)
         passed += chunk;
     }
     __syncthreads();
-    cur.b = s_b;
-    cur.s = span_of<TILE>(a, cur.b);
+    cur.load(a, s_b);
+    cur.enter<TILE>(a, s_b);
     const long long in = run.lo - s_before * heads;
     cur.hb = static_cast<int>(divide(in, cur.s.tiles));
     cur.tile = static_cast<int>(in - static_cast<long long>(cur.hb) * cur.s.tiles);
-    cur.fetch_next(a);
     cur.place(a);
     return run;
 }
@@ -201,12 +210,12 @@ __device__ Run find_run(const AttnArgs& a, int heads, Cursor& cur)
 // Row of the output of head `i` of the item's group block, and how many heads the block has.
 __device__ __forceinline__ uint64_t out_row(const AttnArgs& a, int b, int hb, int i)
 {
-    const int h = hb / a.group_blocks, gb = hb - h * a.group_blocks;
-    return (static_cast<uint64_t>(b) * a.kv_heads + h) * a.group + gb * kAttnMaxHeads + i;
+    const int h = a.group_blocks == 1 ? hb : hb / a.group_blocks, gb = hb - h * a.group_blocks;
+    return (static_cast<uint64_t>(b) * a.kv_heads + h) * a.group + gb * a.block_heads + i;
 }
 __device__ __forceinline__ int heads_of(const AttnArgs& a, int hb)
 {
-    return min(a.group - (hb % a.group_blocks) * kAttnMaxHeads, kAttnMaxHeads);
+    return a.group_blocks == 1 ? a.group : min(a.group - (hb % a.group_blocks) * a.block_heads, a.block_heads);
 }
 
 __device__ __forceinline__ float lse_of(float top2, float total)
@@ -259,7 +268,7 @@ struct AttnShape {
     using CT = CT_;
     static constexpr int DIM = DIM_, HEADS = HEADS_;
     static constexpr bool SMALL = sizeof(CT) == 1, WIDE = sizeof(CT) == 4;
-    static constexpr int TILE = attn_tile(sizeof(CT));
+    static constexpr int TILE = attn_tile(sizeof(CT), DIM);
     static constexpr int TOKENS = TILE / kAttnWarps;  // a warp's tokens of a tile
     static constexpr int CHUNKS = DIM * sizeof(CT) / 16;
     static constexpr int QCHUNKS = DIM * sizeof(T) / 16;
@@ -271,8 +280,8 @@ struct AttnShape {
     static constexpr int QROWS = kAttnWarps * 2 * HALF;  // where a stage's queries begin
     static constexpr int STAGE = QROWS + HEADS * QPITCH * 16;
     static constexpr int INFO = kAttnWarps * (TOKENS * 8 + 16);
-    // Shared memory of a block that is no stage's (the fp32 kernel's: queries, and weights of a tile).
-    static constexpr int OTHER = WIDE ? HEADS * DIM * 4 + TILE * HEADS * 4 + kAttnWarps * HEADS * 4 : 0;
+    // Shared memory of a block besides: the fp32 kernel's weights of a tile.
+    static constexpr int OTHER = WIDE ? (TILE + kAttnWarps) * HEADS * 4 : 0;
     static constexpr int OPITCH = DIM + 4;  // floats; the epilogue's rows, one per warp and head, lie in a used stage
     static_assert(kAttnWarps * HEADS * OPITCH * 4 <= STAGE, "the epilogue fits a stage");
     static constexpr int fits(int bytes)
@@ -280,16 +289,16 @@ struct AttnShape {
         const int n = (bytes - kSmemReservedPerBlock - 1024 - INFO - OTHER) / (STAGE + INFO);
         return n < 5 ? n : 5;
     }
-    // Blocks of an SM.  A tile of few bytes takes a warp longer than they take to come, so that more warps help: four
-    // blocks of heads up to 64 elements (31.8 against 34.3 us with two on 93 MB of fp16 cache), three of 8-bit ones up to
-    // 128 (93.5 against 98.6 us on 533 MB) and of fp32 ones with two query heads (40.0 against 41.6 us on 194 MB).  For 128
-    // 16-bit elements two blocks with deeper rings are as good (511 MB in 256 rows: 87.1 against 85.5 us with three; 67 MB
-    // in one: 18.0 against 18.3 to 20 us).  Long heads leave room for two stages in one block only.
-    static constexpr int WANT = HEADS == 8 && DIM <= 64 && !WIDE ? 4 : (HEADS == 8 && DIM <= 128 && SMALL) || HEADS == 2 ? 3 : 2;
+    // Blocks of an SM: three where registers and two stages of each fit, which short rows and 8-bit elements gain from most
+    // (256 rows of 1 to 200 tokens, 8 key-value heads of 128 bf16 elements: 38.1 against 46.0 us with two; 511 MB of them in
+    // 256 longer rows: 84.0 against 87.5; 67 MB in one: 18.8 against 17.7; 533 MB of e4m3: 93.5 against 98.6); two for
+    // stages over 48 KB or where a block of 8 or 16 heads needs the registers of a third.  Long heads leave room for two
+    // stages in one block only.
+    static constexpr int WANT = HEADS == 2 || (HEADS == 8 && DIM <= 128 && STAGE < 48 * 1024 && (!WIDE || DIM <= 64)) ? 3 : 2;
     static constexpr int BLOCKS = fits(kSmemPerSM / WANT) >= 2 ? WANT : 1;
     static constexpr int STAGES = fits(kSmemPerSM / BLOCKS);
     static constexpr int RING = STAGES + 1;  // descriptions of tiles: one more is written than copies are under way
-    static constexpr int SMEM = STAGES * STAGE + OTHER;
+    static constexpr int SMEM = STAGES * STAGE;
     static __device__ __forceinline__ int chunk(int row, int c)
     {
         return CHUNKS % 8 == 0 ? row * PITCH + (c ^ (row & 7)) : row * PITCH + c;
@@ -319,7 +328,6 @@ struct Feed {
     int heads, n, warp, lane, chunks, qchunks;
     Cursor cur;
     uint64_t policy;
-    int page = -1, slot = 0;
     int described = 0, ring_w = 0, ring_i = P::STAGES - 1, ring_r = 0, stage_w = P::STAGES - 1, stage_r = 0;
 
     __device__ Feed(const AttnArgs& a_, Tile* tiles_, char* smem_, int n_, const Cursor& c)
@@ -335,41 +343,50 @@ struct Feed {
             asm("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(policy));
     }
 
-    // The next tile's description, in two steps: its pages' numbers are on their way between them.
-    __device__ __forceinline__ void look_up()
+    // The next tile's description, in two steps, with its pages' numbers on their way between them.
+    struct Pending {
+        int page = -1, slot = 0;
+        uint64_t head_offset;
+        Tile* tile = nullptr;
+    } pending;
+    __device__ __forceinline__ void open(Pending& p)
     {
+        p.tile = nullptr;
         if (described >= n)
             return;
+        p.tile = &tiles[ring_w];
         const int token = (cur.s.tile0 + cur.tile) * P::TILE + warp * P::TOKENS + lane;
-        page = -1;
+        p.page = -1;
         if (lane < P::TOKENS && token >= cur.s.start && token < cur.s.end) {
             const uint32_t column = __umulhi(2u * token, a.page_magic) >> a.page_shift;
-            slot = token - static_cast<int>(column) * a.page_size;
-            page = cur.table[column];
+            p.slot = token - static_cast<int>(column) * a.page_size;
+            p.page = cur.table[column];
         }
-    }
-    __device__ __forceinline__ void describe()
-    {
-        if (described >= n)
-            return;
-        Tile& tile = tiles[ring_w];
-        const bool in = page >= 0 && page < a.pages;
-        const uint32_t mask = __ballot_sync(~0u, in);
-        if (lane < P::TOKENS)
-            tile.offset[lane] = in ? static_cast<long long>(static_cast<uint32_t>(page) * a.page_stride +
-                                                            static_cast<uint32_t>(slot) * a.token_stride + cur.head_offset)
-                                   : 0;
+        p.head_offset = cur.head_offset;
         if (lane == 0) {
             const bool begins = cur.tile == 0, ends = cur.tile + 1 == cur.s.tiles;
-            tile.b = cur.b;
-            tile.hb = cur.hb;
-            tile.flags = (begins || described == 0 ? kTileFirst : 0) | (ends || described + 1 == n ? kTileLast : 0) |
-                         (begins ? kTileBegins : 0) | (ends ? kTileEnds : 0);
-            tile.in = mask;
+            p.tile->b = cur.b;
+            p.tile->hb = cur.hb;
+            p.tile->flags = (begins || described == 0 ? kTileFirst : 0) | (ends || described + 1 == n ? kTileLast : 0) |
+                            (begins ? kTileBegins : 0) | (ends ? kTileEnds : 0);
         }
-        cur.advance<P::TILE>(a, heads);
         ++described;
         ring_w = ring_w + 1 == P::RING ? 0 : ring_w + 1;
+        if (described < n)
+            cur.advance<P::TILE>(a, heads);
+    }
+    __device__ __forceinline__ void close(const Pending& p)
+    {
+        if (p.tile == nullptr)
+            return;
+        const bool in = p.page >= 0 && p.page < a.pages;
+        const uint32_t mask = __ballot_sync(~0u, in);
+        if (lane < P::TOKENS)
+            p.tile->offset[lane] = in ? static_cast<long long>(static_cast<uint32_t>(p.page) * a.page_stride +
+                                                               static_cast<uint32_t>(p.slot) * a.token_stride + p.head_offset)
+                                      : 0;
+        if (lane == 0)
+            p.tile->in = mask;
     }
     // The warp's copies of a described tile, and its share of a new item's queries.  Chunks beyond the head's elements
     // and tokens that are left out become zeros.
@@ -425,17 +442,19 @@ struct Feed {
     // Fills the ring before the first tile.
     __device__ __forceinline__ void start()
     {
-#pragma unroll 1
-        while (described < P::STAGES && described < n) {
-            look_up();
-            describe();
-        }
-        __syncwarp();
-#pragma unroll 1
-        for (int i = 0; i + 1 < P::STAGES; ++i) {
-            if (i < n)
-                issue(tiles[i], i);
-            cp_async_commit();
+        Pending p[P::STAGES];
+#pragma unroll
+        for (int i = 0; i < P::STAGES; ++i)
+            open(p[i]);
+#pragma unroll
+        for (int i = 0; i < P::STAGES; ++i) {
+            close(p[i]);
+            __syncwarp();
+            if (i + 1 < P::STAGES) {
+                if (i < n)
+                    issue(tiles[i], i);
+                cp_async_commit();
+            }
         }
     }
     // Waits for tile t's copies and sends the next ones on their way.
@@ -446,11 +465,11 @@ struct Feed {
         if (t + P::STAGES - 1 < n)
             issue(tiles[ring_i], stage_w);
         cp_async_commit();
-        look_up();
+        open(pending);
     }
     __device__ __forceinline__ void next()
     {
-        describe();
+        close(pending);
         ring_r = ring_r + 1 == P::RING ? 0 : ring_r + 1;
         ring_i = ring_i + 1 == P::RING ? 0 : ring_i + 1;
         stage_r = stage_r + 1 == P::STAGES ? 0 : stage_r + 1;
@@ -467,7 +486,7 @@ __device__ __forceinline__ void write_part(const AttnArgs& a, const WarpTile<P::
 {
     using T = typename P::T;
     const bool whole = began && (tile.flags & kTileEnds);
-    const int g = heads_of(a, tile.hb), fours = a.head_dim / 4, slots = min(a.group, kAttnMaxHeads);
+    const int g = heads_of(a, tile.hb), fours = a.head_dim / 4, slots = min(a.group, a.block_heads);
     float* part = a.part + (2ull * blockIdx.x + (began ? 1 : 0)) * a.slot_floats;
     if (began && threadIdx.x == 0) {  // tells the join which blocks have the item's parts
         int last = static_cast<int>(blockIdx.x);
@@ -477,7 +496,7 @@ __device__ __forceinline__ void write_part(const AttnArgs& a, const WarpTile<P::
         a.blocks_of[static_cast<uint64_t>(tile.b) * (a.kv_heads * a.group_blocks) + tile.hb] = make_int2(static_cast<int>(blockIdx.x), last);
     }
     for (int x = threadIdx.x; x < g * fours; x += kAttnThreads) {
-        const int head = x / fours, d = (x - head * fours) * 4;
+        const int head = static_cast<int>(static_cast<uint32_t>(x) * a.fours_magic >> 32), d = (x - head * fours) * 4;
         float best = s_top[0][head], sum = 0.0f;
 #pragma unroll
         for (int w = 1; w < kAttnWarps; ++w)
@@ -508,6 +527,18 @@ __device__ __forceinline__ void write_part(const AttnArgs& a, const WarpTile<P::
     }
 }
 
+// a * b + c of two numbers at once.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c)
+{
+    float2 d;
+    asm("{\n\t.reg .b64 x, y, z;\n\t"
+        "mov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
+        "fma.rn.f32x2 z, x, y, z;\n\tmov.b64 {%0, %1}, z;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
+}
+
 // Maximum or sum over the eight lanes that differ in the lane's upper three bits.
 __device__ __forceinline__ float column_max(float x)
 {
@@ -525,27 +556,33 @@ __device__ __forceinline__ float column_sum(float x)
 }
 
 // ---------------------------------------------------------------------------
-// The fp32 kernel: multiply-adds, as no matrix instruction keeps 24 bits.
-// Scores: a warp's eight tokens take four lanes each, which share the head's
-// chunks and then exchange halves of their heads' sums, so that each ends with
-// the sums of a quarter of the heads.  Weighted values: a lane takes four
-// elements of the head (half of the tokens where those are fewer than lanes)
-// and every head's weights from shared memory.
+// The fp32 kernel: multiply-adds, as no matrix instruction keeps 24 bits.  A
+// lane has four elements of the head (eight of the longest), of the queries in
+// registers, and forms its part of every token's and head's product; then the
+// lanes halve what they hold in five exchanges, each keeping and receiving a
+// half, and end with one token's sums for a quarter of the heads.  So a cached
+// element is read from shared memory once, and no query is.  (Four lanes a
+// token, the queries in shared memory, read those four times as often as the
+// cache: 68 us on 269 MB with 8 heads, its loads at 64 % of the pipe.)  For the
+// weighted values the same elements take every token's weights, from shared
+// memory.  Heads of up to 64 elements take half of the lanes, and each half
+// half of the tokens.
 // ---------------------------------------------------------------------------
 template <typename P>
 __global__ void __launch_bounds__(kAttnThreads, P::BLOCKS)
 k_attn_fma(const AttnArgs a)
 {
-    constexpr int HEADS = P::HEADS, DIM = P::DIM, COLS = DIM / 4, CPL = (COLS + 31) / 32, HALVES = COLS <= 16 ? 2 : 1;
+    constexpr int HEADS = P::HEADS, COLS = P::DIM / 4, CPL = (COLS + 31) / 32, HALVES = COLS <= 16 ? 2 : 1;
     constexpr int HL = HEADS >= 4 ? HEADS / 4 : 1;  // heads whose sums a lane ends with
-    static_assert(P::TOKENS == 8 && P::CHUNKS % 8 == 0, "four lanes a token");
+    constexpr int MINE = P::TOKENS / HALVES;        // tokens a lane has a part of
+    static_assert(P::TOKENS == 8, "eight tokens by four quarters of the heads");
     extern __shared__ __align__(128) char smem[];
     __shared__ __align__(16) WarpTile<P::TOKENS> s_tiles[kAttnWarps][P::RING];
     __shared__ float s_top[kAttnWarps][HEADS], s_total[kAttnWarps][HEADS];
-    float* const s_q = reinterpret_cast<float*>(smem + P::STAGES * P::STAGE);  // [HEADS][DIM]
+    __shared__ __align__(16) float s_weights[kAttnWarps][(P::TOKENS + 1) * HEADS];  // [TOKENS][HEADS], then [HEADS] factors
     pdl_enter();
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    float* const s_p = s_q + HEADS * DIM + warp * (P::TOKENS + 1) * HEADS;  // [TOKENS][HEADS], then [HEADS] factors
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    float* const s_p = s_weights[warp];
     float* const s_fix = s_p + P::TOKENS * HEADS;
 
     Cursor cur;
@@ -555,12 +592,11 @@ k_attn_fma(const AttnArgs a)
     Feed<P> feed(a, s_tiles[warp], smem, static_cast<int>(min(run.n, static_cast<long long>(INT_MAX))), cur);
     feed.start();
 
-    // Lanes of a token differ in bits 0 and 1; tokens r and r + 4 lie beside each other, so that the eight lanes of one
-    // 128-byte read meet no bank twice.
-    const int quarter = lane & 3, token = lane >> 3 | (lane & 4);
-    const int head0 = HEADS >= 4 ? (quarter & 2 ? HEADS / 2 : 0) + (quarter & 1 ? HEADS / 4 : 0) : quarter >> 1;
-    const int col = HALVES == 2 ? lane & 15 : lane;
-    float4 o[HEADS][CPL];
+    const int quarter = lane & 3, token = lane >> 2;
+    const int head0 = HEADS >= 4 ? quarter * HL : quarter >> 1;
+    const int col = HALVES == 2 ? lane & 15 : lane, row0 = HALVES == 2 ? (lane >> 4) * MINE : 0;
+    const auto has = [&](int c) { return COLS % 32 == 0 || HALVES == 2 || col + 32 * c < COLS; };
+    float4 q[HEADS][CPL], o[HEADS][CPL];
     float top[HL], total[HL];
     bool began = false;  // whether the block's part of the item begins it
     int first = 0;       // the part's first tile
@@ -576,62 +612,65 @@ k_attn_fma(const AttnArgs a)
             began = flags & kTileBegins;
             first = t;
             __syncthreads();  // the queries are the block's
-            for (int x = tid; x < HEADS * P::QCHUNKS; x += kAttnThreads) {
-                const int row = x / P::QCHUNKS, c = x - row * P::QCHUNKS;
-                *reinterpret_cast<float4*>(s_q + row * DIM + c * 4) =
-                    *reinterpret_cast<const float4*>(stage + P::QROWS + P::qchunk(row, c) * 16);
-            }
+#pragma unroll
+            for (int h = 0; h < HEADS; ++h)
+#pragma unroll
+                for (int c = 0; c < CPL; ++c) {
+                    q[h][c] = o[h][c] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                    if (has(c))
+                        q[h][c] = *reinterpret_cast<const float4*>(stage + P::QROWS + P::qchunk(h, col + 32 * c) * 16);
+                }
 #pragma unroll
             for (int i = 0; i < HL; ++i) {
                 top[i] = -INFINITY;
                 total[i] = 0.0f;
             }
-#pragma unroll
-            for (int h = 0; h < HEADS; ++h)
-#pragma unroll
-                for (int c = 0; c < CPL; ++c)
-                    o[h][c] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            __syncthreads();
+            __syncthreads();  // a warp ahead may bring the next queries here
         }
 
-        float dot[HEADS];
+        float dot[MINE * HEADS];
 #pragma unroll
-        for (int h = 0; h < HEADS; ++h)
-            dot[h] = 0.0f;
-#pragma unroll 4
-        for (int i = 0; i < P::CHUNKS / 4; ++i) {
-            const int c = 4 * i + quarter;
-            const float4 k = *reinterpret_cast<const float4*>(ks + P::chunk(token, c) * 16);
+        for (int j = 0; j < MINE; ++j) {
+            float4 k[CPL];
+#pragma unroll
+            for (int c = 0; c < CPL; ++c) {
+                k[c] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                if (has(c))
+                    k[c] = *reinterpret_cast<const float4*>(ks + P::chunk(row0 + j, col + 32 * c) * 16);
+            }
 #pragma unroll
             for (int h = 0; h < HEADS; ++h) {
-                const float4 q = *reinterpret_cast<const float4*>(s_q + h * DIM + c * 4);
-                dot[h] = fmaf(q.x, k.x, fmaf(q.y, k.y, fmaf(q.z, k.z, fmaf(q.w, k.w, dot[h]))));
+                float2 x = make_float2(0.0f, 0.0f);
+#pragma unroll
+                for (int c = 0; c < CPL; ++c) {
+                    x = fma2(make_float2(q[h][c].x, q[h][c].y), make_float2(k[c].x, k[c].y), x);
+                    x = fma2(make_float2(q[h][c].z, q[h][c].w), make_float2(k[c].z, k[c].w), x);
+                }
+                dot[j * HEADS + h] = x.x + x.y;
             }
         }
-        float s[HL];
-        if constexpr (HEADS >= 4) {
-            float two[HEADS / 2];
+        // Lane bits 4 to 2 choose the token (bit 4 does already where it chooses the half), bits 1 and 0 the heads.
+        int held = MINE * HEADS;
 #pragma unroll
-            for (int i = 0; i < HEADS / 2; ++i) {
-                const float keep = quarter & 2 ? dot[i + HEADS / 2] : dot[i], send = quarter & 2 ? dot[i] : dot[i + HEADS / 2];
-                two[i] = keep + __shfl_xor_sync(~0u, send, 2);
-            }
+        for (int w = 16 / HALVES; w > 0; w >>= 1) {
+            if (held > 1) {
+                held /= 2;
 #pragma unroll
-            for (int i = 0; i < HL; ++i) {
-                const float keep = quarter & 1 ? two[i + HL] : two[i], send = quarter & 1 ? two[i] : two[i + HL];
-                s[i] = keep + __shfl_xor_sync(~0u, send, 1);
+                for (int i = 0; i < MINE * HEADS / 2; ++i)
+                    if (i < held) {
+                        const float keep = lane & w ? dot[i + held] : dot[i], send = lane & w ? dot[i] : dot[i + held];
+                        dot[i] = keep + __shfl_xor_sync(~0u, send, w);
+                    }
+            } else {
+                dot[0] += __shfl_xor_sync(~0u, dot[0], w);
             }
-        } else {
-            const float keep = quarter & 2 ? dot[HEADS - 1] : dot[0], send = quarter & 2 ? dot[0] : dot[HEADS - 1];
-            s[0] = keep + __shfl_xor_sync(~0u, send, 2);
-            s[0] += __shfl_xor_sync(~0u, s[0], 1);
         }
         const bool in = (tile.in >> token & 1) != 0;
         bool moved = false;
         float fix[HL];
 #pragma unroll
         for (int i = 0; i < HL; ++i) {
-            float x = s[i] * a.scale2;
+            float x = dot[i] * a.scale2;
             if (a.softcap > 0.0f)
                 x = a.softcap2 * tanhf(x * (0.5f * kLn2));
             x = in ? x : -INFINITY;
@@ -661,16 +700,26 @@ k_attn_fma(const AttnArgs a)
         }
         __syncwarp();
 #pragma unroll
-        for (int j = 0; j < P::TOKENS / HALVES; ++j) {
-            const int row = HALVES == 2 ? j + (lane >> 4) * (P::TOKENS / 2) : j;
+        for (int j = 0; j < MINE; ++j) {
+            const int row = row0 + j;
+            float p[HEADS];
+            if constexpr (HEADS >= 4) {
+#pragma unroll
+                for (int h = 0; h < HEADS; h += 4)
+                    *reinterpret_cast<float4*>(p + h) = *reinterpret_cast<const float4*>(s_p + row * HEADS + h);
+            } else {
+                *reinterpret_cast<float2*>(p) = *reinterpret_cast<const float2*>(s_p + row * HEADS);
+            }
 #pragma unroll
             for (int c = 0; c < CPL; ++c) {
-                if (COLS % 32 == 0 || HALVES == 2 || col + 32 * c < COLS) {
+                if (has(c)) {
                     const float4 v = *reinterpret_cast<const float4*>(vs + P::chunk(row, col + 32 * c) * 16);
 #pragma unroll
                     for (int h = 0; h < HEADS; ++h) {
-                        const float p = s_p[row * HEADS + h];
-                        o[h][c] = make_float4(fmaf(p, v.x, o[h][c].x), fmaf(p, v.y, o[h][c].y), fmaf(p, v.z, o[h][c].z), fmaf(p, v.w, o[h][c].w));
+                        const float2 two = make_float2(p[h], p[h]);
+                        const float2 x = fma2(two, make_float2(v.x, v.y), make_float2(o[h][c].x, o[h][c].y));
+                        const float2 y = fma2(two, make_float2(v.z, v.w), make_float2(o[h][c].z, o[h][c].w));
+                        o[h][c] = make_float4(x.x, x.y, y.x, y.y);
                     }
                 }
             }
@@ -724,7 +773,8 @@ k_attn_fma(const AttnArgs a)
 // operands from the cache come out of shared memory by ldmatrix as they lie
 // there.  Weights enter the second product as a pair of 16-bit numbers, their
 // rounding and what it leaves (17 bits and more together), which costs an
-// instruction that the memory's pace hides.  8-bit elements become fp16 in
+// instruction that the memory's pace hides; for bf16 queries on an 8-bit cache
+// the first of them, in fp16, is enough.  8-bit elements become fp16 in
 // registers, exactly; queries too large or small for fp16 are scaled by a
 // power of two per head first.
 // ---------------------------------------------------------------------------
@@ -774,6 +824,8 @@ k_attn_mma(const AttnArgs a)
     using T = typename P::T;
     using MT = typename std::conditional<P::SMALL, __half, typename P::CT>::type;  // of the instructions' operands
     constexpr int TOKENS = P::TOKENS, KB = TOKENS / 16, NT = P::HEADS / 8, MTILES = P::DIM / 16, KSTEPS = P::DIM / 16;
+    // fp16 weights alone are eight times finer than a bf16 result.
+    constexpr bool LOW = !(P::SMALL && std::is_same<T, __nv_bfloat16>::value);
     extern __shared__ __align__(128) char smem[];
     __shared__ __align__(16) WarpTile<TOKENS> s_tiles[kAttnWarps][P::RING];
     __shared__ float s_top[kAttnWarps][P::HEADS], s_total[kAttnWarps][P::HEADS];
@@ -958,9 +1010,11 @@ k_attn_mma(const AttnArgs a)
                     total[nt][0] += p0;
                     total[nt][1] += p1;
                     const uint32_t h = Lanes<MT>::word(p0, p1);
-                    const float2 back = Lanes<MT>::two(h);
                     hi[kb][nt][r] = transposed(h);
-                    lo[kb][nt][r] = transposed(Lanes<MT>::word(p0 - back.x, p1 - back.y));
+                    if constexpr (LOW) {
+                        const float2 back = Lanes<MT>::two(h);
+                        lo[kb][nt][r] = transposed(Lanes<MT>::word(p0 - back.x, p1 - back.y));
+                    }
                 }
             }
         }
@@ -992,7 +1046,8 @@ k_attn_mma(const AttnArgs a)
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt) {
                             mma16816<MT>(o[nt][2 * j + c], v, hi[kb][nt][0], hi[kb][nt][1]);
-                            mma16816<MT>(o[nt][2 * j + c], v, lo[kb][nt][0], lo[kb][nt][1]);
+                            if constexpr (LOW)
+                                mma16816<MT>(o[nt][2 * j + c], v, lo[kb][nt][0], lo[kb][nt][1]);
                         }
                     }
                 }
@@ -1059,7 +1114,7 @@ k_attn_join(const AttnArgs a, const int columns)
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int tid = threadIdx.x;
     const int heads = a.kv_heads * a.group_blocks;
-    const int slots = min(a.group, kAttnMaxHeads), fours = a.head_dim / 4;
+    const int slots = min(a.group, a.block_heads), fours = a.head_dim / 4;
     const int cuts = (slots * fours + columns - 1) / columns;
     const int item = blockIdx.x / cuts;
     const int2 blocks = a.blocks_of[item];
@@ -1069,7 +1124,7 @@ k_attn_join(const AttnArgs a, const int columns)
     const int b = item / heads, hb = item - b * heads;
     const int parts = c1 - c0 + 1, groups = kJoinThreads / columns, group = tid / columns;
     const int x = (blockIdx.x - item * cuts) * columns + tid % columns;
-    const int h = x / fours, e = (x - h * fours) * 4;
+    const int h = static_cast<int>(static_cast<uint32_t>(x) * a.fours_magic >> 32), e = (x - h * fours) * 4;
     const bool mine = h < heads_of(a, hb);
     float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     float top = -INFINITY, total = 0.0f;
@@ -1142,7 +1197,7 @@ cudaError_t launch_tiles(Kernel kernel, const AttnArgs& a, int most, int sms, in
     int groups = 2;
     while (groups < 32 && 8ull * groups * items <= static_cast<uint64_t>(blocks))
         groups *= 2;
-    const int columns = kJoinThreads / groups, slots = a.group < kAttnMaxHeads ? a.group : kAttnMaxHeads;
+    const int columns = kJoinThreads / groups, slots = a.group < a.block_heads ? a.group : a.block_heads;
     const uint64_t joins = items * ((slots * (a.head_dim / 4) + columns - 1) / columns);
     if (joins > static_cast<uint64_t>(INT_MAX))
         return cudaErrorInvalidConfiguration;
@@ -1168,11 +1223,10 @@ cudaError_t launch_heads(const AttnArgs& a, int most, int sms, cudaStream_t s)
 template <typename T, typename CT, int DIM>
 cudaError_t launch_dim(const AttnArgs& a, int most, int sms, cudaStream_t s)
 {
-    if constexpr (sizeof(CT) == 4) {
-        if (a.group <= 2)
-            return launch_heads<T, CT, DIM, 2>(a, most, sms, s);
-    }
-    return a.group <= 8 ? launch_heads<T, CT, DIM, 8>(a, most, sms, s) : launch_heads<T, CT, DIM, 16>(a, most, sms, s);
+    if constexpr (sizeof(CT) == 4)
+        return a.group <= 2 ? launch_heads<T, CT, DIM, 2>(a, most, sms, s) : launch_heads<T, CT, DIM, 8>(a, most, sms, s);
+    else
+        return a.group <= 8 ? launch_heads<T, CT, DIM, 8>(a, most, sms, s) : launch_heads<T, CT, DIM, 16>(a, most, sms, s);
 }
 
 template <typename T, typename CT>

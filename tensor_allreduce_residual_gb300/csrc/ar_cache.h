@@ -63,31 +63,35 @@ struct AttnArgs {
     int page_shift;
     int capacity;             // tokens a table row can hold
     int kv_heads, group;      // group: query heads of one key-value head
-    int group_blocks;         // group cut into blocks of at most kAttnMaxHeads
+    int group_blocks;         // the group cut into blocks of at most block_heads
+    int block_heads;          // attn_block_heads()
     int head_dim;
     int window;
     float scale2;             // of the scores, k_scale included, in base 2; with softcap twice that over softcap
     float softcap;
     float softcap2;           // softcap in base 2
     float v_scale;
+    uint64_t fours_magic;     // x / (head_dim / 4) == x * fours_magic >> 32 for x below 16 * 64
     int slot_floats;          // floats of one partial slot
 };
 
-// Query heads of one key-value head that one block attends for at once.
-constexpr int kAttnMaxHeads = 16;
+// Query heads of one key-value head that one block attends for at once, at most.  A larger group reads its tiles again for
+// every so many: 8 in fp32, whose 16 would not fit the registers with their queries.
+__host__ __device__ constexpr int attn_block_heads(int cache_esize) { return cache_esize == 4 ? 8 : 16; }
 // Blocks of the attention kernel, at most: four per SM of the 152.  The workspace holds two slots for each.
 constexpr int kAttnMaxBlocks = 608;
 constexpr int kAttnMaxDim = 256;
 
-// Cached tokens of one tile: what a block loads, and the work is cut into.
-__host__ __device__ constexpr int attn_tile(int cache_esize) { return 128 / cache_esize; }
-
-// A partial slot: [heads][head_dim] sums, [heads] maxima, [heads] sums of weights (heads = min(group, 16)).
-__host__ __device__ inline int attn_slot_floats(int group, int head_dim)
+// Cached tokens of one tile: what a block loads at once, and the work is cut into.  A warp takes a quarter: 8 tokens in
+// fp32, else one block of 16, or two where they are 128 elements of 8 bits or up to 96 of 16 (93 MB of fp16 heads of 64:
+// 21.3 against 22.6 us with one).
+__host__ __device__ constexpr int attn_tile(int cache_esize, int head_dim)
 {
-    const int heads = group < kAttnMaxHeads ? group : kAttnMaxHeads;
-    return (heads * (head_dim + 2) + 3) / 4 * 4;
+    return cache_esize == 4 ? 32 : cache_esize == 2 && head_dim > 96 ? 64 : 128;
 }
+
+// A partial slot: [heads][head_dim] sums, [heads] maxima, [heads] sums of weights.
+__host__ __device__ inline int attn_slot_floats(int heads, int head_dim) { return (heads * (head_dim + 2) + 3) / 4 * 4; }
 
 // At most `most` blocks of the attention kernel, and no more than `sms` SMs hold at once; then the join kernel.
 template <typename T, typename CT>

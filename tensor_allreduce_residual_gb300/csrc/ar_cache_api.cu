@@ -96,18 +96,29 @@ int check_attention(const ar_kv_cache* c, int q_heads)
     return AR_OK;
 }
 
+int group_blocks_of(const ar_kv_cache* c, int q_heads)
+{
+    const int block_heads = ar::attn_block_heads(cache_esize_of(c->dtype));
+    return (q_heads / c->kv_heads + block_heads - 1) / block_heads;
+}
+
 // Sequences times key-value heads times blocks of query heads.
 size_t attention_items(const ar_kv_cache* c, int q_heads)
 {
-    const int group_blocks = (q_heads / c->kv_heads + ar::kAttnMaxHeads - 1) / ar::kAttnMaxHeads;
-    return static_cast<size_t>(c->batch) * c->kv_heads * group_blocks;
+    return static_cast<size_t>(c->batch) * c->kv_heads * group_blocks_of(c, q_heads);
+}
+
+int slot_floats_of(const ar_kv_cache* c, int q_heads)
+{
+    const int group = q_heads / c->kv_heads, block_heads = ar::attn_block_heads(cache_esize_of(c->dtype));
+    return ar::attn_slot_floats(group < block_heads ? group : block_heads, c->head_dim);
 }
 
 // Blocks of the attention kernel, at most: no more than there can be tiles.
 int attention_blocks(const ar_kv_cache* c, int q_heads)
 {
     const long long cap = static_cast<long long>(c->max_pages) * c->page_size;
-    const long long tile = ar::attn_tile(cache_esize_of(c->dtype));
+    const long long tile = ar::attn_tile(cache_esize_of(c->dtype), c->head_dim);
     const long long items = static_cast<long long>(attention_items(c, q_heads));
     const long long tiles = (cap < INT_MAX ? cap : INT_MAX) / tile + 2;
     const long long most = ar::kAttnMaxBlocks;
@@ -207,7 +218,7 @@ size_t ar_paged_attention_workspace_size(const ar_kv_cache* cache, int q_heads)
     if (check_attention(c, q_heads) != AR_OK)
         return 0;
     const size_t blocks = static_cast<size_t>(attention_blocks(c, q_heads));
-    const size_t slot = static_cast<size_t>(ar::attn_slot_floats(q_heads / c->kv_heads, c->head_dim)) * sizeof(float);
+    const size_t slot = static_cast<size_t>(slot_floats_of(c, q_heads)) * sizeof(float);
     return (attention_items(c, q_heads) * sizeof(int2) + 255) / 256 * 256 + (2 * blocks * slot + 255) / 256 * 256;
 }
 
@@ -261,10 +272,11 @@ int ar_paged_attention(const ar_kv_cache* cache, const void* q, size_t q_stride,
     while ((1ll << a.page_shift) < c->page_size)
         ++a.page_shift;
     a.page_magic = static_cast<uint32_t>(((1ull << (31 + a.page_shift)) + c->page_size - 1) / c->page_size);
-    a.capacity = static_cast<int>(cap < INT_MAX - 64 ? cap : INT_MAX - 64);  // a tile's end stays an int
+    a.capacity = static_cast<int>(cap < INT_MAX - 255 ? cap : INT_MAX - 255);  // a tile's end stays an int
     a.kv_heads = c->kv_heads;
     a.group = q_heads / c->kv_heads;
-    a.group_blocks = (a.group + ar::kAttnMaxHeads - 1) / ar::kAttnMaxHeads;
+    a.group_blocks = group_blocks_of(c, q_heads);
+    a.block_heads = ar::attn_block_heads(static_cast<int>(ce));
     a.head_dim = c->head_dim;
     a.window = window;
     constexpr float kLog2e = 1.4426950408889634f;
@@ -272,7 +284,8 @@ int ar_paged_attention(const ar_kv_cache* cache, const void* q, size_t q_stride,
     a.softcap = softcap;
     a.softcap2 = softcap * kLog2e;
     a.v_scale = c->v_scale;
-    a.slot_floats = ar::attn_slot_floats(a.group, c->head_dim);
+    a.fours_magic = magic_of(c->head_dim / 4);
+    a.slot_floats = slot_floats_of(c, q_heads);
 
     int dev = 0, sms = 0;
     if (cudaGetDevice(&dev) != cudaSuccess ||
