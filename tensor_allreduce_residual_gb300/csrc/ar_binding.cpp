@@ -225,9 +225,9 @@ int fill_cache(ar_kv_cache* c, PyObject* k_pages, PyObject* v_pages, PyObject* p
     c->batch = size32(batch, "page_table");
     c->max_pages = size32(columns, "page_table");
     c->table_stride = size32(stride, "page_table");
-    c->lengths = ints(lengths, "lengths", batch, dev);
-    if (c->lengths == nullptr)
+    if (!given(lengths))
         bad("lengths must be given");
+    c->lengths = ints(lengths, "lengths", batch, dev);
     return dev;
 }
 

@@ -529,3 +529,107 @@ def test_a_layers_steps_over_ranks(ranks, cache):
         y_ref = x / (x.square().mean(1, keepdim=True) + 1e-6).sqrt()
         check(y, y_ref, y_ref.abs() * 2.0 ** -16 + 2 * half_step(y_ref, torch.bfloat16), "norm")
         residual = res
+
+
+# ------------------------------------------------------------------ refusals, empty calls, threads
+
+def test_calls_refuse_tensors_that_do_not_fit():
+    c = Cache([20, 5], 2, 64, 16, "bf16", columns=2)
+    q = torch.zeros(2, 4, 64, device="cuda", dtype=torch.bfloat16)
+    kv = torch.zeros(2, 2, 64, device="cuda", dtype=torch.bfloat16)
+    good = dict(q=q, k_pages=c.k, v_pages=c.v, page_table=c.table, lengths=c.n)
+    for change in (dict(q=q.half()), dict(q=q[:1]), dict(q=q[..., :32]), dict(q=q.transpose(0, 1)), dict(q=q.cpu()), dict(v_pages=c.v[:, :8]),
+                   dict(v_pages=c.v.half()), dict(k_pages=c.k[0], v_pages=c.v[0]), dict(k_pages=c.k.cpu(), v_pages=c.v.cpu()),
+                   dict(page_table=c.table.long()), dict(page_table=c.table[:1]), dict(page_table=c.table.cpu()), dict(lengths=c.n.long()),
+                   dict(lengths=c.n[:1]), dict(out=torch.empty_like(q)[:1]), dict(out=torch.empty(2, 4, 64, device="cuda")),
+                   dict(lse=torch.empty(2, 4)), dict(lse=torch.empty(4, 2, device="cuda").t()), dict(layout="nhd"),
+                   dict(workspace=torch.empty(1 << 20, dtype=torch.uint8))):
+        with pytest.raises((ValueError, ar.ARError)):
+            ar.ar_paged_attention(**{**good, **change})
+    for change, status in ((dict(q=q[:, :3]), ar.AR_ERR_INVALID_ARG), (dict(window=-1), ar.AR_ERR_INVALID_ARG), (dict(softcap=math.nan), ar.AR_ERR_INVALID_ARG),
+                           (dict(k_scale=0.0), ar.AR_ERR_INVALID_ARG), (dict(workspace=torch.empty(16, dtype=torch.uint8, device="cuda")), ar.AR_ERR_WORKSPACE)):
+        with pytest.raises(ar.ARError) as e:
+            ar.ar_paged_attention(**{**good, **change})
+        assert e.value.status == status
+    wide = torch.zeros(3, 16, 2, 68, device="cuda", dtype=torch.bfloat16)   # rows that begin between vectors
+    with pytest.raises(ar.ARError) as e:
+        ar.ar_paged_attention(q, wide[..., 4:], wide[..., 4:], c.table, c.n)
+    assert e.value.status == ar.AR_ERR_UNSUPPORTED
+    with pytest.raises(TypeError):
+        ar.ar_paged_attention(None, c.k, c.v, c.table, c.n)
+    fine = dict(k_pages=c.k, v_pages=c.v, page_table=c.table, lengths=c.n, k=kv, v=kv)
+    freq = torch.ones(32, device="cuda")
+    for change in (dict(k=kv[:1]), dict(v=kv.half()), dict(k=kv.float(), v=kv.float()), dict(q=q, q_out=q[:, :2]), dict(q_out=q), dict(inv_freq=freq.half()),
+                   dict(inv_freq=torch.ones(33, device="cuda")), dict(positions=c.n[:1]), dict(seq_start=c.n), dict(rotary_scale=math.inf)):
+        with pytest.raises((ValueError, ar.ARError)):
+            ar.ar_kv_append(**{**fine, **change})
+    for parts, lse in (([q], [q]), ([q, q[:1]], [freq[:8].view(2, 4)] * 2), ([q, q.float()], [freq[:8].view(2, 4)] * 2), ([q] * 17, [freq[:8].view(2, 4)] * 17)):
+        with pytest.raises(ValueError):
+            ar.ar_attention_join(parts, lse)
+    torch.cuda.synchronize()
+
+
+def test_empty_calls():
+    k = torch.zeros(1, 16, 2, 64, device="cuda", dtype=torch.float16)
+    table, n = torch.zeros(0, 3, device="cuda", dtype=torch.int32), torch.zeros(0, device="cuda", dtype=torch.int32)
+    none = torch.zeros(0, 4, 64, device="cuda", dtype=torch.float16)
+    out, lse = ar.ar_paged_attention(none, k, k, table, n, return_lse=True)
+    assert out.shape == (0, 4, 64) and lse.shape == (0, 4)
+    q = ar.ar_kv_append(k, k, table, n, none[:, :2], none[:, :2], q=none)
+    assert q.shape == (0, 4, 64)
+    out, lse = ar.ar_attention_join([none], [none[..., 0].float()], return_lse=True)
+    assert out.shape == (0, 4, 64) and lse.shape == (0, 4)
+
+
+def test_a_captured_step_makes_its_own_scratch():
+    """Append and attention captured together without given buffers, replayed as the cache grows."""
+    lengths = [30, 1, 64]
+    c = Cache([n + 3 for n in lengths], 2, 64, 16, "bf16", seed=3)
+    g = _gen(3)
+    qkv = _normal(g, 3, 12, 64).to(torch.bfloat16)
+    q, k, v = qkv.split([8, 2, 2], dim=1)
+    freq = torch.rand(32, generator=g, device="cuda")
+
+    def step():
+        turned = ar.ar_kv_append(*c.args, k, v, q=q, inv_freq=freq)
+        return turned, *ar.ar_paged_attention(turned, *c.args, return_lse=True)
+
+    c.n.copy_(torch.tensor(lengths, dtype=torch.int32))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        turned, out, lse = step()
+    for i in range(1, 4):
+        c.n.add_(1)
+        qkv.copy_(_normal(g, 3, 12, 64))
+        graph.replay()
+        now = [n + i for n in lengths]
+        ref, ref_lse, room, room_lse = model.attention(turned, c.k, c.v, c.table, now, scale=0.125)
+        check(out, ref, room + half_step(ref, out.dtype), f"step {i}")
+        check(lse, ref_lse, room_lse, f"step {i} lse")
+
+
+def test_calls_of_several_threads():
+    import threading
+    c = [Cache([700, 3, 90], 1, 64, 16, "fp16", seed=s) for s in range(4)]
+    q = [_normal(_gen(s), 3, 8, 64).half() for s in range(4)]
+    want = [ar.ar_paged_attention(q[s], *c[s].args) for s in range(4)]
+    torch.cuda.synchronize()
+    wrong = []
+
+    def work(s):
+        stream = torch.cuda.Stream()
+        with torch.cuda.stream(stream):
+            for _ in range(50):
+                if not torch.equal(ar.ar_paged_attention(q[s], *c[s].args), want[s]):
+                    wrong.append(s)
+    threads = [threading.Thread(target=work, args=(s,)) for s in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong
