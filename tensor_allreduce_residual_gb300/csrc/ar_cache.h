@@ -78,8 +78,8 @@ struct AttnArgs {
 // Query heads of one key-value head that one block attends for at once, at most.  A larger group reads its tiles again for
 // every so many: 8 in fp32, whose 16 would not fit the registers with their queries.
 __host__ __device__ constexpr int attn_block_heads(int cache_esize) { return cache_esize == 4 ? 8 : 16; }
-// Blocks of the attention kernel, at most: four per SM of the 152.  The workspace holds two slots for each.
-constexpr int kAttnMaxBlocks = 608;
+// Blocks of the attention kernel, at most: three per SM of the 152.  The workspace holds two slots for each.
+constexpr int kAttnMaxBlocks = 456;
 constexpr int kAttnMaxDim = 256;
 
 // Cached tokens of one tile: what a block loads at once, and the work is cut into.  A warp takes a quarter: 8 tokens in
