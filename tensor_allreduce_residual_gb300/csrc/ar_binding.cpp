@@ -79,6 +79,14 @@ long long integer(PyObject* o)
     return x;
 }
 
+bool truth(PyObject* o)
+{
+    const int x = PyObject_IsTrue(o);
+    if (x < 0)
+        throw Raised();
+    return x != 0;
+}
+
 int int32(PyObject* o, const char* what)
 {
     const long long x = integer(o);
@@ -278,7 +286,7 @@ PyObject* kv_append(PyObject* const* a)
         p.rotary_dim = static_cast<int>(2 * f.numel());
         p.inv_freq = static_cast<const float*>(f.data_ptr());
     }
-    p.interleaved = PyObject_IsTrue(a[11]);
+    p.interleaved = truth(a[11]);
     p.rotary_scale = static_cast<float>(number(a[12]));
     check("ar_kv_append", g_append(&cache, &p, s.handle));
     if (made.defined())
@@ -322,7 +330,7 @@ PyObject* paged_attention(PyObject* const* a)
     if (given(a[12])) {
         lse = tensor(a[12], "lse");
         dense(lse, "lse", {batch, q_heads}, at::kFloat, dev);
-    } else if (PyObject_IsTrue(a[13])) {
+    } else if (truth(a[13])) {
         lse = empty({batch, q_heads}, at::kFloat, q);
     }
     void* workspace;
@@ -402,7 +410,7 @@ PyObject* attention_join(PyObject* const* a)
     if (given(a[3])) {
         lse = tensor(a[3], "lse_out");
         dense(lse, "lse_out", rows, at::kFloat, dev);
-    } else if (PyObject_IsTrue(a[4])) {
+    } else if (truth(a[4])) {
         lse = empty(rows, at::kFloat, p0);
     }
     const int64_t dim = shape.back();
