@@ -102,24 +102,42 @@ __device__ __forceinline__ void store_cached(void* base, uint64_t e, float* f, f
     }
 }
 
+__device__ __forceinline__ void rotate(float& x, float& y, float cosine, float sine)
+{
+    const float u = x, v = y;
+    x = u * cosine - v * sine;
+    y = v * cosine + u * sine;
+}
+
+// Where the table has pair j of a row.  The 2^group_log pairs of a 16-bit vector are read two at a time by threads with the
+// vectors beside it: the first two of all vectors, then the next two, so that they lie side by side and meet no bank twice
+// (in order, eight bytes a read at steps of 64 met four times and kept the L1 pipe at 79 %: 63.0 against 61.4 us for the
+// prompts).  group_log 0: in order, for fp32, whose steps are shorter.
+__device__ __forceinline__ int turn_place(int j, int half, int group_log)
+{
+    const int in = j & ((1 << group_log) - 1);
+    return group_log == 0 ? j : ((in >> 1) * (half >> group_log) + (j >> group_log)) * 2 + (j & 1);
+}
+
 // ---------------------------------------------------------------------------
 // The append.  A block takes up to kAppendMaxTokens rows: it finds their
 // sequences (one pass over seq_start, all threads at once: a binary search's
 // chain of loads would cost more than the row's copy), fills a table of their
 // cosines and sines in shared memory, which all heads of a row share, and then
 // walks the rows' units: pairs of vectors that rotate into each other, or
-// single vectors.  Bound by HBM for prompts (365 MB in 63 us, 5.8 TB/s) and for
-// single tokens by the chain of loads length, page, store (3.0 us for 8 rows).
+// single vectors.  Bound by HBM for prompts (365 MB in 61 us, 6.0 TB/s; a copy
+// of as many bytes takes 55 us) and for single tokens by the chain of loads
+// length, page, store (3.0 us for 8 rows).
 // What hides the loads is the number of threads: forms that kept several units
 // a thread in flight, or a head's cosines and sines in registers, ran fewer of
-// them and took 69 to 94 us for the same prompts; hence one unit at a time and
+// them and took 66 to 94 us for the same prompts; hence one unit at a time and
 // eight blocks an SM.
 // ---------------------------------------------------------------------------
 template <typename T, typename CT, bool VEC>
 __global__ void __launch_bounds__(kAppendThreads, 8)
 k_kv_append(const AppendArgs a)
 {
-    extern __shared__ float2 s_turn[];  // [rows][half]
+    extern __shared__ __align__(16) float2 s_turn[];  // [rows][half], by turn_place
     __shared__ int s_seq[kAppendMaxTokens];
     __shared__ int s_pos[kAppendMaxTokens];
     __shared__ int64_t s_dst[kAppendMaxTokens];  // element offset in the cache, -1: not cached
@@ -166,12 +184,14 @@ k_kv_append(const AppendArgs a)
         s_dst[tid] = dst;
     }
     __syncthreads();
+    const int group_log = VEC && L == 8 ? (a.interleaved ? 2 : 3) : 0;
     for (int x = tid; x < rows * a.half; x += kAppendThreads) {
-        const int row = x >= a.half;
-        s_turn[x] = cos_sin(turn_fraction(a.inv_freq[x - row * a.half]), s_pos[row], a.rotary_scale);
+        const int row = x >= a.half, j = x - row * a.half;
+        s_turn[row * a.half + turn_place(j, a.half, group_log)] = cos_sin(turn_fraction(a.inv_freq[j]), s_pos[row], a.rotary_scale);
     }
     __syncthreads();
 
+    const int vectors = a.half >> group_log;
     const int q_units = a.q_heads * a.head_units;
     const int k_units = q_units + a.kv_heads * a.head_units;
     const int all = k_units + a.kv_heads * a.v_units;
@@ -215,11 +235,10 @@ k_kv_append(const AppendArgs a)
             Part<T, VEC>::load(src, from + d, f);
             if (d < 2 * a.half) {
 #pragma unroll
-                for (int l = 0; l + 1 < L; l += 2) {
-                    const float2 cs = turn[(d + l) / 2];
-                    const float x0 = f[l], y0 = f[l + 1];
-                    f[l] = x0 * cs.x - y0 * cs.y;
-                    f[l + 1] = y0 * cs.x + x0 * cs.y;
+                for (int l = 0; l + 3 < L; l += 4) {
+                    const float4 cs = *reinterpret_cast<const float4*>(turn + (L == 8 ? (l / 4 * vectors + c) * 2 : (c * L + l) / 2));
+                    rotate(f[l], f[l + 1], cs.x, cs.y);
+                    rotate(f[l + 2], f[l + 3], cs.z, cs.w);
                 }
             }
             store(d, f);
@@ -228,12 +247,15 @@ k_kv_append(const AppendArgs a)
             const int d1 = a.interleaved ? d0 + 1 : d0 + a.half;
             Part<T, VEC>::load(src, from + d0, f);
             Part<T, VEC>::load(src, from + d1, g);
+            if constexpr (VEC) {
 #pragma unroll
-            for (int l = 0; l < L; ++l) {
-                const float2 cs = turn[c * L + l];
-                const float x0 = f[l], y0 = g[l];
-                f[l] = x0 * cs.x - y0 * cs.y;
-                g[l] = y0 * cs.x + x0 * cs.y;
+                for (int l = 0; l < L; l += 2) {
+                    const float4 cs = *reinterpret_cast<const float4*>(turn + (L == 8 ? (l / 2 * vectors + c) * 2 : c * L + l));
+                    rotate(f[l], g[l], cs.x, cs.y);
+                    rotate(f[l + 1], g[l + 1], cs.z, cs.w);
+                }
+            } else {
+                rotate(f[0], g[0], turn[c].x, turn[c].y);
             }
             store(d0, f);
             store(d1, g);

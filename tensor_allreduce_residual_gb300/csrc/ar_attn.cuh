@@ -14,6 +14,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <atomic>
 #include <climits>
 #include <type_traits>
 
@@ -1179,10 +1180,11 @@ k_attn_join(const AttnArgs a, const int columns)
     }
 }
 
-// Launches `kernel`, `per_sm` blocks of which fit an SM, and then the join.
-template <typename T, typename Kernel>
-cudaError_t launch_tiles(Kernel kernel, const AttnArgs& a, int most, int sms, int per_sm, size_t smem, cudaStream_t s)
+// Launches shape P's kernel, and then the join.
+template <typename P>
+cudaError_t launch_shape(void (*kernel)(AttnArgs), const AttnArgs& a, int most, int sms, cudaStream_t s)
 {
+    int per_sm = P::BLOCKS;
     const uint64_t items = static_cast<uint64_t>(a.batch) * a.kv_heads * a.group_blocks;
     // Few items: a third block an SM adds more to the join than it takes from the loads (67 MB in one row of 131072
     // tokens: 17.7 against 18.6 us).
@@ -1198,13 +1200,28 @@ cudaError_t launch_tiles(Kernel kernel, const AttnArgs& a, int most, int sms, in
     const uint64_t joins = items * ((slots * (a.head_dim / 4) + columns - 1) / columns);
     if (joins > static_cast<uint64_t>(INT_MAX))
         return cudaErrorInvalidConfiguration;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    // The kernel's shared memory limit is raised once a device (0.4 us of a call's 7).  A context that was reset since has
+    // lost it: its launch fails, and is made again with the limit raised.
+    static std::atomic<uint64_t> raised{0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+    const bool before = (raised.load(std::memory_order_relaxed) & bit) != 0;
+    const auto raise = [&] { return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, P::SMEM); };
+    if (e == cudaSuccess && !before)
+        e = raise();
+    if (e == cudaSuccess)
+        e = launch_k(kernel, dim3(blocks), dim3(kAttnThreads), P::SMEM, s, a);
+    if (e == cudaErrorInvalidValue && before) {
+        cudaGetLastError();
+        e = raise();
+        if (e == cudaSuccess)
+            e = launch_k(kernel, dim3(blocks), dim3(kAttnThreads), P::SMEM, s, a);
+    }
     if (e != cudaSuccess)
         return e;
-    e = launch_k(kernel, dim3(blocks), dim3(kAttnThreads), smem, s, a);
-    if (e != cudaSuccess)
-        return e;
-    return launch_k(k_attn_join<T>, dim3(static_cast<unsigned>(joins)), dim3(kJoinThreads), 0, s, a, columns);
+    raised.fetch_or(bit, std::memory_order_relaxed);
+    return launch_k(k_attn_join<typename P::T>, dim3(static_cast<unsigned>(joins)), dim3(kJoinThreads), 0, s, a, columns);
 }
 
 template <typename T, typename CT, int DIM, int HEADS>
@@ -1212,9 +1229,9 @@ cudaError_t launch_heads(const AttnArgs& a, int most, int sms, cudaStream_t s)
 {
     using P = AttnShape<T, CT, DIM, HEADS>;
     if constexpr (P::WIDE)
-        return launch_tiles<T>(k_attn_fma<P>, a, most, sms, P::BLOCKS, P::SMEM, s);
+        return launch_shape<P>(k_attn_fma<P>, a, most, sms, s);
     else
-        return launch_tiles<T>(k_attn_mma<P>, a, most, sms, P::BLOCKS, P::SMEM, s);
+        return launch_shape<P>(k_attn_mma<P>, a, most, sms, s);
 }
 
 template <typename T, typename CT, int DIM>
