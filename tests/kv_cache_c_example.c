@@ -41,7 +41,7 @@ static void ok(int status, const char* what)
     }
 }
 
-int main(int argc, char** argv)
+static int run(int argc, char** argv)
 {
     const size_t nq = 2 * HEADS * DIM, nkv = (size_t)TOKENS * KV_HEADS * DIM, in_count = nq + 2 * nkv + DIM / 2;
     float* in = (float*)malloc(in_count * sizeof(float));
@@ -122,6 +122,19 @@ int main(int argc, char** argv)
     if (!f || fwrite(out, sizeof(float), 2 * nq, f) != 2 * nq)
         return 2;
     fclose(f);
-    printf("kv_cache_c_example: ok\n");
+    free(in);
+    free(out);
     return 0;
+}
+
+int main(int argc, char** argv)
+{
+    int failed = run(argc, argv);
+    if (!failed && cudaDeviceReset() != cudaSuccess)
+        failed = 1;
+    if (!failed)
+        failed = run(argc, argv);
+    if (!failed)
+        printf("kv_cache_c_example: ok\n");
+    return failed;
 }

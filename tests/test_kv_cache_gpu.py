@@ -633,3 +633,44 @@ def test_calls_of_several_threads():
     for t in threads:
         t.join()
     assert not wrong
+
+
+@pytest.mark.parametrize("dtype,cache", [("bf16", "bf16"), ("fp32", "fp32")])
+def test_attention_of_thousands_of_rows(dtype, cache):
+    """More rows than blocks, threads and a block's lengths by far; tokens of one page each, several rows on the same page."""
+    B, K, D, page, pages = 6001, 2, 64, 4, 500
+    g = _gen(12)
+    k, v = (_normal(g, pages, page, K, D).to(TORCH[cache]) for _ in range(2))
+    table = torch.randint(0, pages, (B, 1), generator=g, device="cuda", dtype=torch.int32)
+    n = torch.randint(0, page + 1, (B,), generator=g, device="cuda", dtype=torch.int32)
+    q = _normal(g, B, 2 * K, D).to(TORCH[dtype])
+    out, lse = ar.ar_paged_attention(q, k, v, table, n, return_lse=True)
+    kk, vv = (x[table[:, 0].long()].double().repeat_interleave(2, 2) for x in (k, v))   # [B, page, 2 K, D]
+    z = torch.einsum("bhd,bjhd->bhj", q.double(), kk) / 8
+    mass = (torch.einsum("bhd,bjhd->bhj", q.double().abs(), kk.abs()) / 8).amax(2)
+    z = z.masked_fill(torch.arange(page, device="cuda")[None, None] >= n[:, None, None], -math.inf)
+    p = torch.where(n[:, None, None] > 0, torch.softmax(z, 2), 0.0)
+    want, size = torch.einsum("bhj,bjhd->bhd", p, vv), torch.einsum("bhj,bjhd->bhd", p, vv.abs())
+    delta = (2 * (D + 2) * mass + 8 * z.masked_fill(z == -math.inf, 0).abs().amax(2).clamp(min=1)) * U32   # as in the model
+    check(out, want, size * (4 * delta + 2.0 ** -16 + 4 * (page + 16) * U32)[..., None] + half_step(want, out.dtype), "out")
+    check(lse, torch.logsumexp(z, 2), 2 * delta + 4 * (page + 24) * U32 * (1 + mass), "lse")
+
+
+def test_sequences_that_share_pages_and_ranks_that_are_one():
+    c = Cache([70, 70, 33], 2, 64, 16, "bf16")
+    c.table = c.table.clone()
+    c.table[1] = c.table[0]
+    c.table[2, :3] = c.table[0, :3]
+    q = _normal(_gen(4), 1, 8, 64).to(torch.bfloat16).expand(3, 8, 64).contiguous()
+    out, lse = _attend(c, q, "shared")
+    same = ar.ar_attention_join([out[:1], out[:1]], [lse[:1], lse[:1]])   # twice the same keys: the same mean
+    check(same, out[:1].double(), half_step(out[:1].double(), out.dtype) * 2.0 ** -6, "twice")
+
+
+def test_the_default_stream_by_its_handle():
+    c = Cache([50], 1, 64, 16, "fp16")
+    q = _normal(_gen(4), 1, 4, 64).half()
+    want = ar.ar_paged_attention(q, *c.args)
+    got = ar.ar_paged_attention(q, *c.args, stream=0)
+    torch.cuda.synchronize()
+    assert torch.equal(got, want)
