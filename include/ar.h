@@ -756,8 +756,8 @@ int ar_paged_attention(const ar_kv_cache* cache, const void* q, size_t q_stride,
  *   lse       host array of R device pointers, each fp32 [rows]
  *   out       device [rows, head_dim]; may be one of the partials
  *   lse_out   device fp32 [rows], or NULL; not one of lse
- * Any element-aligned pointer; 16-byte aligned ones with head_dim a multiple of 16 /
- * element size take the packed path.  rows == 0 launches nothing.
+ * Any element-aligned pointer; 16-byte aligned ones with head_dim of at least
+ * 16 / element size take the packed path.  rows == 0 launches nothing.
  * Errors: AR_ERR_INVALID_ARG (R out of range, rows < 0, head_dim < 1, NULL
  *         or not element-aligned pointer, lse_out among lse), AR_ERR_UNSUPPORTED (unknown dtype),
  *         AR_ERR_CUDA.

@@ -103,11 +103,13 @@ struct JoinArgs {
     void* out;
     float* lse_out;           // nullable
     int R;
-    int row_units;            // vectors (packed) or elements of a row
-    uint64_t units;           // rows * row_units
+    int dim;                  // elements of a row
+    uint64_t elements;        // rows * dim
+    uint64_t units;           // threads' worth: set by the launcher
 };
 
+// `aligned`: the partials and out are 16-byte aligned.
 template <typename T>
-cudaError_t launch_join(const JoinArgs& a, bool packed, cudaStream_t s);
+cudaError_t launch_join(const JoinArgs& a, bool aligned, cudaStream_t s);
 
 }  // namespace ar

@@ -310,8 +310,7 @@ int ar_attention_join(const void* const* partials, const float* const* lse, int 
         return AR_OK;
     if (partials == nullptr || lse == nullptr || !element_ok(out, esize) || !aligned(lse_out, 4))
         return AR_ERR_INVALID_ARG;
-    const int lanes = 16 / esize;
-    bool packed = head_dim % lanes == 0 && aligned(out, 16);
+    bool packed = aligned(out, 16);
     ar::JoinArgs a{};
     for (int r = 0; r < R; ++r) {
         if (!element_ok(partials[r], esize) || !element_ok(lse[r], 4) || lse[r] == lse_out)
@@ -323,8 +322,8 @@ int ar_attention_join(const void* const* partials, const float* const* lse, int 
     a.out = out;
     a.lse_out = lse_out;
     a.R = R;
-    a.row_units = packed ? head_dim / lanes : head_dim;
-    a.units = static_cast<uint64_t>(rows) * static_cast<uint64_t>(a.row_units);
+    a.dim = head_dim;
+    a.elements = static_cast<uint64_t>(rows) * static_cast<uint64_t>(head_dim);
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     return status_of([&] {
         switch (dtype) {
