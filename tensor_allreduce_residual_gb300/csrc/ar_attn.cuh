@@ -820,6 +820,9 @@ k_attn_mma(const AttnArgs a)
     constexpr int TOKENS = P::TOKENS, KB = TOKENS / 16, NT = P::HEADS / 8, MTILES = P::DIM / 16, KSTEPS = P::DIM / 16;
     // fp16 weights alone are eight times finer than a bf16 result.
     constexpr bool LOW = !(P::SMALL && std::is_same<T, __nv_bfloat16>::value);
+    // Weights in fp16 are 2^15 times as large, the largest 2^15: those down to 2^-29 of it keep all their bits, and thousands
+    // of small ones do not vanish beside a few large.
+    constexpr float LIFT = std::is_same<MT, __half>::value ? 0x1p15f : 1.0f;
     extern __shared__ __align__(128) char smem[];
     __shared__ __align__(16) WarpTile<TOKENS> s_tiles[kAttnWarps][P::RING];
     __shared__ float s_top[kAttnWarps][P::HEADS], s_total[kAttnWarps][P::HEADS];
@@ -1003,11 +1006,11 @@ k_attn_mma(const AttnArgs a)
                     const float p1 = exp2_fast(s[kb][nt][2 * r + 1] - base[1]);
                     total[nt][0] += p0;
                     total[nt][1] += p1;
-                    const uint32_t h = Lanes<MT>::word(p0, p1);
+                    const uint32_t h = Lanes<MT>::word(p0 * LIFT, p1 * LIFT);
                     hi[kb][nt][r] = transposed(h);
                     if constexpr (LOW) {
                         const float2 back = Lanes<MT>::two(h);
-                        lo[kb][nt][r] = transposed(Lanes<MT>::word(p0 - back.x, p1 - back.y));
+                        lo[kb][nt][r] = transposed(Lanes<MT>::word(fmaf(p0, LIFT, -back.x), fmaf(p1, LIFT, -back.y)));
                     }
                 }
             }
@@ -1070,7 +1073,7 @@ k_attn_mma(const AttnArgs a)
 #pragma unroll
                     for (int w = 1; w < kAttnWarps; ++w)
                         best = fmaxf(best, s_top[w][head]);
-                    const float fix = exp2_fast(top[nt][i] - base_of(best));
+                    const float fix = exp2_fast(top[nt][i] - base_of(best)) * (1.0f / LIFT);
                     float* out = rows + (warp * P::HEADS + head) * P::OPITCH;
 #pragma unroll
                     for (int m = 0; m < MTILES; ++m) {

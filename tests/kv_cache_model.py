@@ -48,11 +48,12 @@ def attention(q, k_pages, v_pages, table, lengths, *, scale, window=0, softcap=0
 
     With u = 2^-24 and every product and sum rounded at most twice that far (a matrix unit may cut off where an adder
     rounds): a dot product of d terms is off by 2 (d + 2) u sum |q k|; the score, the exponent's base change and e^x add
-    8 u max(1, |s|) more; softcap only shrinks these.  So each weight is off by a factor e^(+-2 delta), relative to
+    8 u max(1, |s|) more; softcap only shrinks these.
+    So each weight is off by a factor e^(+-2 delta), relative to
     their sum 4 delta at the most.  Each weight is rounded to a pair of 16-bit numbers, to 2^-16 of it, or for bf16 queries
-    on an 8-bit cache to one of fp16, to 2^-11; in fp16 a weight under 2^-14 of the largest to 2^-25 of that, so that n of
-    them add 2^-25 sum |v| to a sum of weights of 1 at least.  The sums of n weighted values and of n weights are off by
-    2 (n + 16) u each.
+    on an 8-bit cache to one of fp16, to 2^-11; in fp16 the largest is 2^15, and a weight under 2^-29 of it is rounded to
+    2^-40 of it, so that n of them add 2^-40 sum |v| to a sum of weights of 1 at least.  The sums of n weighted values and
+    of n weights are off by 2 (n + 16) u each.
     """
     pages, ps = k_pages.shape[0], by_token(k_pages, layout).shape[1]
     B, H, D = q.shape
@@ -77,7 +78,8 @@ def attention(q, k_pages, v_pages, table, lengths, *, scale, window=0, softcap=0
         mass = torch.einsum("hd,jhd->hj", qb.abs(), k.abs()) * abs(scale)
         if softcap:
             s = softcap * torch.tanh(s / softcap)
-        delta = ((2 * (D + 2) * mass + 8 * s.abs().clamp(min=1)) * U32).amax(1)
+        delta = 2 * (D + 2) * U32 * mass + 8 * s.abs().clamp(min=1) * U32
+        delta = delta.amax(1)
         p = torch.softmax(s, 1)
         out[b], lse[b] = torch.einsum("hj,jhd->hd", p, v), torch.logsumexp(s, 1)
         size = torch.einsum("hj,jhd->hd", p, v.abs())
@@ -85,7 +87,7 @@ def attention(q, k_pages, v_pages, table, lengths, *, scale, window=0, softcap=0
         once = q.dtype == torch.bfloat16 and k_pages.dtype == TORCH["e4m3"]
         e_out[b] = size * (4 * delta + 2.0 ** (-11 if once else -16) + sums)[:, None]
         if q.dtype == torch.float16 or k_pages.dtype == TORCH["e4m3"]:
-            e_out[b] += 2.0 ** -25 * v.abs().sum(0)
+            e_out[b] += 2.0 ** -40 * v.abs().sum(0)
         e_lse[b] = 2 * delta + sums + 4 * U32 * (1 + lse[b].abs())
     return out, lse, e_out, e_lse
 

@@ -1,0 +1,47 @@
+"""Attention over the paged cache where numbers lie far apart: weights far below the largest."""
+import pytest
+import torch
+
+import tensor_allreduce_residual_gb300 as ar
+from tensor_allreduce_residual_gb300 import _build
+from tests import kv_cache_model as model
+from tests.kv_cache_model import TORCH, check, half_step
+
+pytestmark = pytest.mark.gpu
+
+PAIRS = [("fp32", "fp32"), ("bf16", "bf16"), ("fp16", "fp16"), ("bf16", "e4m3"), ("fp16", "e4m3")]
+
+
+@pytest.fixture(scope="module", autouse=True)
+def cuda_library():
+    assert torch.cuda.is_available()
+    torch.cuda.set_device(0)
+    _build.build()
+    ar.lib()
+
+
+def _pages(keys, dtype):
+    """keys or values [tokens, dim] as pages of 16 tokens of one head."""
+    return keys.reshape(-1, 16, 1, keys.shape[1]).to(TORCH[dtype])
+
+
+def _check(q, k, v, what, rows=1, **kw):
+    """Attention of q [heads, dim], repeated over `rows` sequences that share all pages, against the formula."""
+    tokens = k.shape[0] * 16
+    table = torch.arange(k.shape[0], dtype=torch.int32, device="cuda").expand(rows, -1).contiguous()
+    n = torch.full((rows,), tokens, dtype=torch.int32, device="cuda")
+    out, lse = ar.ar_paged_attention(q.expand(rows, *q.shape).contiguous(), k, v, table, n, return_lse=True, **kw)
+    ref, ref_lse, room, room_lse = model.attention(q[None], k, v, table[:1], [tokens], **kw)
+    check(out, ref.expand_as(out), (room + half_step(ref, out.dtype)).expand_as(out), f"{what} out")
+    check(lse, ref_lse.expand_as(lse), room_lse.expand_as(lse), f"{what} lse")
+
+
+@pytest.mark.parametrize("dtype,cache", PAIRS)
+@pytest.mark.parametrize("rows", [1, 600])   # split over many blocks, or a row in one
+def test_many_weights_far_below_the_largest(dtype, cache, rows):
+    """A few tokens whose weights are e^18 times the others' and whose values are 0: the result is all others'."""
+    k, v = torch.zeros(4000, 64, device="cuda"), torch.full((4000, 64), 96.0, device="cuda")
+    for j in (0, 16, 32, 48, 64, 96):
+        k[j], v[j] = 18 / 256, 0.0
+    q = torch.full((4, 64), 4.0, device="cuda").to(TORCH[dtype])
+    _check(q, _pages(k, cache), _pages(v, cache), f"{dtype} {cache}", rows, scale=1.0)
