@@ -875,11 +875,13 @@ k_attn_mma(const AttnArgs a)
                             most = fmaxf(most, fmaxf(fmaxf(fabsf(x.x), fabsf(x.y)), fmaxf(fabsf(y.x), fabsf(y.y))));
                         }
                     }
+                    // The largest element becomes 2^14 or more: elements down to 2^-28 of it keep all their bits.  (Scaled to 1, those
+                    // under 2^-25 of it would vanish.)
                     int e = 0;
                     if constexpr (!std::is_same<T, __half>::value) {
                         most = fmaxf(most, __shfl_xor_sync(~0u, most, 1));
                         most = fmaxf(most, __shfl_xor_sync(~0u, most, 2));
-                        e = min(max(static_cast<int>(__float_as_uint(most) >> 23) - 127, -126), 126);
+                        e = max(static_cast<int>(__float_as_uint(most) >> 23) - 127, -112) - 14;
                         const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
 #pragma unroll
                         for (int j = 0; j < KSTEPS; ++j)

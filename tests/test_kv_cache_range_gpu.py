@@ -1,4 +1,5 @@
-"""Attention over the paged cache where numbers lie far apart: weights far below the largest."""
+"""Attention over the paged cache where numbers lie far apart: weights far below the largest, queries with elements far
+below the largest."""
 import pytest
 import torch
 
@@ -45,3 +46,15 @@ def test_many_weights_far_below_the_largest(dtype, cache, rows):
         k[j], v[j] = 18 / 256, 0.0
     q = torch.full((4, 64), 4.0, device="cuda").to(TORCH[dtype])
     _check(q, _pages(k, cache), _pages(v, cache), f"{dtype} {cache}", rows, scale=1.0)
+
+
+@pytest.mark.parametrize("dtype,cache", PAIRS)
+def test_query_elements_far_below_the_largest(dtype, cache):
+    """One element is 2^26 times the rest, where every key is 0: the scores are the rest's."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(3)
+    k, v = (torch.randn(496, 64, generator=g, device="cuda") for _ in range(2))
+    k[:, 0] = 0.0
+    q = torch.randn(4, 64, generator=g, device="cuda").to(TORCH["bf16"]).float() * 2.0 ** -12
+    q[:, 0] = 2.0 ** 14
+    _check(q.to(TORCH[dtype]), _pages(k, cache), _pages(v, cache), f"{dtype} {cache}", scale=2.0 ** 10)
