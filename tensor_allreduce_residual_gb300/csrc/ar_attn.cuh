@@ -228,11 +228,14 @@ __device__ __forceinline__ float exp2_fast(float x)
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
-// tanh(x) of 2 x in base 2, off by 2^-22 at the most: (e - 1) / (e + 1) with e = e^(2 x).
+// tanh(x) of 2 x in base 2, off by 2^-20 of it at the most, so that a softcap far above the scores leaves them as they are:
+// (e - 1) / (e + 1) with e = e^(2 x), and below 0.3, where e - 1 would lose bits, five terms of the series.
 __device__ __forceinline__ float tanh_fast(float two_x)
 {
-    const float e = exp2_fast(fminf(two_x, 64.0f));
-    return __fdividef(e - 1.0f, e + 1.0f);
+    const float e = exp2_fast(two_x > 64.0f ? 64.0f : two_x);  // a NaN stays one
+    const float x = two_x * (0.5f * kLn2), y = x * x;
+    const float series = fmaf(fmaf(fmaf(fmaf(62.0f / 2835.0f, y, -17.0f / 315.0f), y, 2.0f / 15.0f), y, -1.0f / 3.0f), y * x, x);
+    return fabsf(x) < 0.3f ? series : __fdividef(e - 1.0f, e + 1.0f);
 }
 // What a maximum is subtracted as: minus infinity stands for no token yet, and 0 in its place keeps differences defined.
 __device__ __forceinline__ float base_of(float top) { return top == -INFINITY ? 0.0f : top; }

@@ -48,7 +48,8 @@ def attention(q, k_pages, v_pages, table, lengths, *, scale, window=0, softcap=0
 
     With u = 2^-24 and every product and sum rounded at most twice that far (a matrix unit may cut off where an adder
     rounds): a dot product of d terms is off by 2 (d + 2) u sum |q k|; the score, the exponent's base change and e^x add
-    8 u max(1, |s|) more; softcap only shrinks these.  A bf16 query on an 8-bit cache is
+    8 u max(1, |s|) more; softcap shrinks these, and adds 16 u |s| for its tanh: (e - 1) / (e + 1) of |x| >= 0.3 is off by
+    e / (e - 1) <= 2.2 times e^(2x)'s 4 u, and by 5 u for its steps and the division.  A bf16 query on an 8-bit cache is
     scaled to fp16 with its largest element at 2^14 or more, so that elements are off by 2^-39 of the largest.
     So each weight is off by a factor e^(+-2 delta), relative to
     their sum 4 delta at the most.  Each weight is rounded to a pair of 16-bit numbers, to 2^-16 of it, or for bf16 queries
@@ -79,7 +80,7 @@ def attention(q, k_pages, v_pages, table, lengths, *, scale, window=0, softcap=0
         mass = torch.einsum("hd,jhd->hj", qb.abs(), k.abs()) * abs(scale)
         if softcap:
             s = softcap * torch.tanh(s / softcap)
-        delta = 2 * (D + 2) * U32 * mass + 8 * s.abs().clamp(min=1) * U32
+        delta = 2 * (D + 2) * U32 * mass + (8 * s.abs().clamp(min=1) + (16 * s.abs() if softcap else 0)) * U32
         if q.dtype == torch.bfloat16 and k_pages.dtype == TORCH["e4m3"]:
             delta = delta + 2.0 ** -39 * abs(scale) * qb.abs().amax(1)[:, None] * k.abs().sum(2).T
         delta = delta.amax(1)

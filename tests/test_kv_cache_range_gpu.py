@@ -1,5 +1,7 @@
 """Attention over the paged cache where numbers lie far apart: weights far below the largest, queries with elements far
-below the largest."""
+below the largest, softcaps far above the scores."""
+import math
+
 import pytest
 import torch
 
@@ -58,3 +60,26 @@ def test_query_elements_far_below_the_largest(dtype, cache):
     q = torch.randn(4, 64, generator=g, device="cuda").to(TORCH["bf16"]).float() * 2.0 ** -12
     q[:, 0] = 2.0 ** 14
     _check(q.to(TORCH[dtype]), _pages(k, cache), _pages(v, cache), f"{dtype} {cache}", scale=2.0 ** 10)
+
+
+@pytest.mark.parametrize("dtype,cache", PAIRS)
+@pytest.mark.parametrize("softcap", [0.5, 30.0, 1e4, 1e7])
+def test_softcaps_near_to_and_far_above_the_scores(dtype, cache, softcap):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(5)
+    k, v = (torch.randn(496, 64, generator=g, device="cuda") for _ in range(2))
+    q = (torch.randn(4, 64, generator=g, device="cuda") * 2).to(TORCH[dtype])
+    _check(q, _pages(k, cache), _pages(v, cache), f"{dtype} {cache}", scale=0.25, softcap=softcap)
+
+
+@pytest.mark.parametrize("dtype,cache", PAIRS)
+def test_nan_passes_a_softcap(dtype, cache):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(6)
+    k, v = (_pages(torch.randn(96, 64, generator=g, device="cuda"), cache) for _ in range(2))
+    k.view(torch.uint8 if cache == "e4m3" else k.dtype)[2, 3] = 0x7F if cache == "e4m3" else math.nan
+    table = torch.arange(6, dtype=torch.int32, device="cuda")[None]
+    q = torch.ones(1, 4, 64, device="cuda", dtype=TORCH[dtype])
+    for n, nan in ((96, True), (35, False)):   # token 35 is the NaN
+        out, lse = ar.ar_paged_attention(q, k, v, table, torch.tensor([n], dtype=torch.int32, device="cuda"), softcap=20.0, return_lse=True)
+        assert bool((out.isnan() == nan).all()) and bool((lse.isnan() == nan).all())
