@@ -661,8 +661,8 @@ typedef struct {
                                and row b is the last token of sequence b */
     const int* positions;   /* device [tokens]: the position a row is rotated by, or NULL: its index
                                in its sequence */
-    const float* inv_freq;  /* device [rotary_dim / 2]: angle per position of each pair; NULL with
-                               rotary_dim == 0 */
+    const float* inv_freq;  /* device [rotary_dim / 2]: angle per position of each pair, finite; NULL
+                               with rotary_dim == 0 */
     int rotary_dim;         /* even, 0 .. head_dim: leading elements of a head that are rotated */
     int interleaved;        /* 0: element j pairs with j + rotary_dim / 2; 1: 2j pairs with 2j + 1 */
     float rotary_scale;     /* multiplies cosines and sines; finite */
@@ -722,7 +722,9 @@ size_t ar_paged_attention_workspace_size(const ar_kv_cache* cache, int q_heads);
  *   lengths, page_table  read on the device: a captured graph follows them
  *   q             device [batch, q_heads, head_dim], rows of a sequence
  *                 q_stride elements apart
- *   scale         finite; applied to the scores
+ *   scale         finite; applied to the scores.  scale * k_scale, twice that
+ *                 over softcap, and softcap stay finite in fp32 with a factor
+ *                 of log2(e)
  *   window        >= 0, 0 for none
  *   softcap       finite, >= 0, 0 for none
  *   out           device [batch, q_heads, head_dim], dense

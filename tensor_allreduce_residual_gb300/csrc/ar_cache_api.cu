@@ -234,6 +234,10 @@ int ar_paged_attention(const ar_kv_cache* cache, const void* q, size_t q_stride,
         return st;
     if (!std::isfinite(scale) || window < 0 || !std::isfinite(softcap) || softcap < 0.0f)
         return AR_ERR_INVALID_ARG;
+    constexpr float kLog2e = 1.4426950408889634f;
+    const float scale2 = scale * c->k_scale * kLog2e * (softcap > 0.0f ? 2.0f / softcap : 1.0f), softcap2 = softcap * kLog2e;
+    if (!std::isfinite(scale2) || !std::isfinite(softcap2))
+        return AR_ERR_INVALID_ARG;  // an infinite factor would make scores of 0 NaN
     if (c->batch == 0)
         return AR_OK;
     const size_t e = static_cast<size_t>(esize_of(dtype));
@@ -279,10 +283,9 @@ int ar_paged_attention(const ar_kv_cache* cache, const void* q, size_t q_stride,
     a.block_heads = ar::attn_block_heads(static_cast<int>(ce));
     a.head_dim = c->head_dim;
     a.window = window;
-    constexpr float kLog2e = 1.4426950408889634f;
-    a.scale2 = scale * c->k_scale * kLog2e * (softcap > 0.0f ? 2.0f / softcap : 1.0f);
+    a.scale2 = scale2;
     a.softcap = softcap;
-    a.softcap2 = softcap * kLog2e;
+    a.softcap2 = softcap2;
     a.v_scale = c->v_scale;
     a.fours_magic = magic_of(c->head_dim / 4);
     a.slot_floats = slot_floats_of(c, q_heads);

@@ -94,6 +94,12 @@ def test_attention_refusals(L, kw, kind):
     assert _attend(L, **kw) == STATUS[kind]
 
 
+@pytest.mark.parametrize("cache,kw", [({}, dict(scale=3e38)), (dict(k_scale=1e20), dict(scale=-1e20)), ({}, dict(scale=2.0, softcap=1e-38)),
+                                      ({}, dict(softcap=3e38))])
+def test_attention_refuses_factors_that_overflow(L, cache, kw):
+    assert _attend(L, _cache(**cache), **kw) == STATUS["arg"]
+
+
 @pytest.mark.parametrize("kw", [dict(k=FAKE + 8), dict(v=FAKE + 2), dict(head_dim=120, token_stride=244), dict(head_dim=100, token_stride=256),
                                 dict(head_dim=264, token_stride=528, head_stride=264, page_stride=16 * 528), dict(page_stride=16 * 256 + 4),
                                 dict(head_stride=132, token_stride=264, page_stride=16 * 264),
