@@ -3,6 +3,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <algorithm>
 #include <climits>
 
 #include "ar_cache.h"
@@ -125,7 +126,7 @@ __device__ __forceinline__ int turn_place(int j, int half, int group_log)
 // chain of loads would cost more than the row's copy), fills a table of their
 // cosines and sines in shared memory, which all heads of a row share, and then
 // walks the rows' units: pairs of vectors that rotate into each other, or
-// single vectors.  Bound by HBM for prompts (365 MB in 61 us, 6.0 TB/s; a copy
+// single vectors.  Bound by HBM for prompts (365 MB in 60 us, 6.1 TB/s; a copy
 // of as many bytes takes 55 us) and for single tokens by the chain of loads
 // length, page, store (3.0 us for 8 rows).
 // What hides the loads is the number of threads: forms that kept several units
@@ -184,9 +185,17 @@ k_kv_append(const AppendArgs a)
         s_dst[tid] = dst;
     }
     __syncthreads();
+    // At most two rows in fp32, whose registers are the fewest: the division costs it more than further rows give (2296 rows
+    // of 18 heads of 80: 8.1 against 7.0 us).
+    const auto row_of = [&](int x, int each, uint64_t magic) {
+        if constexpr (sizeof(T) == 4)
+            return static_cast<int>(x >= each);
+        else
+            return a.block_tokens == 1 ? 0 : static_cast<int>(static_cast<uint32_t>(x) * magic >> 32);
+    };
     const int group_log = VEC && L == 8 ? (a.interleaved ? 2 : 3) : 0;
     for (int x = tid; x < rows * a.half; x += kAppendThreads) {
-        const int row = x >= a.half, j = x - row * a.half;
+        const int row = row_of(x, a.half, a.turn_magic), j = x - row * a.half;
         s_turn[row * a.half + turn_place(j, a.half, group_log)] = cos_sin(turn_fraction(a.inv_freq[j]), s_pos[row], a.rotary_scale);
     }
     __syncthreads();
@@ -197,7 +206,7 @@ k_kv_append(const AppendArgs a)
     const int all = k_units + a.kv_heads * a.v_units;
     const int pairs = a.half / L;  // units that are pairs (the vector path of interleaved pairs has none)
     for (int x = tid; x < rows * all; x += kAppendThreads) {
-        const int row = x >= all;
+        const int row = row_of(x, all, a.row_magic);
         const int u = x - row * all;
         const int64_t dst = s_dst[row];
         const uint64_t t = static_cast<uint64_t>(t0 + row);
@@ -267,13 +276,26 @@ k_kv_append(const AppendArgs a)
     }
 }
 
+// Bytes of rows that a block takes, at most, where it takes more than one, and how many blocks run at once.
+constexpr int kAppendBytes = 32 * 1024;
+constexpr int kAppendBlocks = 152 * 8;
+
 template <typename T, typename CT>
 cudaError_t launch_append(const AppendArgs& args, bool vec, cudaStream_t s)
 {
     AppendArgs a = args;
-    // Few rows: one a block, for latency.  Many: two, which share the block's start (2296 rows of 18 fp32 heads of 80
-    // elements: 8.6 us, with one a block 9.8 and with four 10.5; 8912 rows of 80 bf16 heads of 128: 63, 66.6 and 63).
-    a.block_tokens = a.tokens <= 1024 ? 1 : kAppendMaxTokens;
+    // Few rows: one a block, for latency.  Many: as many as give the block's threads work and leave two blocks for every one
+    // that can run (32768 rows of 8 query and one key-value bf16 heads of 128: 40 us with eight, 49 with two, 69 with one;
+    // 8192 rows of 24 and 4: 26.7 with two, 30.4 with one), but no two rows that alone fill them (of 128 and 8: 94.4 with
+    // one, 98.0 with two).
+    const int row_units = (a.q_heads + a.kv_heads) * a.head_units + a.kv_heads * a.v_units;
+    const int row_bytes = (a.q_heads + 2 * a.kv_heads) * a.head_dim * static_cast<int>(sizeof(T));
+    const int by_blocks = a.tokens <= 1024 ? 1 : std::max(2, a.tokens / (2 * kAppendBlocks));
+    a.block_tokens = std::max(1, std::min({kAppendBytes / row_bytes, by_blocks, sizeof(T) == 4 ? 2 : kAppendMaxTokens}));
+    if (a.block_tokens > 1) {
+        a.turn_magic = a.half > 0 ? ((1ull << 32) + a.half - 1) / a.half : 0;
+        a.row_magic = ((1ull << 32) + row_units - 1) / row_units;
+    }
     const unsigned grid = static_cast<unsigned>((a.tokens + a.block_tokens - 1) / a.block_tokens);
     const size_t smem = static_cast<size_t>(a.block_tokens) * a.half * sizeof(float2);
     return vec ? launch_k(k_kv_append<T, CT, true>, dim3(grid), dim3(kAppendThreads), smem, s, a)

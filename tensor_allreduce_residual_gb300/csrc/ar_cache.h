@@ -32,13 +32,14 @@ struct AppendArgs {
     int half;                 // rotated pairs of a head
     int interleaved;
     float rotary_scale, k_scale, v_scale;
-    int block_tokens;         // rows a block takes
+    int block_tokens;         // rows a block takes: set by the launcher, as are the magics below
+    uint64_t turn_magic, row_magic;  // of `half` and of a row's units, used where block_tokens > 1
     int head_units, v_units;  // units of one q or k head, and of one v head
     uint64_t head_magic, v_magic;  // ceil(2^32 / units): u / units == u * magic >> 32 for u * units < 2^32
 };
 
 // Rows a block of the append kernel may take, and its threads.
-constexpr int kAppendMaxTokens = 2;
+constexpr int kAppendMaxTokens = 8;
 constexpr int kAppendThreads = 256;
 
 // One unit is a 16-byte vector of T (vec) or one element, a pair of them where the pair's halves lie apart.

@@ -382,6 +382,14 @@ def test_append_many_rows_and_sequences():
     _append_and_check([n + 2 for n in new], new, 3, 1, 64, 64, 16, "bf16", "e4m3", "NHD", padding=5)
 
 
+@pytest.mark.parametrize("rows", [7300, 19999])   # a block takes three and eight rows of 16 bits
+@pytest.mark.parametrize("dtype,cache,dim,rotary", [("bf16", "bf16", 16, 16), ("fp16", "e4m3", 9, 6), ("fp32", "fp32", 16, 8)])
+def test_append_many_short_rows(rows, dtype, cache, dim, rotary):
+    new = [1, 0, rows // 3, 2, 0, 0, rows // 2, 5]
+    new.append(rows - sum(new))
+    _append_and_check([n + 3 for n in new], new, 2, 1, dim, rotary, 64, dtype, cache, "HND", padding=4)
+
+
 def test_append_saturates_and_keeps_nan():
     c = Cache([2], 1, 16, 4, "e4m3")
     k = torch.tensor([[1e4, -1e4, math.inf, -math.inf, math.nan] + [448.0, 464.0, 500.0, -465.0, 0.0, -0.0] + [2.0 ** -9, 2.0 ** -10, 1.5 * 2.0 ** -9, 2.0 ** -11, 17.0]],
