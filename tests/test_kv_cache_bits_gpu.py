@@ -1,0 +1,53 @@
+"""The paged key-value cache calls where a result shows the bits of what it is made of: weights against values that
+cancel, factors at the ends of fp32, sines of small angles."""
+import math
+
+import pytest
+import torch
+
+import tensor_allreduce_residual_gb300 as ar
+from tensor_allreduce_residual_gb300 import _build
+from tests import kv_cache_model as model
+from tests.kv_cache_model import TORCH, check, half_step
+
+pytestmark = pytest.mark.gpu
+
+PAIRS = [("fp32", "fp32"), ("bf16", "bf16"), ("fp16", "fp16"), ("bf16", "e4m3"), ("fp16", "e4m3")]
+
+
+@pytest.fixture(scope="module", autouse=True)
+def cuda_library():
+    assert torch.cuda.is_available()
+    torch.cuda.set_device(0)
+    _build.build()
+    ar.lib()
+
+
+def _ints(*values):
+    return torch.tensor(values, dtype=torch.int32, device="cuda")
+
+
+@pytest.mark.parametrize("dtype,cache", PAIRS)
+@pytest.mark.parametrize("heads", [4, 16])
+@pytest.mark.parametrize("pairs", [1, 50])
+@pytest.mark.parametrize("dim", [16, 128])
+def test_weights_keep_their_bits_against_values_that_cancel(dtype, cache, heads, pairs, dim):
+    """Tokens in pairs of values -1 and n, the latter weighing about 1 / n: where n is the head's, the result is what is left
+    of them, far below each.  The model's bound for fp32 queries has weights of 17 bits; one element of the query is not 0,
+    so that no scaling of it loses any."""
+    n = torch.tensor([3.0, 5.0, 7.0, 9.0, 11.0, 13.0, 15.0, 10.0], device="cuda")
+    k, v = torch.zeros(pairs, 2, dim, device="cuda"), torch.full((pairs, 2, dim), -1.0, device="cuda")
+    k[:, 1, 0] = -1.0
+    v[:, 1] = n.repeat(dim // 8)
+    tokens = 2 * pairs
+    pages = torch.zeros(2, -(-tokens // 16) * 16, dim, device="cuda")
+    pages[0, :tokens], pages[1, :tokens] = k.view(-1, dim), v.view(-1, dim)
+    k, v = (x.reshape(-1, 16, 1, dim).to(TORCH[cache]) for x in pages)
+    q = torch.zeros(1, heads, dim, device="cuda")
+    q[0, :, 0] = n.log().repeat(2)[:heads]
+    q = q.to(TORCH[dtype])
+    table = torch.arange(k.shape[0], dtype=torch.int32, device="cuda")[None]
+    out, lse = ar.ar_paged_attention(q, k, v, table, _ints(tokens), scale=1.0, return_lse=True)
+    ref, ref_lse, room, room_lse = model.attention(q.float(), k, v, table, [tokens], scale=1.0)
+    check(out, ref, room + half_step(ref, out.dtype), f"{dtype} {cache} out")
+    check(lse, ref_lse, room_lse, f"{dtype} {cache} lse")
