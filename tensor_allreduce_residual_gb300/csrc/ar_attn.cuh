@@ -15,6 +15,7 @@
 #include <cuda_fp16.h>
 
 #include <atomic>
+#include <cfloat>
 #include <climits>
 #include <type_traits>
 
@@ -896,7 +897,8 @@ k_attn_mma(const AttnArgs a)
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
                         const int eh = __shfl_sync(~0u, e, (2 * t4 + i) * 4);
-                        qscale[nt][i] = ldexpf(a.scale2, eh);
+                        // Finite: an infinite factor would make the scores of keys that are 0 NaN.
+                        qscale[nt][i] = fmaxf(fminf(ldexpf(a.scale2, eh), FLT_MAX), -FLT_MAX);
                     }
                 }
 #pragma unroll

@@ -51,3 +51,20 @@ def test_weights_keep_their_bits_against_values_that_cancel(dtype, cache, heads,
     ref, ref_lse, room, room_lse = model.attention(q.float(), k, v, table, [tokens], scale=1.0)
     check(out, ref, room + half_step(ref, out.dtype), f"{dtype} {cache} out")
     check(lse, ref_lse, room_lse, f"{dtype} {cache} lse")
+
+
+@pytest.mark.parametrize("dtype,cache", [p for p in PAIRS if p[0] != "fp16"])
+@pytest.mark.parametrize("softcap", [0.0, 30.0])
+def test_large_queries_and_scales_of_keys_that_are_zero(dtype, cache, softcap):
+    """The query's size times the scale is over fp32's range, the scores are 0: every token weighs the same."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(7)
+    k = torch.zeros(3, 16, 1, 64, device="cuda").to(TORCH[cache])
+    v = torch.randn(3, 16, 1, 64, generator=g, device="cuda").to(TORCH[cache])
+    q = torch.full((1, 4, 64), 2.0 ** 120, device="cuda").to(TORCH[dtype])
+    q[0, 2] = -q[0, 2]
+    table = _ints(0, 1, 2)[None]
+    out, lse = ar.ar_paged_attention(q, k, v, table, _ints(37), scale=2.0 ** 40, softcap=softcap, return_lse=True)
+    ref, ref_lse, room, room_lse = model.attention(q, k, v, table, [37], scale=2.0 ** 40, softcap=softcap)
+    check(out, ref, room + half_step(ref, out.dtype), f"{dtype} {cache} out")
+    check(lse, ref_lse, room_lse, f"{dtype} {cache} lse")
