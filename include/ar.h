@@ -677,8 +677,9 @@ typedef struct {
  *     cache k, v at token p  = rotated k / k_scale, v / v_scale
  *     q_out row              = rotated q
  * Arithmetic is fp32 with the angle reduced exactly from a 64-bit fixed-point
- * product, so far positions lose nothing; each result is rounded once, to
- * nearest even, and AR_FP8_E4M3 saturates at +-448 (a NaN stays one).
+ * product, so far positions and small angles lose nothing; each result is
+ * rounded once, to nearest even, and AR_FP8_E4M3 saturates at +-448 (a NaN
+ * stays one).
  *   - Rows before seq_start[0] or from seq_start[batch] on are padding:
  *     neither cached nor written to q_out.
  *   - A row whose p lies outside [0, max_pages * page_size) (lengths[b] == 0

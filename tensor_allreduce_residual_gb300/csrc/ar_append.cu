@@ -17,7 +17,8 @@ namespace ar {
 // turn, whose product with the position wraps around at whole turns by itself,
 // so the reduction is exact for any 32-bit position and costs one integer
 // multiply (a product in fp32 would be off by 0.06 rad at position 2^20, and
-// fp64 runs at 1/64 of the fp32 rate here).
+// fp64 runs at 1/64 of the fp32 rate here).  Angles of up to pi a position are
+// off by less than 2^-60 rad a position.
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ uint64_t turn_fraction(float inv_freq)
 {
@@ -43,11 +44,14 @@ __device__ __forceinline__ uint64_t turn_fraction(float inv_freq)
 __device__ __forceinline__ float2 cos_sin(uint64_t fraction, int position, float scale)
 {
     const uint64_t turn = fraction * static_cast<uint64_t>(static_cast<int64_t>(position));
-    // The upper half as a signed number is the angle in half turns times 2^31, in [-1, 1).
-    const float half_turns = static_cast<float>(static_cast<int32_t>(turn >> 32)) * 0x1p-31f;
+    // The nearest whole quarter, and what is left: at most an eighth of a turn either way, of which fp32 keeps 24 bits however
+    // small it is, and so do its sine and cosine, one of which is small near each quarter.
+    const uint32_t quarter = static_cast<uint32_t>((turn + (1ull << 61)) >> 62);
+    const int64_t rest = static_cast<int64_t>(turn - (static_cast<uint64_t>(quarter) << 62));
     float s, c;
-    sincospif(half_turns, &s, &c);
-    return make_float2(c * scale, s * scale);
+    sincospif(__ll2float_rn(rest) * 0x1p-63f, &s, &c);
+    const float x = (quarter & 1) != 0 ? s : c, y = (quarter & 1) != 0 ? c : s;
+    return make_float2(quarter == 1 || quarter == 2 ? -x * scale : x * scale, quarter >= 2 ? -y * scale : y * scale);
 }
 
 // ---------------------------------------------------------------------------

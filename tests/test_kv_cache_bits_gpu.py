@@ -68,3 +68,31 @@ def test_large_queries_and_scales_of_keys_that_are_zero(dtype, cache, softcap):
     ref, ref_lse, room, room_lse = model.attention(q, k, v, table, [37], scale=2.0 ** 40, softcap=softcap)
     check(out, ref, room + half_step(ref, out.dtype), f"{dtype} {cache} out")
     check(lse, ref_lse, room_lse, f"{dtype} {cache} lse")
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("dim", [2, 64])   # elements, and vectors
+def test_rotation_of_small_angles_keeps_their_bits(interleaved, dim):
+    """(0, 1) turns to (-sin a, cos a), each of the fp32 result's own size whatever the angle, near whole quarters of a turn
+    too.  The angle of a position is off by less than 2^-64 turns for the fraction's 64 bits and its own size times 2^-62 for
+    1 / 2 pi's, 2^-60 together up to pi; and relative to itself after whole quarters by u = 2^-24; sine and cosine by two
+    steps, 4 u; the scale, the product and the sum by u each: 8 u of the result."""
+    half = dim // 2
+    freq = torch.tensor([1.0, 0.1, 1e-2, 1e-3, 1e-4, 1e-5, 1e-6, 3e-8], device="cuda")
+    freq = torch.cat([freq, math.pi / 2 ** torch.arange(8, device="cuda").float()]).repeat(2)
+    positions = [0, 1, -1, 2, 3, 7, 100, 1000, 4097, -5000, 100003, (1 << 20) + 1]
+    for f in freq[:16].split(half) if half < 16 else [freq]:
+        rows = len(positions)
+        x = torch.zeros(rows, 1, dim, device="cuda")
+        x[..., 1::2] = 1.0
+        if not interleaved:
+            x = torch.cat([x[..., 0::2], x[..., 1::2]], -1).contiguous()
+        k = torch.zeros(1, rows, 1, dim, device="cuda")
+        v = torch.zeros_like(k)
+        got = ar.ar_kv_append(k, v, _ints(0)[None], _ints(rows), x, x, q=x, seq_start=_ints(0, rows), positions=_ints(*positions),
+                              inv_freq=f, interleaved=interleaved, rotary_scale=0.75)
+        pos = _ints(*positions)
+        ref = model.rotate(x.double(), pos, f, interleaved, 0.75)
+        room = 8 * model.U32 * ref.abs() + ((pos.double().abs() + 1) * 2.0 ** -60)[:, None, None]
+        check(got, ref, room, "q")
+        check(k[0], ref, room, "k")
