@@ -339,8 +339,12 @@ k_attention_join(const JoinArgs a)
     typename U::raw v[R];
 #pragma unroll
     for (int r = 0; r < R; ++r)
-        if (i < a.units)
-            v[r] = U::load(a.partials[r], i);
+        if (i < a.units) {
+            if constexpr (UNITS == kJoinElements)
+                v[r] = U::load(a.partials[r], i);
+            else
+                v[r] = ld_stream16_rw(static_cast<const uint4*>(a.partials[r]) + i);  // out may be one of them
+        }
     // A 64-bit division would cost more than the loads of a small row.
     const uint32_t dim = static_cast<uint32_t>(a.dim);
     const auto row_of = [&](uint64_t x) { return a.elements >> 32 == 0 ? static_cast<uint32_t>(x) / dim : x / dim; };
