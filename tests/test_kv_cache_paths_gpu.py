@@ -8,7 +8,7 @@ import torch
 import tensor_allreduce_residual_gb300 as ar
 from tensor_allreduce_residual_gb300 import _build
 from tests.kv_cache_model import TORCH, check, half_step
-from tests.test_kv_cache_gpu import _gen, _join_room, _normal
+from tests.test_kv_cache_gpu import _append_and_check, _gen, _join_room, _normal
 
 pytestmark = pytest.mark.gpu
 
@@ -48,3 +48,14 @@ def test_join_over_many_blocks_and_into_each_partial(R, dtype, rows, dim, offset
         into, again = ar.ar_attention_join(o, lse, out=o[r], return_lse=True)
         assert into is o[r] and torch.equal(into, out) and torch.equal(again, got)
         o[r].copy_(kept)
+
+
+# The 16-bit vector path at several rows a block, whose table of cosines and sines is in another order: three and eight rows,
+# one vector a half and several; the 8-byte vectors of an 8-bit cache; two rows in fp32.
+@pytest.mark.parametrize("rows", [7301, 19998])
+@pytest.mark.parametrize("dtype,cache,dim,rotary", [("bf16", "bf16", 16, 16), ("fp16", "e4m3", 64, 32), ("bf16", "bf16", 64, 64), ("fp32", "fp32", 16, 8)])
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_append_of_several_rows_a_block(rows, dtype, cache, dim, rotary, interleaved):
+    new = [2, 0, 0, rows // 3, 1, 0, rows // 2, 4]
+    new.append(rows - sum(new))
+    _append_and_check([n + 5 for n in new], new, 2, 1, dim, rotary, 64, dtype, cache, "NHD", interleaved=interleaved, padding=3, in_place=True)
