@@ -323,6 +323,18 @@ template cudaError_t launch_append<__nv_bfloat16, __nv_fp8_e4m3>(const AppendArg
 // ---------------------------------------------------------------------------
 enum JoinUnits { kJoinElements, kJoinRows, kJoinAcross };  // single elements, vectors of one row, vectors of two rows
 
+// A streaming 16-byte load of what the launch may overwrite: out may be one of the partials, and the read-only path, which
+// the sums take, asks for memory that nothing writes meanwhile.
+__device__ __forceinline__ uint4 ld_stream16_rw(const void* p)
+{
+    uint4 r;
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
+                 : "l"(p)
+                 : "memory");
+    return r;
+}
+
 // Rows that a block's elements can touch.
 __host__ __device__ inline int join_rows(int lanes, int dim) { return (kFlatThreads * lanes - 1) / dim + 2; }
 
@@ -343,7 +355,7 @@ k_attention_join(const JoinArgs a)
             if constexpr (UNITS == kJoinElements)
                 v[r] = U::load(a.partials[r], i);
             else
-                v[r] = ld_stream16_rw(static_cast<const uint4*>(a.partials[r]) + i);  // out may be one of them
+                v[r] = ld_stream16_rw(static_cast<const uint4*>(a.partials[r]) + i);
         }
     // A 64-bit division would cost more than the loads of a small row.
     const uint32_t dim = static_cast<uint32_t>(a.dim);

@@ -69,24 +69,6 @@ __device__ __forceinline__ uint4 ld_stream16(const void* p)
     return r;
 }
 
-// The same for what the launch may overwrite: the read-only path asks for memory that nothing writes meanwhile.
-__device__ __forceinline__ uint4 ld_stream16_rw(const void* p)
-{
-    uint4 r;
-#if AR_L2_PREFETCH_256B
-    asm volatile("ld.global.L1::no_allocate.L2::256B.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
-                 : "l"(p)
-                 : "memory");
-#else
-    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
-                 : "l"(p)
-                 : "memory");
-#endif
-    return r;
-}
-
 // Small read-mostly operands (weight, bias: one row reused by every row).
 __device__ __forceinline__ uint4 ld_cached16(const void* p)
 {
