@@ -12,6 +12,7 @@ ranks' partial outputs of a row-parallel linear layer, kept in one GPU's HBM.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 from typing import Optional, Sequence
 
@@ -567,10 +568,16 @@ def _bound_calls():
     """The extension module, bound to the loaded library."""
     global _calls
     L = lib()
-    from . import _binding
-    _binding.bind(ARError, *(ctypes.cast(f, ctypes.c_void_p).value for f in (
+    from . import _build
+    path = _build.binding_path()
+    if not os.path.exists(path):
+        raise RuntimeError(f"{path} is missing: build it first (tensor_allreduce_residual_gb300._build.build())")
+    spec = importlib.util.spec_from_file_location(f"{__name__}._binding", path)
+    binding = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(binding)
+    binding.bind(ARError, *(ctypes.cast(f, ctypes.c_void_p).value for f in (
         L.ar_kv_append, L.ar_paged_attention_workspace_size, L.ar_paged_attention, L.ar_attention_join)))
-    _calls = _binding
+    _calls = binding
     return _calls
 
 

@@ -11,7 +11,8 @@ barrier's timeout test).  Only ar_api.cu and ar_peer.cu differ, so only
 they are compiled twice.
 _binding.so is the CPython extension that marshals the paged key-value cache
 calls from torch tensors (host code only, compiled by g++ against torch's
-headers).
+headers).  Where it cannot be built the other calls, which do not need it, are
+built all the same.
 
 The tests of forced launch shapes and of bounded waits, and the shape sweeps
 that build the AUTO table, load it; everything else loads libar.so, which
@@ -24,6 +25,7 @@ import shutil
 import subprocess
 import sys
 import sysconfig
+import warnings
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -32,7 +34,6 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libar.so")
 TEST_LIB = os.path.join(PKG, "libar_test.so")
-BINDING = os.path.join(PKG, "_binding.so")
 BINDING_SOURCE = os.path.join(CSRC, "ar_binding.cpp")
 
 SOURCES = ["ar_api.cu", "ar_kern_f32.cu", "ar_kern_f16.cu", "ar_kern_bf16.cu", "ar_noalloc.cu", "ar_host.cu",
@@ -52,12 +53,25 @@ def nvcc() -> str:
     return exe
 
 
-def _stale() -> bool:
-    if not all(os.path.exists(f) for f in (LIB, TEST_LIB, BINDING)):
+def binding_path() -> str:
+    """Where the extension module lies."""
+    return os.path.join(PKG, "_binding.so")
+
+
+def _older(outputs: list, deps: list) -> bool:
+    """Whether an output is missing or older than what it is made of."""
+    if not all(os.path.exists(f) for f in outputs):
         return True
-    t = min(os.path.getmtime(f) for f in (LIB, TEST_LIB, BINDING))
-    deps = [os.path.join(CSRC, f) for f in SOURCES + HEADERS] + [os.path.join(INCLUDE, "ar.h"), BINDING_SOURCE, __file__]
-    return any(os.path.getmtime(d) > t for d in deps)
+    t = min(os.path.getmtime(f) for f in outputs)
+    return any(os.path.getmtime(d) > t for d in [*deps, os.path.join(INCLUDE, "ar.h"), __file__])
+
+
+def _stale() -> bool:
+    return _older([LIB, TEST_LIB], [os.path.join(CSRC, f) for f in SOURCES + HEADERS])
+
+
+def _binding_stale() -> bool:
+    return _older([binding_path()], [BINDING_SOURCE])
 
 
 def _binding_command(out: str) -> list:
@@ -74,10 +88,21 @@ def _binding_command(out: str) -> list:
             "-ltorch_cuda", "-lc10_cuda", "-lc10"]
 
 
-def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:
-    """Compile and link libar.so, libar_test.so and _binding.so if any source is newer; returns libar.so's path."""
-    if not force and not _stale():
-        return LIB
+def _start(cmd: list, verbose: bool) -> subprocess.Popen:
+    if verbose:
+        print(" ".join(cmd), file=sys.stderr)
+    return subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)
+
+
+def _succeeded(p: subprocess.Popen, show: bool) -> bool:
+    """Waits for a compiler; its output is shown where asked for, or where it failed."""
+    out, _ = p.communicate()
+    if out and (show or p.returncode != 0):
+        print(out, file=sys.stderr)
+    return p.returncode == 0
+
+
+def _build_library(verbose: bool, ptxas_info: bool) -> None:
     os.makedirs(BUILD, exist_ok=True)
     cc = nvcc()
     procs = []
@@ -89,25 +114,11 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
         cmd = [cc, *ARCH, *FLAGS, *defs, "-c", os.path.join(CSRC, src), "-o", obj]
         if ptxas_info:
             cmd.insert(1, "-Xptxas=-v")
-        if verbose:
-            print(" ".join(cmd), file=sys.stderr)
-        procs.append((src, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)))
+        procs.append((src, _start(cmd, verbose)))
         objs.append(obj)
-    binding = f"{BINDING}.{os.getpid()}.tmp"
-    cmd = _binding_command(binding)
-    if verbose:
-        print(" ".join(cmd), file=sys.stderr)
-    procs.append(("ar_binding.cpp", subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)))
-    failed = []
-    for src, p in procs:
-        out, _ = p.communicate()
-        if out and (verbose or ptxas_info or p.returncode != 0):
-            print(out, file=sys.stderr)
-        if p.returncode != 0:
-            failed.append(src)
+    failed = [src for src, p in procs if not _succeeded(p, verbose or ptxas_info)]
     if failed:
-        raise RuntimeError(f"the compiler failed on {failed}")
-    os.replace(binding, BINDING)
+        raise RuntimeError(f"nvcc failed on {failed}")
     product = objs[:len(SOURCES)]
     swap = {os.path.join(BUILD, "ar_api.o"): objs[-2], os.path.join(BUILD, "ar_peer.o"): objs[-1]}
     test = [swap.get(o, o) for o in product]
@@ -115,6 +126,34 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
         tmp = f"{lib}.{os.getpid()}.tmp"
         subprocess.run([cc, *ARCH, "-shared", "-o", tmp, *lib_objs], check=True)
         os.replace(tmp, lib)
+
+
+def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:
+    """Compile and link libar.so, libar_test.so and the extension module where a source is newer; returns libar.so's path.
+
+    An extension module that cannot be built is warned of, and an older one taken away: the calls that go through it then
+    raise, all others work.
+    """
+    made, binding, tmp = True, None, f"{binding_path()}.{os.getpid()}.tmp"
+    if force or _binding_stale():
+        try:
+            binding = _start(_binding_command(tmp), verbose)   # beside the library's units
+        except Exception as e:   # no compiler, or none of torch's headers
+            print(e, file=sys.stderr)
+            made = False
+    try:
+        if force or _stale():
+            _build_library(verbose, ptxas_info)
+    finally:
+        if binding is not None:
+            made = _succeeded(binding, verbose)
+            if made:
+                os.replace(tmp, binding_path())
+    if not made:
+        if os.path.exists(binding_path()):
+            os.remove(binding_path())
+        warnings.warn("the extension module could not be compiled: ar_kv_append, ar_paged_attention and ar_attention_join "
+                      "are not available from Python")
     return LIB
 
 

@@ -323,8 +323,8 @@ template cudaError_t launch_append<__nv_bfloat16, __nv_fp8_e4m3>(const AppendArg
 // ---------------------------------------------------------------------------
 enum JoinUnits { kJoinElements, kJoinRows, kJoinAcross };  // single elements, vectors of one row, vectors of two rows
 
-// A streaming 16-byte load of what the launch may overwrite: out may be one of the partials, and the read-only path, which
-// the sums take, asks for memory that nothing writes meanwhile.
+// A streaming 16-byte load of what the launch may overwrite: out may be one of the partials, and the read-only path asks for
+// memory that nothing writes meanwhile.
 __device__ __forceinline__ uint4 ld_stream16_rw(const void* p)
 {
     uint4 r;
