@@ -9,9 +9,9 @@ of the bounded-wait tests and the programmatic-launch switch, each read from
 the environment, and a communicator over local buffers for the peer
 barrier's timeout test).  Only ar_api.cu and ar_peer.cu differ, so only
 they are compiled twice.
-_binding.so is the CPython extension that marshals the paged key-value cache
+_binding-*.so is the CPython extension that marshals the paged key-value cache
 calls from torch tensors (host code only, compiled by g++ against torch's
-headers).  Where it cannot be built the other calls, which do not need it, are
+headers; its name tells torch's and Python's versions).  Where it cannot be built the other calls, which do not need it, are
 built all the same.
 
 The tests of forced launch shapes and of bounded waits, and the shape sweeps
@@ -20,12 +20,15 @@ reads no environment variable.
 """
 from __future__ import annotations
 
+import importlib.machinery
 import os
 import shutil
 import subprocess
 import sys
 import sysconfig
 import warnings
+
+import torch
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -54,8 +57,9 @@ def nvcc() -> str:
 
 
 def binding_path() -> str:
-    """Where the extension module lies."""
-    return os.path.join(PKG, "_binding.so")
+    """The extension module of this Python and torch, whose C++ interfaces it is compiled against: one of other versions has
+    another name, and is neither loaded nor taken for built."""
+    return os.path.join(PKG, f"_binding-torch{torch.__version__}{importlib.machinery.EXTENSION_SUFFIXES[0]}")
 
 
 def _older(outputs: list, deps: list) -> bool:
@@ -76,7 +80,6 @@ def _binding_stale() -> bool:
 
 def _binding_command(out: str) -> list:
     """The g++ command of the extension module: torch's own headers and libraries, and CUDA's for its stream type."""
-    import torch
     root = os.path.dirname(torch.__file__)
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
     includes = [INCLUDE, os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
