@@ -42,7 +42,7 @@ BINDING_SOURCE = os.path.join(CSRC, "ar_binding.cpp")
 SOURCES = ["ar_api.cu", "ar_kern_f32.cu", "ar_kern_f16.cu", "ar_kern_bf16.cu", "ar_noalloc.cu", "ar_host.cu",
            "ar_peer.cu", "ar_cache_api.cu", "ar_append.cu", "ar_attn_f32.cu", "ar_attn_f16.cu", "ar_attn_bf16.cu"]
 HEADERS = ["ar_internal.h", "ar_kernels.cuh", "ar_tma.cuh", "ar_lamport.cuh", "ar_launch.cuh", "ar_launch_k.cuh",
-           "ar_auto_table.h", "ar_cache.h", "ar_attn.cuh"]
+           "ar_auto_table.h", "ar_cache.h", "ar_split.h", "ar_attn.cuh"]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",

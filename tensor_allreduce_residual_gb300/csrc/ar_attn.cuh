@@ -22,6 +22,7 @@
 #include "ar_cache.h"
 #include "ar_kernels.cuh"
 #include "ar_launch_k.cuh"
+#include "ar_split.h"
 
 namespace ar {
 
@@ -72,29 +73,6 @@ template <int TILE>
 __device__ __forceinline__ Span span_of(const AttnArgs& a, int b)
 {
     return span_of_length<TILE>(a, a.lengths[b]);
-}
-
-// The run of tiles of block `c` of `blocks`: the first total % blocks blocks take one more.
-struct Run {
-    long long total;  // tiles of the line
-    long long lo;
-    long long n;
-};
-// a / b of a >= 0, b > 0: a 64-bit division takes five times as long as a 32-bit one, and is hardly ever needed.
-__device__ __forceinline__ long long divide(long long a, long long b)
-{
-    return (a | b) <= 0xffffffffll ? static_cast<uint32_t>(a) / static_cast<uint32_t>(b) : a / b;
-}
-__device__ __forceinline__ Run run_of(long long total, int blocks, int c)
-{
-    const long long q = divide(total, blocks), r = total - q * blocks;
-    return {total, c * q + min(static_cast<long long>(c), r), q + (c < r)};
-}
-// The block whose run has tile x.
-__device__ __forceinline__ int block_of(long long total, int blocks, long long x)
-{
-    const long long q = divide(total, blocks), r = total - q * blocks, edge = r * (q + 1);
-    return static_cast<int>(x < edge ? divide(x, q + 1) : r + divide(x - edge, q));
 }
 
 // Where a warp is on the line.  All lanes hold the same, but for `lengths`, of which each has one of 32 sequences'.
@@ -486,7 +464,7 @@ __device__ __forceinline__ void write_part(const AttnArgs& a, const WarpTile<P::
     using T = typename P::T;
     const bool whole = began && (tile.flags & kTileEnds);
     const int g = heads_of(a, tile.hb), fours = a.head_dim / 4, slots = min(a.group, a.block_heads);
-    float* part = a.part + (2ull * blockIdx.x + (began ? 1 : 0)) * a.slot_floats;
+    float* part = a.part + slot_of(static_cast<int>(blockIdx.x), began) * a.slot_floats;
     if (began && threadIdx.x == 0) {  // tells the join which blocks have the item's parts
         int last = static_cast<int>(blockIdx.x);
         if (!whole)
@@ -1138,8 +1116,7 @@ k_attn_join(const AttnArgs a, const int columns)
             n[i] = 0.0f;
             v[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
             if (p < parts) {
-                // Part 0 lies in its block's slot 1 (it begins the item), the others in their blocks' slots 0.
-                const float* part = a.part + (2ull * (c0 + p) + (p == 0 ? 1 : 0)) * a.slot_floats;
+                const float* part = a.part + slot_of(c0 + p, p == 0) * a.slot_floats;  // part 0 begins the item
                 m[i] = part[slots * a.head_dim + h];
                 n[i] = part[slots * (a.head_dim + 1) + h];
                 v[i] = *reinterpret_cast<const float4*>(part + h * a.head_dim + e);
