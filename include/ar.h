@@ -714,7 +714,8 @@ size_t ar_paged_attention_workspace_size(const ar_kv_cache* cache, int q_heads);
  * table entries that are no page.  With no token left, out is 0 and lse is
  * -infinity.  Cached values that are left out are never read into a result,
  * whatever they hold.  An infinite value that is attended to makes its
- * element of the result infinite or NaN.
+ * element of the result infinite or NaN, as do values whose weighted sum
+ * passes fp32's range before it is divided by the sum of weights.
  * One pass over the cache: sequences and heads are cut into tiles, the
  * launch's blocks take equal runs of them whatever the lengths, and parts of
  * one row's tokens that fell to several blocks are joined, in a fixed order,

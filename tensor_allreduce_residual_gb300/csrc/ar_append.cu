@@ -136,7 +136,8 @@ __device__ __forceinline__ int turn_place(int j, int half, int group_log)
 // What hides the loads is the number of threads: forms that kept several units
 // a thread in flight, or a head's cosines and sines in registers, ran fewer of
 // them and took 66 to 94 us for the same prompts; hence one unit at a time and
-// eight blocks an SM.
+// eight blocks an SM, for whose 32 registers the 16-bit vector kernels spill 24
+// to 28 bytes a thread.
 // ---------------------------------------------------------------------------
 template <typename T, typename CT, bool VEC>
 __global__ void __launch_bounds__(kAppendThreads, 8)
@@ -288,10 +289,11 @@ template <typename T, typename CT>
 cudaError_t launch_append(const AppendArgs& args, bool vec, cudaStream_t s)
 {
     AppendArgs a = args;
-    // Few rows: one a block, for latency.  Many: as many as give the block's threads work and leave two blocks for every one
-    // that can run (32768 rows of 8 query and one key-value bf16 heads of 128: 40 us with eight, 49 with two, 69 with one;
-    // 8192 rows of 24 and 4: 26.7 with two, 30.4 with one), but no two rows that alone fill them (of 128 and 8: 94.4 with
-    // one, 98.0 with two).
+    // Few rows: one a block, for latency.  From 1025 on two at least, where that leaves a block under 32 KB: at 8 query heads
+    // and one key-value head of 128 bf16 elements 4.3 us either way for 1025 rows, 5.6 against 6.7 for 1500, 10.2 against
+    // 13.8 for 4096.  More from 7296 on, as many as leave two blocks for every one that can run: 8192 rows 15.0 us with
+    // three, 16.2 with two, 21.7 with one, 32768 rows 41.3 with eight, 44.7 with four, 70.6 with one.  At 24 and 4 heads 8192
+    // rows take 26.9 us with two to four and 30.8 with one; at 64 and 8, one row of which is 20 KB, 55.7 with one.
     const int row_units = (a.q_heads + a.kv_heads) * a.head_units + a.kv_heads * a.v_units;
     const int row_bytes = (a.q_heads + 2 * a.kv_heads) * a.head_dim * static_cast<int>(sizeof(T));
     const int by_blocks = a.tokens <= 1024 ? 1 : std::max(2, a.tokens / (2 * kAppendBlocks));

@@ -201,6 +201,8 @@ __device__ __forceinline__ float out_scale(const AttnArgs& a, float total)
     return total == 0.0f ? 0.0f : a.v_scale / total;
 }
 
+// 2^x, off by 2^-22 of it at the most, less than a pair of 16-bit numbers leaves of a weight.  Results under 2^-126, which
+// no sum of weights from 1 on shows, are 0.
 __device__ __forceinline__ float exp2_fast(float x)
 {
     float y;
@@ -267,10 +269,11 @@ struct AttnShape {
         return n < 5 ? n : 5;
     }
     // Blocks of an SM: three where registers and two stages of each fit, which short rows and 8-bit elements gain from most
-    // (256 rows of 1 to 200 tokens, 8 key-value heads of 128 bf16 elements: 38.1 against 46.0 us with two; 511 MB of them in
-    // 256 longer rows: 84.0 against 87.5; 67 MB in one: 18.8 against 17.7; 533 MB of e4m3: 93.5 against 98.6); two for
-    // stages over 48 KB or where a block of 8 or 16 heads needs the registers of a third.  Long heads leave room for two
-    // stages in one block only.
+    // (256 rows of 1 to 200 tokens, 8 key-value heads of 128 bf16 elements: 37.8 against 45.9 us with two; 511 MB of them in
+    // longer rows: 83.9 against 84.7; 533 MB of e4m3: 86.1 against 90.4; 93 MB of fp16 heads of 64: 21.7 against 24.3); two
+    // for stages over 48 KB or where a block of 8 or 16 heads needs the registers of a third.  One where the shared memory
+    // has no room for two stages of each: heads over 192, over 128 in 8 bits, of 72 to 96 in 16 bits with more than 8 query
+    // heads, and over 128 in fp32 with one or two (of those, 129 to 192 would fit two blocks).
     static constexpr int WANT = HEADS == 2 || (HEADS == 8 && DIM <= 128 && STAGE < 48 * 1024 && (!WIDE || DIM <= 64)) ? 3 : 2;
     static constexpr int BLOCKS = fits(kSmemPerSM / WANT) >= 2 ? WANT : 1;
     static constexpr int STAGES = fits(kSmemPerSM / BLOCKS);
@@ -542,7 +545,8 @@ __device__ __forceinline__ float column_sum(float x)
 // cache: 68 us on 269 MB with 8 heads, its loads at 64 % of the pipe.)  For the
 // weighted values the same elements take every token's weights, from shared
 // memory.  Heads of up to 64 elements take half of the lanes, and each half
-// half of the tokens.
+// half of the tokens.  With 8 query heads of more than 128 elements it spills
+// 80 to 148 bytes a thread (0.67 of the copy rate, as at 128 without).
 // ---------------------------------------------------------------------------
 template <typename P>
 __global__ void __launch_bounds__(kAttnThreads, P::BLOCKS)
@@ -751,9 +755,10 @@ k_attn_fma(const AttnArgs a)
 // rounding and what it leaves (17 bits and more together), which costs an
 // instruction that the memory's pace hides (bf16 queries on 533 MB of e4m3:
 // 85.6 us, with the first number alone 85.1; 16 heads of 128 on 134 MB: 37.0
-// against 34.0).  8-bit elements become fp16 in
-// registers, exactly; queries too large or small for fp16 are scaled by a
-// power of two per head first.
+// against 34.0).  8-bit elements become fp16 in registers, exactly; queries too
+// large or small for fp16 are scaled by a power of two per head first.  The
+// kernels of 16 query heads of 256 elements spill 68 bytes a thread in 16 bits
+// and about 400 in 8 (0.53 and 0.36 of the copy rate).
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ void ldmatrix4(uint32_t addr, uint32_t* r)
 {
@@ -1169,8 +1174,10 @@ cudaError_t launch_shape(void (*kernel)(AttnArgs), const AttnArgs& a, int most, 
 {
     int per_sm = P::BLOCKS;
     const uint64_t items = static_cast<uint64_t>(a.batch) * a.kv_heads * a.group_blocks;
-    // Few items: a third block an SM adds more to the join than it takes from the loads (67 MB in one row of 131072
-    // tokens: 17.7 against 18.6 us).
+    // Few items: a third block an SM adds more to the join than it takes from the loads, unless the items are long.  With
+    // two and three blocks, bf16 heads of 128: 17 MB in one item 10.9 and 14.2 us, in 8 11.3 and 12.7, in 16 11.2 and 12.7;
+    // 67 MB in one 17.9 and 19.2, in 8 17.8 and 18.2, in 16 18.0 and 18.1; 134 MB of fp16 heads of 64 in 8 26.8 and 26.0, in
+    // 16 26.7 and 26.0.  The lengths, which would tell more than the items, are not on the host.
     if (items <= 8 && per_sm > 2)
         per_sm = 2;
     const int blocks = most < sms * per_sm ? most : sms * per_sm;

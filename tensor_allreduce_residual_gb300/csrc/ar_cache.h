@@ -84,8 +84,11 @@ constexpr int kAttnMaxBlocks = 456;
 constexpr int kAttnMaxDim = 256;
 
 // Cached tokens of one tile: what a block loads at once, and the work is cut into.  A warp takes a quarter: 8 tokens in
-// fp32, else one block of 16, or two where they are 128 elements of 8 bits or up to 96 of 16 (93 MB of fp16 heads of 64:
-// 21.3 against 22.6 us with one).
+// fp32; one block of 16 for 16-bit heads over 96; two for those up to 96, and for 8-bit heads of any size.
+// 128 tokens against 64, 64 rows of 4096 tokens, 2 key-value heads of 8 query heads each: bf16 heads of 64 26.1
+// against 28.0 us; e4m3 heads of 64 21.0 against 24.7, of 128 28.2 against 31.4.  The other way round: bf16 heads of 96 39.5
+// against 38.6, with 16 query heads 47.8 against 42.4; e4m3 heads of 192 49.6 against 44.4, of 256 55.0 against 49.6, but of
+// 256 with 16 query heads, whose ends of rows fill more than a stage of 64 tokens, 104 against 118.
 __host__ __device__ constexpr int attn_tile(int cache_esize, int head_dim)
 {
     return cache_esize == 4 ? 32 : cache_esize == 2 && head_dim > 96 ? 64 : 128;
