@@ -77,7 +77,8 @@ struct AttnArgs {
 };
 
 // Query heads of one key-value head that one block attends for at once, at most.  A larger group reads its tiles again for
-// every so many: 8 in fp32, whose 16 would not fit the registers with their queries.
+// every so many: 8 in fp32, whose 16 would not fit a warp's registers with their queries (269 MB at 8 heads 58.6 us, at 16
+// 108; bf16 at 16 48.2, at 32 84.4).
 __host__ __device__ constexpr int attn_block_heads(int cache_esize) { return cache_esize == 4 ? 8 : 16; }
 // Blocks of the attention kernel, at most: three per SM of the 152.  The workspace holds two slots for each.
 constexpr int kAttnMaxBlocks = 456;
