@@ -218,7 +218,7 @@ def prepare(case, seed):
         shape = (2 * case["pairs"] + 3, case["page"], case["kv_heads"], case["dim"])
         order = torch.randperm(shape[0], generator=g, device="cuda").to(torch.int32)
         src = order[case["pairs"]:2 * case["pairs"]].clone()
-        src[::5] = src[0]  # a page that several sequences share is copied for each
+        src[::5] = src[0].clone()  # a page that several sequences share is copied for each
         return {"case": case, "src": src, "dst": order[: case["pairs"]].clone(),
                 "k_pages": [_pages(case, g, shape, scales[0]) for _ in range(case["layers"])],
                 "v_pages": [_pages(case, g, shape, scales[1]) for _ in range(case["layers"])]}
