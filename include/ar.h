@@ -46,6 +46,7 @@
 #define TENSOR_ALLREDUCE_RESIDUAL_AR_H
 
 #include <stddef.h>
+#include <stdint.h>
 
 #ifdef __cplusplus
 extern "C" {
@@ -697,6 +698,88 @@ typedef struct {
  */
 int ar_kv_append(const ar_kv_cache* cache, const ar_append_params* p, ar_stream_t stream);
 
+/*
+ * ar_kv_append_axes -- ar_kv_append with positions on several axes (time,
+ * height and width of images and video): pair j turns by
+ *     a = positions[pair_axis[j] * axis_stride + row] * inv_freq[j]
+ * and everything else is as there.  p->positions is required and holds
+ * `axes` rows of p->tokens positions.
+ *   axes         1 .. AR_MAX_AXES
+ *   axis_stride  >= p->tokens with axes > 1: elements from one axis to the
+ *                next
+ *   pair_axis    host [rotary_dim / 2], each below axes; read during the
+ *                call.  Axes may lie in blocks or take turns
+ * Errors: those of ar_kv_append, and AR_ERR_INVALID_ARG for axes out of
+ * range, an axis_stride too small, missing positions or pair_axis, or an
+ * entry of pair_axis that is no axis.
+ */
+#define AR_MAX_AXES 4
+int ar_kv_append_axes(const ar_kv_cache* cache, const ar_append_params* p, int axes, size_t axis_stride,
+                      const unsigned char* pair_axis, ar_stream_t stream);
+
+/*
+ * ar_kv_compact -- what follows the verification of drafted tokens: of the
+ * drafted tokens of every sequence (the last n of its lengths[b]) those that
+ * were kept move up behind its context, in every layer's cache at once.
+ * With C = lengths[b] - n:
+ *     token C + j  =  token C + kept[b][j] as it was before,  j < count
+ *     new_lengths[b] = C + count
+ * where count is the number of entries up to the first that is not above the
+ * one before it (-1 before the first) and below n: kept drafts are named in
+ * ascending order, and -1 ends the list.  The tokens behind C + count - 1
+ * are left as the moves left them.
+ *   cache        shape, dtype and strides that all layers share, the page
+ *                table and the lengths, drafted tokens included; its k, v and
+ *                scales are not read
+ *   k, v         host arrays of `layers` (1 .. AR_MAX_LAYERS) device pointers:
+ *                each layer's pages of keys and of values
+ *   kept         device [batch, most_kept], rows kept_stride apart
+ *   seq_start    device [batch + 1]: n = seq_start[b + 1] - seq_start[b], as
+ *                ar_kv_append took the tokens; or NULL: n = drafted
+ *   new_lengths  device [batch]; shares no element with lengths, kept,
+ *                seq_start or the page table
+ *   - A sequence with n <= 0 or lengths[b] < n (an idle one of a padded
+ *     batch) keeps its tokens and its length.
+ *   - A token is not moved from or to a place outside the table or on an
+ *     entry that is no page.
+ *   - The drafted tokens' pages belong to one sequence each: where two
+ *     sequences share one, which of them moved last there is not defined.
+ * Everything is read on the device: a captured graph follows it.
+ * batch == 0 launches nothing.
+ * Errors: AR_ERR_INVALID_ARG (NULL or not element-aligned pointer, layers
+ *         < 1, most_kept or drafted < 0, a size or stride that is too small,
+ *         new_lengths over an input), AR_ERR_UNSUPPORTED (dtype, heads or
+ *         head_dim over 1024, more than AR_MAX_LAYERS layers), AR_ERR_CUDA.
+ */
+#define AR_MAX_LAYERS 128
+int ar_kv_compact(const ar_kv_cache* cache, void* const* k, void* const* v, int layers, const int* kept,
+                  size_t kept_stride, int most_kept, const int* seq_start, int drafted, int* new_lengths,
+                  ar_stream_t stream);
+
+/*
+ * ar_kv_copy_pages -- copies pages within every layer's cache: page dst[i]
+ * becomes page src[i], for a sequence that forks (the pages of its context
+ * are shared through the page tables, the page being filled is copied) or a
+ * pool that is put in order.
+ *   cache   shape, dtype and strides that all layers share; its k, v, scales,
+ *           page table and lengths are not read
+ *   k, v    host arrays of `layers` (1 .. AR_MAX_LAYERS) device pointers
+ *   src, dst  device [pairs]
+ *   - A pair that names no page of [0, pages), or the same page twice, moves
+ *     nothing and counts for nothing below.
+ *   - One page may be the source of many pairs.
+ *   - Of several pairs with one destination the last one is made.  A pair
+ *     whose source is another pair's destination is left out, so that no
+ *     result depends on the order of copies.
+ * pairs == 0 launches nothing.
+ * Errors: AR_ERR_INVALID_ARG (NULL or not element-aligned pointer, layers
+ *         < 1, pairs < 0, a size or stride that is too small),
+ *         AR_ERR_UNSUPPORTED (dtype, heads or head_dim over 1024, more than
+ *         AR_MAX_LAYERS layers), AR_ERR_CUDA.
+ */
+int ar_kv_copy_pages(const ar_kv_cache* cache, void* const* k, void* const* v, int layers, const int* src,
+                     const int* dst, int pairs, ar_stream_t stream);
+
 /* Bytes of device workspace that ar_paged_attention needs with this cache
  * (its sizes and dtype are read, no pointer is) and q_heads query heads,
  * whatever the lengths; a multiple of 256.  0 for arguments that the call
@@ -748,10 +831,80 @@ int ar_paged_attention(const ar_kv_cache* cache, const void* q, size_t q_stride,
                        int window, float softcap, void* out, float* lse, void* workspace,
                        size_t workspace_bytes, int dtype, ar_stream_t stream);
 
+/* The drafted tokens of ar_tree_attention. */
+typedef struct {
+    const void* q;          /* device [tokens, q_heads, head_dim], a token's rows side by side */
+    int tokens;
+    int q_heads;            /* 1 .. 1024, a multiple of kv_heads */
+    int dtype;              /* ar_dtype of q and out */
+    size_t q_stride;        /* elements from one token of q to the next */
+    const int* seq_start;   /* device [batch + 1], ascending, as in ar_append_params; NULL: tokens is a
+                               multiple of batch and every sequence has tokens / batch rows */
+    const uint64_t* mask;   /* device [tokens, mask_words], or NULL */
+    int mask_words;         /* 1 .. 1024 with a mask */
+    float scale;            /* finite; limits as in ar_paged_attention */
+    int window;             /* >= 0, 0 for none */
+    float softcap;          /* finite, >= 0, 0 for none */
+    void* out;              /* device [tokens, q_heads, head_dim], dense */
+    float* lse;             /* device [tokens, q_heads], or NULL */
+} ar_tree_params;
+
+/* Bytes of device workspace that ar_tree_attention needs with this cache (its
+ * sizes and dtype are read, no pointer is), q_heads query heads and `tokens`
+ * rows, whatever the lengths; a multiple of 256.  0 for arguments that the
+ * call refuses. */
+size_t ar_tree_attention_workspace_size(const ar_kv_cache* cache, int q_heads, int tokens);
+
+/*
+ * ar_tree_attention -- attention of several new tokens of every sequence, a
+ * tree of drafted tokens or a chain of them, over the sequence's cached
+ * tokens.  The n rows seq_start[b] .. seq_start[b + 1] - 1 are the last n of
+ * the lengths[b] tokens of sequence b, whose keys and values ar_kv_append has
+ * put into the cache; the C = lengths[b] - n tokens before them are their
+ * context.  Row i of a sequence sees its whole context and, of the drafted
+ * tokens,
+ *     with a mask     token j where bit j % 64 of word j / 64 of the row's mask is set (a
+ *                     tree: the row's ancestors and itself); tokens beyond the mask's words
+ *                     are not seen, bits from n on count for nothing
+ *     without one     the tokens 0 .. i: a chain, or a chunk of a prompt
+ * and with window > 0 the last `window` of all of these, in the order of the
+ * cache: along a tree's path the tokens less than `window` back.  Over the
+ * tokens that a row sees, without those outside the table or on entries that
+ * are no page,
+ *     s_j = scale * k_scale * q . k_j   (softcap > 0: softcap * tanh(s_j / softcap))
+ *     out = v_scale * sum_j e^(s_j - m) v_j / sum_j e^(s_j - m),  m = max_j s_j
+ *     lse = m + ln sum_j e^(s_j - m)
+ * as in ar_paged_attention, which gives the same for n = 1 up to rounding.  A
+ * row that sees nothing has out 0 and lse -infinity.  Cached values that a
+ * row does not see are never read into its result, whatever they hold.
+ *   - Rows of q before seq_start[0] or from seq_start[batch] on are padding:
+ *     their rows of out and lse are left as they were.
+ *   - lengths[b] < n (an idle sequence) leaves no context, and of the drafted
+ *     tokens those that the cache has: index C + j from 0 on.
+ *   - Lengths outside [0, max_pages * page_size] are as in ar_kv_append:
+ *     tokens from the table's end on are not in the cache.
+ * One pass over the cache for each 16 to 256 rows of a key-value head, split
+ * evenly over the SMs as in ar_paged_attention.  Statistics and sums are
+ * fp32, weights keep 16 bits or more.  Results repeat bit for bit for the same
+ * inputs; a sequence's rounding may depend on the other sequences.
+ *   workspace  device, 16-byte aligned, of at least
+ *              ar_tree_attention_workspace_size(cache, q_heads, tokens) bytes;
+ *              its content does not matter.  Calls that may run at the same
+ *              time (two graphs among them) need separate ones.
+ * Alignment and head_dim as in ar_paged_attention; tokens * q_heads / kv_heads
+ * < 2^31 - 255.  tokens == 0 or batch == 0 launches nothing.
+ * Errors: AR_ERR_INVALID_ARG (NULL or not element-aligned pointer, bad size,
+ *         tokens no multiple of batch without seq_start, scale, window, softcap or
+ *         mask_words out of range), AR_ERR_UNSUPPORTED (dtypes, alignment, head_dim over 256),
+ *         AR_ERR_WORKSPACE (missing, misaligned or too small), AR_ERR_CUDA.
+ */
+int ar_tree_attention(const ar_kv_cache* cache, const ar_tree_params* p, void* workspace, size_t workspace_bytes,
+                      ar_stream_t stream);
+
 /*
  * ar_attention_join -- reduces R partial attentions of the same queries over
  * disjoint parts of their keys (the R ranks' parts of the cache, each from
- * ar_paged_attention) to the attention over all of them:
+ * ar_paged_attention or ar_tree_attention) to the attention over all of them:
  *     M = max_r lse_r,   out = sum_r e^(lse_r - M) partial_r / sum_r e^(lse_r - M),
  *     lse_out = M + ln sum_r e^(lse_r - M)
  * in fp32, in rank order.  A part with lse_r = -infinity counts nothing,

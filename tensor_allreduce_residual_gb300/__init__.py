@@ -39,6 +39,7 @@ AR_MAX_RANKS = 16
 AR_CONFIG_USE_MEMCPY, AR_CONFIG_RESIDUAL_RMS_NORM = 1, 2
 AR_NOALLOC_SCRATCH_BYTES = 1 << 20
 AR_IPC_HANDLE_BYTES = 64
+AR_MAX_AXES, AR_MAX_LAYERS = 4, 128
 
 STRATEGIES = {"NCCL": AR_NCCL, "ONESHOT": AR_ONESHOT, "TWOSHOT": AR_TWOSHOT, "AUTO": AR_AUTO}
 STRATEGY_NAMES = {v: k for k, v in STRATEGIES.items()}
@@ -125,6 +126,25 @@ class ArAppendParams(ctypes.Structure):
     ]
 
 
+class ArTreeParams(ctypes.Structure):
+    """Mirror of the C struct ar_tree_params."""
+    _fields_ = [
+        ("q", ctypes.c_void_p),
+        ("tokens", ctypes.c_int),
+        ("q_heads", ctypes.c_int),
+        ("dtype", ctypes.c_int),
+        ("q_stride", ctypes.c_size_t),
+        ("seq_start", ctypes.c_void_p),
+        ("mask", ctypes.c_void_p),
+        ("mask_words", ctypes.c_int),
+        ("scale", ctypes.c_float),
+        ("window", ctypes.c_int),
+        ("softcap", ctypes.c_float),
+        ("out", ctypes.c_void_p),
+        ("lse", ctypes.c_void_p),
+    ]
+
+
 # ar_kernel codes and the kernel names they stand for
 KERNEL_NAMES = {1: "k_fused_oneshot", 2: "k_fused_oneshot", 3: "k_fused_oneshot_persist",
                 4: "k_fused_oneshot_tma", 5: "k_twoshot_phase1+k_twoshot_phase2", 6: "k_fused_oneshot_cluster"}
@@ -194,6 +214,13 @@ def lib() -> ctypes.CDLL:
     L.ar_paged_attention.argtypes = [pkv, vp, sz, i, ctypes.c_float, i, ctypes.c_float, vp, vp, vp, sz, i, vp]
     L.ar_paged_attention.restype = i
     L.ar_attention_join.argtypes, L.ar_attention_join.restype = [pvp, pvp, i, i, i, vp, vp, i, vp], i
+    pl = ctypes.POINTER(vp)
+    L.ar_kv_append_axes.argtypes = [pkv, ctypes.POINTER(ArAppendParams), i, sz, ctypes.c_char_p, vp]
+    L.ar_kv_append_axes.restype = i
+    L.ar_kv_compact.argtypes, L.ar_kv_compact.restype = [pkv, pl, pl, i, vp, sz, i, vp, i, vp, vp], i
+    L.ar_kv_copy_pages.argtypes, L.ar_kv_copy_pages.restype = [pkv, pl, pl, i, vp, vp, i, vp], i
+    L.ar_tree_attention_workspace_size.argtypes, L.ar_tree_attention_workspace_size.restype = [pkv, i, i], sz
+    L.ar_tree_attention.argtypes, L.ar_tree_attention.restype = [pkv, ctypes.POINTER(ArTreeParams), vp, sz, vp], i
     if hasattr(L, "ar_comm_create_local"):   # the test build only
         L.ar_comm_create_local.argtypes = [i, i, pvp, sz, sz, ctypes.POINTER(vp)]
         L.ar_comm_create_local.restype = i
@@ -576,7 +603,8 @@ def _bound_calls():
     binding = importlib.util.module_from_spec(spec)
     spec.loader.exec_module(binding)
     binding.bind(ARError, *(ctypes.cast(f, ctypes.c_void_p).value for f in (
-        L.ar_kv_append, L.ar_paged_attention_workspace_size, L.ar_paged_attention, L.ar_attention_join)))
+        L.ar_kv_append, L.ar_paged_attention_workspace_size, L.ar_paged_attention, L.ar_attention_join, L.ar_kv_append_axes,
+        L.ar_kv_compact, L.ar_kv_copy_pages, L.ar_tree_attention_workspace_size, L.ar_tree_attention)))
     _calls = binding
     return _calls
 
@@ -586,16 +614,63 @@ def ar_kv_append(k_pages: torch.Tensor, v_pages: torch.Tensor, page_table: torch
                  q_out: Optional[torch.Tensor] = None, seq_start: Optional[torch.Tensor] = None,
                  positions: Optional[torch.Tensor] = None, inv_freq: Optional[torch.Tensor] = None,
                  interleaved: bool = False, rotary_scale: float = 1.0, layout: str = "NHD", k_scale: float = 1.0,
-                 v_scale: float = 1.0, stream=None) -> Optional[torch.Tensor]:
+                 v_scale: float = 1.0, stream=None, pair_axis: Optional[Sequence[int]] = None) -> Optional[torch.Tensor]:
     """Appends k and v ([tokens, kv_heads, head_dim]) to the cache, keys rotated, and returns q rotated (None without q).
 
     ``lengths`` counts each sequence's tokens with the new ones.  Rows seq_start[b] .. seq_start[b + 1] - 1 are
     sequence b's newest; without seq_start row b is sequence b's one new token.  ``inv_freq`` (float32) holds the
     rotation's angle per position for each pair of elements; None rotates nothing.  q_out may be q.
+    ``pair_axis`` gives each pair's axis where positions have several (time, height, width): ``positions`` is then
+    [axes, tokens], and the call ar_kv_append_axes.
     """
     return (_calls or _bound_calls()).kv_append(
         k_pages, v_pages, page_table, lengths, k, v, q, q_out, seq_start, positions, inv_freq, interleaved, rotary_scale, layout,
-        k_scale, v_scale, None if stream is None else _stream_handle(stream))
+        k_scale, v_scale, None if stream is None else _stream_handle(stream), pair_axis)
+
+
+def ar_kv_compact(k_pages, v_pages, page_table: torch.Tensor, lengths: torch.Tensor, kept: torch.Tensor,
+                  seq_start: Optional[torch.Tensor] = None, drafted: Optional[int] = None, layout: str = "NHD",
+                  new_lengths: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Moves the drafted tokens that were kept up behind their sequences' contexts; returns the new lengths.
+
+    ``k_pages`` and ``v_pages`` are one layer's pages, or a sequence of all layers'.  ``lengths`` counts the drafted
+    tokens, which are each sequence's last: ``drafted`` of them, or seq_start[b + 1] - seq_start[b].  ``kept`` (int32
+    [batch, most kept]) names a sequence's kept drafts in ascending order and ends with -1 where they are fewer.
+    """
+    return (_calls or _bound_calls()).kv_compact(k_pages, v_pages, page_table, lengths, kept, seq_start, drafted, layout,
+                                                 new_lengths, None if stream is None else _stream_handle(stream))
+
+
+def ar_kv_copy_pages(k_pages, v_pages, src: torch.Tensor, dst: torch.Tensor, stream=None) -> None:
+    """Copies pages src (int32) to pages dst, in one layer's pages or in a sequence of all layers'.
+
+    Of pairs with one destination the last is made; a pair whose source is another's destination is left out.
+    """
+    (_calls or _bound_calls()).kv_copy_pages(k_pages, v_pages, src, dst, None if stream is None else _stream_handle(stream))
+
+
+def ar_tree_attention_workspace_size(k_pages: torch.Tensor, v_pages: torch.Tensor, page_table: torch.Tensor,
+                                     lengths: torch.Tensor, q_heads: int, tokens: int, layout: str = "NHD") -> int:
+    """Bytes of workspace ar_tree_attention needs with this cache (0 where it refuses it)."""
+    return (_calls or _bound_calls()).tree_attention_workspace_size(k_pages, v_pages, page_table, lengths, q_heads, tokens, layout)
+
+
+def ar_tree_attention(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, page_table: torch.Tensor,
+                      lengths: torch.Tensor, mask: Optional[torch.Tensor] = None, seq_start: Optional[torch.Tensor] = None,
+                      scale: Optional[float] = None, window: int = 0, softcap: float = 0.0, layout: str = "NHD",
+                      k_scale: float = 1.0, v_scale: float = 1.0, out: Optional[torch.Tensor] = None,
+                      lse: Optional[torch.Tensor] = None, return_lse: bool = False,
+                      workspace: Optional[torch.Tensor] = None, stream=None):
+    """Attention of each sequence's newest tokens, q ([tokens, q_heads, head_dim]), over its cached tokens, theirs among them.
+
+    Rows seq_start[b] .. seq_start[b + 1] - 1 are sequence b's; without seq_start each has tokens / batch.  Bit j of a row's
+    ``mask`` (int64 [tokens, words], 64 tokens a word) says whether it sees the j-th new token of its sequence: a drafted
+    tree's ancestors and itself.  Without a mask a row sees the new tokens up to its own.  All see the tokens before.
+    Returns out, or (out, lse) when ``lse`` is given or ``return_lse``.
+    """
+    return (_calls or _bound_calls()).tree_attention(
+        q, k_pages, v_pages, page_table, lengths, mask, seq_start, scale, window, softcap, layout, k_scale, v_scale, out, lse,
+        return_lse, workspace, None if stream is None else _stream_handle(stream))
 
 
 def ar_paged_attention_workspace_size(k_pages: torch.Tensor, v_pages: torch.Tensor, page_table: torch.Tensor,

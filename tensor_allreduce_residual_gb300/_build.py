@@ -40,9 +40,11 @@ TEST_LIB = os.path.join(PKG, "libar_test.so")
 BINDING_SOURCE = os.path.join(CSRC, "ar_binding.cpp")
 
 SOURCES = ["ar_api.cu", "ar_kern_f32.cu", "ar_kern_f16.cu", "ar_kern_bf16.cu", "ar_noalloc.cu", "ar_host.cu",
-           "ar_peer.cu", "ar_cache_api.cu", "ar_append.cu", "ar_attn_f32.cu", "ar_attn_f16.cu", "ar_attn_bf16.cu"]
+           "ar_peer.cu", "ar_cache_api.cu", "ar_append.cu", "ar_pages.cu", "ar_attn_f32.cu", "ar_attn_f16.cu", "ar_attn_bf16.cu",
+           "ar_tree_f32.cu", "ar_tree_f16.cu", "ar_tree_bf16.cu"]
 HEADERS = ["ar_internal.h", "ar_kernels.cuh", "ar_tma.cuh", "ar_lamport.cuh", "ar_launch.cuh", "ar_launch_k.cuh",
-           "ar_auto_table.h", "ar_cache.h", "ar_split.h", "ar_attn.cuh"]
+           "ar_auto_table.h", "ar_cache.h", "ar_split.h", "ar_attn.cuh", "ar_tree.h", "ar_tree.cuh",
+           "ar_tcgen05.cuh", "ar_tree_mma.cuh"]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
@@ -155,8 +157,8 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
     if not made:
         if os.path.exists(binding_path()):
             os.remove(binding_path())
-        warnings.warn("the extension module could not be compiled: ar_kv_append, ar_paged_attention and ar_attention_join "
-                      "are not available from Python")
+        warnings.warn("the extension module could not be compiled: ar_kv_append, ar_kv_compact, ar_kv_copy_pages, "
+                      "ar_paged_attention, ar_tree_attention and ar_attention_join are not available from Python")
     return LIB
 
 

@@ -15,6 +15,7 @@
 #include "ar.h"
 #include "ar_auto_table.h"
 #include "ar_internal.h"
+#include "ar_tree.h"
 
 namespace {
 
@@ -846,6 +847,13 @@ int ar_device_status(void)
     if (ep != cudaSuccess)
         e = ep;
     total += np;
+    for (const auto take : {&ar::take_tree_wait_timeouts<__half>, &ar::take_tree_wait_timeouts<__nv_bfloat16>}) {
+        unsigned int n = 0;
+        const cudaError_t et = take(&n);
+        if (et != cudaSuccess)
+            e = et;
+        total += n;
+    }
     if (e != cudaSuccess)
         return AR_ERR_CUDA;
     return total != 0 ? AR_ERR_TIMEOUT : AR_OK;

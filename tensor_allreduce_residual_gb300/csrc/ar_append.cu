@@ -5,6 +5,7 @@
 
 #include <algorithm>
 #include <climits>
+#include <type_traits>
 
 #include "ar_cache.h"
 #include "ar_kernels.cuh"
@@ -138,14 +139,18 @@ __device__ __forceinline__ int turn_place(int j, int half, int group_log)
 // them and took 66 to 94 us for the same prompts; hence one unit at a time and
 // eight blocks an SM, for whose 32 registers the 16-bit vector kernels spill 24
 // to 28 bytes a thread.
+// A kernel of its own (Args) takes positions on several axes: a row then has a
+// position for each, and a pair's axis, two bits of the arguments, chooses.
+// Only the table's filling differs.
 // ---------------------------------------------------------------------------
-template <typename T, typename CT, bool VEC>
+template <typename T, typename CT, bool VEC, typename Args>
 __global__ void __launch_bounds__(kAppendThreads, 8)
-k_kv_append(const AppendArgs a)
+k_kv_append(const Args a)
 {
+    constexpr bool AXES = std::is_same<Args, AxesAppendArgs>::value;
     extern __shared__ __align__(16) float2 s_turn[];  // [rows][half], by turn_place
     __shared__ int s_seq[kAppendMaxTokens];
-    __shared__ int s_pos[kAppendMaxTokens];
+    __shared__ int s_pos[kAppendMaxTokens * (AXES ? kMaxAxes : 1)];
     __shared__ int64_t s_dst[kAppendMaxTokens];  // element offset in the cache, -1: not cached
     pdl_enter();
     constexpr int L = Part<T, VEC>::L;
@@ -186,7 +191,12 @@ k_kv_append(const AppendArgs a)
             }
         }
         s_seq[tid] = b < a.batch ? b : -1;
-        s_pos[tid] = a.positions != nullptr ? a.positions[t] : static_cast<int>(p);
+        if constexpr (AXES) {
+            for (int x = 0; x < a.axes; ++x)
+                s_pos[tid * kMaxAxes + x] = a.positions[x * a.axis_stride + t];
+        } else {
+            s_pos[tid] = a.positions != nullptr ? a.positions[t] : static_cast<int>(p);
+        }
         s_dst[tid] = dst;
     }
     __syncthreads();
@@ -201,7 +211,12 @@ k_kv_append(const AppendArgs a)
     const int group_log = VEC && L == 8 ? (a.interleaved ? 2 : 3) : 0;
     for (int x = tid; x < rows * a.half; x += kAppendThreads) {
         const int row = row_of(x, a.half, a.turn_magic), j = x - row * a.half;
-        s_turn[row * a.half + turn_place(j, a.half, group_log)] = cos_sin(turn_fraction(a.inv_freq[j]), s_pos[row], a.rotary_scale);
+        int position;
+        if constexpr (AXES)
+            position = s_pos[row * kMaxAxes + (a.pair_axis[j >> 4] >> (2 * (j & 15)) & 3)];
+        else
+            position = s_pos[row];
+        s_turn[row * a.half + turn_place(j, a.half, group_log)] = cos_sin(turn_fraction(a.inv_freq[j]), position, a.rotary_scale);
     }
     __syncthreads();
 
@@ -285,10 +300,10 @@ k_kv_append(const AppendArgs a)
 constexpr int kAppendBytes = 32 * 1024;
 constexpr int kAppendBlocks = 152 * 8;
 
-template <typename T, typename CT>
-cudaError_t launch_append(const AppendArgs& args, bool vec, cudaStream_t s)
+template <typename T, typename CT, typename Args>
+cudaError_t launch_append(const Args& args, bool vec, cudaStream_t s)
 {
-    AppendArgs a = args;
+    Args a = args;
     // Few rows: one a block, for latency.  From 1025 on two at least, where that leaves a block under 32 KB: at 8 query heads
     // and one key-value head of 128 bf16 elements 4.3 us either way for 1025 rows, 5.6 against 6.7 for 1500, 10.2 against
     // 13.8 for 4096.  More from 7296 on, as many as leave two blocks for every one that can run: 8192 rows 15.0 us with
@@ -304,15 +319,20 @@ cudaError_t launch_append(const AppendArgs& args, bool vec, cudaStream_t s)
     }
     const unsigned grid = static_cast<unsigned>((a.tokens + a.block_tokens - 1) / a.block_tokens);
     const size_t smem = static_cast<size_t>(a.block_tokens) * a.half * sizeof(float2);
-    return vec ? launch_k(k_kv_append<T, CT, true>, dim3(grid), dim3(kAppendThreads), smem, s, a)
-               : launch_k(k_kv_append<T, CT, false>, dim3(grid), dim3(kAppendThreads), smem, s, a);
+    return vec ? launch_k(k_kv_append<T, CT, true, Args>, dim3(grid), dim3(kAppendThreads), smem, s, a)
+               : launch_k(k_kv_append<T, CT, false, Args>, dim3(grid), dim3(kAppendThreads), smem, s, a);
 }
 
 template cudaError_t launch_append<float, float>(const AppendArgs&, bool, cudaStream_t);
+template cudaError_t launch_append<float, float>(const AxesAppendArgs&, bool, cudaStream_t);
 template cudaError_t launch_append<__half, __half>(const AppendArgs&, bool, cudaStream_t);
+template cudaError_t launch_append<__half, __half>(const AxesAppendArgs&, bool, cudaStream_t);
 template cudaError_t launch_append<__half, __nv_fp8_e4m3>(const AppendArgs&, bool, cudaStream_t);
+template cudaError_t launch_append<__half, __nv_fp8_e4m3>(const AxesAppendArgs&, bool, cudaStream_t);
 template cudaError_t launch_append<__nv_bfloat16, __nv_bfloat16>(const AppendArgs&, bool, cudaStream_t);
+template cudaError_t launch_append<__nv_bfloat16, __nv_bfloat16>(const AxesAppendArgs&, bool, cudaStream_t);
 template cudaError_t launch_append<__nv_bfloat16, __nv_fp8_e4m3>(const AppendArgs&, bool, cudaStream_t);
+template cudaError_t launch_append<__nv_bfloat16, __nv_fp8_e4m3>(const AxesAppendArgs&, bool, cudaStream_t);
 
 // ---------------------------------------------------------------------------
 // The join of R partial attentions: a weighted R-way sum, bound by HBM like

@@ -30,6 +30,11 @@ decltype(&ar_kv_append) g_append = nullptr;
 decltype(&ar_paged_attention_workspace_size) g_workspace_size = nullptr;
 decltype(&ar_paged_attention) g_attention = nullptr;
 decltype(&ar_attention_join) g_join = nullptr;
+decltype(&ar_kv_append_axes) g_append_axes = nullptr;
+decltype(&ar_kv_compact) g_compact = nullptr;
+decltype(&ar_kv_copy_pages) g_copy_pages = nullptr;
+decltype(&ar_tree_attention_workspace_size) g_tree_workspace_size = nullptr;
+decltype(&ar_tree_attention) g_tree = nullptr;
 PyObject* g_error = nullptr;  // ARError
 
 // Thrown with a Python exception set.
@@ -189,20 +194,19 @@ size_t row_stride(const Tensor& t, const char* what, int64_t rows, int64_t heads
     return static_cast<size_t>(t.stride(0));
 }
 
-// The cache's tensors, checked, and their device.
-int fill_cache(ar_kv_cache* c, PyObject* k_pages, PyObject* v_pages, PyObject* page_table, PyObject* lengths, PyObject* layout,
-               float k_scale, float v_scale)
+// Which dimension of the pages counts tokens.
+int token_dim(PyObject* layout)
 {
-    const Tensor& k = tensor(k_pages, "k_pages");
-    const Tensor& v = tensor(v_pages, "v_pages");
-    const Tensor& table = tensor(page_table, "page_table");
-    int tokens = 0;
     if (PyUnicode_Check(layout) && PyUnicode_CompareWithASCIIString(layout, "NHD") == 0)
-        tokens = 1;
-    else if (PyUnicode_Check(layout) && PyUnicode_CompareWithASCIIString(layout, "HND") == 0)
-        tokens = 2;
-    else
-        bad("layout must be 'NHD' ([pages, page_size, kv_heads, head_dim]) or 'HND' ([pages, kv_heads, page_size, head_dim])");
+        return 1;
+    if (PyUnicode_Check(layout) && PyUnicode_CompareWithASCIIString(layout, "HND") == 0)
+        return 2;
+    bad("layout must be 'NHD' ([pages, page_size, kv_heads, head_dim]) or 'HND' ([pages, kv_heads, page_size, head_dim])");
+}
+
+// The pages' tensors, checked, and their device.
+int fill_pages(ar_kv_cache* c, const Tensor& k, const Tensor& v, int tokens)
+{
     const int heads = 3 - tokens, dev = cuda_index(k);
     if (dev < 0 || dev != c10::cuda::current_device())
         bad("k_pages must be a CUDA tensor of the current device");
@@ -212,11 +216,6 @@ int fill_cache(ar_kv_cache* c, PyObject* k_pages, PyObject* v_pages, PyObject* p
     const at::ScalarType type = k.scalar_type();
     if (type != at::kFloat && type != at::kHalf && type != at::kBFloat16 && type != at::kFloat8_e4m3fn)
         bad(std::string("unsupported cache dtype ") + c10::toString(type) + "; expected float32, float16, bfloat16 or float8_e4m3fn");
-    if (table.dim() != 2 || table.scalar_type() != at::kInt || cuda_index(table) != dev || (table.stride(1) != 1 && table.size(1) > 1))
-        bad("page_table must be an int32 [batch, pages of a sequence] tensor with dense rows" + on(dev));
-    const int64_t batch = table.size(0), columns = table.size(1), stride = batch > 1 ? table.stride(0) : columns;
-    if (stride < columns)
-        bad("page_table's rows must not overlap");
     c->k = k.data_ptr();
     c->v = v.data_ptr();
     c->dtype = type == at::kFloat8_e4m3fn ? AR_FP8_E4M3 : dtype_code(type);
@@ -227,8 +226,18 @@ int fill_cache(ar_kv_cache* c, PyObject* k_pages, PyObject* v_pages, PyObject* p
     c->page_stride = static_cast<size_t>(k.stride(0));
     c->token_stride = static_cast<size_t>(k.stride(tokens));
     c->head_stride = static_cast<size_t>(k.stride(heads));
-    c->k_scale = k_scale;
-    c->v_scale = v_scale;
+    return dev;
+}
+
+// The page table and the lengths.
+void fill_table(ar_kv_cache* c, PyObject* page_table, PyObject* lengths, int dev)
+{
+    const Tensor& table = tensor(page_table, "page_table");
+    if (table.dim() != 2 || table.scalar_type() != at::kInt || cuda_index(table) != dev || (table.stride(1) != 1 && table.size(1) > 1))
+        bad("page_table must be an int32 [batch, pages of a sequence] tensor with dense rows" + on(dev));
+    const int64_t batch = table.size(0), columns = table.size(1), stride = batch > 1 ? table.stride(0) : columns;
+    if (stride < columns)
+        bad("page_table's rows must not overlap");
     c->page_table = static_cast<const int*>(table.data_ptr());
     c->batch = size32(batch, "page_table");
     c->max_pages = size32(columns, "page_table");
@@ -236,11 +245,68 @@ int fill_cache(ar_kv_cache* c, PyObject* k_pages, PyObject* v_pages, PyObject* p
     if (!given(lengths))
         bad("lengths must be given");
     c->lengths = ints(lengths, "lengths", batch, dev);
+}
+
+// The cache's tensors, checked, and their device.
+int fill_cache(ar_kv_cache* c, PyObject* k_pages, PyObject* v_pages, PyObject* page_table, PyObject* lengths, PyObject* layout,
+               float k_scale, float v_scale)
+{
+    const int tokens = token_dim(layout);
+    const int dev = fill_pages(c, tensor(k_pages, "k_pages"), tensor(v_pages, "v_pages"), tokens);
+    fill_table(c, page_table, lengths, dev);
+    c->k_scale = k_scale;
+    c->v_scale = v_scale;
     return dev;
 }
 
+// A list or tuple of objects.
+struct Items {
+    PyObject* fast;
+    Py_ssize_t n;
+    Items(PyObject* o, const char* what) : fast(PySequence_Fast(o, what))
+    {
+        if (fast == nullptr)
+            throw Raised();
+        n = PySequence_Fast_GET_SIZE(fast);
+    }
+    ~Items() { Py_DECREF(fast); }
+    Items(const Items&) = delete;
+    PyObject* operator[](Py_ssize_t i) const { return PySequence_Fast_GET_ITEM(fast, i); }
+};
+
+// The pages of several layers, one tensor or a sequence of them each, of one shape.
+struct LayerPages {
+    void* k[AR_MAX_LAYERS];
+    void* v[AR_MAX_LAYERS];
+    int n, dev;
+    LayerPages(ar_kv_cache* c, PyObject* k_pages, PyObject* v_pages, int tokens)
+    {
+        if (THPVariable_Check(k_pages) && THPVariable_Check(v_pages)) {
+            n = 1;
+            dev = fill_pages(c, THPVariable_Unpack(k_pages), THPVariable_Unpack(v_pages), tokens);
+            k[0] = c->k;
+            v[0] = c->v;
+            return;
+        }
+        const Items ks(k_pages, "k_pages must be a tensor or a sequence of tensors"), vs(v_pages, "v_pages must be a tensor or a sequence of tensors");
+        if (ks.n < 1 || ks.n != vs.n || ks.n > AR_MAX_LAYERS)
+            bad("k_pages and v_pages must name the same layers, 1 to " + std::to_string(AR_MAX_LAYERS));
+        n = static_cast<int>(ks.n);
+        for (int i = 0; i < n; ++i) {
+            const Tensor& x = tensor(ks[i], "k_pages");
+            const Tensor& y = tensor(vs[i], "v_pages");
+            const Tensor& first = tensor(ks[0], "k_pages");
+            if (x.sizes() != first.sizes() || x.strides() != first.strides() || x.scalar_type() != first.scalar_type())
+                bad("all layers' pages must have one shape, dtype and set of strides");
+            dev = fill_pages(c, x, y, tokens);
+            k[i] = c->k;
+            v[i] = c->v;
+        }
+    }
+};
+
 // kv_append(k_pages, v_pages, page_table, lengths, k, v, q, q_out, seq_start, positions, inv_freq, interleaved,
-//           rotary_scale, layout, k_scale, v_scale, stream)
+//           rotary_scale, layout, k_scale, v_scale, stream, pair_axis)
 PyObject* kv_append(PyObject* const* a)
 {
     ar_kv_cache cache;
@@ -278,7 +344,32 @@ PyObject* kv_append(PyObject* const* a)
         bad("q_out is given without q");
     }
     p.seq_start = ints(a[8], "seq_start", static_cast<int64_t>(cache.batch) + 1, dev);
-    p.positions = ints(a[9], "positions", tokens, dev);
+    unsigned char pair_axis[512];
+    int axes = 0;
+    size_t axis_stride = 0;
+    Py_ssize_t pairs = 0;
+    if (given(a[17])) {
+        const Items axis(a[17], "pair_axis must be a sequence of whole numbers");
+        const Tensor& x = tensor(a[9], "positions");
+        if (x.dim() != 2 || x.size(0) < 1 || x.size(0) > AR_MAX_AXES || x.size(1) != tokens || x.scalar_type() != at::kInt || cuda_index(x) != dev ||
+            (x.stride(1) != 1 && tokens > 1) || (x.size(0) > 1 && x.stride(0) < tokens))
+            bad("positions must be an int32 [axes, " + std::to_string(tokens) + "] tensor with dense rows, 1 to " + std::to_string(AR_MAX_AXES) +
+                " of them" + on(dev));
+        axes = static_cast<int>(x.size(0));
+        axis_stride = static_cast<size_t>(x.stride(0));
+        p.positions = static_cast<const int*>(x.data_ptr());
+        pairs = axis.n;
+        if (pairs > 512)
+            bad("pair_axis must have one entry for each element of inv_freq");
+        for (Py_ssize_t j = 0; j < pairs; ++j) {
+            const long long x = integer(axis[j]);
+            if (x < 0 || x >= axes)
+                bad("pair_axis must hold numbers from 0 to " + std::to_string(axes - 1));
+            pair_axis[j] = static_cast<unsigned char>(x);
+        }
+    } else {
+        p.positions = ints(a[9], "positions", tokens, dev);
+    }
     if (given(a[10])) {
         const Tensor& f = tensor(a[10], "inv_freq");
         if (f.scalar_type() != at::kFloat || cuda_index(f) != dev || !f.is_contiguous() || f.numel() > dim)
@@ -288,7 +379,13 @@ PyObject* kv_append(PyObject* const* a)
     }
     p.interleaved = truth(a[11]);
     p.rotary_scale = static_cast<float>(number(a[12]));
-    check("ar_kv_append", g_append(&cache, &p, s.handle));
+    if (axes > 0) {
+        if (2 * pairs != p.rotary_dim)
+            bad("pair_axis must have one entry for each element of inv_freq");
+        check("ar_kv_append_axes", g_append_axes(&cache, &p, axes, axis_stride, pair_axis, s.handle));
+    } else {
+        check("ar_kv_append", g_append(&cache, &p, s.handle));
+    }
     if (made.defined())
         return THPVariable_Wrap(std::move(made));
     Py_INCREF(result);
@@ -360,20 +457,130 @@ PyObject* paged_attention(PyObject* const* a)
     return both;
 }
 
-// A list or tuple of at most AR_MAX_RANKS objects.
-struct Items {
-    PyObject* fast;
-    Py_ssize_t n;
-    Items(PyObject* o, const char* what) : fast(PySequence_Fast(o, what))
-    {
-        if (fast == nullptr)
-            throw Raised();
-        n = PySequence_Fast_GET_SIZE(fast);
+// kv_compact(k_pages, v_pages, page_table, lengths, kept, seq_start, drafted, layout, new_lengths, stream)
+PyObject* kv_compact(PyObject* const* a)
+{
+    ar_kv_cache cache{};
+    const LayerPages layers(&cache, a[0], a[1], token_dim(a[7]));
+    const int dev = layers.dev;
+    fill_table(&cache, a[2], a[3], dev);
+    const Tensor& kept = tensor(a[4], "kept");
+    if (kept.dim() != 2 || kept.size(0) != cache.batch || kept.scalar_type() != at::kInt || cuda_index(kept) != dev ||
+        (kept.stride(1) != 1 && kept.size(1) > 1) || (cache.batch > 1 && kept.stride(0) < kept.size(1)))
+        bad("kept must be an int32 [batch, kept tokens] tensor with dense rows" + on(dev));
+    const int* seq_start = ints(a[5], "seq_start", static_cast<int64_t>(cache.batch) + 1, dev);
+    if ((seq_start != nullptr) == given(a[6]))
+        bad("either seq_start or drafted must be given");
+    const int drafted = given(a[6]) ? int32(a[6], "drafted") : 0;
+    Stream s(a[9], dev);
+    Tensor out;
+    if (given(a[8])) {
+        out = tensor(a[8], "new_lengths");
+        dense(out, "new_lengths", {cache.batch}, at::kInt, dev);
+    } else {
+        out = empty({cache.batch}, at::kInt, kept);
     }
-    ~Items() { Py_DECREF(fast); }
-    Items(const Items&) = delete;
-    PyObject* operator[](Py_ssize_t i) const { return PySequence_Fast_GET_ITEM(fast, i); }
-};
+    check("ar_kv_compact", g_compact(&cache, layers.k, layers.v, layers.n, static_cast<const int*>(kept.data_ptr()), static_cast<size_t>(kept.stride(0)),
+                                     size32(kept.size(1), "kept"), seq_start, drafted, static_cast<int*>(out.data_ptr()), s.handle));
+    return THPVariable_Wrap(std::move(out));
+}
+
+// kv_copy_pages(k_pages, v_pages, src, dst, stream)
+PyObject* kv_copy_pages(PyObject* const* a)
+{
+    ar_kv_cache cache{};
+    const LayerPages layers(&cache, a[0], a[1], 1);  // whole pages: which dimension counts tokens does not matter
+    const int dev = layers.dev;
+    const Tensor& src = tensor(a[2], "src");
+    const Tensor& dst = tensor(a[3], "dst");
+    if (src.dim() != 1)
+        bad("src must be an int32 [pairs] tensor" + on(dev));
+    dense(src, "src", {src.size(0)}, at::kInt, dev);
+    dense(dst, "dst", {src.size(0)}, at::kInt, dev);
+    Stream s(a[4], dev);
+    check("ar_kv_copy_pages", g_copy_pages(&cache, layers.k, layers.v, layers.n, static_cast<const int*>(src.data_ptr()),
+                                           static_cast<const int*>(dst.data_ptr()), size32(src.size(0), "src"), s.handle));
+    Py_RETURN_NONE;
+}
+
+// tree_attention_workspace_size(k_pages, v_pages, page_table, lengths, q_heads, tokens, layout)
+PyObject* tree_attention_workspace_size(PyObject* const* a)
+{
+    ar_kv_cache cache;
+    fill_cache(&cache, a[0], a[1], a[2], a[3], a[6], 1.0f, 1.0f);
+    return PyLong_FromSize_t(g_tree_workspace_size(&cache, int32(a[4], "q_heads"), int32(a[5], "tokens")));
+}
+
+// tree_attention(q, k_pages, v_pages, page_table, lengths, mask, seq_start, scale, window, softcap, layout, k_scale, v_scale,
+//                out, lse, return_lse, workspace, stream)
+PyObject* tree_attention(PyObject* const* a)
+{
+    ar_kv_cache cache;
+    const int dev = fill_cache(&cache, a[1], a[2], a[3], a[4], a[10], static_cast<float>(number(a[11])), static_cast<float>(number(a[12])));
+    const Tensor& q = tensor(a[0], "q");
+    const at::ScalarType type = q.scalar_type();
+    const int64_t tokens = q.dim() > 0 ? q.size(0) : 0, dim = cache.head_dim;
+    ar_tree_params p{};
+    p.dtype = dtype_code(type);
+    p.tokens = size32(tokens, "q");
+    p.q_stride = row_stride(q, "q", tokens, -1, dim, type, dev);
+    p.q = q.data_ptr();
+    p.q_heads = size32(q.size(1), "q");
+    if (given(a[5])) {
+        const Tensor& mask = tensor(a[5], "mask");
+        if (mask.dim() != 2)
+            bad("mask must be an int64 [" + std::to_string(tokens) + ", words] tensor" + on(dev));
+        dense(mask, "mask", {tokens, mask.size(1)}, at::kLong, dev);
+        p.mask_words = size32(mask.size(1), "mask");
+        if (p.mask_words < 1)
+            bad("mask must have one word of 64 tokens at least");
+        p.mask = static_cast<const uint64_t*>(mask.data_ptr());
+    }
+    p.seq_start = ints(a[6], "seq_start", static_cast<int64_t>(cache.batch) + 1, dev);
+    p.scale = given(a[7]) ? static_cast<float>(number(a[7])) : static_cast<float>(1.0 / std::sqrt(static_cast<double>(dim)));
+    p.window = int32(a[8], "window");
+    p.softcap = static_cast<float>(number(a[9]));
+    Stream s(a[17], dev);
+    Tensor out, lse;
+    Scratch scratch;
+    if (given(a[13])) {
+        out = tensor(a[13], "out");
+        dense(out, "out", {tokens, p.q_heads, dim}, type, dev);
+    } else {
+        out = empty({tokens, p.q_heads, dim}, type, q);
+    }
+    if (given(a[14])) {
+        lse = tensor(a[14], "lse");
+        dense(lse, "lse", {tokens, p.q_heads}, at::kFloat, dev);
+    } else if (truth(a[15])) {
+        lse = empty({tokens, p.q_heads}, at::kFloat, q);
+    }
+    p.out = out.data_ptr();
+    p.lse = lse.defined() ? static_cast<float*>(lse.data_ptr()) : nullptr;
+    void* workspace;
+    size_t bytes;
+    if (given(a[16])) {
+        const Tensor& work = tensor(a[16], "workspace");
+        if (cuda_index(work) != dev || !work.is_contiguous())
+            bad("workspace must be a contiguous tensor" + on(dev));
+        bytes = static_cast<size_t>(work.numel()) * work.element_size();
+        workspace = work.data_ptr();
+    } else {
+        bytes = g_tree_workspace_size(&cache, p.q_heads, p.tokens);
+        if (bytes != 0)
+            scratch.make(bytes);
+        workspace = scratch.p;
+    }
+    check("ar_tree_attention", g_tree(&cache, &p, workspace, bytes, s.handle));
+    if (!lse.defined())
+        return THPVariable_Wrap(std::move(out));
+    PyObject* x = THPVariable_Wrap(std::move(out));
+    PyObject* y = x != nullptr ? THPVariable_Wrap(std::move(lse)) : nullptr;
+    PyObject* both = y != nullptr ? PyTuple_Pack(2, x, y) : nullptr;
+    Py_XDECREF(x);
+    Py_XDECREF(y);
+    return both;
+}
 
 // attention_join(partials, lse, out, lse_out, return_lse, stream)
 PyObject* attention_join(PyObject* const* a)
@@ -429,7 +636,8 @@ PyObject* attention_join(PyObject* const* a)
     return both;
 }
 
-// bind(ARError, address of ar_kv_append, ..._workspace_size, ar_paged_attention, ar_attention_join)
+// bind(ARError, address of ar_kv_append, ar_paged_attention_workspace_size, ar_paged_attention, ar_attention_join,
+//      ar_kv_append_axes, ar_kv_compact, ar_kv_copy_pages, ar_tree_attention_workspace_size, ar_tree_attention)
 PyObject* bind(PyObject* const* a)
 {
     Py_INCREF(a[0]);
@@ -438,6 +646,11 @@ PyObject* bind(PyObject* const* a)
     g_workspace_size = reinterpret_cast<decltype(g_workspace_size)>(integer(a[2]));
     g_attention = reinterpret_cast<decltype(g_attention)>(integer(a[3]));
     g_join = reinterpret_cast<decltype(g_join)>(integer(a[4]));
+    g_append_axes = reinterpret_cast<decltype(g_append_axes)>(integer(a[5]));
+    g_compact = reinterpret_cast<decltype(g_compact)>(integer(a[6]));
+    g_copy_pages = reinterpret_cast<decltype(g_copy_pages)>(integer(a[7]));
+    g_tree_workspace_size = reinterpret_cast<decltype(g_tree_workspace_size)>(integer(a[8]));
+    g_tree = reinterpret_cast<decltype(g_tree)>(integer(a[9]));
     Py_RETURN_NONE;
 }
 
@@ -469,11 +682,15 @@ constexpr PyMethodDef method(const char* name)
 }
 
 PyMethodDef g_methods[] = {
-    method<bind, 5>("bind"),
-    method<kv_append, 17>("kv_append"),
+    method<bind, 10>("bind"),
+    method<kv_append, 18>("kv_append"),
     method<paged_attention_workspace_size, 6>("paged_attention_workspace_size"),
     method<paged_attention, 16>("paged_attention"),
     method<attention_join, 6>("attention_join"),
+    method<kv_compact, 10>("kv_compact"),
+    method<kv_copy_pages, 5>("kv_copy_pages"),
+    method<tree_attention_workspace_size, 7>("tree_attention_workspace_size"),
+    method<tree_attention, 18>("tree_attention"),
     {nullptr, nullptr, 0, nullptr},
 };
 

@@ -38,13 +38,61 @@ struct AppendArgs {
     uint64_t head_magic, v_magic;  // ceil(2^32 / units): u / units == u * magic >> 32 for u * units < 2^32
 };
 
+// Positions on several axes: positions holds `axes` rows of tokens, axis_stride apart, and pair j turns by that of axis
+// pair_axis[j / 16] >> 2 (j % 16) & 3.
+constexpr int kMaxAxes = 4;
+constexpr int kMaxPairs = 512;
+struct AxesAppendArgs : AppendArgs {
+    uint64_t axis_stride;
+    int axes;
+    uint32_t pair_axis[kMaxPairs / 16];
+};
+
 // Rows a block of the append kernel may take, and its threads.
 constexpr int kAppendMaxTokens = 8;
 constexpr int kAppendThreads = 256;
 
 // One unit is a 16-byte vector of T (vec) or one element, a pair of them where the pair's halves lie apart.
-template <typename T, typename CT>
-cudaError_t launch_append(const AppendArgs& a, bool vec, cudaStream_t s);
+template <typename T, typename CT, typename Args>
+cudaError_t launch_append(const Args& a, bool vec, cudaStream_t s);
+
+// The layers of one model whose caches have the same shape, dtype and strides.
+constexpr int kMaxLayers = 128;
+struct Layers {
+    char* k[kMaxLayers];
+    char* v[kMaxLayers];
+};
+
+// A page's (copying) or a token's (compacting) units of 1 to 16 bytes: `inner` units side by side, `mid` of these
+// mid_stride bytes apart, as often as needed outer_stride bytes apart.
+struct CopyArgs {
+    Layers to;
+    const int* src;
+    const int* dst;
+    int pairs, pages;
+    uint32_t units;           // of a page
+    uint32_t inner, mid;
+    uint64_t page_stride, mid_stride, outer_stride;
+    uint32_t segments;        // blocks of a page
+};
+struct CompactArgs {
+    Layers to;
+    const int* table;
+    const int* lengths;
+    const int* seq_start;     // nullable: `drafted` tokens of each sequence
+    const int* kept;
+    int* new_lengths;
+    uint64_t kept_stride;
+    uint64_t page_stride, token_stride, head_stride;
+    uint64_t capacity;
+    int drafted, most_kept, batch, pages, page_size, table_stride;
+    uint32_t inner;           // units of one head of a token
+    uint32_t head_units;      // units of all heads of a token in one layer's keys
+    uint32_t units;           // of a token in all layers, keys and values
+};
+// unit: 1, 2, 4, 8 or 16 bytes, that pointers and strides are multiples of.
+cudaError_t launch_copy_pages(const CopyArgs& a, int layers, int unit, cudaStream_t s);
+cudaError_t launch_compact(const CompactArgs& a, int unit, cudaStream_t s);
 
 // Strides of the cache in bytes.
 struct AttnArgs {

@@ -7,9 +7,11 @@
 #include <climits>
 #include <cmath>
 #include <cstdint>
+#include <initializer_list>
 
 #include "ar.h"
 #include "ar_cache.h"
+#include "ar_tree.h"
 
 namespace {
 
@@ -38,19 +40,43 @@ ar_kv_cache without_idle_strides(const ar_kv_cache* cache)
     return c;
 }
 
+// Sizes and strides of the pages (all zeros for a NULL cache); no pointer is looked at.
+bool page_sizes_ok(const ar_kv_cache* c)
+{
+    return c->pages >= 1 && c->page_size >= 1 && c->kv_heads >= 1 && c->head_dim >= 1;
+}
+bool table_ok(const ar_kv_cache* c) { return c->batch >= 0 && c->max_pages >= 1 && c->table_stride >= c->max_pages; }
+bool page_limits_ok(const ar_kv_cache* c)
+{
+    return cache_esize_of(c->dtype) != 0 && c->kv_heads <= kMaxHeads && c->head_dim <= kMaxHeadDim;
+}
+bool page_strides_ok(const ar_kv_cache* c)
+{
+    const size_t d = static_cast<size_t>(c->head_dim);
+    return (c->pages == 1 || c->page_stride >= d) && (c->page_size == 1 || c->token_stride >= d) &&
+           (c->kv_heads == 1 || c->head_stride >= d);
+}
+
 // Sizes, strides and dtype of the cache (all zeros for a NULL one); no pointer is looked at.
 int check_sizes(const ar_kv_cache* c)
 {
-    if (c->pages < 1 || c->page_size < 1 || c->kv_heads < 1 || c->head_dim < 1 || c->batch < 0 ||
-        c->max_pages < 1 || c->table_stride < c->max_pages)
+    if (!page_sizes_ok(c) || !table_ok(c))
         return AR_ERR_INVALID_ARG;
-    if (cache_esize_of(c->dtype) == 0 || c->kv_heads > kMaxHeads || c->head_dim > kMaxHeadDim)
+    if (!page_limits_ok(c))
         return AR_ERR_UNSUPPORTED;
-    const size_t d = static_cast<size_t>(c->head_dim);
-    if ((c->pages > 1 && c->page_stride < d) || (c->page_size > 1 && c->token_stride < d) ||
-        (c->kv_heads > 1 && c->head_stride < d) || !scale_ok(c->k_scale) || !scale_ok(c->v_scale))
+    if (!page_strides_ok(c) || !scale_ok(c->k_scale) || !scale_ok(c->v_scale))
         return AR_ERR_INVALID_ARG;
     return AR_OK;
+}
+
+// The caches of several layers: their shared shape (with its table where `table`), and how many they are.
+int check_layers(const ar_kv_cache* c, int layers, bool table)
+{
+    if (!page_sizes_ok(c) || (table && !table_ok(c)) || layers < 1)
+        return AR_ERR_INVALID_ARG;
+    if (!page_limits_ok(c) || layers > AR_MAX_LAYERS)
+        return AR_ERR_UNSUPPORTED;
+    return page_strides_ok(c) ? AR_OK : AR_ERR_INVALID_ARG;
 }
 
 int check_dtypes(int dtype, int cache_dtype)
@@ -125,11 +151,67 @@ int attention_blocks(const ar_kv_cache* c, int q_heads)
     return static_cast<int>(items >= most || items * tiles >= most ? most : items * tiles);
 }
 
-}  // namespace
+// token / page_size == (2 token * magic >> 32) >> shift for token < 2^31: m = ceil(2^(31 + l) / d) with 2^l the power of two
+// from d on is below 2^32, and n m >> (31 + l) = n / d below 2^31.
+void page_division(int page_size, uint32_t* magic, int* shift)
+{
+    *shift = 0;
+    while ((1ll << *shift) < page_size)
+        ++*shift;
+    *magic = static_cast<uint32_t>(((1ull << (31 + *shift)) + page_size - 1) / page_size);
+}
 
-extern "C" {
+// Tokens that a row of the table can hold; a tile's end stays an int.
+int capacity_of(const ar_kv_cache* c)
+{
+    const long long cap = static_cast<long long>(c->max_pages) * c->page_size;
+    return static_cast<int>(cap < INT_MAX - 255 ? cap : INT_MAX - 255);
+}
 
-int ar_kv_append(const ar_kv_cache* cache, const ar_append_params* p, ar_stream_t stream)
+// The factors of scores in base 2: false where one is not finite, which would make scores of 0 NaN.
+bool score_factors(float scale, float k_scale, float softcap, float* scale2, float* softcap2)
+{
+    constexpr float kLog2e = 1.4426950408889634f;
+    *scale2 = scale * k_scale * kLog2e * (softcap > 0.0f ? 2.0f / softcap : 1.0f);
+    *softcap2 = softcap * kLog2e;
+    return std::isfinite(*scale2) && std::isfinite(*softcap2);
+}
+
+// Sizes of ar_tree_attention that both it and its workspace size check.
+int check_tree(const ar_kv_cache* c, int q_heads, int tokens)
+{
+    if (int st = check_attention(c, q_heads))
+        return st;
+    if (tokens < 0)
+        return AR_ERR_INVALID_ARG;
+    return static_cast<uint64_t>(tokens) * (q_heads / c->kv_heads) <= INT_MAX - 255 ? AR_OK : AR_ERR_UNSUPPORTED;
+}
+
+struct TreePlan {
+    ar::TreeShape shape;
+    int blocks, slot_rows;
+    size_t slot_floats, part_at, bytes;
+};
+
+TreePlan tree_plan(const ar_kv_cache* c, int q_heads, int tokens)
+{
+    TreePlan p{};
+    const uint64_t rows = static_cast<uint64_t>(tokens) * (q_heads / c->kv_heads);
+    p.shape = ar::tree_shape(cache_esize_of(c->dtype), c->head_dim, rows, c->batch);
+    // No more blocks than there can be tiles: items are at most one a sequence and head more than whole blocks of rows.
+    const uint64_t items = static_cast<uint64_t>(c->kv_heads) * (c->batch + rows / p.shape.rows);
+    const uint64_t tiles = static_cast<uint64_t>(capacity_of(c)) / p.shape.tile + 2, most = ar::kTreeMaxBlocks;
+    p.blocks = static_cast<int>(items >= most || items * tiles >= most ? most : items * tiles);
+    p.slot_rows = static_cast<int>(rows < static_cast<uint64_t>(p.shape.rows) ? rows : p.shape.rows);
+    p.slot_floats = (static_cast<size_t>(p.slot_rows) * (c->head_dim + 2) + 3) / 4 * 4;
+    p.part_at = (p.blocks * sizeof(ar::TreeJob) + 255) / 256 * 256;
+    p.bytes = p.part_at + (2 * p.blocks * p.slot_floats * sizeof(float) + 255) / 256 * 256;
+    return p;
+}
+
+// ar_kv_append, and with `axes` > 0 ar_kv_append_axes.
+int append(const ar_kv_cache* cache, const ar_append_params* p, int axes, size_t axis_stride, const unsigned char* pair_axis,
+           ar_stream_t stream)
 {
     const ar_kv_cache own = without_idle_strides(cache);
     const ar_kv_cache* const c = &own;
@@ -145,6 +227,13 @@ int ar_kv_append(const ar_kv_cache* cache, const ar_append_params* p, ar_stream_
         p->rotary_dim < 0 || p->rotary_dim % 2 != 0 || p->rotary_dim > c->head_dim || !std::isfinite(p->rotary_scale) ||
         (p->rotary_dim > 0 && p->inv_freq == nullptr))
         return AR_ERR_INVALID_ARG;
+    if (axes > 0) {
+        if (axes > 1 && axis_stride < static_cast<size_t>(p->tokens))
+            return AR_ERR_INVALID_ARG;
+        for (int j = 0; j < p->rotary_dim / 2; ++j)
+            if (pair_axis == nullptr || pair_axis[j] >= axes)
+                return AR_ERR_INVALID_ARG;
+    }
     if (has_q && p->q_heads > kMaxHeads)
         return AR_ERR_UNSUPPORTED;
     if (p->tokens == 0)
@@ -152,13 +241,13 @@ int ar_kv_append(const ar_kv_cache* cache, const ar_append_params* p, ar_stream_
     const size_t e = static_cast<size_t>(esize_of(p->dtype)), ce = static_cast<size_t>(cache_esize_of(c->dtype));
     if (!pointers_ok(c) || !element_ok(p->k, e) || !element_ok(p->v, e) || c->batch < 1 ||
         (has_q && !(element_ok(p->q, e) && element_ok(p->q_out, e))) || !aligned(p->seq_start, 4) ||
-        !aligned(p->positions, 4) || !aligned(p->inv_freq, 4))
+        !aligned(p->positions, 4) || !aligned(p->inv_freq, 4) || (axes > 0 && p->positions == nullptr))
         return AR_ERR_INVALID_ARG;
     if (p->tokens > 1 && (p->k_stride < d * c->kv_heads || p->v_stride < d * c->kv_heads ||
                           (has_q && (p->q_stride < d * p->q_heads || p->q_out_stride < d * p->q_heads))))
         return AR_ERR_INVALID_ARG;
 
-    ar::AppendArgs a{};
+    ar::AxesAppendArgs a{};
     a.q = p->q;
     a.k = p->k;
     a.v = p->v;
@@ -206,9 +295,164 @@ int ar_kv_append(const ar_kv_cache* cache, const ar_append_params* p, ar_stream_
     a.head_magic = magic_of(a.head_units);
     a.v_magic = magic_of(a.v_units);
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (axes > 0) {
+        a.axes = axes;
+        a.axis_stride = axes > 1 ? axis_stride : 0;
+        for (int j = 0; j < a.half; ++j)
+            a.pair_axis[j >> 4] |= static_cast<uint32_t>(pair_axis[j]) << 2 * (j & 15);
+        return status_of(by_dtypes(p->dtype, c->dtype, [&](auto t, auto ct) {
+            return ar::launch_append<decltype(t), decltype(ct)>(a, vec, s);
+        }));
+    }
+    const ar::AppendArgs& plain = a;
     return status_of(by_dtypes(p->dtype, c->dtype, [&](auto t, auto ct) {
-        return ar::launch_append<decltype(t), decltype(ct)>(a, vec, s);
+        return ar::launch_append<decltype(t), decltype(ct)>(plain, vec, s);
     }));
+}
+
+// The largest unit of 16 bytes or less that all of these are whole multiples of.
+int unit_of(std::initializer_list<uint64_t> all)
+{
+    int unit = 16;
+    for (const uint64_t x : all)
+        while (x % unit != 0)
+            unit /= 2;
+    return unit;
+}
+
+bool fill_layers(ar::Layers* to, void* const* k, void* const* v, int layers, size_t esize, uint64_t* together)
+{
+    *together = 0;
+    if (k == nullptr || v == nullptr)
+        return false;
+    for (int i = 0; i < layers; ++i) {
+        if (!element_ok(k[i], esize) || !element_ok(v[i], esize))
+            return false;
+        to->k[i] = static_cast<char*>(k[i]);
+        to->v[i] = static_cast<char*>(v[i]);
+        *together |= reinterpret_cast<uintptr_t>(k[i]) | reinterpret_cast<uintptr_t>(v[i]);
+    }
+    return true;
+}
+
+// Whether [a, a + n) and [b, b + m) share an element; either may be NULL.
+bool overlap(const int* a, uint64_t n, const int* b, uint64_t m)
+{
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return a != nullptr && b != nullptr && x < y + 4 * m && y < x + 4 * n;
+}
+
+}  // namespace
+
+extern "C" {
+
+int ar_kv_append(const ar_kv_cache* cache, const ar_append_params* p, ar_stream_t stream)
+{
+    return append(cache, p, 0, 0, nullptr, stream);
+}
+
+int ar_kv_append_axes(const ar_kv_cache* cache, const ar_append_params* p, int axes, size_t axis_stride,
+                      const unsigned char* pair_axis, ar_stream_t stream)
+{
+    if (axes < 1 || axes > AR_MAX_AXES)
+        return AR_ERR_INVALID_ARG;
+    return append(cache, p, axes, axis_stride, pair_axis, stream);
+}
+
+int ar_kv_compact(const ar_kv_cache* cache, void* const* k, void* const* v, int layers, const int* kept, size_t kept_stride,
+                  int most_kept, const int* seq_start, int drafted, int* new_lengths, ar_stream_t stream)
+{
+    const ar_kv_cache own = without_idle_strides(cache);
+    const ar_kv_cache* const c = &own;
+    if (int st = check_layers(c, layers, true))
+        return st;
+    if (most_kept < 0 || (seq_start == nullptr && drafted < 0) ||
+        (c->batch > 1 && kept_stride < static_cast<size_t>(most_kept)))
+        return AR_ERR_INVALID_ARG;
+    if (c->batch == 0)
+        return AR_OK;
+    const uint64_t e = static_cast<uint64_t>(cache_esize_of(c->dtype)), batch = static_cast<uint64_t>(c->batch);
+    ar::CompactArgs a{};
+    uint64_t pointers;
+    if (!fill_layers(&a.to, k, v, layers, e, &pointers) || !element_ok(c->page_table, 4) || !element_ok(c->lengths, 4) ||
+        !aligned(seq_start, 4) || !element_ok(new_lengths, 4) || (most_kept > 0 && !element_ok(kept, 4)))
+        return AR_ERR_INVALID_ARG;
+    a.kept_stride = c->batch > 1 ? kept_stride : 0;
+    if (overlap(new_lengths, batch, c->lengths, batch) || overlap(new_lengths, batch, seq_start, batch + 1) ||
+        overlap(new_lengths, batch, kept, (batch - 1) * a.kept_stride + most_kept) ||
+        overlap(new_lengths, batch, c->page_table, (batch - 1) * c->table_stride + c->max_pages))
+        return AR_ERR_INVALID_ARG;
+    a.table = c->page_table;
+    a.lengths = c->lengths;
+    a.seq_start = seq_start;
+    a.kept = kept;
+    a.new_lengths = new_lengths;
+    a.page_stride = c->page_stride * e;
+    a.token_stride = c->token_stride * e;
+    a.head_stride = c->head_stride * e;
+    a.capacity = static_cast<uint64_t>(c->max_pages) * static_cast<uint64_t>(c->page_size);
+    a.drafted = drafted;
+    a.most_kept = most_kept;
+    a.batch = c->batch;
+    a.pages = c->pages;
+    a.page_size = c->page_size;
+    a.table_stride = c->table_stride;
+    const int unit = unit_of({pointers, a.page_stride, a.token_stride, a.head_stride, c->head_dim * e});
+    a.inner = static_cast<uint32_t>(c->head_dim * e / unit);
+    a.head_units = a.inner * static_cast<uint32_t>(c->kv_heads);
+    a.units = a.head_units * 2u * static_cast<uint32_t>(layers);
+    return status_of(ar::launch_compact(a, unit, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int ar_kv_copy_pages(const ar_kv_cache* cache, void* const* k, void* const* v, int layers, const int* src, const int* dst,
+                     int pairs, ar_stream_t stream)
+{
+    const ar_kv_cache own = without_idle_strides(cache);
+    const ar_kv_cache* const c = &own;
+    if (int st = check_layers(c, layers, false))
+        return st;
+    if (pairs < 0)
+        return AR_ERR_INVALID_ARG;
+    if (pairs == 0)
+        return AR_OK;
+    const uint64_t e = static_cast<uint64_t>(cache_esize_of(c->dtype));
+    ar::CopyArgs a{};
+    uint64_t pointers;
+    if (!fill_layers(&a.to, k, v, layers, e, &pointers) || !element_ok(src, 4) || !element_ok(dst, 4))
+        return AR_ERR_INVALID_ARG;
+    a.src = src;
+    a.dst = dst;
+    a.pairs = pairs;
+    a.pages = c->pages;
+    a.page_stride = c->page_stride * e;
+    // The page's bytes as runs that lie side by side: heads and tokens in the order of their strides, joined where dense.
+    struct Axis {
+        uint64_t n, stride;
+    } near{static_cast<uint64_t>(c->kv_heads), c->head_stride * e}, far{static_cast<uint64_t>(c->page_size), c->token_stride * e};
+    if (near.n == 1 || (far.n > 1 && far.stride < near.stride)) {
+        const Axis x = near;
+        near = far;
+        far = x;
+    }
+    uint64_t run = c->head_dim * e;
+    if (near.n == 1 || near.stride == run) {
+        run *= near.n;
+        near = far;
+        far = {1, 0};
+        if (near.n == 1 || near.stride == run) {
+            run *= near.n;
+            near = {1, 0};
+        }
+    }
+    const int unit = unit_of({pointers, a.page_stride, near.stride, far.stride, run});
+    if (run / unit * near.n * far.n > UINT32_MAX)
+        return AR_ERR_UNSUPPORTED;
+    a.inner = static_cast<uint32_t>(run / unit);
+    a.mid = static_cast<uint32_t>(near.n);
+    a.mid_stride = near.stride;
+    a.outer_stride = far.stride;
+    a.units = static_cast<uint32_t>(run / unit * near.n * far.n);
+    return status_of(ar::launch_copy_pages(a, layers, unit, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 size_t ar_paged_attention_workspace_size(const ar_kv_cache* cache, int q_heads)
@@ -234,10 +478,9 @@ int ar_paged_attention(const ar_kv_cache* cache, const void* q, size_t q_stride,
         return st;
     if (!std::isfinite(scale) || window < 0 || !std::isfinite(softcap) || softcap < 0.0f)
         return AR_ERR_INVALID_ARG;
-    constexpr float kLog2e = 1.4426950408889634f;
-    const float scale2 = scale * c->k_scale * kLog2e * (softcap > 0.0f ? 2.0f / softcap : 1.0f), softcap2 = softcap * kLog2e;
-    if (!std::isfinite(scale2) || !std::isfinite(softcap2))
-        return AR_ERR_INVALID_ARG;  // an infinite factor would make scores of 0 NaN
+    float scale2, softcap2;
+    if (!score_factors(scale, c->k_scale, softcap, &scale2, &softcap2))
+        return AR_ERR_INVALID_ARG;
     if (c->batch == 0)
         return AR_OK;
     const size_t e = static_cast<size_t>(esize_of(dtype));
@@ -253,7 +496,6 @@ int ar_paged_attention(const ar_kv_cache* cache, const void* q, size_t q_stride,
         return AR_ERR_WORKSPACE;
 
     const size_t ce = static_cast<size_t>(cache_esize_of(c->dtype));
-    const long long cap = static_cast<long long>(c->max_pages) * c->page_size;
     ar::AttnArgs a{};
     a.q = static_cast<const char*>(q);
     a.k = static_cast<const char*>(c->k);
@@ -272,11 +514,8 @@ int ar_paged_attention(const ar_kv_cache* cache, const void* q, size_t q_stride,
     a.pages = c->pages;
     a.page_size = c->page_size;
     a.batch = c->batch;
-    // m = ceil(2^(31 + l) / d) with 2^l the power of two from d on is below 2^32, and n m >> (31 + l) = n / d below 2^31.
-    while ((1ll << a.page_shift) < c->page_size)
-        ++a.page_shift;
-    a.page_magic = static_cast<uint32_t>(((1ull << (31 + a.page_shift)) + c->page_size - 1) / c->page_size);
-    a.capacity = static_cast<int>(cap < INT_MAX - 255 ? cap : INT_MAX - 255);  // a tile's end stays an int
+    page_division(c->page_size, &a.page_magic, &a.page_shift);
+    a.capacity = capacity_of(c);
     a.kv_heads = c->kv_heads;
     a.group = q_heads / c->kv_heads;
     a.group_blocks = group_blocks_of(c, q_heads);
@@ -298,6 +537,90 @@ int ar_paged_attention(const ar_kv_cache* cache, const void* q, size_t q_stride,
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     return status_of(by_dtypes(dtype, c->dtype, [&](auto t, auto ct) {
         return ar::launch_attention<decltype(t), decltype(ct)>(a, most, sms, s);
+    }));
+}
+
+size_t ar_tree_attention_workspace_size(const ar_kv_cache* cache, int q_heads, int tokens)
+{
+    const ar_kv_cache own = without_idle_strides(cache);
+    if (check_tree(&own, q_heads, tokens) != AR_OK)
+        return 0;
+    return tree_plan(&own, q_heads, tokens).bytes;
+}
+
+int ar_tree_attention(const ar_kv_cache* cache, const ar_tree_params* p, void* workspace, size_t workspace_bytes, ar_stream_t stream)
+{
+    const ar_kv_cache own = without_idle_strides(cache);
+    const ar_kv_cache* const c = &own;
+    if (p == nullptr)
+        return AR_ERR_INVALID_ARG;
+    if (int st = check_tree(c, p->q_heads, p->tokens))
+        return st;
+    if (int st = check_dtypes(p->dtype, c->dtype))
+        return st;
+    float scale2, softcap2;
+    if (!std::isfinite(p->scale) || p->window < 0 || !std::isfinite(p->softcap) || p->softcap < 0.0f ||
+        !score_factors(p->scale, c->k_scale, p->softcap, &scale2, &softcap2) ||
+        (p->mask != nullptr && (p->mask_words < 1 || p->mask_words > 1024)))
+        return AR_ERR_INVALID_ARG;
+    if (c->batch == 0 ? p->seq_start == nullptr && p->tokens != 0 : p->seq_start == nullptr && p->tokens % c->batch != 0)
+        return AR_ERR_INVALID_ARG;
+    if (c->batch == 0 || p->tokens == 0)
+        return AR_OK;
+    const size_t e = static_cast<size_t>(esize_of(p->dtype)), ce = static_cast<size_t>(cache_esize_of(c->dtype));
+    if (!pointers_ok(c) || !element_ok(p->q, e) || !element_ok(p->out, e) || !aligned(p->lse, 4) || !aligned(p->seq_start, 4) ||
+        !aligned(p->mask, 8) || (p->tokens > 1 && p->q_stride < static_cast<size_t>(p->q_heads) * c->head_dim))
+        return AR_ERR_INVALID_ARG;
+    if (!aligned(p->q, 16) || !aligned(c->k, 16) || !aligned(c->v, 16) || !aligned(p->out, 16) ||
+        (p->tokens > 1 && p->q_stride * e % 16 != 0) || c->head_dim * e % 16 != 0)
+        return AR_ERR_UNSUPPORTED;
+    const TreePlan plan = tree_plan(c, p->q_heads, p->tokens);
+    if (workspace == nullptr || !aligned(workspace, 16) || workspace_bytes < plan.bytes)
+        return AR_ERR_WORKSPACE;
+
+    ar::TreeArgs a{};
+    a.q = static_cast<const char*>(p->q);
+    a.k = static_cast<const char*>(c->k);
+    a.v = static_cast<const char*>(c->v);
+    a.out = static_cast<char*>(p->out);
+    a.lse = p->lse;
+    a.jobs = static_cast<ar::TreeJob*>(workspace);
+    a.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + plan.part_at);
+    a.table = c->page_table;
+    a.lengths = c->lengths;
+    a.seq_start = p->seq_start;
+    a.mask = reinterpret_cast<const uint32_t*>(p->mask);
+    a.q_stride = p->tokens > 1 ? p->q_stride * e : 0;
+    a.page_stride = c->page_stride * ce;
+    a.token_stride = c->token_stride * ce;
+    a.head_stride = c->head_stride * ce;
+    a.table_stride = c->table_stride;
+    a.pages = c->pages;
+    a.page_size = c->page_size;
+    a.batch = c->batch;
+    page_division(c->page_size, &a.page_magic, &a.page_shift);
+    a.capacity = capacity_of(c);
+    a.tokens = p->tokens;
+    a.each = p->tokens / c->batch;
+    a.mask_words = 2 * p->mask_words;
+    a.kv_heads = c->kv_heads;
+    a.group = p->q_heads / c->kv_heads;
+    a.head_dim = c->head_dim;
+    a.window = p->window;
+    a.scale2 = scale2;
+    a.softcap = p->softcap;
+    a.softcap2 = softcap2;
+    a.v_scale = c->v_scale;
+    a.slot_rows = plan.slot_rows;
+    a.slot_floats = plan.slot_floats;
+
+    int dev = 0, sms = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+        return AR_ERR_CUDA;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    return status_of(by_dtypes(p->dtype, c->dtype, [&](auto t, auto ct) {
+        return ar::launch_tree<decltype(t), decltype(ct)>(a, plan.shape, plan.blocks, sms, s);
     }));
 }
 

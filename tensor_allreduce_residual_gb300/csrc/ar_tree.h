@@ -1,0 +1,81 @@
+// ar_tree.h -- kernel arguments of the attention of drafted tokens over a paged
+// cache, and what its kernels share with their host side (ar_tree_api.cu).
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "ar_internal.h"
+
+namespace ar {
+
+// Strides of the cache in bytes.
+struct TreeArgs {
+    const char* q;
+    const char* k;
+    const char* v;
+    char* out;
+    float* lse;               // nullable
+    struct TreeJob* jobs;     // one for each block: the item it begins and others end
+    float* part;              // partial results: two slots per block
+    const int* table;
+    const int* lengths;
+    const int* seq_start;     // nullable: `each` rows a sequence
+    const uint32_t* mask;     // nullable: a row sees the drafted tokens up to its own
+    uint64_t q_stride;        // bytes
+    uint64_t page_stride, token_stride, head_stride;
+    int table_stride, pages, page_size, batch;
+    uint32_t page_magic;      // token / page_size == (2 token * page_magic >> 32) >> page_shift for token < 2^31
+    int page_shift;
+    int capacity;             // tokens a table row can hold
+    int tokens, each;         // rows of q; of each sequence without seq_start
+    int mask_words;           // 32-bit words of a row's mask
+    int kv_heads, group, head_dim;
+    int window;
+    float scale2;             // of the scores, k_scale included, in base 2; with softcap twice that over softcap
+    float softcap;
+    float softcap2;           // softcap in base 2
+    float v_scale;
+    int slot_rows;            // rows of a partial slot: [slot_rows][head_dim] sums, [slot_rows] references, [slot_rows] weights
+    uint64_t slot_floats;
+};
+
+// An item that several blocks have parts of, written by the one that begins it; rows == 0: there is none.
+struct TreeJob {
+    int last;                 // the last block with a part
+    int rows;                 // rows of the item
+    int first;                // the sequence's first row of q
+    int row0;                 // the item's first row in its sequence and head
+    int head;                 // key-value head
+    int pad[3];
+};
+
+constexpr int kTreeMaxDim = 256;
+// Blocks of the attention kernel, at most: two per SM of the 152.
+constexpr int kTreeMaxBlocks = 304;
+
+// Rows of an item (drafted tokens times the query heads of a key-value head) and cached tokens of a tile.
+enum { kTreeFma16, kTreeFma64, kTreeMma128, kTreeMma256 };
+struct TreeShape {
+    int kind, rows, tile;
+};
+
+// The rule, on what the host knows.  `rows`: of all sequences and one key-value head.
+inline TreeShape tree_shape(int cache_esize, int head_dim, uint64_t rows, int batch)
+{
+    if (cache_esize == 4)
+        return rows <= 16ull * batch ? TreeShape{kTreeFma16, 16, 32} : TreeShape{kTreeFma64, 64, 32};
+    if (head_dim > 128)
+        return TreeShape{kTreeMma128, 128, 64};
+    return rows <= 128ull * batch ? TreeShape{kTreeMma128, 128, 128} : TreeShape{kTreeMma256, 256, 128};
+}
+
+// At most `most` blocks of the attention kernel, and no more than `sms` SMs hold at once; then the join kernel.
+template <typename T, typename CT>
+cudaError_t launch_tree(const TreeArgs& a, const TreeShape& shape, int most, int sms, cudaStream_t s);
+
+// Bounded waits that gave up in the kernels of query type T; the count is cleared.
+template <typename T>
+cudaError_t take_tree_wait_timeouts(unsigned int* count);
+
+}  // namespace ar

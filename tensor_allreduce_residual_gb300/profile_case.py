@@ -8,6 +8,9 @@
     python -m tensor_allreduce_residual_gb300.profile_case attention --batch 64 --length 4096 --heads 32 --kv-heads 4
     python -m tensor_allreduce_residual_gb300.profile_case append --batch 4 --length 2048 --heads 64 --kv-heads 8
     python -m tensor_allreduce_residual_gb300.profile_case join --R 8 --tokens 65536
+    python -m tensor_allreduce_residual_gb300.profile_case tree --batch 64 --length 4096 --heads 32 --kv-heads 4 --drafts 16
+    python -m tensor_allreduce_residual_gb300.profile_case compact --batch 256 --length 512 --drafts 32 --kv-heads 8
+    python -m tensor_allreduce_residual_gb300.profile_case copy-pages --batch 64 --length 512 --kv-heads 8
 
 Inputs are the seeded synthetic workloads (drawn on the device), the calls go
 through the C ABI, and nothing is timed or checked: the point is a short,
@@ -29,7 +32,7 @@ if ROOT not in sys.path:
 
 def main(argv=None) -> int:
     p = argparse.ArgumentParser(description="run one library case for a profiler")
-    p.add_argument("op", choices=["fused", "sum", "rmsnorm", "lamport", "append", "attention", "join"])
+    p.add_argument("op", choices=["fused", "sum", "rmsnorm", "lamport", "append", "attention", "join", "tree", "compact", "copy-pages"])
     p.add_argument("--R", type=int, default=8)
     p.add_argument("--tokens", type=int, default=1024)
     p.add_argument("--hidden", type=int, default=8192)
@@ -44,6 +47,7 @@ def main(argv=None) -> int:
     p.add_argument("--head-dim", type=int, default=128)
     p.add_argument("--page", type=int, default=16)
     p.add_argument("--cache", default=None, choices=["fp32", "fp16", "bf16", "e4m3"], help="the cache's type (default: --dtype)")
+    p.add_argument("--drafts", type=int, default=16, help="drafted tokens of each sequence, the last of its length")
     p.add_argument("--warmup", type=int, default=2)
     p.add_argument("--calls", type=int, default=3)
     p.add_argument("--test-library", action="store_true", help="load libar_test.so (AR_ONESHOT_SHAPE applies)")
@@ -73,14 +77,14 @@ def main(argv=None) -> int:
         lse = [torch.randn(a.tokens, device="cuda") for _ in range(a.R)]
         out = torch.empty_like(parts[0])
         call = lambda: ar.ar_attention_join(parts, lse, out=out)  # noqa: E731
-    elif a.op in ("append", "attention"):
+    elif a.op in ("append", "attention", "tree", "compact", "copy-pages"):
         dt = workloads.DTYPES[a.dtype]
         cache_dt = {**workloads.DTYPES, "e4m3": torch.float8_e4m3fn}[a.cache or a.dtype]
         per = -(-a.length // a.page)
         pages = [torch.randn(a.batch * per, a.page, a.kv_heads, a.head_dim, device="cuda").to(cache_dt) for _ in range(2)]
         table = torch.randperm(a.batch * per, device="cuda").to(torch.int32).view(a.batch, per)
         lengths = torch.full((a.batch,), a.length, dtype=torch.int32, device="cuda")
-        rows = a.batch * a.length if a.op == "append" else a.batch
+        rows = a.batch * (a.length if a.op == "append" else a.drafts if a.op == "tree" else 1)
         qkv = torch.randn(rows, a.heads + 2 * a.kv_heads, a.head_dim, device="cuda").to(dt)
         q, k, v = qkv.split([a.heads, a.kv_heads, a.kv_heads], dim=1)
         out = torch.empty(rows, a.heads, a.head_dim, dtype=dt, device="cuda")
@@ -89,8 +93,18 @@ def main(argv=None) -> int:
         if a.op == "append":
             call = lambda: ar.ar_kv_append(*pages, table, lengths, k, v, q=q, q_out=out, seq_start=start,  # noqa: E731
                                            inv_freq=freq)
-        else:
+        elif a.op == "attention":
             call = lambda: ar.ar_paged_attention(q, *pages, table, lengths, out=out)  # noqa: E731
+        elif a.op == "tree":   # every token sees itself and the one before it
+            bits = [3 << max(i - 1, 0) if i else 1 for i in range(min(a.drafts, 62))] + [1] * max(0, a.drafts - 62)
+            mask = torch.tensor(bits * a.batch, device="cuda")[:, None].contiguous()
+            call = lambda: ar.ar_tree_attention(q, *pages, table, lengths, mask=mask, out=out)  # noqa: E731
+        elif a.op == "compact":
+            kept = torch.arange(1, a.drafts, 2, device="cuda", dtype=torch.int32).repeat(a.batch, 1)
+            call = lambda: ar.ar_kv_compact(*pages, table, lengths, kept, drafted=a.drafts)  # noqa: E731
+        else:
+            half = a.batch * per // 2
+            call = lambda: ar.ar_kv_copy_pages(*pages, table.view(-1)[:half], table.view(-1)[half:2 * half])  # noqa: E731
     else:
         f = workloads.fused_inputs(a.R, a.tokens, a.hidden, a.dtype, partial_dist=("N", 0.0, 1.0 / a.R),
                                    residual_dist=("N", 0.0, 4.0),
