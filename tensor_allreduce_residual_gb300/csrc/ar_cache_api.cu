@@ -1,9 +1,12 @@
 // ar_cache_api.cu -- the C ABI of the paged key-value cache calls: argument
 // checks, launch shapes and dispatch on the element types.  Host code only; it
 // allocates nothing.
+#include <cuda.h>
+#include <cudaTypedefs.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <atomic>
 #include <climits>
 #include <cmath>
 #include <cstdint>
@@ -185,6 +188,53 @@ int check_tree(const ar_kv_cache* c, int q_heads, int tokens)
     if (tokens < 0)
         return AR_ERR_INVALID_ARG;
     return static_cast<uint64_t>(tokens) * (q_heads / c->kv_heads) <= INT_MAX - 255 ? AR_OK : AR_ERR_UNSUPPORTED;
+}
+
+// The driver's encoder of tensor maps, or nullptr.
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder()
+{
+    static std::atomic<void*> found{nullptr};
+    void* f = found.load(std::memory_order_acquire);
+    if (f == nullptr) {
+        cudaDriverEntryPointQueryResult how;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &how) != cudaSuccess ||
+            how != cudaDriverEntryPointSuccess) {
+            cudaGetLastError();
+            return nullptr;
+        }
+        found.store(f, std::memory_order_release);
+    }
+    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+}
+
+// Describes the pages for tensor copies of `tile` tokens at most, where they can be: 16-bit elements in boxes of 64, 8-bit ones
+// in boxes of `dim`.
+bool tree_maps(const ar_kv_cache* c, int tile, int dim, ar::TreeMaps* maps, int* token_first)
+{
+    const uint64_t e = static_cast<uint64_t>(cache_esize_of(c->dtype));
+    if (e == 4 || c->page_size % 8 != 0 || !(tile % c->page_size == 0 || c->page_size % tile == 0))
+        return false;
+    const PFN_cuTensorMapEncodeTiled_v12000 encode = tensor_map_encoder();
+    if (encode == nullptr)
+        return false;
+    // An axis of one element needs no stride, but an allowed one.
+    const uint64_t page = c->page_stride * e, token = c->token_stride * e, head = c->head_stride * e;
+    const auto some = [](uint64_t stride) { return stride != 0 ? stride : 16; };
+    *token_first = c->kv_heads == 1 || token <= head;
+    const cuuint64_t sizes[4] = {static_cast<cuuint64_t>(c->head_dim), static_cast<cuuint64_t>(*token_first ? c->page_size : c->kv_heads),
+                                 static_cast<cuuint64_t>(*token_first ? c->kv_heads : c->page_size), static_cast<cuuint64_t>(c->pages)};
+    const cuuint64_t strides[3] = {some(*token_first ? token : head), some(*token_first ? head : token), some(page)};
+    const cuuint32_t tokens = static_cast<cuuint32_t>(c->page_size < tile ? c->page_size : tile);
+    const cuuint32_t box[4] = {e == 1 ? static_cast<cuuint32_t>(dim) : 64u, *token_first ? tokens : 1u, *token_first ? 1u : tokens, 1u};
+    const cuuint32_t steps[4] = {1, 1, 1, 1};
+    const CUtensorMapDataType type = e == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+                                            : c->dtype == AR_FP16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    const auto map = [&](CUtensorMap* to, void* pages) {
+        return encode(to, type, 4, pages, sizes, strides, box, steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                      e == 1 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    };
+    return map(&maps->k, c->k) && map(&maps->v, c->v);
 }
 
 struct TreePlan {
@@ -613,6 +663,8 @@ int ar_tree_attention(const ar_kv_cache* cache, const ar_tree_params* p, void* w
     a.v_scale = c->v_scale;
     a.slot_rows = plan.slot_rows;
     a.slot_floats = plan.slot_floats;
+    ar::TreeMaps maps{};
+    a.boxes = tree_maps(c, plan.shape.tile, ar::tree_dim(c->head_dim), &maps, &a.token_first);
 
     int dev = 0, sms = 0;
     if (cudaGetDevice(&dev) != cudaSuccess ||
@@ -620,7 +672,7 @@ int ar_tree_attention(const ar_kv_cache* cache, const ar_tree_params* p, void* w
         return AR_ERR_CUDA;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     return status_of(by_dtypes(p->dtype, c->dtype, [&](auto t, auto ct) {
-        return ar::launch_tree<decltype(t), decltype(ct)>(a, plan.shape, plan.blocks, sms, s);
+        return ar::launch_tree<decltype(t), decltype(ct)>(a, maps, plan.shape, plan.blocks, sms, s);
     }));
 }
 

@@ -109,14 +109,13 @@ struct TreeCursor {
     __device__ __forceinline__ int rows(const TreeArgs& a) const { return min(ROWS, q.n * a.group - rt * ROWS); }
 };
 
-// Finds the block's run and its first tile.  All THREADS threads; contains barriers.
+// Finds the block's run and its first tile.  All THREADS threads; contains barriers.  s_warp: shared, THREADS / 32 + 2.
 template <int ROWS, int TILE, int THREADS>
-__device__ Run tree_run(const TreeArgs& a, TreeCursor<ROWS, TILE>& cur)
+__device__ Run tree_run(const TreeArgs& a, TreeCursor<ROWS, TILE>& cur, long long* s_warp)
 {
     constexpr int WARPS = THREADS / 32;
-    __shared__ long long s_warp[WARPS];
-    __shared__ int s_b;
-    __shared__ long long s_before;
+    long long& s_before = s_warp[WARPS];
+    long long& s_b = s_warp[WARPS + 1];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int per = (a.batch + THREADS - 1) / THREADS, b0 = min(tid * per, a.batch), b1 = min(b0 + per, a.batch);
     long long mine = 0;
@@ -152,7 +151,7 @@ __device__ Run tree_run(const TreeArgs& a, TreeCursor<ROWS, TILE>& cur)
         s_before = before;
     }
     __syncthreads();
-    cur.b = s_b;
+    cur.b = static_cast<int>(s_b);
     cur.q = tree_seq(a, cur.b);
     const long long each = tree_tiles<ROWS, TILE>(a, cur.q), in = run.lo - s_before * a.kv_heads;
     cur.h = static_cast<int>(divide(in, each));
@@ -311,7 +310,8 @@ k_tree_fma(const TreeArgs a)
     if (tid == 0)
         a.jobs[blockIdx.x].rows = 0;
     TreeCursor<ROWS, TILE> cur;
-    const Run run = tree_run<ROWS, TILE, kTreeFmaThreads>(a, cur);
+    __shared__ long long s_scan[kTreeFmaThreads / 32 + 2];
+    const Run run = tree_run<ROWS, TILE, kTreeFmaThreads>(a, cur, s_scan);
     const int fours = a.head_dim / 4;
     float4 o[RPT][CPT];
     float top[RPT], total[RPT];
@@ -654,12 +654,13 @@ k_tree_join(const TreeArgs a, const int blocks)
 }
 
 // Launches an attention kernel of `blocks` blocks, with its shared memory limit raised, and the join.
-template <typename T>
-cudaError_t launch_tree_kernel(void (*kernel)(TreeArgs), const TreeArgs& a, int threads, int smem, int blocks, int sms, cudaStream_t s)
+template <typename T, typename... Rest>
+cudaError_t launch_tree_kernel(void (*kernel)(TreeArgs, Rest...), const TreeArgs& a, int threads, int smem, int blocks, int sms, cudaStream_t s,
+                               const Rest&... rest)
 {
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e == cudaSuccess)
-        e = launch_k(kernel, dim3(blocks), dim3(threads), smem, s, a);
+        e = launch_k(kernel, dim3(blocks), dim3(threads), smem, s, a, rest...);
     if (e != cudaSuccess)
         return e;
     return launch_k(k_tree_join<T>, dim3(sms * 4), dim3(kTreeJoinThreads), 0, s, a, blocks);

@@ -2,6 +2,7 @@
 // cache, and what its kernels share with their host side (ar_tree_api.cu).
 #pragma once
 
+#include <cuda.h>  // types only: tensor maps are encoded by the driver's function, found at run time
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -36,6 +37,8 @@ struct TreeArgs {
     float softcap;
     float softcap2;           // softcap in base 2
     float v_scale;
+    int boxes;                // whether pages come by tensor copies
+    int token_first;          // whether the maps' second axis is a page's tokens, and not the heads
     int slot_rows;            // rows of a partial slot: [slot_rows][head_dim] sums, [slot_rows] references, [slot_rows] weights
     uint64_t slot_floats;
 };
@@ -50,6 +53,11 @@ struct TreeJob {
     int pad[3];
 };
 
+// The pages of keys and of values as tensors of elements, tokens and heads (the closer pair first) and pages.
+struct TreeMaps {
+    CUtensorMap k, v;
+};
+
 constexpr int kTreeMaxDim = 256;
 // Blocks of the attention kernel, at most: two per SM of the 152.
 constexpr int kTreeMaxBlocks = 304;
@@ -59,6 +67,9 @@ enum { kTreeFma16, kTreeFma64, kTreeMma128, kTreeMma256 };
 struct TreeShape {
     int kind, rows, tile;
 };
+
+// Elements that a head of the matrix kernel has, those of a shorter one followed by zeros.
+inline int tree_dim(int head_dim) { return head_dim <= 64 ? 64 : head_dim <= 128 ? 128 : head_dim <= 192 ? 192 : 256; }
 
 // The rule, on what the host knows.  `rows`: of all sequences and one key-value head.
 inline TreeShape tree_shape(int cache_esize, int head_dim, uint64_t rows, int batch)
@@ -72,7 +83,7 @@ inline TreeShape tree_shape(int cache_esize, int head_dim, uint64_t rows, int ba
 
 // At most `most` blocks of the attention kernel, and no more than `sms` SMs hold at once; then the join kernel.
 template <typename T, typename CT>
-cudaError_t launch_tree(const TreeArgs& a, const TreeShape& shape, int most, int sms, cudaStream_t s);
+cudaError_t launch_tree(const TreeArgs& a, const TreeMaps& maps, const TreeShape& shape, int most, int sms, cudaStream_t s);
 
 // Bounded waits that gave up in the kernels of query type T; the count is cleared.
 template <typename T>

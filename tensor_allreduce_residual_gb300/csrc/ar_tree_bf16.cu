@@ -4,8 +4,8 @@
 
 namespace ar {
 
-template cudaError_t launch_tree<__nv_bfloat16, __nv_bfloat16>(const TreeArgs&, const TreeShape&, int, int, cudaStream_t);
-template cudaError_t launch_tree<__nv_bfloat16, __nv_fp8_e4m3>(const TreeArgs&, const TreeShape&, int, int, cudaStream_t);
+template cudaError_t launch_tree<__nv_bfloat16, __nv_bfloat16>(const TreeArgs&, const TreeMaps&, const TreeShape&, int, int, cudaStream_t);
+template cudaError_t launch_tree<__nv_bfloat16, __nv_fp8_e4m3>(const TreeArgs&, const TreeMaps&, const TreeShape&, int, int, cudaStream_t);
 template cudaError_t take_tree_wait_timeouts<__nv_bfloat16>(unsigned int*);
 
 }  // namespace ar

@@ -4,8 +4,8 @@
 
 namespace ar {
 
-template cudaError_t launch_tree<__half, __half>(const TreeArgs&, const TreeShape&, int, int, cudaStream_t);
-template cudaError_t launch_tree<__half, __nv_fp8_e4m3>(const TreeArgs&, const TreeShape&, int, int, cudaStream_t);
+template cudaError_t launch_tree<__half, __half>(const TreeArgs&, const TreeMaps&, const TreeShape&, int, int, cudaStream_t);
+template cudaError_t launch_tree<__half, __nv_fp8_e4m3>(const TreeArgs&, const TreeMaps&, const TreeShape&, int, int, cudaStream_t);
 template cudaError_t take_tree_wait_timeouts<__half>(unsigned int*);
 
 }  // namespace ar

@@ -5,7 +5,7 @@
 namespace ar {
 
 template <>
-cudaError_t launch_tree<float, float>(const TreeArgs& a, const TreeShape& shape, int most, int sms, cudaStream_t s)
+cudaError_t launch_tree<float, float>(const TreeArgs& a, const TreeMaps&, const TreeShape& shape, int most, int sms, cudaStream_t s)
 {
     return a.head_dim <= 64    ? launch_tree_fma<float, float, 64>(a, shape, most, sms, s)
            : a.head_dim <= 128 ? launch_tree_fma<float, float, 128>(a, shape, most, sms, s)

@@ -9,14 +9,17 @@
 // the item's end.  Weights are two 16-bit numbers, their rounding and what it
 // leaves, so P V takes two products.
 //
-//   warps 0 .. 4 NM - 1     softmax, item ends (warp w reads lanes 32 (w % 4) ..)
-//   4 warps                 copies: queries, and rings of keys and values
-//   1 warp                  allocates tensor memory; one lane issues products
+//   softmax warps (8; 4 for heads over 128), a thread a row (warp w reads lanes 32 (w % 4) ..)
+//   4 copying warps: queries, and rings of keys and values
+//   1 warp that allocates tensor memory; one of its lanes issues products
 //
-// Two score buffers let the next product of scores run while a warpgroup works
-// (NM == 1: of alternating tiles, NM == 2: one for each half).  All hand-overs
-// are mbarriers.  Waits are bounded: one that gave up is counted, raises the
-// block's stop flag, on which all others give up too, and the block leaves.
+// A softmax step takes a warpgroup longer than a tile of bf16 takes from HBM,
+// so heads of up to 128 have two warpgroups, with a score buffer and an O
+// each: with 256 rows (NM == 2) they have a half of the rows each, with up to
+// 128 (NM == 1) alternate tiles, whose two O's are joined at the item's end.
+// All hand-overs are mbarriers.  Waits are bounded: one that gave up is
+// counted, raises the block's stop flag, on which all others give up too, and
+// the block leaves.
 #pragma once
 
 #include "ar_tcgen05.cuh"
@@ -42,6 +45,18 @@ __device__ __forceinline__ bool bar_test(uint32_t bar, uint32_t parity)
     uint32_t done;
     asm volatile("{\n\t.reg .pred p;\n\t"
                  "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+                 "selp.u32 %0, 1, 0, p;\n\t}"
+                 : "=r"(done)
+                 : "r"(bar), "r"(parity)
+                 : "memory");
+    return done != 0;
+}
+// The same, but never suspended: try_wait may hold the thread for microseconds, which a warp with other things to do has not.
+__device__ __forceinline__ bool bar_poll(uint32_t bar, uint32_t parity)
+{
+    uint32_t done;
+    asm volatile("{\n\t.reg .pred p;\n\t"
+                 "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
                  "selp.u32 %0, 1, 0, p;\n\t}"
                  : "=r"(done)
                  : "r"(bar), "r"(parity)
@@ -90,8 +105,8 @@ struct TreeTile {
     TreeSeq q;
     int head, row0, rows, token0, flags;
     int b;
-    uint32_t valid[4];   // of each copying warp's tokens which are in the cache
-    int bad[4];          // whether a value of theirs is infinite or NaN, in a tile that some row sees in part only
+    uint32_t valid[4];   // which tokens are in the cache
+    int bad;             // whether a value is infinite or NaN, in a tile that some row sees in part only
 };
 
 template <typename T_, typename CT_, int DIM_, int NM_>
@@ -102,28 +117,31 @@ struct TreeMmaShape {
     static constexpr int DIM = DIM_, NM = NM_;
     static constexpr bool SMALL = sizeof(CT) == 1, SCALED = SMALL && !std::is_same<T, __half>::value;
     static constexpr bool BF16 = std::is_same<MT, __nv_bfloat16>::value;
-    static constexpr int ROWS = 128 * NM, TOKENS = DIM <= 128 ? 128 : 64, WARP_TOKENS = TOKENS / 4;
-    static constexpr int SOFTMAX = 128 * NM, THREADS = SOFTMAX + 128 + 32;
+    static constexpr int ROWS = 128 * NM, TOKENS = DIM <= 128 ? 128 : 64;
+    static constexpr int GROUPS = DIM <= 128 ? 2 : 1;           // softmax warpgroups, each with an O
+    static constexpr bool SPLIT = GROUPS == 2 && NM == 1;       // they take alternate tiles
+    static_assert(NM <= GROUPS, "a warpgroup for each half of the rows");
+    static constexpr int SOFTMAX = 128 * GROUPS, THREADS = SOFTMAX + 128 + 64;
     static constexpr int Q = ROWS * DIM * 2, SLOT = TOKENS * DIM * 2, RAW = SMALL ? TOKENS * DIM : 0;
-    // Of a block's 227 KB 1 KB goes to the static arrays, at whose end the dynamic part begins aligned, and 2 KB to barriers.
-    static constexpr int MISC = 2048, ROOM = 232448 - 1024 - MISC;
+    static constexpr int MISC = 3072, ROOM = 232448 - MISC;     // a block's 227 KB
     static constexpr int QS = NM == 1 && DIM <= 128 ? 2 : 1;
     static constexpr int RS = !SMALL ? 0 : DIM == 64 ? 8 : 4;
     static constexpr int FIT = (ROOM - QS * Q - RS * RAW) / SLOT, NS = FIT < 8 ? FIT : 8;
     static_assert(NS >= 3, "a tile's keys and values, and the next one's keys");
-    // Fills that are under way before the oldest is waited for.
-    static constexpr int LAG = SMALL ? RS - 1 : NS - 2;
-    // Descriptions of tiles: of as many as fills may be sent before a tile's last one is handed over, and a tile more.
-    static constexpr int TILES = SCALED && DIM > 64 ? 4 : 8;
-    static_assert(2 * TILES >= LAG + 3, "a tile is done before its description is wanted again");
+    static constexpr int ARRIVALS = 8;  // barriers of fills that need hands: by stage (8-bit), or by tile
+    static_assert(RS <= ARRIVALS && (RS == 0 || RS % 4 == 0) && NS <= 8, "a stage is one warp's; a warp has at most four tiles under way");
+    static constexpr int TILES = SCALED ? 4 : 8;  // descriptions of tiles
     static constexpr int SMEM = QS * Q + NS * SLOT + RS * RAW + MISC;
     // Weights may pass their reference's by 2^AHEAD before it is moved, which costs a pass over O.  fp16 weights are 2^LIFT
     // times as large, so that small ones keep their bits: the largest is 2^15.
     static constexpr float AHEAD = BF16 ? 8.0f : 4.0f, LIFT = BF16 ? 0.0f : 11.0f;
-    static constexpr int S_COLUMNS = TOKENS, O_COLUMN = 256;  // score buffers from column 0 on; O of half m at 256 + 128 m
-    static_assert(2 * S_COLUMNS <= O_COLUMN && O_COLUMN + NM * (DIM <= 128 ? 128 : 256) <= 512, "tensor memory");
-    static constexpr int BARS = 2 * NS + 2 * QS + 2 + 2 + NM + 2 * TILES + 1;
-    static_assert(BARS * 8 + 16 + TILES * sizeof(TreeTile) + (SCALED ? QS * ROWS * 4 : 0) <= MISC, "descriptions and barriers");
+    static constexpr int S_COLUMNS = TOKENS, O_COLUMN = 256;  // score buffers from column 0 on; O of group m at 256 + 128 m
+    static_assert(2 * S_COLUMNS <= O_COLUMN && O_COLUMN + (DIM <= 128 ? GROUPS * 128 : 256) <= 512, "tensor memory");
+    static constexpr int BARS = 2 * NS + 2 * QS + 2 + 2 + GROUPS + 2 * TILES + 2 + 1 + ARRIVALS + RS;
+    // A step is a half of the rows of a tile, or a tile.
+    static __device__ __forceinline__ int tile_of(int u) { return NM == 2 ? u >> 1 : u; }
+    static __device__ __forceinline__ int group_of(int u) { return GROUPS == 2 ? u & 1 : 0; }
+    static __device__ __forceinline__ int phase_of(int u) { return GROUPS == 2 ? u >> 1 : u; }  // of the group's O
 };
 
 // Shared memory, by address.
@@ -136,102 +154,190 @@ struct TreeSmem {
         at = smem_addr(dynamic);
         base = dynamic;
     }
-    static constexpr uint32_t KV = P::QS * P::Q, RAW = KV + P::NS * P::SLOT, BAR = RAW + P::RS * P::RAW, TILE = (BAR + P::BARS * 8 + 15) / 16 * 16,
-                              SCALE = TILE + P::TILES * sizeof(TreeTile), END = SCALE + (P::SCALED ? P::QS * P::ROWS * 4 : 0);
+    static constexpr uint32_t KV = P::QS * P::Q, RAW = KV + P::NS * P::SLOT, BAR = RAW + P::RS * P::RAW, TILE = BAR + P::BARS * 8,
+                              SCALE = TILE + P::TILES * sizeof(TreeTile), JOIN = SCALE + (P::SCALED ? P::QS * P::ROWS * 4 : 0),
+                              SCAN = (JOIN + (P::SPLIT ? 128 * 8 : 0) + 7) / 8 * 8, SENT = SCAN + (P::THREADS / 32 + 2) * 8, END = SENT + 16 + 8;
     __device__ __forceinline__ uint32_t q(int slot) const { return at + slot * P::Q; }
     __device__ __forceinline__ uint32_t kv(int slot) const { return at + KV + slot * P::SLOT; }
     __device__ __forceinline__ char* raw(int stage) const { return base + RAW + stage * P::RAW; }
     __device__ __forceinline__ uint32_t bar(int i) const { return at + BAR + 8 * i; }
+    static constexpr int B_Q = 2 * P::NS, B_S = B_Q + 2 * P::QS, B_O = B_S + 4, B_TILE = B_O + P::GROUPS, B_END = B_TILE + 2 * P::TILES, B_RAW = B_END + 3;
+    static_assert(B_RAW + P::ARRIVALS + P::RS == P::BARS, "all barriers");
     __device__ __forceinline__ uint32_t kv_full(int s) const { return bar(s); }
     __device__ __forceinline__ uint32_t kv_empty(int s) const { return bar(P::NS + s); }
-    __device__ __forceinline__ uint32_t q_full(int s) const { return bar(2 * P::NS + s); }
-    __device__ __forceinline__ uint32_t q_empty(int s) const { return bar(2 * P::NS + P::QS + s); }
-    __device__ __forceinline__ uint32_t s_full(int s) const { return bar(2 * P::NS + 2 * P::QS + s); }
-    __device__ __forceinline__ uint32_t p_ready(int s) const { return bar(2 * P::NS + 2 * P::QS + 2 + s); }
-    __device__ __forceinline__ uint32_t o_done(int m) const { return bar(2 * P::NS + 2 * P::QS + 4 + m); }
-    __device__ __forceinline__ uint32_t tile_full(int i) const { return bar(2 * P::NS + 2 * P::QS + 4 + P::NM + i); }
-    __device__ __forceinline__ uint32_t tile_empty(int i) const { return bar(2 * P::NS + 2 * P::QS + 4 + P::NM + P::TILES + i); }
-    __device__ __forceinline__ uint32_t last() const { return bar(P::BARS - 1); }
+    __device__ __forceinline__ uint32_t q_full(int s) const { return bar(B_Q + s); }
+    __device__ __forceinline__ uint32_t q_empty(int s) const { return bar(B_Q + P::QS + s); }
+    __device__ __forceinline__ uint32_t s_full(int s) const { return bar(B_S + s); }
+    __device__ __forceinline__ uint32_t p_ready(int s) const { return bar(B_S + 2 + s); }
+    __device__ __forceinline__ uint32_t o_done(int m) const { return bar(B_O + m); }
+    __device__ __forceinline__ uint32_t tile_full(int i) const { return bar(B_TILE + i); }
+    __device__ __forceinline__ uint32_t tile_empty(int i) const { return bar(B_TILE + P::TILES + i); }
+    __device__ __forceinline__ uint32_t told() const { return bar(B_END); }       // the second group's references are there
+    __device__ __forceinline__ uint32_t taken() const { return bar(B_END + 1); }  // its O has been read
+    __device__ __forceinline__ uint32_t last() const { return bar(B_END + 2); }
+    __device__ __forceinline__ uint32_t arrived(int i) const { return bar(B_RAW + i); }  // copies that need hands
+    __device__ __forceinline__ uint32_t raw_empty(int stage) const { return bar(B_RAW + P::ARRIVALS + stage); }
+    __device__ __forceinline__ uint32_t sent(int warp) const { return at + SENT + 4 * warp; }  // a copying warp's next tile
     __device__ __forceinline__ TreeTile& tile(int t) const { return reinterpret_cast<TreeTile*>(base + TILE)[t % P::TILES]; }
     __device__ __forceinline__ float* scale(int slot) const { return reinterpret_cast<float*>(base + SCALE) + slot * P::ROWS; }
+    __device__ __forceinline__ float2* join() const { return reinterpret_cast<float2*>(base + JOIN); }
+    __device__ __forceinline__ long long* scan() const { return reinterpret_cast<long long*>(base + SCAN); }
+    __device__ __forceinline__ uint32_t* tmem() const { return reinterpret_cast<uint32_t*>(base + END - 8); }
+    __device__ __forceinline__ int* stop() const { return reinterpret_cast<int*>(base + END - 4); }
+    static_assert(TILE % 8 == 0 && JOIN % 8 == 0 && END <= P::SMEM, "shared memory");
 };
 
+// One lane of a converged warp.
+__device__ __forceinline__ bool elected()
+{
+    uint32_t one;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(one));
+    return one != 0;
+}
 // ---------------------------------------------------------------------------
-// The copying warps.  Each has a quarter of a tile's tokens.  16-bit elements
-// go by asynchronous copies straight to the permuted places that the tensor
-// core reads; 8-bit ones to a stage that their own thread then turns into
-// fp16, exactly.  Fills (keys, values, keys ..) are handed over in order, LAG
-// of them after they were sent on their way.
+// The copying warps.  Two take the keys of alternate tiles and two the values,
+// each a whole tile's, so that one looks pages up while others' copies queue
+// for memory (with a quarter of every tile each, all four did the one and then
+// the other: 6000 cycles a tile of 64 KB, half of them for the copies).  16-bit
+// elements go by asynchronous copies straight to the permuted places that the
+// tensor core reads, and arrive at the product's barrier by themselves; 8-bit
+// ones go to a stage that their own thread then turns into fp16, exactly.  A
+// warp goes round what it may do next (queries whose slot is free, a fill
+// whose slot is free, a fill that has arrived and needs its hands) and waits
+// for none while another is possible.  The fence between these writes and the
+// tensor core's reads is the issuing warp's: here it would wait for all copies
+// on their way.
 // ---------------------------------------------------------------------------
 template <typename P>
 struct TreeFeed {
     using Cur = TreeCursor<P::ROWS, P::TOKENS>;
-    static constexpr int CH = P::DIM * static_cast<int>(sizeof(typename P::CT)) / 16, STEPS = P::WARP_TOKENS * CH / 32;
-    static_assert(P::WARP_TOKENS * CH % 32 == 0, "whole steps of a warp");
+    static constexpr int CH = P::DIM * static_cast<int>(sizeof(typename P::CT)) / 16;  // 16-byte chunks of a token
+    static constexpr int BLOCKS = P::TOKENS / 32;  // of 32 tokens, one a lane; CH steps of the warp each
+    static constexpr int STEPS = CH % 8 == 0 ? 8 : 4;  // at once
+    static_assert(CH % STEPS == 0, "whole groups of steps");
     static constexpr int QCH = P::DIM * 2 / 16;
     const TreeArgs& a;
     const TreeSmem<P>& sm;
     volatile int* stop;
     int warp, lane, chunks, qchunks;
-    uint64_t once, often;  // how long L2 keeps lines
-    // Where this tile's token of the lane begins in the cache (lanes below WARP_TOKENS), which of them are in it.
-    uint32_t off_lo = 0, off_hi = 0, in = 0;
-    // The next tile's, while its page number is on its way.
-    int page = -1, slot = 0;
-    uint32_t head = 0;
-    int done = 0;                 // fills handed over
-    uint32_t firsts = 0, mixeds = 0;  // bits of the last 32 tiles, by number
-    int q_wanted = 0, q_filled = 0, q_handed = 0;  // queries of items: met, sent on their way, handed over
+    bool values;             // whose the warp is
+    uint64_t once, often;    // how long L2 keeps lines
+    // The warp's next tile, whose page numbers are on their way.
+    int pages[BLOCKS];
+    uint64_t at[BLOCKS];     // of the lane's tokens in their pages
+    TreeSeq q;
+    int b, h, row0, rows, token0, flags;
+    bool alone;              // whether no other item reads these tokens
+    int tile, passed = 0;    // its number; tiles that the cursor has passed
+    int done;                // the warp's oldest tile that may still need its hands
+    uint32_t mixeds = 0;     // bits of the last 32 tiles, by number
+    uint32_t phases = 0;     // of `arrived`, by number (16-bit)
+    Cur item;                // the next item whose queries are wanted, the tile it begins with, and how many were before
+    int item_tile = 0, filled = 0;
 
-    __device__ TreeFeed(const TreeArgs& a_, const TreeSmem<P>& sm_, volatile int* stop_)
+    __device__ TreeFeed(const TreeArgs& a_, const TreeSmem<P>& sm_, volatile int* stop_, const Cur& cur)
         : a(a_), sm(sm_), stop(stop_), warp((threadIdx.x >> 5) - P::SOFTMAX / 32), lane(threadIdx.x & 31),
-          chunks(a_.head_dim * static_cast<int>(sizeof(typename P::CT)) / 16), qchunks(a_.head_dim * 2 / 16)
+          chunks(a_.head_dim * static_cast<int>(sizeof(typename P::CT)) / 16), qchunks(a_.head_dim * 2 / 16), values(warp & 1), tile(warp >> 1),
+          done(warp >> 1), item(cur)
     {
         asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(once));
         asm("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(often));
     }
+    static __device__ __forceinline__ void arrive_with_copies(uint32_t bar)
+    {
+        asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+    }
     // A row's 16-byte chunk of an operand of `rows` rows.
     static __device__ __forceinline__ uint32_t place(int row, int c, int rows) { return (c >> 3) * (rows * 128) + row * 128 + ((c ^ row) & 7) * 16; }
 
-    __device__ __forceinline__ void look_up(const Cur& cur)
+    // Which of the barriers `arrived` is that of the warp's fill of tile t.
+    __device__ __forceinline__ int arrival(int t) const
     {
-        const int token = (cur.s.tile0 + cur.tile) * P::TOKENS + warp * P::WARP_TOKENS + lane;
-        page = -1;
-        if (lane < P::WARP_TOKENS && token >= cur.s.start && token < cur.s.end) {
-            const uint32_t column = __umulhi(2u * token, a.page_magic) >> a.page_shift;
-            slot = token - static_cast<int>(column) * a.page_size;
-            page = a.table[static_cast<uint64_t>(cur.b) * a.table_stride + column];
+        return P::SMALL ? (2 * t + (values ? 1 : 0)) % (P::SMALL ? P::RS : 1) : (t & 1) * 4 + (t >> 1 & 3);
+    }
+    // What the warp has sent (16-bit) or handed over (8-bit), for the others.
+    __device__ __forceinline__ void tell(int next)
+    {
+        if (P::NS % 4 != 0 && lane == 0)
+            asm volatile("st.release.cta.shared::cta.s32 [%0], %1;" ::"r"(sm.sent(warp)), "r"(next) : "memory");
+    }
+    // Whether fill f's slot is free.  A parity tells two phases apart only, so the fill before it in the slot, another warp's
+    // where the slots are no multiple of the warps, has to have been sent.
+    __device__ __forceinline__ bool free(int f) const
+    {
+        const int before = f - P::NS;
+        if (P::NS % 4 != 0 && before >= 0) {
+            int next;
+            asm volatile("ld.acquire.cta.shared::cta.s32 %0, [%1];" : "=r"(next) : "r"(sm.sent((before & 1) + (before >> 1 & 1) * 2)) : "memory");
+            if (!__all_sync(~0u, next > before >> 1))
+                return false;
         }
-        head = cur.h;
+        return __all_sync(~0u, bar_poll(sm.kv_empty(f % P::NS), (f / P::NS & 1) ^ 1));
     }
-    __device__ __forceinline__ void found()
+    // Moves the cursor on to tile `tile`, the warp's next, and asks for its pages.
+    __device__ __forceinline__ void look(Cur& cur, const Run& line, int n)
     {
-        const bool ok = page >= 0 && page < a.pages;
-        const uint64_t off = ok ? static_cast<uint32_t>(page) * a.page_stride + static_cast<uint32_t>(slot) * a.token_stride + head * a.head_stride : 0;
-        off_lo = static_cast<uint32_t>(off);
-        off_hi = static_cast<uint32_t>(off >> 32);
-        in = __ballot_sync(~0u, ok);
+        for (; passed < n; ++passed) {
+            const int t = passed;
+            const bool begins = cur.tile == 0, ends = cur.tile + 1 == cur.s.tiles, mine = t == tile;
+            const int first_token = (cur.s.tile0 + cur.tile) * P::TOKENS;
+            if (mine) {
+                const bool mixed = tree_mixed(a, cur.q, first_token, P::TOKENS);
+                mixeds = (mixeds & ~(1u << (t & 31))) | (mixed ? 1u : 0u) << (t & 31);
+                q = cur.q;
+                b = cur.b;
+                h = cur.h;
+                row0 = cur.rt * P::ROWS;
+                rows = cur.rows(a);
+                token0 = first_token;
+                flags = (begins || t == 0 ? kTileFirst : 0) | (ends || t + 1 == n ? kTileLast : 0) | (begins ? kTileBegins : 0) | (ends ? kTileEnds : 0) |
+                        (mixed ? kTreeMixed : 0);
+                alone = row_blocks<P::ROWS>(a, cur.q) == 1;
+#pragma unroll
+                for (int k = 0; k < BLOCKS; ++k) {
+                    const int token = first_token + 32 * k + lane;
+                    pages[k] = -1;
+                    if (token >= cur.s.start && token < cur.s.end) {
+                        const uint32_t column = __umulhi(2u * token, a.page_magic) >> a.page_shift;
+                        pages[k] = a.table[static_cast<uint64_t>(cur.b) * a.table_stride + column];
+                        at[k] = static_cast<uint32_t>(token - static_cast<int>(column) * a.page_size) * a.token_stride +
+                                static_cast<uint32_t>(cur.h) * a.head_stride;
+                    }
+                }
+            }
+            if (begins && n - t < cur.s.tiles && threadIdx.x == P::SOFTMAX)
+                leave_job(a, cur, line, t);
+            if (t + 1 < n) {
+                if (ends)
+                    cur.next_item(a);
+                else
+                    ++cur.tile;
+            }
+            if (mine) {
+                ++passed;
+                return;
+            }
+        }
     }
-    // The queries of an item, as its rows, to their slot, which is free.  LATE: they are there on return.
-    template <bool LATE>
-    __device__ __forceinline__ void queries(const TreeSeq& q, int h, int row0, int rows)
+    // The queries of the next item, where their slot is free.  All copying warps take a part.
+    __device__ __forceinline__ bool queries(int n)
     {
-        const int s = q_filled++ % P::QS;
-        const uint32_t to = sm.q(s);
+        const int s = filled % P::QS;
+        if (item_tile >= n || !__all_sync(~0u, bar_poll(sm.q_empty(s), (filled / P::QS & 1) ^ 1)))
+            return false;
+        const int first = item.q.first, h = item.h, row0 = item.rt * P::ROWS, rows = item.rows(a);
+        const uint32_t to = s * P::Q;
         if constexpr (!P::SCALED) {
-#pragma unroll 8
+#pragma unroll 4
             for (int x = warp * 32 + lane; x < P::ROWS * QCH; x += 128) {
                 const int row = x / QCH, c = x - row * QCH, i = (row0 + row) / a.group, g = row0 + row - i * a.group;
                 const bool read = row < rows && c < qchunks;
-                const char* from = a.q;
+                const char* from_q = a.q;
                 if (read)
-                    from += static_cast<uint64_t>(q.first + i) * a.q_stride + (static_cast<uint64_t>(h) * a.group + g) * a.head_dim * 2 + c * 16;
-                const uint32_t dst = (row >> 7) * (128 * P::DIM * 2) + place(row & 127, c, 128);
-                if constexpr (LATE)
-                    *reinterpret_cast<uint4*>(sm.base + (to - sm.at) + dst) = read ? *reinterpret_cast<const uint4*>(from) : make_uint4(0, 0, 0, 0);
-                else
-                    cp_async16(to + dst, from, read);
+                    from_q += static_cast<uint64_t>(first + i) * a.q_stride + (static_cast<uint64_t>(h) * a.group + g) * a.head_dim * 2 + c * 16;
+                cp_async16(sm.at + to + (row >> 7) * (128 * P::DIM * 2) + place(row & 127, c, 128), from_q, read);
             }
+            arrive_with_copies(sm.q_full(s));
         } else {
             // bf16 queries on an 8-bit cache: scaled by a power of two a row, so that the largest element becomes 2^14 or more
             // and those down to 2^-28 of it keep all their bits in fp16.
@@ -241,7 +347,7 @@ struct TreeFeed {
                 const int i = (row0 + row) / a.group, g = row0 + row - i * a.group;
                 uint4 w = make_uint4(0, 0, 0, 0);
                 if (row < rows && lane < qchunks)
-                    w = *reinterpret_cast<const uint4*>(a.q + static_cast<uint64_t>(q.first + i) * a.q_stride +
+                    w = *reinterpret_cast<const uint4*>(a.q + static_cast<uint64_t>(first + i) * a.q_stride +
                                                         (static_cast<uint64_t>(h) * a.group + g) * a.head_dim * 2 + lane * 16);
                 const float2 f[4] = {Lanes<typename P::T>::two(w.x), Lanes<typename P::T>::two(w.y), Lanes<typename P::T>::two(w.z),
                                      Lanes<typename P::T>::two(w.w)};
@@ -260,140 +366,402 @@ struct TreeFeed {
                     x.y = Lanes<__half>::word(f[1].x * down, f[1].y * down);
                     x.z = Lanes<__half>::word(f[2].x * down, f[2].y * down);
                     x.w = Lanes<__half>::word(f[3].x * down, f[3].y * down);
-                    *reinterpret_cast<uint4*>(sm.base + (to - sm.at) + (row >> 7) * (128 * P::DIM * 2) + place(row & 127, lane, 128)) = x;
+                    *reinterpret_cast<uint4*>(sm.base + to + (row >> 7) * (128 * P::DIM * 2) + place(row & 127, lane, 128)) = x;
                 }
                 if (lane == 0)  // finite: an infinite factor would make the scores of keys that are 0 NaN
                     scale[row] = fmaxf(fminf(ldexpf(a.scale2, e), FLT_MAX), -FLT_MAX);
             }
+            bar_arrive(sm.q_full(s));
         }
-    }
-    __device__ __forceinline__ uint32_t q_phase() const { return (q_filled / P::QS & 1) ^ 1; }
-    // Sends fill f (of keys or of values) on its way.
-    __device__ __forceinline__ bool send(int f, const char* from, uint64_t policy)
-    {
-        uint32_t to;
-        if constexpr (P::SMALL) {
-            to = smem_addr(sm.raw(f % P::RS));
-        } else {
-            if (!bar_wait(sm.kv_empty(f % P::NS), (f / P::NS & 1) ^ 1, stop))
-                return false;
-            to = sm.kv(f % P::NS);
-        }
-#pragma unroll
-        for (int i = 0; i < STEPS; ++i) {
-            const int row = (lane + 32 * i) / CH, c = lane + 32 * i - row * CH;
-            const uint32_t lo = __shfl_sync(~0u, off_lo, row), hi = __shfl_sync(~0u, off_hi, row);
-            const bool read = (in >> row & 1) != 0 && c < chunks;
-            const uint64_t at = read ? (static_cast<uint64_t>(hi) << 32 | lo) + c * 16 : 0;
-            // an 8-bit chunk lies where its own thread finds it
-            const uint32_t dst = P::SMALL ? to + (i * 128 + warp * 32 + lane) * 16 : to + place(warp * P::WARP_TOKENS + row, c, P::TOKENS);
-            cp_async16(dst, from + at, read, policy);
-        }
-        cp_async_commit();
+        ++filled;
+        item_tile += item.s.tiles - item.tile;
+        if (item_tile < n)
+            item.next_item(a);
         return true;
     }
-    // Hands over the oldest fill, whose copies have arrived.
-    __device__ __forceinline__ bool hand_over()
+    // Sends tile `tile`'s keys or values on their way, and says what the tile is.
+    __device__ __forceinline__ void send(Cur& cur, const Run& line, int n)
     {
-        const int f = done++, t = f >> 1;
-        const bool values = f & 1, mixed = values && (mixeds >> (t & 31) & 1) != 0, first = !values && (firsts >> (t & 31) & 1) != 0;
-        if (first && q_filled == q_handed) {
-            // The queries' slot was not free when the keys were sent.  It is when what was handed over before has been used.
-            if (!bar_wait(sm.q_empty(q_filled % P::QS), q_phase(), stop) || !bar_wait(sm.tile_full(t % P::TILES), t / P::TILES & 1, stop))
-                return false;
-            const TreeTile& tile = sm.tile(t);
-            queries<true>(tile.q, tile.head, tile.row0, tile.rows);
+        const int t = tile, f = 2 * t + (values ? 1 : 0);
+        uint32_t in[BLOCKS], lo[BLOCKS], hi[BLOCKS];
+        bool whole = chunks == CH;
+#pragma unroll
+        for (int k = 0; k < BLOCKS; ++k) {
+            const bool ok = pages[k] >= 0 && pages[k] < a.pages;
+            const uint64_t off = ok ? static_cast<uint32_t>(pages[k]) * a.page_stride + at[k] : 0;
+            lo[k] = static_cast<uint32_t>(off);
+            hi[k] = static_cast<uint32_t>(off >> 32);
+            in[k] = __ballot_sync(~0u, ok);
+            whole = whole && in[k] == ~0u;
         }
+        if (!values && lane == 0) {
+            TreeTile& x = sm.tile(t);
+            x.q = q;
+            x.head = h;
+            x.row0 = row0;
+            x.rows = rows;
+            x.token0 = token0;
+            x.b = b;
+            x.flags = flags;
+#pragma unroll
+            for (int k = 0; k < BLOCKS; ++k)
+                x.valid[k] = in[k];
+            bar_arrive(sm.tile_full(t % P::TILES));
+        }
+        const bool hands = P::SMALL || (values && (flags & kTreeMixed));
+        const char* const base = values ? a.v : a.k;
+        const uint32_t to = P::SMALL ? smem_addr(sm.raw(f % (P::SMALL ? P::RS : 1))) : sm.kv(f % P::NS);
+        const uint64_t policy = alone ? once : often;
+        tile += 2;
+        look(cur, line, n);
+#pragma unroll
+        for (int k = 0; k < BLOCKS; ++k) {
+#pragma unroll 1
+            for (int i0 = 0; i0 < CH; i0 += STEPS) {
+                uint32_t x[STEPS], y[STEPS];  // all shuffles, then all copies
+#pragma unroll
+                for (int i = 0; i < STEPS; ++i) {
+                    const int row = (lane + 32 * (i0 + i)) / CH;
+                    x[i] = __shfl_sync(~0u, lo[k], row);
+                    y[i] = __shfl_sync(~0u, hi[k], row);
+                }
+#pragma unroll
+                for (int i = 0; i < STEPS; ++i) {
+                    const int row = (lane + 32 * (i0 + i)) / CH, c = lane + 32 * (i0 + i) - row * CH;
+                    const char* const from = base + (static_cast<uint64_t>(y[i]) << 32 | x[i]) + c * 16;
+                    // an 8-bit chunk lies where its own thread finds it
+                    const uint32_t dst = P::SMALL ? to + ((k * CH + i0 + i) * 32 + lane) * 16 : to + place(32 * k + row, c, P::TOKENS);
+                    if (whole) {
+                        cp_async16_all(dst, from, policy);
+                    } else {
+                        const bool read = (in[k] >> row & 1) != 0 && c < chunks;
+                        cp_async16(dst, read ? from : base, read, policy);
+                    }
+                }
+            }
+        }
+        arrive_with_copies(hands ? sm.arrived(arrival(t)) : sm.kv_full(f % P::NS));
+        if (!P::SMALL)
+            tell(tile);
+    }
+    // 8-bit: turns the warp's oldest fill, once it is here and its slot is free, into fp16 and hands it over.
+    __device__ __forceinline__ bool convert()
+    {
+        const int t = done, f = 2 * t + (values ? 1 : 0);
+        constexpr int RS = P::SMALL ? P::RS : 1;
+        if (t >= tile || !free(f) || !__all_sync(~0u, bar_poll(sm.arrived(arrival(t)), f / RS & 1)))
+            return false;
+        done += 2;
+        const bool mixed = values && (mixeds >> (t & 31) & 1) != 0;
         char* const to = sm.base + (sm.kv(f % P::NS) - sm.at);
+        const char* const raw = sm.raw(f % RS);
         bool bad = false;
-        if constexpr (P::SMALL) {
-            if (!bar_wait(sm.kv_empty(f % P::NS), (f / P::NS & 1) ^ 1, stop))
-                return false;
-            const char* const raw = sm.raw(f % P::RS);
+#pragma unroll 1
+        for (int i0 = 0; i0 < BLOCKS * CH; i0 += STEPS) {
+            uint4 all[STEPS];  // loads before stores, which the compiler may not exchange
+#pragma unroll
+            for (int i = 0; i < STEPS; ++i)
+                all[i] = *reinterpret_cast<const uint4*>(raw + ((i0 + i) * 32 + lane) * 16);
 #pragma unroll
             for (int i = 0; i < STEPS; ++i) {
-                const int row = (lane + 32 * i) / CH, c = lane + 32 * i - row * CH;
-                const uint4 w = *reinterpret_cast<const uint4*>(raw + (i * 128 + warp * 32 + lane) * 16);
-                uint32_t h[8] = {half2_of_e4m3(w.x), half2_of_e4m3(w.x >> 16), half2_of_e4m3(w.y), half2_of_e4m3(w.y >> 16),
+                const int row = (lane + 32 * (i0 + i)) / CH, c = lane + 32 * (i0 + i) - row * CH;
+                const uint4 w = all[i];
+                uint32_t x[8] = {half2_of_e4m3(w.x), half2_of_e4m3(w.x >> 16), half2_of_e4m3(w.y), half2_of_e4m3(w.y >> 16),
                                  half2_of_e4m3(w.z), half2_of_e4m3(w.z >> 16), half2_of_e4m3(w.w), half2_of_e4m3(w.w >> 16)};
                 if (mixed) {
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        const uint32_t x = not_finite<__half>(h[k]);
-                        bad = bad || x != 0;
-                        h[k] &= ~x;
+                    for (int j = 0; j < 8; ++j) {
+                        const uint32_t y = not_finite<__half>(x[j]);
+                        bad = bad || y != 0;
+                        x[j] &= ~y;
                     }
                 }
-                const int r = warp * P::WARP_TOKENS + row;
-                *reinterpret_cast<uint4*>(to + place(r, 2 * c, P::TOKENS)) = make_uint4(h[0], h[1], h[2], h[3]);
-                *reinterpret_cast<uint4*>(to + place(r, 2 * c + 1, P::TOKENS)) = make_uint4(h[4], h[5], h[6], h[7]);
-            }
-        } else if (mixed) {
-#pragma unroll 4
-            for (int i = 0; i < STEPS; ++i) {
-                const int row = (lane + 32 * i) / CH, c = lane + 32 * i - row * CH;
-                uint4* const p = reinterpret_cast<uint4*>(to + place(warp * P::WARP_TOKENS + row, c, P::TOKENS));
-                const uint4 w = *p;
-                const uint4 x = make_uint4(not_finite<typename P::MT>(w.x), not_finite<typename P::MT>(w.y), not_finite<typename P::MT>(w.z),
-                                           not_finite<typename P::MT>(w.w));
-                if ((x.x | x.y | x.z | x.w) != 0) {
-                    bad = true;
-                    *p = make_uint4(w.x & ~x.x, w.y & ~x.y, w.z & ~x.z, w.w & ~x.w);
-                }
+                *reinterpret_cast<uint4*>(to + place(row, 2 * c, P::TOKENS)) = make_uint4(x[0], x[1], x[2], x[3]);
+                *reinterpret_cast<uint4*>(to + place(row, 2 * c + 1, P::TOKENS)) = make_uint4(x[4], x[5], x[6], x[7]);
             }
         }
-        if (bad)
-            sm.tile(t).bad[warp] = 1;
-        fence_async_proxy();
+        if (mixed) {
+            bad = __any_sync(~0u, bad);
+            if (lane == 0)
+                sm.tile(t).bad = bad;
+        }
+        bar_arrive(sm.kv_full(f % P::NS));
+        tell(done);
+        return true;
+    }
+    // 16-bit: the values of the warp's oldest tile that rows see in part, once they are here: infinite ones and NaN become 0.
+    __device__ __forceinline__ bool look_through()
+    {
+        while (done < tile && (!values || (mixeds >> (done & 31) & 1) == 0))
+            done += 2;
+        if (done >= tile)
+            return false;
+        const int t = done, s = (2 * t + 1) % P::NS, i = arrival(t);
+        if (!__all_sync(~0u, bar_poll(sm.arrived(i), phases >> i & 1)))
+            return false;
+        phases ^= 1u << i;
+        done += 2;
+        uint4* const all = reinterpret_cast<uint4*>(sm.base + (sm.kv(s) - sm.at));
+        bool bad = false;
+#pragma unroll 8
+        for (int i = lane; i < P::TOKENS * CH; i += 32) {  // wherever the chunks lie
+            const uint4 w = all[i];
+            const uint4 x = make_uint4(not_finite<typename P::MT>(w.x), not_finite<typename P::MT>(w.y), not_finite<typename P::MT>(w.z),
+                                       not_finite<typename P::MT>(w.w));
+            if ((x.x | x.y | x.z | x.w) != 0) {
+                bad = true;
+                all[i] = make_uint4(w.x & ~x.x, w.y & ~x.y, w.z & ~x.z, w.w & ~x.w);
+            }
+        }
+        bad = __any_sync(~0u, bad);
+        if (lane == 0)
+            sm.tile(t).bad = bad;
         __syncwarp();
-        if (lane == 0) {
-            if (first)
-                bar_arrive(sm.q_full(q_handed % P::QS));
-            bar_arrive(sm.kv_full(f % P::NS));
+        bar_arrive(sm.kv_full(s));
+        return true;
+    }
+    // Whether the warp's next fill has where to go.
+    __device__ __forceinline__ bool room() const
+    {
+        if (P::SMALL ? (tile - done) / 2 >= P::RS / 4 : !free(2 * tile + (values ? 1 : 0)))
+            return false;
+        return values || __all_sync(~0u, bar_poll(sm.tile_empty(tile % P::TILES), (tile / P::TILES & 1) ^ 1));
+    }
+    // Whether nothing has happened for too long, or the block stops.
+    __device__ __forceinline__ bool gave_up(unsigned long long& idle_since) const
+    {
+        unsigned long long now;
+        asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(now));
+        idle_since = idle_since == 0 ? now : idle_since;
+        const bool late = now - idle_since > kTreeWaitLimitNs;
+        if (late && *stop == 0) {
+            *stop = 1;
+            atomicAdd(&g_tree_wait_timeouts, 1u);
         }
-        q_handed += first;
+        return __any_sync(~0u, late || *stop != 0);
+    }
+    // Waits for a phase, and fills queries' slots meanwhile.  Suspended between looks: a warp that polls takes others'
+    // instructions out of the cache.
+    __device__ __forceinline__ bool until(uint32_t bar, uint32_t parity, int n)
+    {
+        if (__all_sync(~0u, bar_test(bar, parity)))
+            return true;
+        unsigned long long idle_since = 0;
+        do
+            if (queries(n))
+                idle_since = 0;
+            else if (gave_up(idle_since))
+                return false;
+        while (!__all_sync(~0u, bar_test(bar, parity)));
+        return true;
+    }
+    // What tensor copies leave to do: queries, and of the fills that need hands a quarter each.
+    __device__ bool help(int n)
+    {
+        uint32_t used = 0;  // phases of `arrived` (16-bit)
+        for (int t = 0; t < n; ++t) {
+            queries(n);
+            if (!until(sm.tile_full(t % P::TILES), t / P::TILES & 1, n))
+                return false;
+            TreeTile& x = sm.tile(t);
+            const bool mixed = x.flags & kTreeMixed;
+            if constexpr (P::SMALL) {
+                for (int f = 2 * t; f < 2 * t + 2; ++f) {
+                    constexpr int RS = P::SMALL ? P::RS : 1;
+                    if (!until(sm.arrived(f % RS), f / RS & 1, n) || !until(sm.kv_empty(f % P::NS), (f / P::NS & 1) ^ 1, n))
+                        return false;
+                    const bool sift = (f & 1) != 0 && mixed;
+                    char* const to = sm.base + (sm.kv(f % P::NS) - sm.at);
+                    const char* const raw = sm.raw(f % RS);
+                    bool bad = false;
+                    constexpr int QUARTER = BLOCKS * CH / 4, ONCE = QUARTER % 4 == 0 ? 4 : 2;  // steps of the warp, and at once
+                    static_assert(QUARTER % ONCE == 0 && BLOCKS * CH % 4 == 0, "whole groups of steps");
+#pragma unroll 1
+                    for (int i0 = 0; i0 < QUARTER; i0 += ONCE) {
+                        uint4 all[ONCE];
+#pragma unroll
+                        for (int i = 0; i < ONCE; ++i)
+                            all[i] = *reinterpret_cast<const uint4*>(raw + (((i0 + i) * 4 + warp) * 32 + lane) * 16);
+#pragma unroll
+                        for (int i = 0; i < ONCE; ++i) {
+                            const int at_chunk = ((i0 + i) * 4 + warp) * 32 + lane, row = at_chunk / CH, c = at_chunk - row * CH;
+                            const uint4 w = all[i];
+                            uint32_t y[8] = {half2_of_e4m3(w.x), half2_of_e4m3(w.x >> 16), half2_of_e4m3(w.y), half2_of_e4m3(w.y >> 16),
+                                             half2_of_e4m3(w.z), half2_of_e4m3(w.z >> 16), half2_of_e4m3(w.w), half2_of_e4m3(w.w >> 16)};
+                            if (sift) {
+                                const bool in = x.valid[row >> 5] >> (row & 31) & 1;
+#pragma unroll
+                                for (int j = 0; j < 8; ++j) {
+                                    const uint32_t z = not_finite<__half>(y[j]);
+                                    bad = bad || (in && z != 0);
+                                    y[j] = in ? y[j] & ~z : 0u;
+                                }
+                            }
+                            *reinterpret_cast<uint4*>(to + place(row, 2 * c, P::TOKENS)) = make_uint4(y[0], y[1], y[2], y[3]);
+                            *reinterpret_cast<uint4*>(to + place(row, 2 * c + 1, P::TOKENS)) = make_uint4(y[4], y[5], y[6], y[7]);
+                        }
+                    }
+                    if (bad)
+                        x.bad = 1;
+                    __syncwarp();
+                    if (lane == 0) {
+                        bar_arrive(sm.kv_full(f % P::NS));
+                        bar_arrive(sm.raw_empty(f % RS));
+                    }
+                }
+            } else if (mixed) {
+                const int s = (2 * t + 1) % P::NS, i = t % P::ARRIVALS;
+                if (!until(sm.arrived(i), used >> i & 1, n))
+                    return false;
+                used ^= 1u << i;
+                // Infinite values and NaN, and whatever lies where no token is, become 0.
+                bool bad = false;
+                char* const to = sm.base + (sm.kv(s) - sm.at);
+#pragma unroll 4
+                for (int j = warp * 32 + lane; j < P::TOKENS * P::DIM / 8; j += 128) {
+                    const int row = j / (P::DIM / 8), c = j - row * (P::DIM / 8);
+                    const bool in = x.valid[row >> 5] >> (row & 31) & 1;
+                    uint4* const p = reinterpret_cast<uint4*>(to + place(row, c, P::TOKENS));
+                    const uint4 w = *p;
+                    const uint4 y = make_uint4(not_finite<typename P::MT>(w.x), not_finite<typename P::MT>(w.y), not_finite<typename P::MT>(w.z),
+                                               not_finite<typename P::MT>(w.w));
+                    const bool found = (y.x | y.y | y.z | y.w) != 0;
+                    bad = bad || (in && found);
+                    if (!in)
+                        *p = make_uint4(0, 0, 0, 0);
+                    else if (found)
+                        *p = make_uint4(w.x & ~y.x, w.y & ~y.y, w.z & ~y.z, w.w & ~y.w);
+                }
+                if (bad)
+                    x.bad = 1;
+                __syncwarp();
+                if (lane == 0)
+                    bar_arrive(sm.kv_full(s));
+            }
+            __syncwarp();
+            if (lane == 0)
+                bar_arrive(sm.tile_empty(t % P::TILES));
+        }
+        unsigned long long idle_since = 0;
+        while (item_tile < n)  // the last items' queries may have no room yet
+            if (queries(n))
+                idle_since = 0;
+            else if (gave_up(idle_since))
+                return false;
         return true;
     }
     __device__ bool run(Cur cur, const Run& line, int n)
     {
+        look(cur, line, n);
+        unsigned long long idle_since = 0;
+        for (;;) {
+            bool moved;
+            if constexpr (P::SMALL)
+                moved = convert();
+            else
+                moved = look_through();
+            if (queries(n))
+                moved = true;
+            if (tile < n && room()) {
+                send(cur, line, n);
+                moved = true;
+            }
+            if (moved) {
+                idle_since = 0;
+                continue;
+            }
+            if (tile >= n && done >= n && item_tile >= n)
+                return true;
+            if (gave_up(idle_since))
+                return false;
+        }
+    }
+};
+
+// ---------------------------------------------------------------------------
+// Tensor copies, where pages and tiles divide each other and pages are whole
+// groups of eight tokens: one warp looks the tile's pages up and one of its
+// lanes asks for a box of up to 64 elements (16-bit; all of them in 8 bits) by
+// a page's tokens at a time, which arrives permuted as the tensor core reads
+// it.  What it brings for tokens that are not in the cache, and the rows of
+// pages that are none, are the helping warps' to clear.
+// ---------------------------------------------------------------------------
+template <typename P>
+struct TreeBoxes {
+    using Cur = TreeCursor<P::ROWS, P::TOKENS>;
+    const TreeArgs& a;
+    const TreeSmem<P>& sm;
+    const TreeMaps& maps;
+    volatile int* stop;
+    int lane, box, runs, blocks;  // tokens of a box, boxes of tokens and of elements in a tile
+    int run_of, block;            // the lane's box
+    uint64_t once, often;
+    int page = -1, slot = 0;
+
+    __device__ TreeBoxes(const TreeArgs& a_, const TreeSmem<P>& sm_, const TreeMaps& maps_, volatile int* stop_)
+        : a(a_), sm(sm_), maps(maps_), stop(stop_), lane(threadIdx.x & 31), box(min(a_.page_size, P::TOKENS)), runs(P::TOKENS / box),
+          blocks(P::SMALL ? 1 : (a_.head_dim + 63) / 64), run_of(lane / blocks), block(lane - run_of * blocks)
+    {
+        asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(once));
+        asm("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(often));
+    }
+    // The page of the lane's box; there are 32 at most (16 by 2 of 8 tokens, 8 by 4).
+    __device__ __forceinline__ void look_up(const Cur& cur)
+    {
+        const int token = (cur.s.tile0 + cur.tile) * P::TOKENS + run_of * box;
+        page = -1;
+        if (run_of < runs && token < cur.s.end && token + box > cur.s.start) {
+            const uint32_t column = __umulhi(2u * token, a.page_magic) >> a.page_shift;
+            slot = token - static_cast<int>(column) * a.page_size;
+            page = a.table[static_cast<uint64_t>(cur.b) * a.table_stride + column];
+        }
+    }
+    __device__ __forceinline__ void copy(uint32_t to, const void* map, int x, int token, int head, int at_page, uint32_t bar, uint64_t policy)
+    {
+        const int c1 = a.token_first ? token : head, c2 = a.token_first ? head : token;
+        asm volatile("cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1, {%2, %3, %4, %5}], [%6], %7;" ::"r"(to),
+                     "l"(map), "r"(x), "r"(c1), "r"(c2), "r"(at_page), "r"(bar), "l"(policy)
+                     : "memory");
+    }
+    __device__ bool run(Cur cur, const Run& line, int n)
+    {
         look_up(cur);
-        bool first = true;
         for (int t = 0; t < n; ++t) {
-            found();
             const bool begins = cur.tile == 0, ends = cur.tile + 1 == cur.s.tiles;
-            const int token0 = (cur.s.tile0 + cur.tile) * P::TOKENS;
-            const bool mixed = tree_mixed(a, cur.q, token0, P::TOKENS);
-            first = first || begins;
+            const int token0 = (cur.s.tile0 + cur.tile) * P::TOKENS, head = cur.h;
+            const int good = page >= 0 && page < a.pages ? page : -1, at_slot = slot;
+            const uint32_t there = __ballot_sync(~0u, good >= 0);  // boxes
+            uint32_t valid[P::TOKENS / 32];
+            bool whole = true;
+#pragma unroll
+            for (int k = 0; k < P::TOKENS / 32; ++k) {
+                const int token = token0 + 32 * k + lane;
+                valid[k] = __ballot_sync(~0u, token >= cur.s.start && token < cur.s.end && (there >> ((32 * k + lane) / box * blocks) & 1) != 0);
+                whole = whole && valid[k] == ~0u;
+            }
+            const bool mixed = !whole || tree_mixed(a, cur.q, token0, P::TOKENS);
             if (!bar_wait(sm.tile_empty(t % P::TILES), (t / P::TILES & 1) ^ 1, stop))
                 return false;
-            TreeTile& tile = sm.tile(t);
             if (lane == 0) {
-                tile.valid[warp] = in;
-                tile.bad[warp] = 0;
-                if (warp == 0) {
-                    tile.q = cur.q;
-                    tile.head = cur.h;
-                    tile.row0 = cur.rt * P::ROWS;
-                    tile.rows = cur.rows(a);
-                    tile.token0 = token0;
-                    tile.b = cur.b;
-                    tile.flags = (first ? kTileFirst : 0) | (ends || t + 1 == n ? kTileLast : 0) | (begins ? kTileBegins : 0) | (ends ? kTileEnds : 0) |
-                                 (mixed ? kTreeMixed : 0);
-                    if (begins && n - t < cur.s.tiles)
-                        leave_job(a, cur, line, t);
-                }
+                TreeTile& x = sm.tile(t);
+                x.q = cur.q;
+                x.head = head;
+                x.row0 = cur.rt * P::ROWS;
+                x.rows = cur.rows(a);
+                x.token0 = token0;
+                x.b = cur.b;
+                x.bad = 0;
+                x.flags = (begins || t == 0 ? kTileFirst : 0) | (ends || t + 1 == n ? kTileLast : 0) | (begins ? kTileBegins : 0) | (ends ? kTileEnds : 0) |
+                          (mixed ? kTreeMixed : 0);
+#pragma unroll
+                for (int k = 0; k < P::TOKENS / 32; ++k)
+                    x.valid[k] = valid[k];
+                if (begins && n - t < cur.s.tiles)
+                    leave_job(a, cur, line, t);
                 bar_arrive(sm.tile_full(t % P::TILES));
             }
-            firsts = (firsts & ~(1u << (t & 31))) | (first ? 1u : 0u) << (t & 31);
-            mixeds = (mixeds & ~(1u << (t & 31))) | (mixed ? 1u : 0u) << (t & 31);
-            // The queries go with the keys where their slot is free and those of no earlier item wait for one.
-            if (first) {
-                ++q_wanted;
-                if (q_filled + 1 == q_wanted && __all_sync(~0u, bar_test(sm.q_empty(q_filled % P::QS), q_phase())))
-                    queries<false>(cur.q, cur.h, cur.rt * P::ROWS, cur.rows(a));
-            }
+            __syncwarp();
             const uint64_t policy = row_blocks<P::ROWS>(a, cur.q) == 1 ? once : often;
-            first = false;
             if (t + 1 < n) {
                 if (ends)
                     cur.next_item(a);
@@ -402,26 +770,43 @@ struct TreeFeed {
                 look_up(cur);
             }
             for (int f = 2 * t; f < 2 * t + 2; ++f) {
-                if (!send(f, f & 1 ? a.v : a.k, policy))
-                    return false;
-                if (f - done >= P::LAG) {
-                    cp_async_wait<P::LAG>();
-                    if (!hand_over())
+                uint32_t to, bar;
+                bool hands = P::SMALL;
+                if constexpr (P::SMALL) {
+                    constexpr int RS = P::SMALL ? P::RS : 1;
+                    if (!bar_wait(sm.raw_empty(f % RS), (f / RS & 1) ^ 1, stop))
                         return false;
+                    to = smem_addr(sm.raw(f % RS));
+                    bar = sm.arrived(f % RS);
+                } else {
+                    if (!bar_wait(sm.kv_empty(f % P::NS), (f / P::NS & 1) ^ 1, stop))
+                        return false;
+                    to = sm.kv(f % P::NS);
+                    hands = (f & 1) != 0 && mixed;
+                    bar = hands ? sm.arrived(t % P::ARRIVALS) : sm.kv_full(f % P::NS);
                 }
+                if (elected()) {
+                    const uint32_t bytes = __popc(there) * box * (P::SMALL ? P::DIM : 128);
+                    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+                    if (!hands)  // in the place of the helping warps
+                        asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], 3;" ::"r"(bar) : "memory");
+                }
+                __syncwarp();
+                if (good >= 0)  // each lane asks for its box
+                    copy(to + (P::SMALL ? run_of * box * P::DIM : block * (P::TOKENS * 128) + run_of * box * 128), f & 1 ? &maps.v : &maps.k, 64 * block,
+                         at_slot, head, good, bar, policy);
+                __syncwarp();
             }
         }
-        cp_async_wait<0>();
-        while (done < 2 * n)
-            if (!hand_over())
-                return false;
         return true;
     }
 };
 
 // ---------------------------------------------------------------------------
-// The products, issued by one thread: scores of step u + 1, then the weighted
-// values of step u, a step being a half of the rows of a tile.
+// The products: scores of step u + 1, then the weighted values of step u.  The
+// whole warp goes through the loop and one lane issues, so that descriptors and
+// addresses stay in uniform registers (a lane alone took some 150 cycles to
+// issue each).
 // ---------------------------------------------------------------------------
 template <typename P>
 __device__ bool tree_products(const TreeArgs& a, const TreeSmem<P>& sm, uint32_t tmem, int n, volatile int* stop)
@@ -432,61 +817,76 @@ __device__ bool tree_products(const TreeArgs& a, const TreeSmem<P>& sm, uint32_t
     int items = 0;        // whose queries have been waited for
     uint32_t firsts = 0;  // which of the last tiles begin the block's part of an item, by number
     const auto scores = [&](int u) {
-        const int t = u / P::NM, m = u % P::NM, s = 2 * t % P::NS;
+        const int t = P::tile_of(u), m = u % P::NM, s = 2 * t % P::NS;
         if (m == 0) {
-            if (!bar_wait_one(sm.tile_full(t % P::TILES), t / P::TILES & 1, stop))
+            if (!bar_wait(sm.tile_full(t % P::TILES), t / P::TILES & 1, stop))
                 return false;
-            const bool first = sm.tile(t).flags & kTileFirst;
+            const bool first = __shfl_sync(~0u, sm.tile(t).flags, 0) & kTileFirst;
             firsts = (firsts & ~(1u << (t & 31))) | (first ? 1u : 0u) << (t & 31);
             if (first) {
-                if (!bar_wait_one(sm.q_full(items % P::QS), items / P::QS & 1, stop))
+                if (!bar_wait(sm.q_full(items % P::QS), items / P::QS & 1, stop))
                     return false;
                 ++items;
             }
-            if (!bar_wait_one(sm.kv_full(s), 2 * t / P::NS & 1, stop))
+            if (!bar_wait(sm.kv_full(s), 2 * t / P::NS & 1, stop))
                 return false;
+            fence_async_proxy();  // between the copying warps' writes, which the barrier has shown, and the product's reads
         }
-        const int flags = sm.tile(t).flags;
+        const bool last = __shfl_sync(~0u, sm.tile(t).flags, 0) & kTileLast;
         tcgen05_after_sync();
-        const uint32_t q = sm.q((items - 1) % P::QS) + m * (128 * P::DIM * 2), k = sm.kv(s), d = tmem + (u & 1) * P::S_COLUMNS;
-        for (int j = 0; j < ksteps; ++j)
-            mma_shared(d, operand_desc(q + (j >> 2) * (128 * 128) + (j & 3) * 32, 16, 1024), operand_desc(k + (j >> 2) * (P::TOKENS * 128) + (j & 3) * 32, 16, 1024),
-                       desc_s, j > 0);
-        tcgen05_commit(sm.s_full(u & 1));
-        if (m == P::NM - 1) {
-            tcgen05_commit(sm.kv_empty(s));
-            if (flags & kTileLast)
-                tcgen05_commit(sm.q_empty((items - 1) % P::QS));
+        const uint64_t q = operand_desc(sm.q((items - 1) % P::QS) + m * (128 * P::DIM * 2), 16, 1024), k = operand_desc(sm.kv(s), 16, 1024);
+        const uint32_t d = tmem + (u & 1) * P::S_COLUMNS;
+        if (elected()) {
+            // 32 bytes on, then the next 64 elements' block; addresses count 16 bytes
+#pragma unroll
+            for (int j = 0; j < P::DIM / 16; ++j)
+                if (j < ksteps)
+                    mma_shared(d, q + (j >> 2) * (128 * 128 / 16) + (j & 3) * 2, k + (j >> 2) * (P::TOKENS * 128 / 16) + (j & 3) * 2, desc_s, j > 0);
+            tcgen05_commit(sm.s_full(u & 1));
+            if (m == P::NM - 1) {
+                tcgen05_commit(sm.kv_empty(s));
+                if (last)
+                    tcgen05_commit(sm.q_empty((items - 1) % P::QS));
+            }
         }
+        __syncwarp();
         return true;
     };
     if (!scores(0))
         return false;
     for (int u = 0; u < steps; ++u) {
-        const int t = u / P::NM, m = u % P::NM, f = 2 * t + 1, s = f % P::NS;
-        const bool begins = firsts >> (t & 31) & 1;
+        const int t = P::tile_of(u), f = 2 * t + 1, s = f % P::NS;
+        // Of the group's O: with alternate tiles, two of an item are first ones.
+        const bool begins = (firsts >> (t & 31) & 1) != 0 || (P::SPLIT && t > 0 && (firsts >> (t - 1 & 31) & 1) != 0);
         if (u + 1 < steps) {
             // The scores' buffer holds the weights of step u - 1 until its product is done.
-            if (u > 0 && !bar_wait_one(sm.o_done((u - 1) % P::NM), (u - 1) / P::NM & 1, stop))
+            if (u > 0 && !bar_wait(sm.o_done(P::group_of(u - 1)), P::phase_of(u - 1) & 1, stop))
                 return false;
             if (!scores(u + 1))
                 return false;
         }
-        if (!bar_wait_one(sm.p_ready(u & 1), u >> 1 & 1, stop))
+        if (!bar_wait(sm.p_ready(u & 1), u >> 1 & 1, stop))
             return false;
-        if (m == 0 && !bar_wait_one(sm.kv_full(s), f / P::NS & 1, stop))
-            return false;
-        tcgen05_after_sync();
-        const uint32_t p = tmem + (u & 1) * P::S_COLUMNS, o = tmem + P::O_COLUMN + m * 128, v = sm.kv(s);
-        for (int j = 0; j < P::TOKENS / 16; ++j) {
-            const uint64_t b = operand_desc(v + j * 2048, P::TOKENS * 128, 1024);
-            const uint32_t w = p + (j >> 1) * 32 + (j & 1) * 8;  // of 32 tokens 16 columns of weights, then 16 of what they leave
-            mma_tensor(o, w, b, desc_o, !(begins && j == 0));
-            mma_tensor(o, w + 16, b, desc_o, true);
+        if (u % P::NM == 0) {
+            if (!bar_wait(sm.kv_full(s), f / P::NS & 1, stop))
+                return false;
+            fence_async_proxy();
         }
-        tcgen05_commit(sm.o_done(m));
-        if (m == P::NM - 1)
-            tcgen05_commit(sm.kv_empty(s));
+        tcgen05_after_sync();
+        const uint32_t p = tmem + (u & 1) * P::S_COLUMNS, o = tmem + P::O_COLUMN + P::group_of(u) * 128;
+        const uint64_t v = operand_desc(sm.kv(s), P::TOKENS * 128, 1024);
+        if (elected()) {
+#pragma unroll
+            for (int j = 0; j < P::TOKENS / 16; ++j) {
+                const uint32_t w = p + (j >> 1) * 32 + (j & 1) * 8;  // of 32 tokens 16 columns of weights, then 16 of what they leave
+                mma_tensor(o, w, v + j * (2048 / 16), desc_o, !(begins && j == 0));
+                mma_tensor(o, w + 16, v + j * (2048 / 16), desc_o, true);
+            }
+            tcgen05_commit(sm.o_done(P::group_of(u)));
+            if (u % P::NM == P::NM - 1)
+                tcgen05_commit(sm.kv_empty(s));
+        }
+        __syncwarp();
     }
     return true;
 }
@@ -501,9 +901,11 @@ struct TreeSoft {
     const TreeArgs& a;
     const TreeSmem<P>& sm;
     volatile int* stop;
-    int m, row, lane;
-    uint32_t lanes;  // the warp's lanes in an address of tensor memory
-    uint32_t o;
+    int m, row, lane;    // group, row of the item
+    uint32_t lanes;      // the warp's lanes in an address of tensor memory
+    uint32_t o;          // the group's O
+    int joins = 0;       // items whose two O's were joined
+    bool awaits = false; // the second group's O of the last of them may not have been read yet
     float factor = 0.0f, reference = -INFINITY, total = 0.0f;
     TreeRow sees;
 
@@ -512,27 +914,20 @@ struct TreeSoft {
         const int warp = threadIdx.x >> 5;
         lane = threadIdx.x & 31;
         m = warp >> 2;
-        row = threadIdx.x;  // of the item
+        row = P::SPLIT ? threadIdx.x & 127 : threadIdx.x;
         lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
         o = tmem + lanes + P::O_COLUMN + m * 128;
-    }
-    static __device__ __forceinline__ uint32_t valid_word(const TreeTile& tile, int c)
-    {
-        if constexpr (P::WARP_TOKENS == 32)
-            return tile.valid[c];
-        else
-            return tile.valid[2 * c] | tile.valid[2 * c + 1] << 16;
     }
     // Which of 32 tokens of a tile the row sees.
     __device__ __forceinline__ uint32_t seen(const TreeTile& tile, int c) const
     {
-        const uint32_t word = valid_word(tile, c);
+        const uint32_t word = tile.valid[c];
         return tile.flags & kTreeMixed ? word & sees.sees(tile.token0 + 32 * c) : word;
     }
     // Weights of a tile whose scores lie at `s`.  PART: not every row sees every token.  CAP: with softcap.  One loop over
     // groups of 32 tokens, not unrolled: the four warps' instructions have to stay in the cache.
     template <bool PART, bool CAP>
-    __device__ __forceinline__ bool weights(const TreeTile& tile, uint32_t s, bool first, int t)
+    __device__ __forceinline__ bool weights(const TreeTile& tile, uint32_t s, bool first, int u)
     {
         constexpr int CHUNKS = P::TOKENS / 32;
         float most = -INFINITY;
@@ -557,7 +952,7 @@ struct TreeSoft {
         if (first || most - P::LIFT > reference + P::AHEAD)
             reference = most - P::LIFT;
         if (!first && __any_sync(~0u, reference != before)) {
-            if (!bar_wait(sm.o_done(m), (t - 1) & 1, stop))
+            if (!bar_wait(sm.o_done(m), P::phase_of(u) - 1 & 1, stop))
                 return false;
             tcgen05_after_sync();
             const float fix = reference == before ? 1.0f : exp2_fast(before - reference);
@@ -602,25 +997,25 @@ struct TreeSoft {
         tcgen05_wait_store();
         return true;
     }
-    __device__ __forceinline__ bool weights(const TreeTile& tile, uint32_t s, bool first, int t, bool part)
+    __device__ __forceinline__ bool weights(const TreeTile& tile, uint32_t s, bool first, int u, bool part)
     {
         if (a.softcap > 0.0f)
-            return weights<true, true>(tile, s, first, t);
-        return part ? weights<true, false>(tile, s, first, t) : weights<false, false>(tile, s, first, t);
+            return weights<true, true>(tile, s, first, u);
+        return part ? weights<true, false>(tile, s, first, u) : weights<false, false>(tile, s, first, u);
     }
-    // Waits for tile t's product with the values; the one before was waited for already.
-    __device__ __forceinline__ bool weighted(int t)
+    // Waits for step u's product with the values; the group's one before was waited for already.
+    __device__ __forceinline__ bool weighted(int u)
     {
-        if (!bar_wait(sm.o_done(m), t & 1, stop))
+        if (!bar_wait(sm.o_done(m), P::phase_of(u) & 1, stop))
             return false;
         tcgen05_after_sync();
         return true;
     }
     // Values that are infinite or NaN, in a tile that rows see in part: the product took 0 for them, and the rows that see
     // them get them here, out of the cache once more.
-    __device__ __forceinline__ bool poison(const TreeTile& tile, int t, bool valid)
+    __device__ __forceinline__ bool poison(const TreeTile& tile, int u, bool valid)
     {
-        if (!weighted(t))
+        if (!weighted(u))
             return false;
 #pragma unroll 1
         for (int c0 = 0; c0 < a.head_dim; c0 += 32) {
@@ -631,7 +1026,7 @@ struct TreeSoft {
 #pragma unroll 1
             for (int c = 0; c < P::TOKENS / 32 && valid; ++c) {
 #pragma unroll 1
-                for (uint32_t word = valid_word(tile, c) & sees.sees(tile.token0 + 32 * c); word != 0; word &= word - 1) {
+                for (uint32_t word = tile.valid[c] & sees.sees(tile.token0 + 32 * c); word != 0; word &= word - 1) {
                     const int token = tile.token0 + 32 * c + __ffs(word) - 1;
                     const uint32_t column = __umulhi(2u * token, a.page_magic) >> a.page_shift;
                     const int page = a.table[static_cast<uint64_t>(tile.b) * a.table_stride + column];
@@ -662,73 +1057,126 @@ struct TreeSoft {
         tcgen05_before_sync();
         return true;
     }
-    // The end of the block's part of an item: the result, or the part.
-    __device__ __forceinline__ bool finish(const TreeTile& tile, int t, bool began, bool any, bool valid)
+    // Before the group's O is written anew, or its references: that the first group has read them.
+    __device__ __forceinline__ bool joined()
     {
-        if (!weighted(t))
+        if (P::SPLIT && awaits) {
+            if (!bar_wait(sm.taken(), joins - 1 & 1, stop))
+                return false;
+            awaits = false;
+        }
+        return true;
+    }
+    // The end of the block's part of an item: the result, or the part.  u: the group's last step of it, -1: it had none.
+    __device__ __forceinline__ bool finish(const TreeTile& tile, int u, bool began, bool any, bool valid)
+    {
+        if (u >= 0 && !weighted(u))
             return false;
-        if (!any)
-            return true;
-        const bool whole = began && (tile.flags & kTileEnds);
-        const uint64_t out = valid ? tree_out_row(a, tile.q.first, tile.head, tile.row0 + row) : 0;
-        float* const part = a.part + slot_of(static_cast<int>(blockIdx.x), began) * a.slot_floats;
-        const float f = total == 0.0f ? 0.0f : a.v_scale / total;
-#pragma unroll 1
-        for (int c = 0; c < a.head_dim; c += 32) {
-            uint32_t x[32];
-            tmem_load32(o + c, x);
-            tcgen05_wait_load();
-            if (!valid)
-                continue;
-            if (whole) {
-                T* const to = reinterpret_cast<T*>(a.out) + out * a.head_dim + c;
-#pragma unroll
-                for (int i = 0; i < 32; i += 8)
-                    if (c + i < a.head_dim) {
-                        uint4 w;
-                        w.x = Lanes<T>::word(__uint_as_float(x[i]) * f, __uint_as_float(x[i + 1]) * f);
-                        w.y = Lanes<T>::word(__uint_as_float(x[i + 2]) * f, __uint_as_float(x[i + 3]) * f);
-                        w.z = Lanes<T>::word(__uint_as_float(x[i + 4]) * f, __uint_as_float(x[i + 5]) * f);
-                        w.w = Lanes<T>::word(__uint_as_float(x[i + 6]) * f, __uint_as_float(x[i + 7]) * f);
-                        *reinterpret_cast<uint4*>(to + i) = w;
-                    }
-            } else {
-                float* const to = part + static_cast<uint64_t>(row) * a.head_dim + c;
-#pragma unroll
-                for (int i = 0; i < 32; i += 4)
-                    if (c + i < a.head_dim)
-                        *reinterpret_cast<uint4*>(to + i) = make_uint4(x[i], x[i + 1], x[i + 2], x[i + 3]);
+        float mine = 1.0f, others = 0.0f;  // what the two O's are multiplied by
+        bool both = false;                 // whether the other one has a tile
+        const uint32_t other = o + 128;
+        if constexpr (P::SPLIT) {
+            if (m == 1) {
+                if (!joined())
+                    return false;
+                sm.join()[row] = make_float2(reference, u >= 0 ? total : -1.0f);
+                tcgen05_before_sync();
+                __syncwarp();
+                if (lane == 0)
+                    bar_arrive(sm.told());
+                ++joins;
+                awaits = true;
+                return true;
+            }
+            if (!bar_wait(sm.told(), joins++ & 1, stop))
+                return false;
+            tcgen05_after_sync();
+            const float2 x = sm.join()[row];
+            both = !(x.y < 0.0f);
+            if (both) {  // without a tile of the first group's own its reference is minus infinity, its sum 0
+                const float best = fmaxf(reference, x.x), base = base_of(best);
+                mine = exp2_fast(reference - base);
+                others = exp2_fast(x.x - base);
+                total = total * mine + x.y * others;
+                reference = best;
             }
         }
-        if (valid && whole && a.lse != nullptr)
-            a.lse[out] = lse_of(reference, total);
-        if (valid && !whole) {
-            part[static_cast<uint64_t>(a.slot_rows) * a.head_dim + row] = reference;
-            part[static_cast<uint64_t>(a.slot_rows) * (a.head_dim + 1) + row] = total;
+        if (any) {
+            const bool whole = began && (tile.flags & kTileEnds);
+            const uint64_t out = valid ? tree_out_row(a, tile.q.first, tile.head, tile.row0 + row) : 0;
+            float* const part = a.part + slot_of(static_cast<int>(blockIdx.x), began) * a.slot_floats;
+            const float f = !whole ? 1.0f : total == 0.0f ? 0.0f : a.v_scale / total;
+#pragma unroll 1
+            for (int c = 0; c < a.head_dim; c += 32) {
+                uint32_t x[32];
+                tmem_load32(o + c, x);
+                tcgen05_wait_load();
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                    x[i] = u < 0 ? 0u : __float_as_uint(__uint_as_float(x[i]) * mine);
+                if (both) {
+                    uint32_t y[32];
+                    tmem_load32(other + c, y);
+                    tcgen05_wait_load();
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        x[i] = __float_as_uint(fmaf(__uint_as_float(y[i]), others, __uint_as_float(x[i])));
+                }
+                if (!valid)
+                    continue;
+                if (whole) {
+                    T* const to = reinterpret_cast<T*>(a.out) + out * a.head_dim + c;
+#pragma unroll
+                    for (int i = 0; i < 32; i += 8)
+                        if (c + i < a.head_dim) {
+                            uint4 w;
+                            w.x = Lanes<T>::word(__uint_as_float(x[i]) * f, __uint_as_float(x[i + 1]) * f);
+                            w.y = Lanes<T>::word(__uint_as_float(x[i + 2]) * f, __uint_as_float(x[i + 3]) * f);
+                            w.z = Lanes<T>::word(__uint_as_float(x[i + 4]) * f, __uint_as_float(x[i + 5]) * f);
+                            w.w = Lanes<T>::word(__uint_as_float(x[i + 6]) * f, __uint_as_float(x[i + 7]) * f);
+                            *reinterpret_cast<uint4*>(to + i) = w;
+                        }
+                } else {
+                    float* const to = part + static_cast<uint64_t>(row) * a.head_dim + c;
+#pragma unroll
+                    for (int i = 0; i < 32; i += 4)
+                        if (c + i < a.head_dim)
+                            *reinterpret_cast<uint4*>(to + i) = make_uint4(x[i], x[i + 1], x[i + 2], x[i + 3]);
+                }
+            }
+            if (valid && whole && a.lse != nullptr)
+                a.lse[out] = lse_of(reference, total);
+            if (valid && !whole) {
+                part[static_cast<uint64_t>(a.slot_rows) * a.head_dim + row] = reference;
+                part[static_cast<uint64_t>(a.slot_rows) * (a.head_dim + 1) + row] = total;
+            }
+        }
+        if constexpr (P::SPLIT) {
+            tcgen05_before_sync();
+            __syncwarp();
+            if (lane == 0)
+                bar_arrive(sm.taken());
         }
         return true;
     }
     __device__ bool run(uint32_t tmem, int n)
     {
         bool began = false, valid = false, any = false;
-        int items = 0;
+        int items = 0, own = -1;  // the group's last step of the item
         for (int t = 0; t < n; ++t) {
             if (!bar_wait(sm.tile_full(t % P::TILES), t / P::TILES & 1, stop))
                 return false;
             const TreeTile& tile = sm.tile(t);
             const int flags = tile.flags;
-            const bool first = flags & kTileFirst;
-            const int u = t * P::NM + m;
-            if (!bar_wait(sm.s_full(u & 1), u >> 1 & 1, stop))
-                return false;
-            tcgen05_after_sync();
-            if (first) {
+            const int u = P::NM == 2 ? 2 * t + m : t;
+            if (flags & kTileFirst) {
                 began = flags & kTileBegins;
                 valid = row < tile.rows;
                 any = __any_sync(~0u, valid);
                 sees.make(a, tile.q, (tile.row0 + (valid ? row : 0)) / a.group);
                 reference = -INFINITY;
                 total = 0.0f;
+                own = -1;
                 factor = a.scale2;
                 if constexpr (P::SCALED) {
                     if (!bar_wait(sm.q_full(items % P::QS), items / P::QS & 1, stop))
@@ -740,33 +1188,40 @@ struct TreeSoft {
                 }
                 ++items;
             }
-            if (any) {
-                bool part = flags & kTreeMixed;
+            if (!P::SPLIT || (t & 1) == m) {
+                if (!bar_wait(sm.s_full(u & 1), u >> 1 & 1, stop))
+                    return false;
+                tcgen05_after_sync();
+                if (any) {
+                    bool part = flags & kTreeMixed;
 #pragma unroll
-                for (int w = 0; w < 4; ++w)
-                    part = part || tile.valid[w] != (P::WARP_TOKENS == 32 ? ~0u : 0xffffu);
-                const uint32_t s = tmem + lanes + (u & 1) * P::S_COLUMNS;
-                if (!weights(tile, s, first, t, part))
+                    for (int w = 0; w < P::TOKENS / 32; ++w)
+                        part = part || tile.valid[w] != ~0u;
+                    const uint32_t s = tmem + lanes + (u & 1) * P::S_COLUMNS;
+                    if (!weights(tile, s, own < 0, u, part))
+                        return false;
+                }
+                bool bad = false;
+                if (flags & kTreeMixed) {  // the values have to be there first; once the weights are, their slot may be filled anew
+                    const int f = 2 * t + 1;
+                    if (!bar_wait(sm.kv_full(f % P::NS), f / P::NS & 1, stop))
+                        return false;
+                    bad = any && *const_cast<const volatile int*>(&tile.bad) != 0;
+                }
+                // A parity tells two phases apart only: the last product has to be seen done before the next can be.
+                if (P::phase_of(u) > 0 && !bar_wait(sm.o_done(m), P::phase_of(u) - 1 & 1, stop))
+                    return false;
+                if (!joined())
+                    return false;
+                tcgen05_before_sync();
+                __syncwarp();
+                if (lane == 0)
+                    bar_arrive(sm.p_ready(u & 1));
+                own = u;
+                if (bad && !poison(tile, u, valid))
                     return false;
             }
-            bool bad = false;
-            if (flags & kTreeMixed) {  // the values have to be there first; once the weights are, their slot may be filled anew
-                const int f = 2 * t + 1;
-                if (!bar_wait(sm.kv_full(f % P::NS), f / P::NS & 1, stop))
-                    return false;
-                const volatile int* const found = tile.bad;
-                bad = any && (found[0] | found[1] | found[2] | found[3]) != 0;
-            }
-            // A parity tells two phases apart only: the last product has to be seen done before the next can be.
-            if (t > 0 && !bar_wait(sm.o_done(m), (t - 1) & 1, stop))
-                return false;
-            tcgen05_before_sync();
-            __syncwarp();
-            if (lane == 0)
-                bar_arrive(sm.p_ready(u & 1));
-            if (bad && !poison(tile, t, valid))
-                return false;
-            if ((flags & kTileLast) && !finish(tile, t, began, any, valid))
+            if ((flags & kTileLast) && !finish(tile, own, began, any, valid))
                 return false;
             __syncwarp();
             if (lane == 0)
@@ -778,53 +1233,58 @@ struct TreeSoft {
 
 template <typename P>
 __global__ void __launch_bounds__(P::THREADS, 1)
-k_tree_mma(const TreeArgs a)
+k_tree_mma(const TreeArgs a, const __grid_constant__ TreeMaps maps)
 {
-    extern __shared__ __align__(1024) char dynamic[];
-    __shared__ uint32_t s_tmem;
-    __shared__ int s_stop;
-    static_assert(TreeSmem<P>::END <= P::SMEM, "shared memory");
+    extern __shared__ __align__(1024) char dynamic[];  // all of a block's shared memory: it begins aligned
     pdl_enter();
     const TreeSmem<P> sm(dynamic);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     constexpr int COPY = P::SOFTMAX / 32, ISSUE = COPY + 4;
+    volatile int* const stop = sm.stop();
     if (warp == ISSUE)
-        tmem_alloc(smem_addr(&s_tmem), 512);
+        tmem_alloc(smem_addr(sm.tmem()), 512);
     if (threadIdx.x == 0) {
-        s_stop = 0;
+        *stop = 0;
         for (int i = 0; i < P::NS; ++i) {
-            bar_init(sm.kv_full(i), 4);
+            bar_init(sm.kv_full(i), a.boxes ? 4 : 32);  // the helping warps, or a copying warp's threads
             bar_init(sm.kv_empty(i), 1);
         }
         for (int i = 0; i < P::QS; ++i) {
-            bar_init(sm.q_full(i), 4);
+            bar_init(sm.q_full(i), 128);
             bar_init(sm.q_empty(i), P::SCALED ? 1 + P::SOFTMAX / 32 : 1);  // the product's, and the factors' readers
         }
         for (int i = 0; i < 2; ++i) {
             bar_init(sm.s_full(i), 1);
             bar_init(sm.p_ready(i), 4);
         }
-        for (int i = 0; i < P::NM; ++i)
+        for (int i = 0; i < P::GROUPS; ++i)
             bar_init(sm.o_done(i), 1);
         for (int i = 0; i < P::TILES; ++i) {
-            bar_init(sm.tile_full(i), 4);
-            bar_init(sm.tile_empty(i), P::SOFTMAX / 32);
+            bar_init(sm.tile_full(i), 1);
+            bar_init(sm.tile_empty(i), P::SOFTMAX / 32 + (a.boxes ? 4 : 0));
         }
+        bar_init(sm.told(), 4);
+        bar_init(sm.taken(), 4);
         bar_init(sm.last(), 1);
+        for (int i = 0; i < P::ARRIVALS; ++i)
+            bar_init(sm.arrived(i), a.boxes ? 1 : 32);
+        for (int i = 0; i < P::RS; ++i)
+            bar_init(sm.raw_empty(i), 4);
+        for (int i = 0; i < 4; ++i)
+            *reinterpret_cast<int*>(dynamic + TreeSmem<P>::SENT + 4 * i) = i >> 1;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         a.jobs[blockIdx.x].rows = 0;
     }
     tcgen05_before_sync();
     __syncthreads();
     tcgen05_after_sync();
-    const uint32_t tmem = s_tmem;
-    volatile int* const stop = &s_stop;
+    const uint32_t tmem = __shfl_sync(~0u, *sm.tmem(), 0);
     TreeCursor<P::ROWS, P::TOKENS> cur;
-    const Run line = tree_run<P::ROWS, P::TOKENS, P::THREADS>(a, cur);  // the job's 0 is written before: it contains a barrier
+    const Run line = tree_run<P::ROWS, P::TOKENS, P::THREADS>(a, cur, sm.scan());  // the job's 0 is written before: it contains a barrier
     const int n = static_cast<int>(min(line.n, static_cast<long long>(INT_MAX / 4)));
     if (n > 0) {
         if (warp == ISSUE) {
-            if (lane == 0 && !tree_products<P>(a, sm, tmem, n, stop)) {
+            if (!tree_products<P>(a, sm, tmem, n, stop) && lane == 0) {
                 // Stopped: the products under way end before shared and tensor memory are given back.
                 tcgen05_commit(sm.last());
                 unsigned long long t0, t;
@@ -834,10 +1294,16 @@ k_tree_mma(const TreeArgs a)
                 while (!bar_test(sm.last(), 0) && t - t0 < kTreeWaitLimitNs);
             }
             __syncwarp();
+        } else if (warp > ISSUE) {
+            if (a.boxes) {
+                TreeBoxes<P> boxes(a, sm, maps, stop);
+                boxes.run(cur, line, n);
+            }
+            __syncwarp();
         } else if (warp >= COPY) {
-            TreeFeed<P> feed(a, sm, stop);
-            if (!feed.run(cur, line, n))
-                cp_async_wait<0>();
+            TreeFeed<P> feed(a, sm, stop, cur);
+            if (!(a.boxes ? feed.help(n) : feed.run(cur, line, n)))
+                asm volatile("cp.async.wait_all;" ::: "memory");
             __syncwarp();
         } else {
             TreeSoft<P> soft(a, sm, tmem, stop);
@@ -867,26 +1333,26 @@ cudaError_t take_tree_wait_timeouts(unsigned int* count)
 }
 
 template <typename T, typename CT, int DIM>
-cudaError_t launch_tree_mma(const TreeArgs& a, const TreeShape& shape, int most, int sms, cudaStream_t s)
+cudaError_t launch_tree_mma(const TreeArgs& a, const TreeMaps& maps, const TreeShape& shape, int most, int sms, cudaStream_t s)
 {
     const int blocks = most < sms ? most : sms;
     if constexpr (DIM <= 128) {
         if (shape.rows == 256) {
             using P = TreeMmaShape<T, CT, DIM, 2>;
-            return launch_tree_kernel<T>(k_tree_mma<P>, a, P::THREADS, P::SMEM, blocks, sms, s);
+            return launch_tree_kernel<T>(k_tree_mma<P>, a, P::THREADS, P::SMEM, blocks, sms, s, maps);
         }
     }
     using P = TreeMmaShape<T, CT, DIM, 1>;
-    return launch_tree_kernel<T>(k_tree_mma<P>, a, P::THREADS, P::SMEM, blocks, sms, s);
+    return launch_tree_kernel<T>(k_tree_mma<P>, a, P::THREADS, P::SMEM, blocks, sms, s, maps);
 }
 
 template <typename T, typename CT>
-cudaError_t launch_tree(const TreeArgs& a, const TreeShape& shape, int most, int sms, cudaStream_t s)
+cudaError_t launch_tree(const TreeArgs& a, const TreeMaps& maps, const TreeShape& shape, int most, int sms, cudaStream_t s)
 {
-    return a.head_dim <= 64    ? launch_tree_mma<T, CT, 64>(a, shape, most, sms, s)
-           : a.head_dim <= 128 ? launch_tree_mma<T, CT, 128>(a, shape, most, sms, s)
-           : a.head_dim <= 192 ? launch_tree_mma<T, CT, 192>(a, shape, most, sms, s)
-                               : launch_tree_mma<T, CT, 256>(a, shape, most, sms, s);
+    return a.head_dim <= 64    ? launch_tree_mma<T, CT, 64>(a, maps, shape, most, sms, s)
+           : a.head_dim <= 128 ? launch_tree_mma<T, CT, 128>(a, maps, shape, most, sms, s)
+           : a.head_dim <= 192 ? launch_tree_mma<T, CT, 192>(a, maps, shape, most, sms, s)
+                               : launch_tree_mma<T, CT, 256>(a, maps, shape, most, sms, s);
 }
 
 }  // namespace ar

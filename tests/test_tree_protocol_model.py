@@ -20,66 +20,148 @@ class Bar:
         return (self.phase - 1) & 1 == parity
 
 
-def run(NM, NS, QS, LAG, TILES, items, seed, small=False, scaled=False):
-    """items: (tiles, whether its last tiles are mixed).  Returns what every stuck process waits for, or None."""
+def run(NM, GROUPS, NS, QS, RS, TILES, items, seed, scaled=False, boxes=False):
+    """items: (tiles, whether its last tiles are mixed).  RS > 0: 8-bit, copied to stages first.  boxes: a warp asks for tensor
+    copies, and the copying warps help.  Returns what every stuck process waits for, or None."""
     r = random.Random(seed)
     tiles = [(i == 0, i == n - 1, mixed and i >= n - 2) for n, mixed in items for i in range(n)]
-    n, warps = len(tiles), 4 * NM
-    kv_full, kv_empty = [Bar(4) for _ in range(NS)], [Bar(1) for _ in range(NS)]
+    n, warps, small = len(tiles), 4 * GROUPS, RS > 0
+    split = GROUPS == 2 and NM == 1
+    kv_full, kv_empty = [Bar(4 if boxes else 1) for _ in range(NS)], [Bar(1) for _ in range(NS)]
     q_full, q_empty = [Bar(4) for _ in range(QS)], [Bar(1 + (warps if scaled else 0)) for _ in range(QS)]
-    s_full, p_ready, o_done = [Bar(1), Bar(1)], [Bar(4), Bar(4)], [Bar(1) for _ in range(NM)]
-    tile_full, tile_empty = [Bar(4) for _ in range(TILES)], [Bar(warps) for _ in range(TILES)]
-    queue = []                # products in order, with the barriers they complete
+    s_full, p_ready, o_done = [Bar(1), Bar(1)], [Bar(4), Bar(4)], [Bar(1) for _ in range(GROUPS)]
+    tile_full, tile_empty = [Bar(1) for _ in range(TILES)], [Bar(warps + (4 if boxes else 0)) for _ in range(TILES)]
+    arrived, sent, raw_empty = [Bar(1) for _ in range(8)], [0, 0, 1, 1], [Bar(4) for _ in range(RS)]
+    given = {}
+    told, taken = Bar(4), Bar(4)
+    queue, copies = [], []    # products in order, with the barriers they complete; copies on their way
     content = [None] * NS     # the fill that lies in a slot: what the products must find
-    handed, used = {}, set()
+    used = set()
+    state = {"o": [None, None]}   # who may touch a group's O: None, or "read" while the first group reads the second's
 
     def wait(bar, phase, what):
         """Of the phase with this number, by its parity, as the kernel does."""
         return bar, phase & 1, phase, what
 
-    def copy(w):
-        wanted = filled = given = done = 0
+    def ready(bar, phase):
+        """A test that does not wait."""
+        good = bar.test(phase & 1)
+        assert good == (bar.phase == phase + 1), "a parity of another phase"
+        return good
 
-        def hand_over():
-            nonlocal filled, given, done
-            f = done
-            done += 1
-            t, first = f >> 1, f & 1 == 0 and tiles[f >> 1][0]
-            if first and filled == given:
-                yield wait(q_empty[filled % QS], filled // QS - 1, f"late queries of tile {t}")
-                yield wait(tile_full[t % TILES], t // TILES, f"description of tile {t}")
-                filled += 1
-            if small:
-                yield wait(kv_empty[f % NS], f // NS - 1, f"slot of fill {f}")
-            if first:
-                q_full[given % QS].arrive()
-                given += 1
-            handed[f] = handed.get(f, 0) + 1
-            if handed[f] == 4:
-                content[f % NS] = f
+    def copy(w):
+        """Keys (w 0 and 2) or values (1 and 3) of alternate tiles."""
+        values, tile, done, filled = w & 1, w >> 1, w >> 1, 0
+        uses = [0] * 8            # phases of `arrived` that were waited for (16-bit)
+        begins = [t for t in range(n) if tiles[t][0]]
+        arrival = (lambda t: (2 * t + values) % RS) if small else (lambda t: (t & 1) * 4 + (t >> 1 & 3))
+
+        def give(f):
+            content[f % NS] = f
             kv_full[f % NS].arrive()
+
+        def free(f):
+            before = f - NS
+            if NS % 4 and before >= 0 and not sent[(before & 1) + (before >> 1 & 1) * 2] > before >> 1:
+                return False
+            return ready(kv_empty[f % NS], f // NS - 1)
+
+        while True:
+            moved = False
+            if small:
+                f = 2 * done + values
+                if done < tile and free(f) and ready(arrived[arrival(done)], f // RS):
+                    done, moved = done + 2, True
+                    give(f)
+                    sent[w] = done
+            else:
+                while done < tile and not (values and tiles[done][2]):
+                    done += 2
+                if done < tile and ready(arrived[arrival(done)], uses[arrival(done)]):
+                    uses[arrival(done)] += 1
+                    give(2 * done + 1)
+                    done, moved = done + 2, True
+            if filled < len(begins) and ready(q_empty[filled % QS], filled // QS - 1):
+                copies.append(q_full[filled % QS].arrive)
+                filled, moved = filled + 1, True
+            if tile < n:
+                f = 2 * tile + values
+                room = (tile - done) // 2 < RS // 4 if small else free(f)
+                if room and (values or ready(tile_empty[tile % TILES], tile // TILES - 1)):
+                    if not values:
+                        tile_full[tile % TILES].arrive()
+                    hands = small or (values and tiles[tile][2])
+                    copies.append(arrived[arrival(tile)].arrive if hands else lambda f=f: give(f))
+                    tile, moved = tile + 2, True
+                    if not small:
+                        sent[w] = tile
+            if not moved and tile >= n and done >= n and filled == len(begins):
+                return
+            yield None
+
+    def ask():
+        """The warp of tensor copies."""
+        def land(f):
+            content[f % NS] = f
+            for _ in range(4):
+                kv_full[f % NS].arrive()
 
         for t in range(n):
             yield wait(tile_empty[t % TILES], t // TILES - 1, f"room for tile {t}")
             tile_full[t % TILES].arrive()
-            if tiles[t][0]:
-                wanted += 1
-                if filled + 1 == wanted and q_empty[filled % QS].test((filled // QS & 1) ^ 1):
-                    filled += 1
             for f in (2 * t, 2 * t + 1):
-                if not small:
+                if small:
+                    yield wait(raw_empty[f % RS], f // RS - 1, f"stage of fill {f}")
+                    copies.append(arrived[f % RS].arrive)
+                else:
                     yield wait(kv_empty[f % NS], f // NS - 1, f"slot of fill {f}")
-                if f - done >= LAG:
-                    yield from hand_over()
-        while done < 2 * n:
-            yield from hand_over()
+                    copies.append(arrived[t % 8].arrive if f & 1 and tiles[t][2] else lambda f=f: land(f))
+
+    def help_out(w):
+        begins, filled, uses = [t for t in range(n) if tiles[t][0]], 0, [0] * 8
+
+        def until(bar, phase):
+            """Fills queries' slots while it waits."""
+            nonlocal filled
+            while not ready(bar, phase):
+                if filled < len(begins) and ready(q_empty[filled % QS], filled // QS - 1):
+                    copies.append(q_full[filled % QS].arrive)
+                    filled += 1
+                yield None
+
+        def give(f):
+            given[f] = given.get(f, 0) + 1
+            if given[f] == 4:
+                content[f % NS] = f
+            kv_full[f % NS].arrive()
+
+        for t in range(n):
+            yield from until(tile_full[t % TILES], t // TILES)
+            if small:
+                for f in (2 * t, 2 * t + 1):
+                    yield from until(arrived[f % RS], f // RS)
+                    yield from until(kv_empty[f % NS], f // NS - 1)
+                    give(f)
+                    raw_empty[f % RS].arrive()
+            elif tiles[t][2]:
+                yield from until(arrived[t % 8], uses[t % 8])
+                uses[t % 8] += 1
+                give(2 * t + 1)
+            tile_empty[t % TILES].arrive()
+        while filled < len(begins):
+            if ready(q_empty[filled % QS], filled // QS - 1):
+                copies.append(q_full[filled % QS].arrive)
+                filled += 1
+            yield None
 
     def issue():
         begun = 0
+        tile_of = (lambda u: u // 2) if NM == 2 else (lambda u: u)
+        group_of, phase_of = ((lambda u: u & 1), (lambda u: u >> 1)) if GROUPS == 2 else ((lambda u: 0), (lambda u: u))
 
         def scores(u):
             nonlocal begun
-            t, m = divmod(u, NM)
+            t, m = tile_of(u), u % NM
             if m == 0:
                 yield wait(tile_full[t % TILES], t // TILES, f"tile {t}")
                 if tiles[t][0]:
@@ -87,63 +169,91 @@ def run(NM, NS, QS, LAG, TILES, items, seed, small=False, scaled=False):
                     begun += 1
                 yield wait(kv_full[2 * t % NS], 2 * t // NS, f"keys of tile {t}")
             last = tiles[t][1] or t == n - 1
-            queue.append(((2 * t,), [s_full[u & 1]] + ([kv_empty[2 * t % NS]] + ([q_empty[(begun - 1) % QS]] if last else []) if m == NM - 1 else [])))
+            queue.append((2 * t, None, [s_full[u & 1]] +
+                          ([kv_empty[2 * t % NS]] + ([q_empty[(begun - 1) % QS]] if last else []) if m == NM - 1 else [])))
 
         yield from scores(0)
         for u in range(n * NM):
-            t, m = divmod(u, NM)
-            f = 2 * t + 1
+            f = 2 * tile_of(u) + 1
             if u + 1 < n * NM:
                 if u > 0:
-                    yield wait(o_done[(u - 1) % NM], (u - 1) // NM, f"product {u - 1}")
+                    yield wait(o_done[group_of(u - 1)], phase_of(u - 1), f"product {u - 1}")
                 yield from scores(u + 1)
             yield wait(p_ready[u & 1], u >> 1, f"weights {u}")
-            if m == 0:
-                yield wait(kv_full[f % NS], f // NS, f"values of tile {t}")
-            queue.append(((f,), [o_done[m]] + ([kv_empty[f % NS]] if m == NM - 1 else [])))
+            if u % NM == 0:
+                yield wait(kv_full[f % NS], f // NS, f"values of step {u}")
+            queue.append((f, group_of(u), [o_done[group_of(u)]] + ([kv_empty[f % NS]] if u % NM == NM - 1 else [])))
 
     def softmax(w):
-        m, begun = w // 4, 0
+        m, begun, joins, awaits, own = w // 4, 0, 0, False, -1
+        phase_of = (lambda u: u >> 1) if GROUPS == 2 else (lambda u: u)
         for t in range(n):
             yield wait(tile_full[t % TILES], t // TILES, f"tile {t}")
-            u = t * NM + m
-            yield wait(s_full[u & 1], u >> 1, f"scores {u}")
+            u = 2 * t + m if NM == 2 else t
             if tiles[t][0]:
+                own = -1
                 if scaled:
                     yield wait(q_full[begun % QS], begun // QS, f"factors of tile {t}")
                     q_empty[begun % QS].arrive()
                 begun += 1
-            elif r.random() < 0.5:   # the reference moves
-                yield wait(o_done[m], t - 1, f"product before tile {t}")
-            if tiles[t][2]:
-                yield wait(kv_full[(2 * t + 1) % NS], (2 * t + 1) // NS, f"values of tile {t}")
-            if t > 0:
-                yield wait(o_done[m], t - 1, f"product before tile {t}")
-            p_ready[u & 1].arrive()
-            if tiles[t][1] or t == n - 1 or (tiles[t][2] and r.random() < 0.5):
-                yield wait(o_done[m], t, f"product of tile {t}")
+            if not split or t & 1 == m:
+                yield wait(s_full[u & 1], u >> 1, f"scores {u}")
+                if own >= 0 and r.random() < 0.5:   # the reference moves
+                    yield wait(o_done[m], phase_of(u) - 1, f"product before step {u}")
+                if tiles[t][2]:
+                    yield wait(kv_full[(2 * t + 1) % NS], (2 * t + 1) // NS, f"values of tile {t}")
+                if phase_of(u) > 0:
+                    yield wait(o_done[m], phase_of(u) - 1, f"product before step {u}")
+                if split and awaits:
+                    yield wait(taken, joins - 1, f"the join before step {u}")
+                    awaits = False
+                p_ready[u & 1].arrive()
+                own = u
+                if tiles[t][2] and r.random() < 0.5:
+                    yield wait(o_done[m], phase_of(u), f"product of step {u}")
+            if tiles[t][1] or t == n - 1:
+                if own >= 0:
+                    yield wait(o_done[m], phase_of(own), f"product of step {own}")
+                if split and m == 1:
+                    if awaits:
+                        yield wait(taken, joins - 1, f"the join before tile {t}")
+                    told.arrive()
+                    joins, awaits = joins + 1, True
+                elif split:
+                    yield wait(told, joins, f"references at tile {t}")
+                    joins += 1
+                    state["o"][1] = (state["o"][1] or 0) + 1
+                    yield None   # reading both
+                    state["o"][1] -= 1
+                    taken.arrive()
             tile_empty[t % TILES].arrive()
 
-    running = {f"copy {w}": copy(w) for w in range(4)}
+    running = {f"copy {w}": help_out(w) if boxes else copy(w) for w in range(4)}
+    if boxes:
+        running["ask"] = ask()
     running["issue"] = issue()
     running.update({f"softmax {w}": softmax(w) for w in range(warps)})
-    waits = dict.fromkeys(running)
+    waits, idle = dict.fromkeys(running), 0
     while running:
-        ready = [k for k in running if waits[k] is None or waits[k][0].test(waits[k][1])]
-        for k in ready:
+        can = [k for k in running if waits[k] is None or waits[k][0].test(waits[k][1])]
+        for k in can:
             if waits[k] is not None:   # not before its phase, and not after the next one with its parity
                 assert waits[k][0].phase == waits[k][2] + 1, (k, waits[k][3])
-        choice = ready + (["tensor core"] if queue else [])
-        if not choice:
-            return {k: waits[k][3] for k in running}
+        choice = can + (["tensor core"] if queue else []) + (["memory"] * 2 if copies else [])
+        idle = idle + 1 if all(k.startswith("copy") for k in choice) else 0
+        if not choice or idle > 20000:   # copying warps never wait: they look for something to do
+            return {k: waits[k] and waits[k][3] for k in running}
         k = r.choice(choice)
         if k == "tensor core":
-            fills, bars = queue.pop(0)
-            for f in fills:
-                assert content[f % NS] == f, "a product reads another fill than its own"
-                used.add(f)
+            f, o, bars = queue.pop(0)
+            assert content[f % NS] == f, "a product reads another fill than its own"
+            assert o is None or not state["o"][o], "an O is written that is still read"
+            used.add(f)
             for b in bars:
                 b.arrive()
+            continue
+        if k == "memory":
+            copies.pop(r.randrange(min(len(copies), 6)))()
             continue
         try:
             waits[k] = next(running[k])
@@ -153,19 +263,19 @@ def run(NM, NS, QS, LAG, TILES, items, seed, small=False, scaled=False):
     return None
 
 
-# NM, NS, QS, LAG, TILES, small, scaled as TreeMmaShape has them
-SHAPES = {"16 bit, 64, 128 rows": (1, 8, 2, 6, 8), "16 bit, 64, 256 rows": (2, 8, 1, 6, 8), "16 bit, 128, 128 rows": (1, 5, 2, 3, 8),
-          "16 bit, 128, 256 rows": (2, 5, 1, 3, 8), "16 bit, 192": (1, 7, 1, 5, 8), "16 bit, 256": (1, 5, 1, 3, 8),
-          "8 bit, 64, 128 rows": (1, 8, 2, 7, 8, True, True), "8 bit, 64, 256 rows": (2, 8, 1, 7, 8, True, True),
-          "8 bit, 128, 128 rows": (1, 3, 2, 3, 4, True, True), "8 bit, 128, 256 rows": (2, 3, 1, 3, 4, True, True),
-          "8 bit, 192": (1, 5, 1, 3, 4, True, True), "8 bit, 256": (1, 3, 1, 3, 4, True, True), "8 bit, 256, fp16 queries": (1, 3, 1, 3, 8, True, False)}
+# NM, GROUPS, NS, QS, RS, TILES, scaled as TreeMmaShape has them
+SHAPES = {"16 bit, 64, 128 rows": (1, 2, 8, 2, 0, 8), "16 bit, 64, 256 rows": (2, 2, 8, 1, 0, 8), "16 bit, 128, 128 rows": (1, 2, 5, 2, 0, 8),
+          "16 bit, 128, 256 rows": (2, 2, 5, 1, 0, 8), "16 bit, 192": (1, 1, 7, 1, 0, 8), "16 bit, 256": (1, 1, 5, 1, 0, 8),
+          "8 bit, 64, 128 rows": (1, 2, 8, 2, 8, 4, True), "8 bit, 64, 256 rows": (2, 2, 8, 1, 8, 4, True),
+          "8 bit, 128, 128 rows": (1, 2, 3, 2, 4, 4, True), "8 bit, 128, 256 rows": (2, 2, 3, 1, 4, 4, True),
+          "8 bit, 192": (1, 1, 5, 1, 4, 4, True), "8 bit, 256": (1, 1, 3, 1, 4, 4, True), "8 bit, 256, fp16 queries": (1, 1, 3, 1, 4, 8)}
 
 
+@pytest.mark.parametrize("boxes", [False, True])
 @pytest.mark.parametrize("shape", SHAPES)
-def test_every_run_ends_and_every_wait_is_for_its_own_phase(shape):
-    NM, NS, QS, LAG, TILES, small, scaled = (SHAPES[shape] + (False, False))[:7]
-    for seed in range(60):
+def test_every_run_ends_and_every_wait_is_for_its_own_phase(shape, boxes):
+    for seed in range(40):
         r = random.Random(seed)
         items = [(r.choice([1, 1, 2, 3, 5, 9]), r.random() < 0.7) for _ in range(r.randint(1, 8))]
-        stuck = run(NM, NS, QS, LAG, TILES, items, seed, small, scaled)
+        stuck = run(*SHAPES[shape][:6], items, seed, len(SHAPES[shape]) > 6, boxes)
         assert stuck is None, (items, stuck)
