@@ -207,16 +207,17 @@ PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder()
     return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
 }
 
-// Describes the pages for tensor copies of `tile` tokens at most, where they can be: 16-bit elements in boxes of 64, 8-bit ones
-// in boxes of `dim`.
-bool tree_maps(const ar_kv_cache* c, int tile, int dim, ar::TreeMaps* maps, int* token_first)
+// Describes the pages for tensor copies, where they can be: pages of whole groups of eight tokens.  Returns a copy's tokens, the
+// largest power of two that divides a page, `tile` at most; 0: they cannot be.  16-bit elements come by 64, 8-bit ones by `dim`.
+int tree_maps(const ar_kv_cache* c, int tile, int dim, ar::TreeMaps* maps, int* token_first)
 {
     const uint64_t e = static_cast<uint64_t>(cache_esize_of(c->dtype));
-    if (e == 4 || c->page_size % 8 != 0 || !(tile % c->page_size == 0 || c->page_size % tile == 0))
-        return false;
+    const int whole = c->page_size & -c->page_size, tokens = whole < tile ? whole : tile;
+    if (e == 4 || tokens < 8)
+        return 0;
     const PFN_cuTensorMapEncodeTiled_v12000 encode = tensor_map_encoder();
     if (encode == nullptr)
-        return false;
+        return 0;
     // An axis of one element needs no stride, but an allowed one.
     const uint64_t page = c->page_stride * e, token = c->token_stride * e, head = c->head_stride * e;
     const auto some = [](uint64_t stride) { return stride != 0 ? stride : 16; };
@@ -224,8 +225,8 @@ bool tree_maps(const ar_kv_cache* c, int tile, int dim, ar::TreeMaps* maps, int*
     const cuuint64_t sizes[4] = {static_cast<cuuint64_t>(c->head_dim), static_cast<cuuint64_t>(*token_first ? c->page_size : c->kv_heads),
                                  static_cast<cuuint64_t>(*token_first ? c->kv_heads : c->page_size), static_cast<cuuint64_t>(c->pages)};
     const cuuint64_t strides[3] = {some(*token_first ? token : head), some(*token_first ? head : token), some(page)};
-    const cuuint32_t tokens = static_cast<cuuint32_t>(c->page_size < tile ? c->page_size : tile);
-    const cuuint32_t box[4] = {e == 1 ? static_cast<cuuint32_t>(dim) : 64u, *token_first ? tokens : 1u, *token_first ? 1u : tokens, 1u};
+    const cuuint32_t rows = static_cast<cuuint32_t>(tokens);
+    const cuuint32_t box[4] = {e == 1 ? static_cast<cuuint32_t>(dim) : 64u, *token_first ? rows : 1u, *token_first ? 1u : rows, 1u};
     const cuuint32_t steps[4] = {1, 1, 1, 1};
     const CUtensorMapDataType type = e == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8
                                             : c->dtype == AR_FP16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
@@ -234,7 +235,7 @@ bool tree_maps(const ar_kv_cache* c, int tile, int dim, ar::TreeMaps* maps, int*
                       e == 1 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
                       CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
     };
-    return map(&maps->k, c->k) && map(&maps->v, c->v);
+    return map(&maps->k, c->k) && map(&maps->v, c->v) ? tokens : 0;
 }
 
 struct TreePlan {

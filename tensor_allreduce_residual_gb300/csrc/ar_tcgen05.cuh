@@ -24,10 +24,17 @@ __device__ __forceinline__ void tcgen05_after_sync() { asm volatile("tcgen05.fen
 __device__ __forceinline__ void tcgen05_wait_load() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tcgen05_wait_store() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// A barrier arrival when all products issued by this thread so far are done.
-__device__ __forceinline__ void tcgen05_commit(uint32_t bar)
+// The instructions that one lane of a converged warp issues take a truth value instead of standing in a branch: outside of
+// one, their descriptors and addresses, which all lanes have alike, stay in uniform registers (in a branch each product took
+// some 126 cycles to issue, twice its own time).
+
+// A barrier arrival when all products issued by this lane so far are done.
+__device__ __forceinline__ void tcgen05_commit(uint32_t bar, bool issue = true)
 {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+    asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %1, 0;\n\t"
+                 "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar),
+                 "r"(issue ? 1u : 0u)
+                 : "memory");
 }
 
 // What shared memory writes of this thread have to pass before the tensor core reads them.
@@ -49,18 +56,18 @@ __host__ __device__ constexpr uint32_t product_desc(bool bf16, int n, bool b_wid
 }
 
 // d = a b (+ d): the first operand in shared memory, or in tensor memory.
-__device__ __forceinline__ void mma_shared(uint32_t d, uint64_t a, uint64_t b, uint32_t desc, bool add)
+__device__ __forceinline__ void mma_shared(uint32_t d, uint64_t a, uint64_t b, uint32_t desc, bool add, bool issue)
 {
-    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-                 "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-                 "l"(a), "l"(b), "r"(desc), "r"(add ? 1u : 0u)
+    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %4, 0;\n\tsetp.ne.u32 q, %5, 0;\n\t"
+                 "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+                 "l"(a), "l"(b), "r"(desc), "r"(add ? 1u : 0u), "r"(issue ? 1u : 0u)
                  : "memory");
 }
-__device__ __forceinline__ void mma_tensor(uint32_t d, uint32_t a, uint64_t b, uint32_t desc, bool add)
+__device__ __forceinline__ void mma_tensor(uint32_t d, uint32_t a, uint64_t b, uint32_t desc, bool add, bool issue)
 {
-    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-                 "r"(a), "l"(b), "r"(desc), "r"(add ? 1u : 0u)
+    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %4, 0;\n\tsetp.ne.u32 q, %5, 0;\n\t"
+                 "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+                 "r"(a), "l"(b), "r"(desc), "r"(add ? 1u : 0u), "r"(issue ? 1u : 0u)
                  : "memory");
 }
 

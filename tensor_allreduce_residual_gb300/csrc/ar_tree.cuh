@@ -266,13 +266,20 @@ __device__ __forceinline__ void leave_job(const TreeArgs& a, const TreeCursor<RO
 // w * RPT .. of ROWS, and its 16 lanes share a tile's 32 tokens, and then the
 // head's elements.  A row's maximum, sum and weights stay within its
 // half-warp, so the weights meet in shared memory without a block barrier.
+// Tiles come by asynchronous copies into a ring, STAGES - 1 of them ahead;
+// page numbers a tile earlier still.
 // ---------------------------------------------------------------------------
 constexpr int kTreeFmaThreads = 256;
 
 template <int ROWS, int DIM>
 struct TreeFmaShape {
     static constexpr int TILE = 32, PITCH = DIM + 4, PPITCH = TILE + 4;
-    static constexpr int SMEM = ((ROWS + 2 * TILE) * PITCH + ROWS * PPITCH) * 4;
+    static constexpr int STAGE = 2 * TILE * PITCH * 4, FIXED = (ROWS * PITCH + ROWS * PPITCH) * 4;
+    // Two blocks an SM where three stages of each fit, one otherwise.
+    static constexpr int BLOCKS = ROWS == 16 && FIXED + 3 * STAGE <= 112 * 1024 ? 2 : 1;
+    static constexpr int FIT = ((BLOCKS == 2 ? 112 : 224) * 1024 - FIXED) / STAGE, STAGES = FIT < 4 ? FIT : 4;
+    static_assert(STAGES >= 2, "a tile ahead");
+    static constexpr int SMEM = FIXED + STAGES * STAGE;
 };
 
 // Four elements of the cache or of q as fp32.
@@ -292,33 +299,93 @@ __device__ __forceinline__ float4 load_four(const char* p)
     }
 }
 
-template <typename T, typename CT, int DIM, int ROWS>
-__global__ void __launch_bounds__(kTreeFmaThreads)
+template <int DIM, int ROWS>
+__global__ void __launch_bounds__(kTreeFmaThreads, TreeFmaShape<ROWS, DIM>::BLOCKS)
 k_tree_fma(const TreeArgs a)
 {
     using P = TreeFmaShape<ROWS, DIM>;
-    constexpr int TILE = P::TILE, RPT = ROWS / 16, FOURS = DIM / 4, CPT = (FOURS + 15) / 16;
+    using Cur = TreeCursor<ROWS, P::TILE>;
+    constexpr int TILE = P::TILE, RPT = ROWS / 16, FOURS = DIM / 4, CPT = (FOURS + 15) / 16, STAGES = P::STAGES;
     extern __shared__ __align__(128) char smem[];
-    __shared__ uint32_t s_in;
-    __shared__ int64_t s_offset[TILE];
+    __shared__ uint32_t s_in[STAGES + 1];
+    __shared__ int64_t s_offset[STAGES + 1][TILE];
+    __shared__ long long s_scan[kTreeFmaThreads / 32 + 2];
     float* const sq = reinterpret_cast<float*>(smem);
-    float* const sk = sq + ROWS * P::PITCH;
-    float* const sv = sk + TILE * P::PITCH;
-    float* const sp = sv + TILE * P::PITCH;
+    float* const sp = sq + ROWS * P::PITCH;
+    char* const stages = smem + P::FIXED;
     pdl_enter();
     const int tid = threadIdx.x, lane = tid & 31, half = tid >> 4, l16 = tid & 15;
     if (tid == 0)
         a.jobs[blockIdx.x].rows = 0;
-    TreeCursor<ROWS, TILE> cur;
-    __shared__ long long s_scan[kTreeFmaThreads / 32 + 2];
+    Cur cur;
     const Run run = tree_run<ROWS, TILE, kTreeFmaThreads>(a, cur, s_scan);
-    const int fours = a.head_dim / 4;
+    const int fours = a.head_dim / 4, n = static_cast<int>(min(run.n, static_cast<long long>(INT_MAX / 2)));
+    // The first warp looks pages up, tile `looked` next; all copy, tile `sent` next.
+    Cur ahead = cur;
+    int looked = 0, sent = 0;
+    const auto look = [&] {
+        if (looked >= n)
+            return;
+        if (tid < 32) {
+            const int token = (ahead.s.tile0 + ahead.tile) * TILE + lane;
+            int page = -1;
+            int64_t at = 0;
+            if (token >= ahead.s.start && token < ahead.s.end) {
+                const uint32_t column = __umulhi(2u * token, a.page_magic) >> a.page_shift;
+                page = a.table[static_cast<uint64_t>(ahead.b) * a.table_stride + column];
+                if (page >= a.pages)
+                    page = -1;
+                at = static_cast<int64_t>(static_cast<uint32_t>(page) * a.page_stride +
+                                          static_cast<uint32_t>(token - static_cast<int>(column) * a.page_size) * a.token_stride +
+                                          static_cast<uint32_t>(ahead.h) * a.head_stride);
+            }
+            s_offset[looked % (STAGES + 1)][lane] = at;
+            const uint32_t in = __ballot_sync(~0u, page >= 0);
+            if (lane == 0)
+                s_in[looked % (STAGES + 1)] = in;
+        }
+        if (++looked < n) {
+            if (ahead.tile + 1 == ahead.s.tiles)
+                ahead.next_item(a);
+            else
+                ++ahead.tile;
+        }
+    };
+    uint64_t policy;
+    asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(policy));
+    const auto send = [&] {  // whose offsets a barrier has shown
+        if (sent < n) {
+            const uint32_t in = s_in[sent % (STAGES + 1)];
+            const uint32_t to = smem_addr(stages + sent % STAGES * P::STAGE);
+#pragma unroll 4
+            for (int x = tid; x < TILE * FOURS; x += kTreeFmaThreads) {
+                const int r = x / FOURS, c = x - r * FOURS;
+                const bool read = (in >> r & 1) != 0 && c < fours;
+                const int64_t at = read ? s_offset[sent % (STAGES + 1)][r] + 16 * c : 0;
+                const uint32_t dst = to + (r * P::PITCH + 4 * c) * 4;
+                cp_async16(dst, a.k + at, read, policy);
+                cp_async16(dst + TILE * P::PITCH * 4, a.v + at, read, policy);
+            }
+        }
+        ++sent;
+        cp_async_commit();
+    };
+    if (n > 0) {
+#pragma unroll 1
+        for (int i = 0; i < STAGES; ++i)
+            look();
+        __syncthreads();
+#pragma unroll 1
+        for (int i = 0; i < STAGES - 1; ++i)
+            send();
+    }
     float4 o[RPT][CPT];
     float top[RPT], total[RPT];
     TreeRow row[RPT];
     bool valid[RPT], began = false;
-    long long first = 0;  // the run's tile that the block's part of the item begins with
-    for (long long t = 0; t < run.n; ++t) {
+    int first = 0;  // the run's tile that the block's part of the item begins with
+#pragma unroll 1
+    for (int t = 0; t < n; ++t) {
         const int row0 = cur.rt * ROWS, rows = cur.rows(a);
         if (t == 0 || cur.tile == 0) {
             began = cur.tile == 0;
@@ -328,8 +395,8 @@ k_tree_fma(const TreeArgs a)
                 float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
                 if (r < rows && c < fours) {
                     const int i = (row0 + r) / a.group, g = row0 + r - i * a.group;
-                    v = load_four<T>(a.q + static_cast<uint64_t>(cur.q.first + i) * a.q_stride +
-                                     (static_cast<uint64_t>(cur.h * a.group + g) * a.head_dim + 4 * c) * sizeof(T));
+                    v = *reinterpret_cast<const float4*>(a.q + static_cast<uint64_t>(cur.q.first + i) * a.q_stride +
+                                                         (static_cast<uint64_t>(cur.h * a.group + g) * a.head_dim + 4 * c) * sizeof(float));
                 }
                 *reinterpret_cast<float4*>(sq + r * P::PITCH + 4 * c) = v;
             }
@@ -345,44 +412,21 @@ k_tree_fma(const TreeArgs a)
                     o[i][c] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
             }
         }
+        cp_async_wait<STAGES - 2>();
+        __syncthreads();  // tile t is here, the stage of tile t - 1 and its description are free
+        send();
+        look();
         const int token0 = (cur.s.tile0 + cur.tile) * TILE;
-        if (tid < 32) {
-            const int token = token0 + lane;
-            int page = -1;
-            int64_t at = 0;
-            if (token >= cur.s.start && token < cur.s.end) {
-                const uint32_t column = __umulhi(2u * token, a.page_magic) >> a.page_shift;
-                page = a.table[static_cast<uint64_t>(cur.b) * a.table_stride + column];
-                if (page >= a.pages)
-                    page = -1;
-                at = static_cast<int64_t>(static_cast<uint32_t>(page) * a.page_stride +
-                                          static_cast<uint32_t>(token - static_cast<int>(column) * a.page_size) * a.token_stride +
-                                          static_cast<uint32_t>(cur.h) * a.head_stride);
-            }
-            s_offset[lane] = at;
-            const uint32_t in = __ballot_sync(~0u, page >= 0);
-            if (lane == 0)
-                s_in = in;
-        }
-        __syncthreads();
-        const uint32_t in = s_in;
-        for (int x = tid; x < TILE * FOURS; x += kTreeFmaThreads) {
-            const int r = x / FOURS, c = x - r * FOURS;
-            float4 k = make_float4(0.0f, 0.0f, 0.0f, 0.0f), v = k;
-            if ((in >> r & 1) != 0 && c < fours) {
-                k = load_four<CT>(a.k + s_offset[r] + 4 * c * sizeof(CT));
-                v = load_four<CT>(a.v + s_offset[r] + 4 * c * sizeof(CT));
-            }
-            *reinterpret_cast<float4*>(sk + r * P::PITCH + 4 * c) = k;
-            *reinterpret_cast<float4*>(sv + r * P::PITCH + 4 * c) = v;
-        }
-        __syncthreads();
+        const uint32_t in = s_in[t % (STAGES + 1)];
+        const float* const sk = reinterpret_cast<const float*>(stages + t % STAGES * P::STAGE);
+        const float* const sv = sk + TILE * P::PITCH;
         const bool mixed = tree_mixed(a, cur.q, token0, TILE);
         // Tokens l16 and l16 + 16 of the tile, for the half-warp's rows.
         float2 dot[RPT][2];
 #pragma unroll
         for (int i = 0; i < RPT; ++i)
             dot[i][0] = dot[i][1] = make_float2(0.0f, 0.0f);
+#pragma unroll 4
         for (int c = 0; c < fours; ++c) {
             const float4 k0 = *reinterpret_cast<const float4*>(sk + l16 * P::PITCH + 4 * c);
             const float4 k1 = *reinterpret_cast<const float4*>(sk + (l16 + 16) * P::PITCH + 4 * c);
@@ -425,28 +469,35 @@ k_tree_fma(const TreeArgs a)
             }
         }
         __syncwarp();
-        for (int j = 0; j < TILE; ++j) {
-            float p[RPT];
+        const auto weigh = [&](auto some) {  // some: a weight may be -1
+#pragma unroll 4
+            for (int j = 0; j < TILE; ++j) {
+                float p[RPT];
 #pragma unroll
-            for (int i = 0; i < RPT; ++i)
-                p[i] = sp[(half * RPT + i) * P::PPITCH + j];
+                for (int i = 0; i < RPT; ++i)
+                    p[i] = sp[(half * RPT + i) * P::PPITCH + j];
 #pragma unroll
-            for (int c = 0; c < CPT; ++c) {
-                const int col = l16 + 16 * c;
-                if (FOURS % 16 == 0 || col < FOURS) {
-                    const float4 v = *reinterpret_cast<const float4*>(sv + j * P::PITCH + 4 * col);
+                for (int c = 0; c < CPT; ++c) {
+                    const int col = l16 + 16 * c;
+                    if (FOURS % 16 == 0 || col < FOURS) {
+                        const float4 v = *reinterpret_cast<const float4*>(sv + j * P::PITCH + 4 * col);
 #pragma unroll
-                    for (int i = 0; i < RPT; ++i)
-                        if (p[i] >= 0.0f) {
-                            const float2 x = fma2(make_float2(p[i], p[i]), make_float2(v.x, v.y), make_float2(o[i][c].x, o[i][c].y));
-                            const float2 y = fma2(make_float2(p[i], p[i]), make_float2(v.z, v.w), make_float2(o[i][c].z, o[i][c].w));
-                            o[i][c] = make_float4(x.x, x.y, y.x, y.y);
-                        }
+                        for (int i = 0; i < RPT; ++i)
+                            if (!decltype(some)::value || p[i] >= 0.0f) {
+                                const float2 x = fma2(make_float2(p[i], p[i]), make_float2(v.x, v.y), make_float2(o[i][c].x, o[i][c].y));
+                                const float2 y = fma2(make_float2(p[i], p[i]), make_float2(v.z, v.w), make_float2(o[i][c].z, o[i][c].w));
+                                o[i][c] = make_float4(x.x, x.y, y.x, y.y);
+                            }
+                    }
                 }
             }
-        }
+        };
+        if (mixed || in != ~0u)
+            weigh(std::true_type{});
+        else
+            weigh(std::false_type{});
         const bool ends = cur.tile + 1 == cur.s.tiles;
-        if (ends || t + 1 == run.n) {
+        if (ends || t + 1 == n) {
             const bool whole = began && ends;
             float* const part = a.part + slot_of(static_cast<int>(blockIdx.x), began) * a.slot_floats;
             if (began && !whole && tid == 0)
@@ -467,7 +518,7 @@ k_tree_fma(const TreeArgs a)
                     if (col >= fours)
                         continue;
                     if (whole)
-                        store_four(reinterpret_cast<T*>(a.out) + out * a.head_dim + 4 * col, o[i][c], sum == 0.0f ? 0.0f : a.v_scale / sum);
+                        store_four(reinterpret_cast<float*>(a.out) + out * a.head_dim + 4 * col, o[i][c], sum == 0.0f ? 0.0f : a.v_scale / sum);
                     else
                         *reinterpret_cast<float4*>(part + static_cast<uint64_t>(r) * a.head_dim + 4 * col) = o[i][c];
                 }
@@ -480,15 +531,16 @@ k_tree_fma(const TreeArgs a)
                     }
                 }
             }
+            __syncthreads();  // the next item's queries come where these are
         }
-        if (t + 1 < run.n) {
+        if (t + 1 < n) {
             if (ends)
                 cur.next_item(a);
             else
                 ++cur.tile;
         }
-        __syncthreads();
     }
+    cp_async_wait<0>();
 }
 
 // ---------------------------------------------------------------------------
@@ -499,7 +551,7 @@ k_tree_fma(const TreeArgs a)
 // ---------------------------------------------------------------------------
 constexpr int kTreeJoinThreads = 256;
 constexpr int kTreeJoinWarps = kTreeJoinThreads / 32;
-constexpr int kFewParts = 4;
+constexpr int kFewParts = 8;
 
 struct TreeSum {
     float top = -INFINITY, total = 0.0f;
@@ -579,6 +631,7 @@ __global__ void __launch_bounds__(kTreeJoinThreads)
 k_tree_join(const TreeArgs a, const int blocks)
 {
     __shared__ int s_few[kTreeMaxBlocks + 1], s_long[kTreeMaxBlocks + 1];  // rows of the jobs before each
+    __shared__ TreeJob s_job[kTreeMaxBlocks];
     __shared__ float4 s_o[kTreeJoinWarps][kTreeMaxDim / 4];
     __shared__ float2 s_w[kTreeJoinWarps];
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -586,6 +639,7 @@ k_tree_join(const TreeArgs a, const int blocks)
     for (int i = tid; i < blocks; i += kTreeJoinThreads) {
         const TreeJob job = a.jobs[i];
         const bool few = job.last - i < kFewParts;
+        s_job[i] = job;
         s_few[i + 1] = few ? job.rows : 0;
         s_long[i + 1] = few ? 0 : job.rows;
     }
@@ -619,19 +673,21 @@ k_tree_join(const TreeArgs a, const int blocks)
         }
         return lo;
     };
-    const int few = s_few[blocks], many = s_long[blocks];
-    for (int x = blockIdx.x * kTreeJoinWarps + warp; x < few; x += gridDim.x * kTreeJoinWarps) {
-        const int j = find(s_few, x);
-        const TreeJob job = a.jobs[j];
+    // Each warp takes rows side by side, most often of one job.
+    const int few = s_few[blocks], many = s_long[blocks], warps = gridDim.x * kTreeJoinWarps;
+    const int each = (few + warps - 1) / warps, x0 = (blockIdx.x * kTreeJoinWarps + warp) * each, x1 = min(x0 + each, few);
+    int j = x0 < x1 ? find(s_few, x0) : 0;
+    for (int x = x0; x < x1; ++x) {
+        while (s_few[j + 1] <= x)
+            ++j;
         TreeSum sum;
-        sum.gather(a, j, job.last - j + 1, x - s_few[j], 0, 1);
-        sum.write<T>(a, job, x - s_few[j]);
+        sum.gather(a, j, s_job[j].last - j + 1, x - s_few[j], 0, 1);
+        sum.write<T>(a, s_job[j], x - s_few[j]);
     }
     for (int x = blockIdx.x; x < many; x += gridDim.x) {
-        const int j = find(s_long, x);
-        const TreeJob job = a.jobs[j];
+        const int i = find(s_long, x);
         TreeSum sum;
-        sum.gather(a, j, job.last - j + 1, x - s_long[j], warp, kTreeJoinWarps);
+        sum.gather(a, i, s_job[i].last - i + 1, x - s_long[i], warp, kTreeJoinWarps);
 #pragma unroll
         for (int c = 0; c < kTreeMaxDim / 128; ++c)
             s_o[warp][lane + 32 * c] = sum.o[c];
@@ -647,7 +703,7 @@ k_tree_join(const TreeArgs a, const int blocks)
                 const float m[1] = {s_w[w].x}, n[1] = {s_w[w].y};
                 sum.add<1>(v, m, n);
             }
-            sum.write<T>(a, job, x - s_long[j]);
+            sum.write<T>(a, s_job[i], x - s_long[i]);
         }
         __syncthreads();
     }
@@ -666,12 +722,18 @@ cudaError_t launch_tree_kernel(void (*kernel)(TreeArgs, Rest...), const TreeArgs
     return launch_k(k_tree_join<T>, dim3(sms * 4), dim3(kTreeJoinThreads), 0, s, a, blocks);
 }
 
-template <typename T, typename CT, int DIM>
+template <int DIM, int ROWS>
+cudaError_t launch_tree_rows(const TreeArgs& a, int most, int sms, cudaStream_t s)
+{
+    using P = TreeFmaShape<ROWS, DIM>;
+    const int blocks = most < P::BLOCKS * sms ? most : P::BLOCKS * sms;
+    return launch_tree_kernel<float>(k_tree_fma<DIM, ROWS>, a, kTreeFmaThreads, P::SMEM, blocks, sms, s);
+}
+
+template <int DIM>
 cudaError_t launch_tree_fma(const TreeArgs& a, const TreeShape& shape, int most, int sms, cudaStream_t s)
 {
-    const int blocks = most < 2 * sms ? most : 2 * sms;
-    return shape.rows == 16 ? launch_tree_kernel<T>(k_tree_fma<T, CT, DIM, 16>, a, kTreeFmaThreads, TreeFmaShape<16, DIM>::SMEM, blocks, sms, s)
-                            : launch_tree_kernel<T>(k_tree_fma<T, CT, DIM, 64>, a, kTreeFmaThreads, TreeFmaShape<64, DIM>::SMEM, blocks, sms, s);
+    return shape.rows == 16 ? launch_tree_rows<DIM, 16>(a, most, sms, s) : launch_tree_rows<DIM, 64>(a, most, sms, s);
 }
 
 }  // namespace ar

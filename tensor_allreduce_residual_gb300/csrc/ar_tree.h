@@ -37,7 +37,7 @@ struct TreeArgs {
     float softcap;
     float softcap2;           // softcap in base 2
     float v_scale;
-    int boxes;                // whether pages come by tensor copies
+    int boxes;                // tokens of a tensor copy, 0: pages do not come by them
     int token_first;          // whether the maps' second axis is a page's tokens, and not the heads
     int slot_rows;            // rows of a partial slot: [slot_rows][head_dim] sums, [slot_rows] references, [slot_rows] weights
     uint64_t slot_floats;

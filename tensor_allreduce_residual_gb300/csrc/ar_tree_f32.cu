@@ -7,9 +7,9 @@ namespace ar {
 template <>
 cudaError_t launch_tree<float, float>(const TreeArgs& a, const TreeMaps&, const TreeShape& shape, int most, int sms, cudaStream_t s)
 {
-    return a.head_dim <= 64    ? launch_tree_fma<float, float, 64>(a, shape, most, sms, s)
-           : a.head_dim <= 128 ? launch_tree_fma<float, float, 128>(a, shape, most, sms, s)
-                               : launch_tree_fma<float, float, 256>(a, shape, most, sms, s);
+    return a.head_dim <= 64    ? launch_tree_fma<64>(a, shape, most, sms, s)
+           : a.head_dim <= 128 ? launch_tree_fma<128>(a, shape, most, sms, s)
+                               : launch_tree_fma<256>(a, shape, most, sms, s);
 }
 
 }  // namespace ar

@@ -121,27 +121,47 @@ struct TreeMmaShape {
     static constexpr int GROUPS = DIM <= 128 ? 2 : 1;           // softmax warpgroups, each with an O
     static constexpr bool SPLIT = GROUPS == 2 && NM == 1;       // they take alternate tiles
     static_assert(NM <= GROUPS, "a warpgroup for each half of the rows");
-    static constexpr int SOFTMAX = 128 * GROUPS, THREADS = SOFTMAX + 128 + 64;
+    static constexpr int SOFTMAX = 128 * GROUPS, THREADS = SOFTMAX + 128 + 128;
     static constexpr int Q = ROWS * DIM * 2, SLOT = TOKENS * DIM * 2, RAW = SMALL ? TOKENS * DIM : 0;
     static constexpr int MISC = 3072, ROOM = 232448 - MISC;     // a block's 227 KB
-    static constexpr int QS = NM == 1 && DIM <= 128 ? 2 : 1;
+    static constexpr int QS = NM == 1 && DIM <= 128 && !(SMALL && DIM == 128) ? 2 : 1;  // 8-bit: a fourth slot of keys or values instead
     static constexpr int RS = !SMALL ? 0 : DIM == 64 ? 8 : 4;
-    static constexpr int FIT = (ROOM - QS * Q - RS * RAW) / SLOT, NS = FIT < 8 ? FIT : 8;
+    static constexpr int FIT = (ROOM - QS * Q - RS * RAW) / SLOT, NS = FIT < 10 ? FIT : 10;
+    // A step's tokens and the score buffers.  With 256 rows a half of a tile, so that a group has two buffers and its next scores
+    // run while it works on these.  (Tiles of half the size instead cost twice the hand-overs, with up to 128 rows too: 374
+    // against 251 us on 286 MB of e4m3.)
+    static constexpr int HALVES = NM == 2 ? 2 : 1, STEP_TOKENS = TOKENS / HALVES, BUFFERS = 2 * HALVES;
     static_assert(NS >= 3, "a tile's keys and values, and the next one's keys");
+    // Fill f is the keys of tile f / 2, or its values where f is odd.  Keys and values have rings of their own, so that the warps
+    // that bring one never wait for those that bring the other.
+    static constexpr int KS = NS / 2, VS = NS - KS;
+    static __device__ __forceinline__ int slot(int f) { return f & 1 ? KS + (f >> 1) % VS : (f >> 1) % KS; }
+    static __device__ __forceinline__ int round(int f) { return f & 1 ? (f >> 1) / VS : (f >> 1) / KS; }
+    // The fill before f in its slot.
+    static __device__ __forceinline__ int before(int f) { return f - 2 * (f & 1 ? VS : KS); }
     static constexpr int ARRIVALS = 8;  // barriers of fills that need hands: by stage (8-bit), or by tile
-    static_assert(RS <= ARRIVALS && (RS == 0 || RS % 4 == 0) && NS <= 8, "a stage is one warp's; a warp has at most four tiles under way");
-    static constexpr int TILES = SCALED ? 4 : 8;  // descriptions of tiles
+    static_assert(RS <= ARRIVALS && (RS == 0 || RS % 4 == 0) && NS <= 16, "a stage is one warp's; a warp has at most four tiles under way");
+    static constexpr int TILES = SCALED ? 6 : 8;  // descriptions of tiles
+    // Items whose queries' powers of two are kept.  Item i's queries come when the scores of item i - QS are done, and those of a
+    // step when the weights of BUFFERS steps before are used: a group's first step of item i - EXPONENTS is behind that.
+    static constexpr int EXPONENTS = NM == 2 ? 4 : 6;
+    static_assert(EXPONENTS >= QS + 3, "powers are read before they are written over");
     static constexpr int SMEM = QS * Q + NS * SLOT + RS * RAW + MISC;
     // Weights may pass their reference's by 2^AHEAD before it is moved, which costs a pass over O.  fp16 weights are 2^LIFT
     // times as large, so that small ones keep their bits: the largest is 2^15.
     static constexpr float AHEAD = BF16 ? 8.0f : 4.0f, LIFT = BF16 ? 0.0f : 11.0f;
-    static constexpr int S_COLUMNS = TOKENS, O_COLUMN = 256;  // score buffers from column 0 on; O of group m at 256 + 128 m
-    static_assert(2 * S_COLUMNS <= O_COLUMN && O_COLUMN + (DIM <= 128 ? GROUPS * 128 : 256) <= 512, "tensor memory");
-    static constexpr int BARS = 2 * NS + 2 * QS + 2 + 2 + GROUPS + 2 * TILES + 2 + 1 + ARRIVALS + RS;
-    // A step is a half of the rows of a tile, or a tile.
-    static __device__ __forceinline__ int tile_of(int u) { return NM == 2 ? u >> 1 : u; }
+    static constexpr int S_COLUMNS = STEP_TOKENS, O_COLUMN = 256;  // score buffers from column 0 on; O of group m at 256 + 128 m
+    static_assert(BUFFERS * S_COLUMNS <= O_COLUMN && O_COLUMN + (DIM <= 128 ? GROUPS * 128 : 256) <= 512, "tensor memory");
+    static constexpr int BARS = 2 * NS + 2 * QS + 3 * BUFFERS + GROUPS + 2 * TILES + 2 + 2 + ARRIVALS + RS;
+    // A step is a half of the rows of a half of a tile, or a tile.
+    static constexpr int TILE_STEPS = NM * HALVES;
+    static __device__ __forceinline__ int tile_of(int u) { return u / TILE_STEPS; }
+    static __device__ __forceinline__ int half_of(int u) { return HALVES == 2 ? u >> 1 & 1 : 0; }
+    static __device__ __forceinline__ bool first_of_tile(int u) { return u % TILE_STEPS == 0; }
+    static __device__ __forceinline__ bool last_of_tile(int u) { return u % TILE_STEPS == TILE_STEPS - 1; }
     static __device__ __forceinline__ int group_of(int u) { return GROUPS == 2 ? u & 1 : 0; }
     static __device__ __forceinline__ int phase_of(int u) { return GROUPS == 2 ? u >> 1 : u; }  // of the group's O
+    static __device__ __forceinline__ int buffer_of(int u) { return u % BUFFERS; }
 };
 
 // Shared memory, by address.
@@ -155,31 +175,32 @@ struct TreeSmem {
         base = dynamic;
     }
     static constexpr uint32_t KV = P::QS * P::Q, RAW = KV + P::NS * P::SLOT, BAR = RAW + P::RS * P::RAW, TILE = BAR + P::BARS * 8,
-                              SCALE = TILE + P::TILES * sizeof(TreeTile), JOIN = SCALE + (P::SCALED ? P::QS * P::ROWS * 4 : 0),
+                              SCALE = TILE + P::TILES * sizeof(TreeTile), JOIN = SCALE + (P::SCALED ? P::EXPONENTS * P::ROWS : 0),
                               SCAN = (JOIN + (P::SPLIT ? 128 * 8 : 0) + 7) / 8 * 8, SENT = SCAN + (P::THREADS / 32 + 2) * 8, END = SENT + 16 + 8;
     __device__ __forceinline__ uint32_t q(int slot) const { return at + slot * P::Q; }
     __device__ __forceinline__ uint32_t kv(int slot) const { return at + KV + slot * P::SLOT; }
     __device__ __forceinline__ char* raw(int stage) const { return base + RAW + stage * P::RAW; }
     __device__ __forceinline__ uint32_t bar(int i) const { return at + BAR + 8 * i; }
-    static constexpr int B_Q = 2 * P::NS, B_S = B_Q + 2 * P::QS, B_O = B_S + 4, B_TILE = B_O + P::GROUPS, B_END = B_TILE + 2 * P::TILES, B_RAW = B_END + 3;
+    static constexpr int B_Q = 2 * P::NS, B_S = B_Q + 2 * P::QS, B_O = B_S + 3 * P::BUFFERS, B_TILE = B_O + P::GROUPS, B_END = B_TILE + 2 * P::TILES, B_RAW = B_END + 4;
     static_assert(B_RAW + P::ARRIVALS + P::RS == P::BARS, "all barriers");
     __device__ __forceinline__ uint32_t kv_full(int s) const { return bar(s); }
     __device__ __forceinline__ uint32_t kv_empty(int s) const { return bar(P::NS + s); }
     __device__ __forceinline__ uint32_t q_full(int s) const { return bar(B_Q + s); }
     __device__ __forceinline__ uint32_t q_empty(int s) const { return bar(B_Q + P::QS + s); }
     __device__ __forceinline__ uint32_t s_full(int s) const { return bar(B_S + s); }
-    __device__ __forceinline__ uint32_t p_ready(int s) const { return bar(B_S + 2 + s); }
+    __device__ __forceinline__ uint32_t p_ready(int s) const { return bar(B_S + P::BUFFERS + s); }
+    __device__ __forceinline__ uint32_t p_used(int s) const { return bar(B_S + 2 * P::BUFFERS + s); }  // weights, by the product
     __device__ __forceinline__ uint32_t o_done(int m) const { return bar(B_O + m); }
     __device__ __forceinline__ uint32_t tile_full(int i) const { return bar(B_TILE + i); }
     __device__ __forceinline__ uint32_t tile_empty(int i) const { return bar(B_TILE + P::TILES + i); }
     __device__ __forceinline__ uint32_t told() const { return bar(B_END); }       // the second group's references are there
     __device__ __forceinline__ uint32_t taken() const { return bar(B_END + 1); }  // its O has been read
-    __device__ __forceinline__ uint32_t last() const { return bar(B_END + 2); }
+    __device__ __forceinline__ uint32_t last(int i) const { return bar(B_END + 2 + i); }
     __device__ __forceinline__ uint32_t arrived(int i) const { return bar(B_RAW + i); }  // copies that need hands
     __device__ __forceinline__ uint32_t raw_empty(int stage) const { return bar(B_RAW + P::ARRIVALS + stage); }
     __device__ __forceinline__ uint32_t sent(int warp) const { return at + SENT + 4 * warp; }  // a copying warp's next tile
     __device__ __forceinline__ TreeTile& tile(int t) const { return reinterpret_cast<TreeTile*>(base + TILE)[t % P::TILES]; }
-    __device__ __forceinline__ float* scale(int slot) const { return reinterpret_cast<float*>(base + SCALE) + slot * P::ROWS; }
+    __device__ __forceinline__ signed char* exponents(int item) const { return reinterpret_cast<signed char*>(base + SCALE) + item % P::EXPONENTS * P::ROWS; }
     __device__ __forceinline__ float2* join() const { return reinterpret_cast<float2*>(base + JOIN); }
     __device__ __forceinline__ long long* scan() const { return reinterpret_cast<long long*>(base + SCAN); }
     __device__ __forceinline__ uint32_t* tmem() const { return reinterpret_cast<uint32_t*>(base + END - 8); }
@@ -255,24 +276,26 @@ struct TreeFeed {
     {
         return P::SMALL ? (2 * t + (values ? 1 : 0)) % (P::SMALL ? P::RS : 1) : (t & 1) * 4 + (t >> 1 & 3);
     }
+    // Whether the fills of a slot are all one warp's.
+    static constexpr bool ALONE = P::KS % 2 == 0 && P::VS % 2 == 0;
     // What the warp has sent (16-bit) or handed over (8-bit), for the others.
     __device__ __forceinline__ void tell(int next)
     {
-        if (P::NS % 4 != 0 && lane == 0)
+        if (!ALONE && lane == 0)
             asm volatile("st.release.cta.shared::cta.s32 [%0], %1;" ::"r"(sm.sent(warp)), "r"(next) : "memory");
     }
-    // Whether fill f's slot is free.  A parity tells two phases apart only, so the fill before it in the slot, another warp's
-    // where the slots are no multiple of the warps, has to have been sent.
+    // Whether fill f's slot is free.  A parity tells two phases apart only, so the fill before it in the slot, where it is another
+    // warp's, has to have been sent.
     __device__ __forceinline__ bool free(int f) const
     {
-        const int before = f - P::NS;
-        if (P::NS % 4 != 0 && before >= 0) {
+        const int before = P::before(f);
+        if (!ALONE && before >= 0) {
             int next;
             asm volatile("ld.acquire.cta.shared::cta.s32 %0, [%1];" : "=r"(next) : "r"(sm.sent((before & 1) + (before >> 1 & 1) * 2)) : "memory");
             if (!__all_sync(~0u, next > before >> 1))
                 return false;
         }
-        return __all_sync(~0u, bar_poll(sm.kv_empty(f % P::NS), (f / P::NS & 1) ^ 1));
+        return __all_sync(~0u, bar_poll(sm.kv_empty(P::slot(f)), (P::round(f) & 1) ^ 1));
     }
     // Moves the cursor on to tile `tile`, the warp's next, and asks for its pages.
     __device__ __forceinline__ void look(Cur& cur, const Run& line, int n)
@@ -341,14 +364,16 @@ struct TreeFeed {
         } else {
             // bf16 queries on an 8-bit cache: scaled by a power of two a row, so that the largest element becomes 2^14 or more
             // and those down to 2^-28 of it keep all their bits in fp16.
-            float* const scale = sm.scale(s);
+            signed char* const exponents = sm.exponents(filled);
+            constexpr int WIDE = QCH <= 8 ? 8 : QCH <= 16 ? 16 : 32, TOGETHER = 32 / WIDE;  // lanes of a row, rows of a step
+            const int c = lane % WIDE;
 #pragma unroll 4
-            for (int row = warp; row < P::ROWS; row += 4) {
+            for (int row = warp * TOGETHER + lane / WIDE; row < P::ROWS; row += 4 * TOGETHER) {
                 const int i = (row0 + row) / a.group, g = row0 + row - i * a.group;
                 uint4 w = make_uint4(0, 0, 0, 0);
-                if (row < rows && lane < qchunks)
+                if (row < rows && c < qchunks)
                     w = *reinterpret_cast<const uint4*>(a.q + static_cast<uint64_t>(first + i) * a.q_stride +
-                                                        (static_cast<uint64_t>(h) * a.group + g) * a.head_dim * 2 + lane * 16);
+                                                        (static_cast<uint64_t>(h) * a.group + g) * a.head_dim * 2 + c * 16);
                 const float2 f[4] = {Lanes<typename P::T>::two(w.x), Lanes<typename P::T>::two(w.y), Lanes<typename P::T>::two(w.z),
                                      Lanes<typename P::T>::two(w.w)};
                 float most = 0.0f;
@@ -356,20 +381,20 @@ struct TreeFeed {
                 for (int k = 0; k < 4; ++k)
                     most = fmaxf(most, fmaxf(fabsf(f[k].x), fabsf(f[k].y)));
 #pragma unroll
-                for (int o = 16; o > 0; o >>= 1)
+                for (int o = WIDE / 2; o > 0; o >>= 1)
                     most = fmaxf(most, __shfl_xor_sync(~0u, most, o));
                 const int e = max(static_cast<int>(__float_as_uint(most) >> 23) - 127, -112) - 14;
                 const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-                if (lane < QCH) {
+                if (c < QCH) {
                     uint4 x;
                     x.x = Lanes<__half>::word(f[0].x * down, f[0].y * down);
                     x.y = Lanes<__half>::word(f[1].x * down, f[1].y * down);
                     x.z = Lanes<__half>::word(f[2].x * down, f[2].y * down);
                     x.w = Lanes<__half>::word(f[3].x * down, f[3].y * down);
-                    *reinterpret_cast<uint4*>(sm.base + to + (row >> 7) * (128 * P::DIM * 2) + place(row & 127, lane, 128)) = x;
+                    *reinterpret_cast<uint4*>(sm.base + to + (row >> 7) * (128 * P::DIM * 2) + place(row & 127, c, 128)) = x;
                 }
-                if (lane == 0)  // finite: an infinite factor would make the scores of keys that are 0 NaN
-                    scale[row] = fmaxf(fminf(ldexpf(a.scale2, e), FLT_MAX), -FLT_MAX);
+                if (c == 0)
+                    exponents[row] = static_cast<signed char>(e);  // -126 .. 114
             }
             bar_arrive(sm.q_full(s));
         }
@@ -410,7 +435,7 @@ struct TreeFeed {
         }
         const bool hands = P::SMALL || (values && (flags & kTreeMixed));
         const char* const base = values ? a.v : a.k;
-        const uint32_t to = P::SMALL ? smem_addr(sm.raw(f % (P::SMALL ? P::RS : 1))) : sm.kv(f % P::NS);
+        const uint32_t to = P::SMALL ? smem_addr(sm.raw(f % (P::SMALL ? P::RS : 1))) : sm.kv(P::slot(f));
         const uint64_t policy = alone ? once : often;
         tile += 2;
         look(cur, line, n);
@@ -440,7 +465,7 @@ struct TreeFeed {
                 }
             }
         }
-        arrive_with_copies(hands ? sm.arrived(arrival(t)) : sm.kv_full(f % P::NS));
+        arrive_with_copies(hands ? sm.arrived(arrival(t)) : sm.kv_full(P::slot(f)));
         if (!P::SMALL)
             tell(tile);
     }
@@ -453,7 +478,7 @@ struct TreeFeed {
             return false;
         done += 2;
         const bool mixed = values && (mixeds >> (t & 31) & 1) != 0;
-        char* const to = sm.base + (sm.kv(f % P::NS) - sm.at);
+        char* const to = sm.base + (sm.kv(P::slot(f)) - sm.at);
         const char* const raw = sm.raw(f % RS);
         bool bad = false;
 #pragma unroll 1
@@ -485,7 +510,7 @@ struct TreeFeed {
             if (lane == 0)
                 sm.tile(t).bad = bad;
         }
-        bar_arrive(sm.kv_full(f % P::NS));
+        bar_arrive(sm.kv_full(P::slot(f)));
         tell(done);
         return true;
     }
@@ -496,7 +521,7 @@ struct TreeFeed {
             done += 2;
         if (done >= tile)
             return false;
-        const int t = done, s = (2 * t + 1) % P::NS, i = arrival(t);
+        const int t = done, s = P::slot(2 * t + 1), i = arrival(t);
         if (!__all_sync(~0u, bar_poll(sm.arrived(i), phases >> i & 1)))
             return false;
         phases ^= 1u << i;
@@ -540,114 +565,124 @@ struct TreeFeed {
         }
         return __any_sync(~0u, late || *stop != 0);
     }
-    // Waits for a phase, and fills queries' slots meanwhile.  Suspended between looks: a warp that polls takes others'
-    // instructions out of the cache.
-    __device__ __forceinline__ bool until(uint32_t bar, uint32_t parity, int n)
+    // 8-bit: a half of a fill, from its stage to its slot.
+    __device__ __forceinline__ void convert_half(TreeTile& x, int f, bool sift)
     {
-        if (__all_sync(~0u, bar_test(bar, parity)))
-            return true;
-        unsigned long long idle_since = 0;
-        do
-            if (queries(n))
-                idle_since = 0;
-            else if (gave_up(idle_since))
-                return false;
-        while (!__all_sync(~0u, bar_test(bar, parity)));
-        return true;
+        constexpr int RS = P::SMALL ? P::RS : 1;
+        char* const to = sm.base + (sm.kv(P::slot(f)) - sm.at);
+        const char* const raw = sm.raw(f % RS);
+        bool bad = false;
+        constexpr int HALF = BLOCKS * CH / 2, ONCE = 4;  // steps of the warp, and at once
+        static_assert(HALF % ONCE == 0, "whole groups of steps");
+        const int which = warp & 1;
+#pragma unroll 1
+        for (int i0 = 0; i0 < HALF; i0 += ONCE) {
+            uint4 all[ONCE];
+#pragma unroll
+            for (int i = 0; i < ONCE; ++i)
+                all[i] = *reinterpret_cast<const uint4*>(raw + (((i0 + i) * 2 + which) * 32 + lane) * 16);
+#pragma unroll
+            for (int i = 0; i < ONCE; ++i) {
+                const int at_chunk = ((i0 + i) * 2 + which) * 32 + lane, row = at_chunk / CH, c = at_chunk - row * CH;
+                const uint4 w = all[i];
+                uint32_t y[8] = {half2_of_e4m3(w.x), half2_of_e4m3(w.x >> 16), half2_of_e4m3(w.y), half2_of_e4m3(w.y >> 16),
+                                 half2_of_e4m3(w.z), half2_of_e4m3(w.z >> 16), half2_of_e4m3(w.w), half2_of_e4m3(w.w >> 16)};
+                if (sift) {
+                    const bool there = x.valid[row >> 5] >> (row & 31) & 1;
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const uint32_t z = not_finite<__half>(y[j]);
+                        bad = bad || (there && z != 0);
+                        y[j] = there ? y[j] & ~z : 0u;
+                    }
+                }
+                *reinterpret_cast<uint4*>(to + place(row, 2 * c, P::TOKENS)) = make_uint4(y[0], y[1], y[2], y[3]);
+                *reinterpret_cast<uint4*>(to + place(row, 2 * c + 1, P::TOKENS)) = make_uint4(y[4], y[5], y[6], y[7]);
+            }
+        }
+        if (bad)
+            x.bad = 1;
     }
-    // What tensor copies leave to do: queries, and of the fills that need hands a quarter each.
+    // 16-bit: infinite values and NaN, and whatever lies where no token is, become 0 in a quarter of a tile's values.
+    __device__ __forceinline__ void sift_quarter(TreeTile& x, int s)
+    {
+        bool bad = false;
+        char* const to = sm.base + (sm.kv(s) - sm.at);
+#pragma unroll 4
+        for (int j = warp * 32 + lane; j < P::TOKENS * P::DIM / 8; j += 128) {
+            const int row = j / (P::DIM / 8), c = j - row * (P::DIM / 8);
+            const bool there = x.valid[row >> 5] >> (row & 31) & 1;
+            uint4* const p = reinterpret_cast<uint4*>(to + place(row, c, P::TOKENS));
+            const uint4 w = *p;
+            const uint4 y = make_uint4(not_finite<typename P::MT>(w.x), not_finite<typename P::MT>(w.y), not_finite<typename P::MT>(w.z),
+                                       not_finite<typename P::MT>(w.w));
+            const bool found = (y.x | y.y | y.z | y.w) != 0;
+            bad = bad || (there && found);
+            if (!there)
+                *p = make_uint4(0, 0, 0, 0);
+            else if (found)
+                *p = make_uint4(w.x & ~y.x, w.y & ~y.y, w.z & ~y.z, w.w & ~y.w);
+        }
+        if (bad)
+            x.bad = 1;
+    }
+    // What tensor copies leave to do: queries, and the fills that need hands: in 8 bits two warps take the keys and two the
+    // values, in 16 bits all four the values of tiles that rows see in part.  One loop over the two stages of a tile (its
+    // description, then its fill), with queries wherever the next stage has to wait.
     __device__ bool help(int n)
     {
+        constexpr int RS = P::SMALL ? P::RS : 1;
+        const int kind = P::SMALL ? warp >> 1 : 1;  // 1: values
         uint32_t used = 0;  // phases of `arrived` (16-bit)
-        for (int t = 0; t < n; ++t) {
-            queries(n);
-            if (!until(sm.tile_full(t % P::TILES), t / P::TILES & 1, n))
-                return false;
+        unsigned long long idle_since = 0;
+        int t = 0;
+        bool described = false;
+        while (t < n || item_tile < n) {
+            const int f = 2 * t + kind;
+            bool can = false;
+            if (t < n) {
+                if (!described)
+                    can = bar_test(sm.tile_full(t % P::TILES), t / P::TILES & 1);
+                else if (P::SMALL)
+                    can = bar_test(sm.arrived(f % RS), f / RS & 1) && bar_test(sm.kv_empty(P::slot(f)), (P::round(f) & 1) ^ 1);
+                else
+                    can = bar_test(sm.arrived(t % P::ARRIVALS), used >> (t % P::ARRIVALS) & 1);
+            }
+            if (!__all_sync(~0u, can)) {
+                if (queries(n))
+                    idle_since = 0;
+                else if (gave_up(idle_since))
+                    return false;
+                continue;
+            }
+            idle_since = 0;
             TreeTile& x = sm.tile(t);
             const bool mixed = x.flags & kTreeMixed;
-            if constexpr (P::SMALL) {
-                for (int f = 2 * t; f < 2 * t + 2; ++f) {
-                    constexpr int RS = P::SMALL ? P::RS : 1;
-                    if (!until(sm.arrived(f % RS), f / RS & 1, n) || !until(sm.kv_empty(f % P::NS), (f / P::NS & 1) ^ 1, n))
-                        return false;
-                    const bool sift = (f & 1) != 0 && mixed;
-                    char* const to = sm.base + (sm.kv(f % P::NS) - sm.at);
-                    const char* const raw = sm.raw(f % RS);
-                    bool bad = false;
-                    constexpr int QUARTER = BLOCKS * CH / 4, ONCE = QUARTER % 4 == 0 ? 4 : 2;  // steps of the warp, and at once
-                    static_assert(QUARTER % ONCE == 0 && BLOCKS * CH % 4 == 0, "whole groups of steps");
-#pragma unroll 1
-                    for (int i0 = 0; i0 < QUARTER; i0 += ONCE) {
-                        uint4 all[ONCE];
-#pragma unroll
-                        for (int i = 0; i < ONCE; ++i)
-                            all[i] = *reinterpret_cast<const uint4*>(raw + (((i0 + i) * 4 + warp) * 32 + lane) * 16);
-#pragma unroll
-                        for (int i = 0; i < ONCE; ++i) {
-                            const int at_chunk = ((i0 + i) * 4 + warp) * 32 + lane, row = at_chunk / CH, c = at_chunk - row * CH;
-                            const uint4 w = all[i];
-                            uint32_t y[8] = {half2_of_e4m3(w.x), half2_of_e4m3(w.x >> 16), half2_of_e4m3(w.y), half2_of_e4m3(w.y >> 16),
-                                             half2_of_e4m3(w.z), half2_of_e4m3(w.z >> 16), half2_of_e4m3(w.w), half2_of_e4m3(w.w >> 16)};
-                            if (sift) {
-                                const bool in = x.valid[row >> 5] >> (row & 31) & 1;
-#pragma unroll
-                                for (int j = 0; j < 8; ++j) {
-                                    const uint32_t z = not_finite<__half>(y[j]);
-                                    bad = bad || (in && z != 0);
-                                    y[j] = in ? y[j] & ~z : 0u;
-                                }
-                            }
-                            *reinterpret_cast<uint4*>(to + place(row, 2 * c, P::TOKENS)) = make_uint4(y[0], y[1], y[2], y[3]);
-                            *reinterpret_cast<uint4*>(to + place(row, 2 * c + 1, P::TOKENS)) = make_uint4(y[4], y[5], y[6], y[7]);
-                        }
-                    }
-                    if (bad)
-                        x.bad = 1;
-                    __syncwarp();
-                    if (lane == 0) {
-                        bar_arrive(sm.kv_full(f % P::NS));
-                        bar_arrive(sm.raw_empty(f % RS));
-                    }
+            if (!described && (P::SMALL || mixed)) {
+                described = true;
+                queries(n);
+                continue;
+            }
+            if (described) {
+                if constexpr (P::SMALL) {
+                    convert_half(x, f, kind == 1 && mixed);
+                } else {
+                    used ^= 1u << t % P::ARRIVALS;
+                    sift_quarter(x, P::slot(f));
                 }
-            } else if (mixed) {
-                const int s = (2 * t + 1) % P::NS, i = t % P::ARRIVALS;
-                if (!until(sm.arrived(i), used >> i & 1, n))
-                    return false;
-                used ^= 1u << i;
-                // Infinite values and NaN, and whatever lies where no token is, become 0.
-                bool bad = false;
-                char* const to = sm.base + (sm.kv(s) - sm.at);
-#pragma unroll 4
-                for (int j = warp * 32 + lane; j < P::TOKENS * P::DIM / 8; j += 128) {
-                    const int row = j / (P::DIM / 8), c = j - row * (P::DIM / 8);
-                    const bool in = x.valid[row >> 5] >> (row & 31) & 1;
-                    uint4* const p = reinterpret_cast<uint4*>(to + place(row, c, P::TOKENS));
-                    const uint4 w = *p;
-                    const uint4 y = make_uint4(not_finite<typename P::MT>(w.x), not_finite<typename P::MT>(w.y), not_finite<typename P::MT>(w.z),
-                                               not_finite<typename P::MT>(w.w));
-                    const bool found = (y.x | y.y | y.z | y.w) != 0;
-                    bad = bad || (in && found);
-                    if (!in)
-                        *p = make_uint4(0, 0, 0, 0);
-                    else if (found)
-                        *p = make_uint4(w.x & ~y.x, w.y & ~y.y, w.z & ~y.z, w.w & ~y.w);
-                }
-                if (bad)
-                    x.bad = 1;
                 __syncwarp();
-                if (lane == 0)
-                    bar_arrive(sm.kv_full(s));
+                if (lane == 0) {
+                    bar_arrive(sm.kv_full(P::slot(f)));
+                    if (P::SMALL)
+                        bar_arrive(sm.raw_empty(f % RS));
+                }
             }
             __syncwarp();
             if (lane == 0)
                 bar_arrive(sm.tile_empty(t % P::TILES));
+            ++t;
+            described = false;
         }
-        unsigned long long idle_since = 0;
-        while (item_tile < n)  // the last items' queries may have no room yet
-            if (queries(n))
-                idle_since = 0;
-            else if (gave_up(idle_since))
-                return false;
         return true;
     }
     __device__ bool run(Cur cur, const Run& line, int n)
@@ -680,10 +715,10 @@ struct TreeFeed {
 
 // ---------------------------------------------------------------------------
 // Tensor copies, where pages and tiles divide each other and pages are whole
-// groups of eight tokens: one warp looks the tile's pages up and one of its
-// lanes asks for a box of up to 64 elements (16-bit; all of them in 8 bits) by
-// a page's tokens at a time, which arrives permuted as the tensor core reads
-// it.  What it brings for tokens that are not in the cache, and the rows of
+// groups of eight tokens: a warp for the keys and one for the values look a
+// tile's pages up, and each lane asks for a box of up to 64 elements (16-bit;
+// all of them in 8 bits) by a page's tokens, which arrives permuted as the
+// tensor core reads it.  What it brings for tokens that are not in the cache, and the rows of
 // pages that are none, are the helping warps' to clear.
 // ---------------------------------------------------------------------------
 template <typename P>
@@ -695,15 +730,21 @@ struct TreeBoxes {
     volatile int* stop;
     int lane, box, runs, blocks;  // tokens of a box, boxes of tokens and of elements in a tile
     int run_of, block;            // the lane's box
+    bool values;                  // whose the warp is
+    int shift[P::TOKENS / 32];    // of the boxes that the lane's tokens of each 32 lie in
     uint64_t once, often;
     int page = -1, slot = 0;
 
     __device__ TreeBoxes(const TreeArgs& a_, const TreeSmem<P>& sm_, const TreeMaps& maps_, volatile int* stop_)
-        : a(a_), sm(sm_), maps(maps_), stop(stop_), lane(threadIdx.x & 31), box(min(a_.page_size, P::TOKENS)), runs(P::TOKENS / box),
-          blocks(P::SMALL ? 1 : (a_.head_dim + 63) / 64), run_of(lane / blocks), block(lane - run_of * blocks)
+        : a(a_), sm(sm_), maps(maps_), stop(stop_), lane(threadIdx.x & 31), box(a_.boxes), runs(P::TOKENS / box),
+          blocks(P::SMALL ? 1 : (a_.head_dim + 63) / 64), run_of(lane / blocks), block(lane - run_of * blocks),
+          values((threadIdx.x >> 5) == P::THREADS / 32 - 1)
     {
         asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(once));
         asm("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(often));
+#pragma unroll
+        for (int k = 0; k < P::TOKENS / 32; ++k)
+            shift[k] = (32 * k + lane) / box * blocks;
     }
     // The page of the lane's box; there are 32 at most (16 by 2 of 8 tokens, 8 by 4).
     __device__ __forceinline__ void look_up(const Cur& cur)
@@ -736,31 +777,33 @@ struct TreeBoxes {
 #pragma unroll
             for (int k = 0; k < P::TOKENS / 32; ++k) {
                 const int token = token0 + 32 * k + lane;
-                valid[k] = __ballot_sync(~0u, token >= cur.s.start && token < cur.s.end && (there >> ((32 * k + lane) / box * blocks) & 1) != 0);
+                valid[k] = __ballot_sync(~0u, token >= cur.s.start && token < cur.s.end && (there >> shift[k] & 1) != 0);
                 whole = whole && valid[k] == ~0u;
             }
             const bool mixed = !whole || tree_mixed(a, cur.q, token0, P::TOKENS);
-            if (!bar_wait(sm.tile_empty(t % P::TILES), (t / P::TILES & 1) ^ 1, stop))
-                return false;
-            if (lane == 0) {
-                TreeTile& x = sm.tile(t);
-                x.q = cur.q;
-                x.head = head;
-                x.row0 = cur.rt * P::ROWS;
-                x.rows = cur.rows(a);
-                x.token0 = token0;
-                x.b = cur.b;
-                x.bad = 0;
-                x.flags = (begins || t == 0 ? kTileFirst : 0) | (ends || t + 1 == n ? kTileLast : 0) | (begins ? kTileBegins : 0) | (ends ? kTileEnds : 0) |
-                          (mixed ? kTreeMixed : 0);
-#pragma unroll
-                for (int k = 0; k < P::TOKENS / 32; ++k)
-                    x.valid[k] = valid[k];
-                if (begins && n - t < cur.s.tiles)
-                    leave_job(a, cur, line, t);
-                bar_arrive(sm.tile_full(t % P::TILES));
+            if (!values) {
+                if (!bar_wait(sm.tile_empty(t % P::TILES), (t / P::TILES & 1) ^ 1, stop))
+                    return false;
+                if (lane == 0) {
+                    TreeTile& x = sm.tile(t);
+                    x.q = cur.q;
+                    x.head = head;
+                    x.row0 = cur.rt * P::ROWS;
+                    x.rows = cur.rows(a);
+                    x.token0 = token0;
+                    x.b = cur.b;
+                    x.bad = 0;
+                    x.flags = (begins || t == 0 ? kTileFirst : 0) | (ends || t + 1 == n ? kTileLast : 0) | (begins ? kTileBegins : 0) | (ends ? kTileEnds : 0) |
+                              (mixed ? kTreeMixed : 0);
+    #pragma unroll
+                    for (int k = 0; k < P::TOKENS / 32; ++k)
+                        x.valid[k] = valid[k];
+                    if (begins && n - t < cur.s.tiles)
+                        leave_job(a, cur, line, t);
+                    bar_arrive(sm.tile_full(t % P::TILES));
+                }
+                __syncwarp();
             }
-            __syncwarp();
             const uint64_t policy = row_blocks<P::ROWS>(a, cur.q) == 1 ? once : often;
             if (t + 1 < n) {
                 if (ends)
@@ -769,7 +812,8 @@ struct TreeBoxes {
                     ++cur.tile;
                 look_up(cur);
             }
-            for (int f = 2 * t; f < 2 * t + 2; ++f) {
+            {
+                const int f = 2 * t + (values ? 1 : 0);
                 uint32_t to, bar;
                 bool hands = P::SMALL;
                 if constexpr (P::SMALL) {
@@ -779,11 +823,11 @@ struct TreeBoxes {
                     to = smem_addr(sm.raw(f % RS));
                     bar = sm.arrived(f % RS);
                 } else {
-                    if (!bar_wait(sm.kv_empty(f % P::NS), (f / P::NS & 1) ^ 1, stop))
+                    if (!bar_wait(sm.kv_empty(P::slot(f)), (P::round(f) & 1) ^ 1, stop))
                         return false;
-                    to = sm.kv(f % P::NS);
+                    to = sm.kv(P::slot(f));
                     hands = (f & 1) != 0 && mixed;
-                    bar = hands ? sm.arrived(t % P::ARRIVALS) : sm.kv_full(f % P::NS);
+                    bar = hands ? sm.arrived(t % P::ARRIVALS) : sm.kv_full(P::slot(f));
                 }
                 if (elected()) {
                     const uint32_t bytes = __popc(there) * box * (P::SMALL ? P::DIM : 128);
@@ -803,89 +847,97 @@ struct TreeBoxes {
 };
 
 // ---------------------------------------------------------------------------
-// The products: scores of step u + 1, then the weighted values of step u.  The
-// whole warp goes through the loop and one lane issues, so that descriptors and
-// addresses stay in uniform registers (a lane alone took some 150 cycles to
-// issue each).
+// The products, a warp for the scores and one for the weighted values: a group
+// of eight or sixteen costs its warp some 400 cycles of waits and barriers
+// beside their own time, which one warp for both spent between them (8100
+// cycles a tile of 128 tokens and 256 rows; the products take 3700).  All lanes
+// go through the loops and one issues.
 // ---------------------------------------------------------------------------
 template <typename P>
-__device__ bool tree_products(const TreeArgs& a, const TreeSmem<P>& sm, uint32_t tmem, int n, volatile int* stop)
+__device__ bool tree_scores(const TreeArgs& a, const TreeSmem<P>& sm, uint32_t tmem, int n, volatile int* stop)
 {
     const int ksteps = (a.head_dim + 15) / 16;
-    const uint32_t desc_s = product_desc(P::BF16, P::TOKENS, false), desc_o = product_desc(P::BF16, 16 * ksteps, true);
-    const int steps = n * P::NM;
-    int items = 0;        // whose queries have been waited for
-    uint32_t firsts = 0;  // which of the last tiles begin the block's part of an item, by number
-    const auto scores = [&](int u) {
-        const int t = P::tile_of(u), m = u % P::NM, s = 2 * t % P::NS;
-        if (m == 0) {
+    const uint32_t desc = product_desc(P::BF16, P::STEP_TOKENS, false);
+    int items = 0;  // whose queries have been waited for
+    bool last = false;
+    for (int u = 0; u < n * P::TILE_STEPS; ++u) {
+        const int t = P::tile_of(u), s = P::slot(2 * t);
+        if (P::first_of_tile(u)) {
             if (!bar_wait(sm.tile_full(t % P::TILES), t / P::TILES & 1, stop))
                 return false;
-            const bool first = __shfl_sync(~0u, sm.tile(t).flags, 0) & kTileFirst;
-            firsts = (firsts & ~(1u << (t & 31))) | (first ? 1u : 0u) << (t & 31);
-            if (first) {
+            const int flags = __shfl_sync(~0u, sm.tile(t).flags, 0);
+            last = flags & kTileLast;
+            if (flags & kTileFirst) {
                 if (!bar_wait(sm.q_full(items % P::QS), items / P::QS & 1, stop))
                     return false;
                 ++items;
             }
-            if (!bar_wait(sm.kv_full(s), 2 * t / P::NS & 1, stop))
+            if (!bar_wait(sm.kv_full(s), P::round(2 * t) & 1, stop))
                 return false;
             fence_async_proxy();  // between the copying warps' writes, which the barrier has shown, and the product's reads
         }
-        const bool last = __shfl_sync(~0u, sm.tile(t).flags, 0) & kTileLast;
+        // The buffer holds the weights of the step that had it before until their product is done.
+        if (!bar_wait(sm.p_used(P::buffer_of(u)), (u / P::BUFFERS & 1) ^ 1, stop))
+            return false;
         tcgen05_after_sync();
-        const uint64_t q = operand_desc(sm.q((items - 1) % P::QS) + m * (128 * P::DIM * 2), 16, 1024), k = operand_desc(sm.kv(s), 16, 1024);
-        const uint32_t d = tmem + (u & 1) * P::S_COLUMNS;
-        if (elected()) {
-            // 32 bytes on, then the next 64 elements' block; addresses count 16 bytes
+        const uint64_t q = operand_desc(sm.q((items - 1) % P::QS) + u % P::NM * (128 * P::DIM * 2), 16, 1024),
+                       k = operand_desc(sm.kv(s) + P::half_of(u) * (P::STEP_TOKENS * 128), 16, 1024);
+        const uint32_t d = tmem + P::buffer_of(u) * P::S_COLUMNS;
+        const bool one = elected();
+        // 32 bytes on, then the next 64 elements' block; addresses count 16 bytes
 #pragma unroll
-            for (int j = 0; j < P::DIM / 16; ++j)
-                if (j < ksteps)
-                    mma_shared(d, q + (j >> 2) * (128 * 128 / 16) + (j & 3) * 2, k + (j >> 2) * (P::TOKENS * 128 / 16) + (j & 3) * 2, desc_s, j > 0);
-            tcgen05_commit(sm.s_full(u & 1));
-            if (m == P::NM - 1) {
-                tcgen05_commit(sm.kv_empty(s));
-                if (last)
-                    tcgen05_commit(sm.q_empty((items - 1) % P::QS));
-            }
+        for (int j = 0; j < P::DIM / 16; ++j)
+            if (j < ksteps)
+                mma_shared(d, q + (j >> 2) * (128 * 128 / 16) + (j & 3) * 2, k + (j >> 2) * (P::TOKENS * 128 / 16) + (j & 3) * 2, desc, j > 0, one);
+        tcgen05_commit(sm.s_full(P::buffer_of(u)), one);
+        if (P::SCALED && one)  // the queries' powers of two, which the wait for the queries has shown this warp, to the softmax too
+            bar_arrive(sm.s_full(P::buffer_of(u)));
+        if (P::last_of_tile(u)) {
+            tcgen05_commit(sm.kv_empty(s), one);
+            if (last)
+                tcgen05_commit(sm.q_empty((items - 1) % P::QS), one);
         }
         __syncwarp();
-        return true;
-    };
-    if (!scores(0))
-        return false;
-    for (int u = 0; u < steps; ++u) {
-        const int t = P::tile_of(u), f = 2 * t + 1, s = f % P::NS;
-        // Of the group's O: with alternate tiles, two of an item are first ones.
-        const bool begins = (firsts >> (t & 31) & 1) != 0 || (P::SPLIT && t > 0 && (firsts >> (t - 1 & 31) & 1) != 0);
-        if (u + 1 < steps) {
-            // The scores' buffer holds the weights of step u - 1 until its product is done.
-            if (u > 0 && !bar_wait(sm.o_done(P::group_of(u - 1)), P::phase_of(u - 1) & 1, stop))
+    }
+    return true;
+}
+
+template <typename P>
+__device__ bool tree_values(const TreeArgs& a, const TreeSmem<P>& sm, uint32_t tmem, int n, volatile int* stop)
+{
+    const uint32_t desc = product_desc(P::BF16, (a.head_dim + 15) / 16 * 16, true);
+    bool first = false, second = false;  // whether the tile is the first of the block's part of an item, or the one after it
+    for (int u = 0; u < n * P::TILE_STEPS; ++u) {
+        const int t = P::tile_of(u), f = 2 * t + 1, s = P::slot(f);
+        if (P::first_of_tile(u)) {
+            if (!bar_wait(sm.tile_full(t % P::TILES), t / P::TILES & 1, stop))
                 return false;
-            if (!scores(u + 1))
-                return false;
-        }
-        if (!bar_wait(sm.p_ready(u & 1), u >> 1 & 1, stop))
-            return false;
-        if (u % P::NM == 0) {
-            if (!bar_wait(sm.kv_full(s), f / P::NS & 1, stop))
+            second = first;
+            first = __shfl_sync(~0u, sm.tile(t).flags, 0) & kTileFirst;
+            if (elected())
+                bar_arrive(sm.tile_empty(t % P::TILES));  // the softmax may be done with it long before this warp looks
+            if (!bar_wait(sm.kv_full(s), P::round(f) & 1, stop))
                 return false;
             fence_async_proxy();
         }
+        // Of the group's O: with alternate tiles, two of an item are first ones.
+        const bool begins = (first && P::half_of(u) == 0) || (P::SPLIT && second);
+        if (!bar_wait(sm.p_ready(P::buffer_of(u)), u / P::BUFFERS & 1, stop))
+            return false;
         tcgen05_after_sync();
-        const uint32_t p = tmem + (u & 1) * P::S_COLUMNS, o = tmem + P::O_COLUMN + P::group_of(u) * 128;
-        const uint64_t v = operand_desc(sm.kv(s), P::TOKENS * 128, 1024);
-        if (elected()) {
+        const uint32_t p = tmem + P::buffer_of(u) * P::S_COLUMNS, o = tmem + P::O_COLUMN + P::group_of(u) * 128;
+        const uint64_t v = operand_desc(sm.kv(s) + P::half_of(u) * (P::STEP_TOKENS * 128), P::TOKENS * 128, 1024);
+        const bool one = elected();
 #pragma unroll
-            for (int j = 0; j < P::TOKENS / 16; ++j) {
-                const uint32_t w = p + (j >> 1) * 32 + (j & 1) * 8;  // of 32 tokens 16 columns of weights, then 16 of what they leave
-                mma_tensor(o, w, v + j * (2048 / 16), desc_o, !(begins && j == 0));
-                mma_tensor(o, w + 16, v + j * (2048 / 16), desc_o, true);
-            }
-            tcgen05_commit(sm.o_done(P::group_of(u)));
-            if (u % P::NM == P::NM - 1)
-                tcgen05_commit(sm.kv_empty(s));
+        for (int j = 0; j < P::STEP_TOKENS / 16; ++j) {
+            const uint32_t w = p + (j >> 1) * 32 + (j & 1) * 8;  // of 32 tokens 16 columns of weights, then 16 of what they leave
+            mma_tensor(o, w, v + j * (2048 / 16), desc, !(begins && j == 0), one);
+            mma_tensor(o, w + 16, v + j * (2048 / 16), desc, true, one);
         }
+        tcgen05_commit(sm.p_used(P::buffer_of(u)), one);
+        tcgen05_commit(sm.o_done(P::group_of(u)), one);
+        if (P::last_of_tile(u))
+            tcgen05_commit(sm.kv_empty(s), one);
         __syncwarp();
     }
     return true;
@@ -929,11 +981,12 @@ struct TreeSoft {
     template <bool PART, bool CAP>
     __device__ __forceinline__ bool weights(const TreeTile& tile, uint32_t s, bool first, int u)
     {
-        constexpr int CHUNKS = P::TOKENS / 32;
+        constexpr int CHUNKS = P::STEP_TOKENS / 32;
+        const int c0 = P::half_of(u) * CHUNKS;  // the step's first 32 tokens
         float most = -INFINITY;
 #pragma unroll 1
         for (int c = 0; c < CHUNKS; ++c) {
-            const uint32_t word = PART ? seen(tile, c) : ~0u;
+            const uint32_t word = PART ? seen(tile, c0 + c) : ~0u;
             uint32_t x[32];
             tmem_load32(s + 32 * c, x);
             tcgen05_wait_load();
@@ -972,7 +1025,7 @@ struct TreeSoft {
         float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll 1
         for (int c = 0; c < CHUNKS; ++c) {
-            const uint32_t word = PART ? seen(tile, c) : ~0u;
+            const uint32_t word = PART ? seen(tile, c0 + c) : ~0u;
             uint32_t x[32], w[32];
             tmem_load32(s + 32 * c, x);
             tcgen05_wait_load();
@@ -1024,7 +1077,7 @@ struct TreeSoft {
             for (int i = 0; i < 32; ++i)
                 add[i] = 0.0f;
 #pragma unroll 1
-            for (int c = 0; c < P::TOKENS / 32 && valid; ++c) {
+            for (int c = P::half_of(u) * (P::STEP_TOKENS / 32); c < (P::half_of(u) + 1) * (P::STEP_TOKENS / 32) && valid; ++c) {
 #pragma unroll 1
                 for (uint32_t word = tile.valid[c] & sees.sees(tile.token0 + 32 * c); word != 0; word &= word - 1) {
                     const int token = tile.token0 + 32 * c + __ffs(word) - 1;
@@ -1168,7 +1221,6 @@ struct TreeSoft {
                 return false;
             const TreeTile& tile = sm.tile(t);
             const int flags = tile.flags;
-            const int u = P::NM == 2 ? 2 * t + m : t;
             if (flags & kTileFirst) {
                 began = flags & kTileBegins;
                 valid = row < tile.rows;
@@ -1178,45 +1230,42 @@ struct TreeSoft {
                 total = 0.0f;
                 own = -1;
                 factor = a.scale2;
-                if constexpr (P::SCALED) {
-                    if (!bar_wait(sm.q_full(items % P::QS), items / P::QS & 1, stop))
-                        return false;
-                    factor = sm.scale(items % P::QS)[row];
-                    __syncwarp();
-                    if (lane == 0)
-                        bar_arrive(sm.q_empty(items % P::QS));
-                }
                 ++items;
             }
-            if (!P::SPLIT || (t & 1) == m) {
-                if (!bar_wait(sm.s_full(u & 1), u >> 1 & 1, stop))
+#pragma unroll 1
+            for (int half = 0; half < P::HALVES && (!P::SPLIT || (t & 1) == m); ++half) {
+                const int u = P::NM == 2 ? 4 * t + 2 * half + m : t;
+                if (!bar_wait(sm.s_full(P::buffer_of(u)), u / P::BUFFERS & 1, stop))
                     return false;
                 tcgen05_after_sync();
+                if (P::SCALED && own < 0)  // finite: an infinite factor would make the scores of keys that are 0 NaN
+                    factor = fmaxf(fminf(ldexpf(a.scale2, sm.exponents(items - 1)[row]), FLT_MAX), -FLT_MAX);
                 if (any) {
                     bool part = flags & kTreeMixed;
 #pragma unroll
                     for (int w = 0; w < P::TOKENS / 32; ++w)
                         part = part || tile.valid[w] != ~0u;
-                    const uint32_t s = tmem + lanes + (u & 1) * P::S_COLUMNS;
+                    const uint32_t s = tmem + lanes + P::buffer_of(u) * P::S_COLUMNS;
                     if (!weights(tile, s, own < 0, u, part))
                         return false;
                 }
                 bool bad = false;
                 if (flags & kTreeMixed) {  // the values have to be there first; once the weights are, their slot may be filled anew
                     const int f = 2 * t + 1;
-                    if (!bar_wait(sm.kv_full(f % P::NS), f / P::NS & 1, stop))
+                    if (!bar_wait(sm.kv_full(P::slot(f)), P::round(f) & 1, stop))
                         return false;
                     bad = any && *const_cast<const volatile int*>(&tile.bad) != 0;
                 }
-                // A parity tells two phases apart only: the last product has to be seen done before the next can be.
-                if (P::phase_of(u) > 0 && !bar_wait(sm.o_done(m), P::phase_of(u) - 1 & 1, stop))
+                // A parity tells two phases apart only: where this step's product is waited for, the group's last one has to be
+                // seen done before it can be.  (The one before that was, when this step's scores were begun.)
+                if ((bad || (flags & kTileLast)) && P::phase_of(u) > 0 && !bar_wait(sm.o_done(m), P::phase_of(u) - 1 & 1, stop))
                     return false;
                 if (!joined())
                     return false;
                 tcgen05_before_sync();
                 __syncwarp();
                 if (lane == 0)
-                    bar_arrive(sm.p_ready(u & 1));
+                    bar_arrive(sm.p_ready(P::buffer_of(u)));
                 own = u;
                 if (bad && !poison(tile, u, valid))
                     return false;
@@ -1239,37 +1288,39 @@ k_tree_mma(const TreeArgs a, const __grid_constant__ TreeMaps maps)
     pdl_enter();
     const TreeSmem<P> sm(dynamic);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    constexpr int COPY = P::SOFTMAX / 32, ISSUE = COPY + 4;
+    constexpr int COPY = P::SOFTMAX / 32, ISSUE = COPY + 4, BOXES = ISSUE + 2;
     volatile int* const stop = sm.stop();
     if (warp == ISSUE)
         tmem_alloc(smem_addr(sm.tmem()), 512);
     if (threadIdx.x == 0) {
         *stop = 0;
         for (int i = 0; i < P::NS; ++i) {
-            bar_init(sm.kv_full(i), a.boxes ? 4 : 32);  // the helping warps, or a copying warp's threads
+            bar_init(sm.kv_full(i), a.boxes ? (P::SMALL ? 2 : 4) : 32);  // the helping warps, or a copying warp's threads
             bar_init(sm.kv_empty(i), 1);
         }
         for (int i = 0; i < P::QS; ++i) {
             bar_init(sm.q_full(i), 128);
-            bar_init(sm.q_empty(i), P::SCALED ? 1 + P::SOFTMAX / 32 : 1);  // the product's, and the factors' readers
+            bar_init(sm.q_empty(i), 1);
         }
-        for (int i = 0; i < 2; ++i) {
-            bar_init(sm.s_full(i), 1);
+        for (int i = 0; i < P::BUFFERS; ++i) {
+            bar_init(sm.s_full(i), P::SCALED ? 2 : 1);
             bar_init(sm.p_ready(i), 4);
+            bar_init(sm.p_used(i), 1);
         }
         for (int i = 0; i < P::GROUPS; ++i)
             bar_init(sm.o_done(i), 1);
         for (int i = 0; i < P::TILES; ++i) {
             bar_init(sm.tile_full(i), 1);
-            bar_init(sm.tile_empty(i), P::SOFTMAX / 32 + (a.boxes ? 4 : 0));
+            bar_init(sm.tile_empty(i), P::SOFTMAX / 32 + 1 + (a.boxes ? 4 : 0));
         }
         bar_init(sm.told(), 4);
         bar_init(sm.taken(), 4);
-        bar_init(sm.last(), 1);
+        bar_init(sm.last(0), 1);
+        bar_init(sm.last(1), 1);
         for (int i = 0; i < P::ARRIVALS; ++i)
             bar_init(sm.arrived(i), a.boxes ? 1 : 32);
         for (int i = 0; i < P::RS; ++i)
-            bar_init(sm.raw_empty(i), 4);
+            bar_init(sm.raw_empty(i), 2);
         for (int i = 0; i < 4; ++i)
             *reinterpret_cast<int*>(dynamic + TreeSmem<P>::SENT + 4 * i) = i >> 1;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -1283,21 +1334,23 @@ k_tree_mma(const TreeArgs a, const __grid_constant__ TreeMaps maps)
     const Run line = tree_run<P::ROWS, P::TOKENS, P::THREADS>(a, cur, sm.scan());  // the job's 0 is written before: it contains a barrier
     const int n = static_cast<int>(min(line.n, static_cast<long long>(INT_MAX / 4)));
     if (n > 0) {
-        if (warp == ISSUE) {
-            if (!tree_products<P>(a, sm, tmem, n, stop) && lane == 0) {
+        if (warp >= BOXES) {
+            if (a.boxes) {
+                TreeBoxes<P> boxes(a, sm, maps, stop);
+                boxes.run(cur, line, n);
+            }
+            __syncwarp();
+        } else if (warp >= ISSUE) {
+            const bool good = warp == ISSUE ? tree_scores<P>(a, sm, tmem, n, stop) : tree_values<P>(a, sm, tmem, n, stop);
+            if (!good && lane == 0) {
                 // Stopped: the products under way end before shared and tensor memory are given back.
-                tcgen05_commit(sm.last());
+                const uint32_t bar = sm.last(warp - ISSUE);
+                tcgen05_commit(bar);
                 unsigned long long t0, t;
                 asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t0));
                 do
                     asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
-                while (!bar_test(sm.last(), 0) && t - t0 < kTreeWaitLimitNs);
-            }
-            __syncwarp();
-        } else if (warp > ISSUE) {
-            if (a.boxes) {
-                TreeBoxes<P> boxes(a, sm, maps, stop);
-                boxes.run(cur, line, n);
+                while (!bar_test(bar, 0) && t - t0 < kTreeWaitLimitNs);
             }
             __syncwarp();
         } else if (warp >= COPY) {

@@ -27,17 +27,42 @@ def run(NM, GROUPS, NS, QS, RS, TILES, items, seed, scaled=False, boxes=False):
     tiles = [(i == 0, i == n - 1, mixed and i >= n - 2) for n, mixed in items for i in range(n)]
     n, warps, small = len(tiles), 4 * GROUPS, RS > 0
     split = GROUPS == 2 and NM == 1
-    kv_full, kv_empty = [Bar(4 if boxes else 1) for _ in range(NS)], [Bar(1) for _ in range(NS)]
-    q_full, q_empty = [Bar(4) for _ in range(QS)], [Bar(1 + (warps if scaled else 0)) for _ in range(QS)]
-    s_full, p_ready, o_done = [Bar(1), Bar(1)], [Bar(4), Bar(4)], [Bar(1) for _ in range(GROUPS)]
-    tile_full, tile_empty = [Bar(1) for _ in range(TILES)], [Bar(warps + (4 if boxes else 0)) for _ in range(TILES)]
-    arrived, sent, raw_empty = [Bar(1) for _ in range(8)], [0, 0, 1, 1], [Bar(4) for _ in range(RS)]
+    # fill f: keys of tile f / 2, or its values where f is odd; each has a ring of its own
+    KS, VS = NS // 2, NS - NS // 2
+
+    def slot(f):
+        return KS + (f >> 1) % VS if f & 1 else (f >> 1) % KS
+
+    def turn(f):
+        return (f >> 1) // (VS if f & 1 else KS)
+
+    def before(f):
+        return f - 2 * (VS if f & 1 else KS)
+
+    hands = 2 if small else 4        # warps that finish a fill
+    kv_full, kv_empty = [Bar(hands if boxes else 1) for _ in range(NS)], [Bar(1) for _ in range(NS)]
+    q_full, q_empty = [Bar(4) for _ in range(QS)], [Bar(1) for _ in range(QS)]
+    H = 2 if NM == 2 else 1        # halves of a tile, a step each
+    B = 2 * H   # score buffers; scores are begun B / 2 steps before the weighted values
+    s_full, p_ready, o_done = [Bar(1) for _ in range(B)], [Bar(4) for _ in range(B)], [Bar(1) for _ in range(GROUPS)]
+    p_used = [Bar(1) for _ in range(B)]
+    tile_full, tile_empty = [Bar(1) for _ in range(TILES)], [Bar(warps + 1 + (4 if boxes else 0)) for _ in range(TILES)]
+    arrived, sent, raw_empty = [Bar(1) for _ in range(8)], [0, 0, 1, 1], [Bar(2) for _ in range(RS)]
     given = {}
     told, taken = Bar(4), Bar(4)
-    queue, copies = [], []    # products in order, with the barriers they complete; copies on their way
+    queues, copies = [[], []], []    # products of each warp in order, with the barriers they complete; copies on their way
+    holds = [None] * 4               # the step whose weights lie in a buffer
     content = [None] * NS     # the fill that lies in a slot: what the products must find
     used = set()
     state = {"o": [None, None]}   # who may touch a group's O: None, or "read" while the first group reads the second's
+
+    POWERS = 4 if NM == 2 else 6   # items whose queries' powers of two are kept
+    powers = [[None] * POWERS for _ in range(4)]
+
+    def fill(w, item):
+        """A warp's part of an item's queries: the powers of two at once."""
+        powers[w][item % POWERS] = item
+        copies.append(q_full[item % QS].arrive)
 
     def wait(bar, phase, what):
         """Of the phase with this number, by its parity, as the kernel does."""
@@ -57,14 +82,14 @@ def run(NM, GROUPS, NS, QS, RS, TILES, items, seed, scaled=False, boxes=False):
         arrival = (lambda t: (2 * t + values) % RS) if small else (lambda t: (t & 1) * 4 + (t >> 1 & 3))
 
         def give(f):
-            content[f % NS] = f
-            kv_full[f % NS].arrive()
+            content[slot(f)] = f
+            kv_full[slot(f)].arrive()
 
         def free(f):
-            before = f - NS
-            if NS % 4 and before >= 0 and not sent[(before & 1) + (before >> 1 & 1) * 2] > before >> 1:
+            x = before(f)
+            if x >= 0 and not sent[(x & 1) + (x >> 1 & 1) * 2] > x >> 1:
                 return False
-            return ready(kv_empty[f % NS], f // NS - 1)
+            return ready(kv_empty[slot(f)], turn(f) - 1)
 
         while True:
             moved = False
@@ -82,7 +107,7 @@ def run(NM, GROUPS, NS, QS, RS, TILES, items, seed, scaled=False, boxes=False):
                     give(2 * done + 1)
                     done, moved = done + 2, True
             if filled < len(begins) and ready(q_empty[filled % QS], filled // QS - 1):
-                copies.append(q_full[filled % QS].arrive)
+                fill(w, filled)
                 filled, moved = filled + 1, True
             if tile < n:
                 f = 2 * tile + values
@@ -90,8 +115,8 @@ def run(NM, GROUPS, NS, QS, RS, TILES, items, seed, scaled=False, boxes=False):
                 if room and (values or ready(tile_empty[tile % TILES], tile // TILES - 1)):
                     if not values:
                         tile_full[tile % TILES].arrive()
-                    hands = small or (values and tiles[tile][2])
-                    copies.append(arrived[arrival(tile)].arrive if hands else lambda f=f: give(f))
+                    needs = small or (values and tiles[tile][2])
+                    copies.append(arrived[arrival(tile)].arrive if needs else lambda f=f: give(f))
                     tile, moved = tile + 2, True
                     if not small:
                         sent[w] = tile
@@ -99,23 +124,24 @@ def run(NM, GROUPS, NS, QS, RS, TILES, items, seed, scaled=False, boxes=False):
                 return
             yield None
 
-    def ask():
-        """The warp of tensor copies."""
+    def ask(values):
+        """The warps of tensor copies, of keys and of values."""
         def land(f):
-            content[f % NS] = f
-            for _ in range(4):
-                kv_full[f % NS].arrive()
+            content[slot(f)] = f
+            for _ in range(hands):
+                kv_full[slot(f)].arrive()
 
         for t in range(n):
-            yield wait(tile_empty[t % TILES], t // TILES - 1, f"room for tile {t}")
-            tile_full[t % TILES].arrive()
-            for f in (2 * t, 2 * t + 1):
-                if small:
-                    yield wait(raw_empty[f % RS], f // RS - 1, f"stage of fill {f}")
-                    copies.append(arrived[f % RS].arrive)
-                else:
-                    yield wait(kv_empty[f % NS], f // NS - 1, f"slot of fill {f}")
-                    copies.append(arrived[t % 8].arrive if f & 1 and tiles[t][2] else lambda f=f: land(f))
+            if not values:
+                yield wait(tile_empty[t % TILES], t // TILES - 1, f"room for tile {t}")
+                tile_full[t % TILES].arrive()
+            f = 2 * t + values
+            if small:
+                yield wait(raw_empty[f % RS], f // RS - 1, f"stage of fill {f}")
+                copies.append(arrived[f % RS].arrive)
+            else:
+                yield wait(kv_empty[slot(f)], turn(f) - 1, f"slot of fill {f}")
+                copies.append(arrived[t % 8].arrive if f & 1 and tiles[t][2] else lambda f=f: land(f))
 
     def help_out(w):
         begins, filled, uses = [t for t in range(n) if tiles[t][0]], 0, [0] * 8
@@ -125,24 +151,24 @@ def run(NM, GROUPS, NS, QS, RS, TILES, items, seed, scaled=False, boxes=False):
             nonlocal filled
             while not ready(bar, phase):
                 if filled < len(begins) and ready(q_empty[filled % QS], filled // QS - 1):
-                    copies.append(q_full[filled % QS].arrive)
+                    fill(w, filled)
                     filled += 1
                 yield None
 
         def give(f):
             given[f] = given.get(f, 0) + 1
-            if given[f] == 4:
-                content[f % NS] = f
-            kv_full[f % NS].arrive()
+            if given[f] == hands:
+                content[slot(f)] = f
+            kv_full[slot(f)].arrive()
 
         for t in range(n):
             yield from until(tile_full[t % TILES], t // TILES)
             if small:
-                for f in (2 * t, 2 * t + 1):
-                    yield from until(arrived[f % RS], f // RS)
-                    yield from until(kv_empty[f % NS], f // NS - 1)
-                    give(f)
-                    raw_empty[f % RS].arrive()
+                f = 2 * t + (w >> 1)
+                yield from until(arrived[f % RS], f // RS)
+                yield from until(kv_empty[slot(f)], turn(f) - 1)
+                give(f)
+                raw_empty[f % RS].arrive()
             elif tiles[t][2]:
                 yield from until(arrived[t % 8], uses[t % 8])
                 uses[t % 8] += 1
@@ -150,66 +176,67 @@ def run(NM, GROUPS, NS, QS, RS, TILES, items, seed, scaled=False, boxes=False):
             tile_empty[t % TILES].arrive()
         while filled < len(begins):
             if ready(q_empty[filled % QS], filled // QS - 1):
-                copies.append(q_full[filled % QS].arrive)
+                fill(w, filled)
                 filled += 1
             yield None
 
-    def issue():
-        begun = 0
-        tile_of = (lambda u: u // 2) if NM == 2 else (lambda u: u)
-        group_of, phase_of = ((lambda u: u & 1), (lambda u: u >> 1)) if GROUPS == 2 else ((lambda u: 0), (lambda u: u))
+    S = NM * H   # steps of a tile
+    group_of, phase_of = ((lambda u: u & 1), (lambda u: u >> 1)) if GROUPS == 2 else ((lambda u: 0), (lambda u: u))
 
-        def scores(u):
-            nonlocal begun
-            t, m = tile_of(u), u % NM
-            if m == 0:
+    def scores():
+        begun = 0
+        for u in range(n * S):
+            t = u // S
+            if u % S == 0:
                 yield wait(tile_full[t % TILES], t // TILES, f"tile {t}")
                 if tiles[t][0]:
                     yield wait(q_full[begun % QS], begun // QS, f"queries of tile {t}")
                     begun += 1
-                yield wait(kv_full[2 * t % NS], 2 * t // NS, f"keys of tile {t}")
+                yield wait(kv_full[slot(2 * t)], turn(2 * t), f"keys of tile {t}")
+            yield wait(p_used[u % B], u // B - 1, f"product {u - B}")
+            assert holds[u % B] is None, "scores are written over weights that are still to be used"
             last = tiles[t][1] or t == n - 1
-            queue.append((2 * t, None, [s_full[u & 1]] +
-                          ([kv_empty[2 * t % NS]] + ([q_empty[(begun - 1) % QS]] if last else []) if m == NM - 1 else [])))
+            queues[0].append((2 * t, None, [s_full[u % B]] +
+                              ([kv_empty[slot(2 * t)]] + ([q_empty[(begun - 1) % QS]] if last else []) if u % S == S - 1 else [])))
 
-        yield from scores(0)
-        for u in range(n * NM):
-            f = 2 * tile_of(u) + 1
-            if u + 1 < n * NM:
-                if u > 0:
-                    yield wait(o_done[group_of(u - 1)], phase_of(u - 1), f"product {u - 1}")
-                yield from scores(u + 1)
-            yield wait(p_ready[u & 1], u >> 1, f"weights {u}")
-            if u % NM == 0:
-                yield wait(kv_full[f % NS], f // NS, f"values of step {u}")
-            queue.append((f, group_of(u), [o_done[group_of(u)]] + ([kv_empty[f % NS]] if u % NM == NM - 1 else [])))
+    def values():
+        for u in range(n * S):
+            t = u // S
+            f = 2 * t + 1
+            if u % S == 0:
+                yield wait(tile_full[t % TILES], t // TILES, f"tile {t}")
+                tile_empty[t % TILES].arrive()
+                yield wait(kv_full[slot(f)], turn(f), f"values of step {u}")
+            yield wait(p_ready[u % B], u // B, f"weights {u}")
+            queues[1].append((f, u, [p_used[u % B], o_done[group_of(u)]] + ([kv_empty[slot(f)]] if u % S == S - 1 else [])))
 
     def softmax(w):
         m, begun, joins, awaits, own = w // 4, 0, 0, False, -1
-        phase_of = (lambda u: u >> 1) if GROUPS == 2 else (lambda u: u)
         for t in range(n):
             yield wait(tile_full[t % TILES], t // TILES, f"tile {t}")
-            u = 2 * t + m if NM == 2 else t
             if tiles[t][0]:
                 own = -1
-                if scaled:
-                    yield wait(q_full[begun % QS], begun // QS, f"factors of tile {t}")
-                    q_empty[begun % QS].arrive()
                 begun += 1
-            if not split or t & 1 == m:
-                yield wait(s_full[u & 1], u >> 1, f"scores {u}")
+            for half in range(H if not split or t & 1 == m else 0):
+                u = 4 * t + 2 * half + m if NM == 2 else t
+                yield wait(s_full[u % B], u // B, f"scores {u}")
+                if scaled and own < 0:
+                    assert powers[w % 4][(begun - 1) % POWERS] == begun - 1, "a row's power of two was written over"
                 if own >= 0 and r.random() < 0.5:   # the reference moves
                     yield wait(o_done[m], phase_of(u) - 1, f"product before step {u}")
                 if tiles[t][2]:
-                    yield wait(kv_full[(2 * t + 1) % NS], (2 * t + 1) // NS, f"values of tile {t}")
-                if phase_of(u) > 0:
+                    yield wait(kv_full[slot(2 * t + 1)], turn(2 * t + 1), f"values of tile {t}")
+                bad = tiles[t][2] and r.random() < 0.5
+                if (bad or tiles[t][1] or t == n - 1) and phase_of(u) > 0:
                     yield wait(o_done[m], phase_of(u) - 1, f"product before step {u}")
                 if split and awaits:
                     yield wait(taken, joins - 1, f"the join before step {u}")
                     awaits = False
-                p_ready[u & 1].arrive()
+                if w % 4 == 0:
+                    holds[u % B] = u
+                p_ready[u % B].arrive()
                 own = u
-                if tiles[t][2] and r.random() < 0.5:
+                if bad:
                     yield wait(o_done[m], phase_of(u), f"product of step {u}")
             if tiles[t][1] or t == n - 1:
                 if own >= 0:
@@ -230,8 +257,8 @@ def run(NM, GROUPS, NS, QS, RS, TILES, items, seed, scaled=False, boxes=False):
 
     running = {f"copy {w}": help_out(w) if boxes else copy(w) for w in range(4)}
     if boxes:
-        running["ask"] = ask()
-    running["issue"] = issue()
+        running.update({"copy keys": ask(0), "copy values": ask(1)})
+    running.update({"scores": scores(), "values": values()})
     running.update({f"softmax {w}": softmax(w) for w in range(warps)})
     waits, idle = dict.fromkeys(running), 0
     while running:
@@ -239,15 +266,18 @@ def run(NM, GROUPS, NS, QS, RS, TILES, items, seed, scaled=False, boxes=False):
         for k in can:
             if waits[k] is not None:   # not before its phase, and not after the next one with its parity
                 assert waits[k][0].phase == waits[k][2] + 1, (k, waits[k][3])
-        choice = can + (["tensor core"] if queue else []) + (["memory"] * 2 if copies else [])
-        idle = idle + 1 if all(k.startswith("copy") for k in choice) else 0
+        choice = can + [q for q in (0, 1) if queues[q]] + (["memory"] * 2 if copies else [])
+        idle = idle + 1 if all(isinstance(k, str) and k.startswith("copy") for k in choice) else 0
         if not choice or idle > 20000:   # copying warps never wait: they look for something to do
             return {k: waits[k] and waits[k][3] for k in running}
         k = r.choice(choice)
-        if k == "tensor core":
-            f, o, bars = queue.pop(0)
-            assert content[f % NS] == f, "a product reads another fill than its own"
-            assert o is None or not state["o"][o], "an O is written that is still read"
+        if k in (0, 1):   # the tensor core: each warp's products in order, the two in any
+            f, u, bars = queues[k].pop(0)
+            assert content[slot(f)] == f, "a product reads another fill than its own"
+            if u is not None:
+                assert not state["o"][group_of(u)], "an O is written that is still read"
+                assert holds[u % B] == u, "a product reads another step's weights"
+                holds[u % B] = None
             used.add(f)
             for b in bars:
                 b.arrive()
@@ -264,11 +294,11 @@ def run(NM, GROUPS, NS, QS, RS, TILES, items, seed, scaled=False, boxes=False):
 
 
 # NM, GROUPS, NS, QS, RS, TILES, scaled as TreeMmaShape has them
-SHAPES = {"16 bit, 64, 128 rows": (1, 2, 8, 2, 0, 8), "16 bit, 64, 256 rows": (2, 2, 8, 1, 0, 8), "16 bit, 128, 128 rows": (1, 2, 5, 2, 0, 8),
+SHAPES = {"16 bit, 64, 128 rows": (1, 2, 10, 2, 0, 8), "16 bit, 64, 256 rows": (2, 2, 10, 1, 0, 8), "16 bit, 128, 128 rows": (1, 2, 5, 2, 0, 8),
           "16 bit, 128, 256 rows": (2, 2, 5, 1, 0, 8), "16 bit, 192": (1, 1, 7, 1, 0, 8), "16 bit, 256": (1, 1, 5, 1, 0, 8),
-          "8 bit, 64, 128 rows": (1, 2, 8, 2, 8, 4, True), "8 bit, 64, 256 rows": (2, 2, 8, 1, 8, 4, True),
-          "8 bit, 128, 128 rows": (1, 2, 3, 2, 4, 4, True), "8 bit, 128, 256 rows": (2, 2, 3, 1, 4, 4, True),
-          "8 bit, 192": (1, 1, 5, 1, 4, 4, True), "8 bit, 256": (1, 1, 3, 1, 4, 4, True), "8 bit, 256, fp16 queries": (1, 1, 3, 1, 4, 8)}
+          "8 bit, 64, 128 rows": (1, 2, 8, 2, 8, 6, True), "8 bit, 64, 256 rows": (2, 2, 8, 1, 8, 6, True),
+          "8 bit, 128, 128 rows": (1, 2, 4, 1, 4, 6, True), "8 bit, 128, 256 rows": (2, 2, 3, 1, 4, 6, True),
+          "8 bit, 192": (1, 1, 5, 1, 4, 6, True), "8 bit, 256": (1, 1, 3, 1, 4, 6, True), "8 bit, 256, fp16 queries": (1, 1, 3, 1, 4, 8)}
 
 
 @pytest.mark.parametrize("boxes", [False, True])
