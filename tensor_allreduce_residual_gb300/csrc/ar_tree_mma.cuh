@@ -123,8 +123,8 @@ struct TreeMmaShape {
     static_assert(NM <= GROUPS, "a warpgroup for each half of the rows");
     static constexpr int SOFTMAX = 128 * GROUPS, THREADS = SOFTMAX + 128 + 128;
     static constexpr int Q = ROWS * DIM * 2, SLOT = TOKENS * DIM * 2, RAW = SMALL ? TOKENS * DIM : 0;
-    static constexpr int MISC = 3072, ROOM = 232448 - MISC;     // a block's 227 KB
-    static constexpr int QS = NM == 1 && DIM <= 128 && !(SMALL && DIM == 128) ? 2 : 1;  // 8-bit: a fourth slot of keys or values instead
+    static constexpr int MISC = 3 * 1024, ROOM = 232448 - MISC;     // a block's 227 KB
+    static constexpr int QS = NM == 1 && DIM == 64 ? 2 : 1;  // heads of 128: another slot of keys or values instead
     static constexpr int RS = !SMALL ? 0 : DIM == 64 ? 8 : 4;
     static constexpr int FIT = (ROOM - QS * Q - RS * RAW) / SLOT, NS = FIT < 10 ? FIT : 10;
     // A step's tokens and the score buffers.  With 256 rows a half of a tile, so that a group has two buffers and its next scores

@@ -294,7 +294,7 @@ def run(NM, GROUPS, NS, QS, RS, TILES, items, seed, scaled=False, boxes=False):
 
 
 # NM, GROUPS, NS, QS, RS, TILES, scaled as TreeMmaShape has them
-SHAPES = {"16 bit, 64, 128 rows": (1, 2, 10, 2, 0, 8), "16 bit, 64, 256 rows": (2, 2, 10, 1, 0, 8), "16 bit, 128, 128 rows": (1, 2, 5, 2, 0, 8),
+SHAPES = {"16 bit, 64, 128 rows": (1, 2, 10, 2, 0, 8), "16 bit, 64, 256 rows": (2, 2, 10, 1, 0, 8), "16 bit, 128, 128 rows": (1, 2, 6, 1, 0, 8),
           "16 bit, 128, 256 rows": (2, 2, 5, 1, 0, 8), "16 bit, 192": (1, 1, 7, 1, 0, 8), "16 bit, 256": (1, 1, 5, 1, 0, 8),
           "8 bit, 64, 128 rows": (1, 2, 8, 2, 8, 6, True), "8 bit, 64, 256 rows": (2, 2, 8, 1, 8, 6, True),
           "8 bit, 128, 128 rows": (1, 2, 4, 1, 4, 6, True), "8 bit, 128, 256 rows": (2, 2, 3, 1, 4, 6, True),
