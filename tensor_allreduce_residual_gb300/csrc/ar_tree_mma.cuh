@@ -3,20 +3,32 @@
 //
 // A block's tile is 128 rows (drafted tokens times query heads of one
 // key-value head; or two such halves) by TOKENS cached tokens.  Scores
-// S = Q K^T go from shared memory into tensor memory; a warpgroup for each
-// half of the rows, a thread a row, turns them into weights P, which lie in
-// tensor memory where the scores lay; O += P V, with O in tensor memory until
-// the item's end.  Weights are two 16-bit numbers, their rounding and what it
-// leaves, so P V takes two products.
+// S = Q K^T go from shared memory into tensor memory; a thread a row turns
+// them into weights P, which lie in tensor memory where the scores lay;
+// O += P V, with O in tensor memory until the item's end.  Weights are two
+// 16-bit numbers, their rounding and what it leaves, so P V takes two products.
 //
-//   softmax warps (8; 4 for heads over 128), a thread a row (warp w reads lanes 32 (w % 4) ..)
-//   4 copying warps: queries, and rings of keys and values
-//   1 warp that allocates tensor memory; one of its lanes issues products
+//   8 softmax warps (4 for heads over 128), a thread a row
+//   4 helping warps: queries, what tensor copies cannot bring, 8-bit to fp16;
+//     where pages do not fit boxes, keys and values as well (TreeFeed)
+//   2 warps that issue products: scores, weighted values
+//   2 warps that ask for tensor copies: keys, values (TreeBoxes)
 //
 // A softmax step takes a warpgroup longer than a tile of bf16 takes from HBM,
 // so heads of up to 128 have two warpgroups, with a score buffer and an O
 // each: with 256 rows (NM == 2) they have a half of the rows each, with up to
 // 128 (NM == 1) alternate tiles, whose two O's are joined at the item's end.
+// Blocks take equal runs of tiles over all items; an item that several blocks
+// have is joined by k_tree_join.
+//
+// What bounds it: 64 sequences of 8192 cached tokens (537 MB of bf16, 64 rows)
+// take 125 us with the join.  A block takes a tile in 1.45 us there, which is
+// 6.8 TB/s, HBM's rate, for 78 us; the rest is the start (3 us, the first
+// tile's way through tensor memory 4 to 9 us), the last tile's softmax and
+// O (5 us), and the join (10 us).  With 256 rows a group's way round, scores,
+// softmax (3500 cycles), weighted values, is longer than a tile's copy: 4 us a
+// tile.  8-bit caches wait for the warps that turn them into fp16.
+//
 // All hand-overs are mbarriers.  Waits are bounded: one that gave up is
 // counted, raises the block's stop flag, on which all others give up too, and
 // the block leaves.
@@ -127,10 +139,10 @@ struct TreeMmaShape {
     static constexpr int QS = NM == 1 && DIM == 64 ? 2 : 1;  // heads of 128: another slot of keys or values instead
     static constexpr int RS = !SMALL ? 0 : DIM == 64 ? 8 : 4;
     static constexpr int FIT = (ROOM - QS * Q - RS * RAW) / SLOT, NS = FIT < 10 ? FIT : 10;
-    // A step's tokens and the score buffers.  With 256 rows a half of a tile, so that a group has two buffers and its next scores
-    // run while it works on these.  (Tiles of half the size instead cost twice the hand-overs, with up to 128 rows too: 374
-    // against 251 us on 286 MB of e4m3.)
-    static constexpr int HALVES = NM == 2 ? 2 : 1, STEP_TOKENS = TOKENS / HALVES, BUFFERS = 2 * HALVES;
+    // Score buffers, one a group (or two for its one group): beside two O's tensor memory has no room for more.  Two a group, of
+    // half a tile each, gain less than the steps' number costs: 275 against 268 us with 256 rows (539 MB of bf16), 144 against
+    // 125 us with up to 128 (537 MB).  Tiles of half the size: 374 against 251 us (286 MB of e4m3).
+    static constexpr int BUFFERS = 2;
     static_assert(NS >= 3, "a tile's keys and values, and the next one's keys");
     // Fill f is the keys of tile f / 2, or its values where f is odd.  Keys and values have rings of their own, so that the warps
     // that bring one never wait for those that bring the other.
@@ -150,15 +162,13 @@ struct TreeMmaShape {
     // Weights may pass their reference's by 2^AHEAD before it is moved, which costs a pass over O.  fp16 weights are 2^LIFT
     // times as large, so that small ones keep their bits: the largest is 2^15.
     static constexpr float AHEAD = BF16 ? 8.0f : 4.0f, LIFT = BF16 ? 0.0f : 11.0f;
-    static constexpr int S_COLUMNS = STEP_TOKENS, O_COLUMN = 256;  // score buffers from column 0 on; O of group m at 256 + 128 m
+    static constexpr int S_COLUMNS = TOKENS, O_COLUMN = 256;  // score buffers from column 0 on; O of group m at 256 + 128 m
     static_assert(BUFFERS * S_COLUMNS <= O_COLUMN && O_COLUMN + (DIM <= 128 ? GROUPS * 128 : 256) <= 512, "tensor memory");
     static constexpr int BARS = 2 * NS + 2 * QS + 3 * BUFFERS + GROUPS + 2 * TILES + 2 + 2 + ARRIVALS + RS;
-    // A step is a half of the rows of a half of a tile, or a tile.
-    static constexpr int TILE_STEPS = NM * HALVES;
-    static __device__ __forceinline__ int tile_of(int u) { return u / TILE_STEPS; }
-    static __device__ __forceinline__ int half_of(int u) { return HALVES == 2 ? u >> 1 & 1 : 0; }
-    static __device__ __forceinline__ bool first_of_tile(int u) { return u % TILE_STEPS == 0; }
-    static __device__ __forceinline__ bool last_of_tile(int u) { return u % TILE_STEPS == TILE_STEPS - 1; }
+    // Step u is half m of the rows of tile t, u = NM t + m.
+    static __device__ __forceinline__ int tile_of(int u) { return u / NM; }
+    static __device__ __forceinline__ bool first_of_tile(int u) { return u % NM == 0; }
+    static __device__ __forceinline__ bool last_of_tile(int u) { return u % NM == NM - 1; }
     static __device__ __forceinline__ int group_of(int u) { return GROUPS == 2 ? u & 1 : 0; }
     static __device__ __forceinline__ int phase_of(int u) { return GROUPS == 2 ? u >> 1 : u; }  // of the group's O
     static __device__ __forceinline__ int buffer_of(int u) { return u % BUFFERS; }
@@ -795,7 +805,7 @@ struct TreeBoxes {
                     x.bad = 0;
                     x.flags = (begins || t == 0 ? kTileFirst : 0) | (ends || t + 1 == n ? kTileLast : 0) | (begins ? kTileBegins : 0) | (ends ? kTileEnds : 0) |
                               (mixed ? kTreeMixed : 0);
-    #pragma unroll
+#pragma unroll
                     for (int k = 0; k < P::TOKENS / 32; ++k)
                         x.valid[k] = valid[k];
                     if (begins && n - t < cur.s.tiles)
@@ -857,10 +867,10 @@ template <typename P>
 __device__ bool tree_scores(const TreeArgs& a, const TreeSmem<P>& sm, uint32_t tmem, int n, volatile int* stop)
 {
     const int ksteps = (a.head_dim + 15) / 16;
-    const uint32_t desc = product_desc(P::BF16, P::STEP_TOKENS, false);
+    const uint32_t desc = product_desc(P::BF16, P::TOKENS, false);
     int items = 0;  // whose queries have been waited for
     bool last = false;
-    for (int u = 0; u < n * P::TILE_STEPS; ++u) {
+    for (int u = 0; u < n * P::NM; ++u) {
         const int t = P::tile_of(u), s = P::slot(2 * t);
         if (P::first_of_tile(u)) {
             if (!bar_wait(sm.tile_full(t % P::TILES), t / P::TILES & 1, stop))
@@ -881,7 +891,7 @@ __device__ bool tree_scores(const TreeArgs& a, const TreeSmem<P>& sm, uint32_t t
             return false;
         tcgen05_after_sync();
         const uint64_t q = operand_desc(sm.q((items - 1) % P::QS) + u % P::NM * (128 * P::DIM * 2), 16, 1024),
-                       k = operand_desc(sm.kv(s) + P::half_of(u) * (P::STEP_TOKENS * 128), 16, 1024);
+                       k = operand_desc(sm.kv(s), 16, 1024);
         const uint32_t d = tmem + P::buffer_of(u) * P::S_COLUMNS;
         const bool one = elected();
         // 32 bytes on, then the next 64 elements' block; addresses count 16 bytes
@@ -907,7 +917,7 @@ __device__ bool tree_values(const TreeArgs& a, const TreeSmem<P>& sm, uint32_t t
 {
     const uint32_t desc = product_desc(P::BF16, (a.head_dim + 15) / 16 * 16, true);
     bool first = false, second = false;  // whether the tile is the first of the block's part of an item, or the one after it
-    for (int u = 0; u < n * P::TILE_STEPS; ++u) {
+    for (int u = 0; u < n * P::NM; ++u) {
         const int t = P::tile_of(u), f = 2 * t + 1, s = P::slot(f);
         if (P::first_of_tile(u)) {
             if (!bar_wait(sm.tile_full(t % P::TILES), t / P::TILES & 1, stop))
@@ -921,21 +931,21 @@ __device__ bool tree_values(const TreeArgs& a, const TreeSmem<P>& sm, uint32_t t
             fence_async_proxy();
         }
         // Of the group's O: with alternate tiles, two of an item are first ones.
-        const bool begins = (first && P::half_of(u) == 0) || (P::SPLIT && second);
+        const bool begins = first || (P::SPLIT && second);
         if (!bar_wait(sm.p_ready(P::buffer_of(u)), u / P::BUFFERS & 1, stop))
             return false;
         tcgen05_after_sync();
         const uint32_t p = tmem + P::buffer_of(u) * P::S_COLUMNS, o = tmem + P::O_COLUMN + P::group_of(u) * 128;
-        const uint64_t v = operand_desc(sm.kv(s) + P::half_of(u) * (P::STEP_TOKENS * 128), P::TOKENS * 128, 1024);
+        const uint64_t v = operand_desc(sm.kv(s), P::TOKENS * 128, 1024);
         const bool one = elected();
 #pragma unroll
-        for (int j = 0; j < P::STEP_TOKENS / 16; ++j) {
+        for (int j = 0; j < P::TOKENS / 16; ++j) {
             const uint32_t w = p + (j >> 1) * 32 + (j & 1) * 8;  // of 32 tokens 16 columns of weights, then 16 of what they leave
             mma_tensor(o, w, v + j * (2048 / 16), desc, !(begins && j == 0), one);
             mma_tensor(o, w + 16, v + j * (2048 / 16), desc, true, one);
         }
+        tcgen05_commit(sm.o_done(P::group_of(u)), one);  // first: who sees the weights used takes this for done
         tcgen05_commit(sm.p_used(P::buffer_of(u)), one);
-        tcgen05_commit(sm.o_done(P::group_of(u)), one);
         if (P::last_of_tile(u))
             tcgen05_commit(sm.kv_empty(s), one);
         __syncwarp();
@@ -981,12 +991,11 @@ struct TreeSoft {
     template <bool PART, bool CAP>
     __device__ __forceinline__ bool weights(const TreeTile& tile, uint32_t s, bool first, int u)
     {
-        constexpr int CHUNKS = P::STEP_TOKENS / 32;
-        const int c0 = P::half_of(u) * CHUNKS;  // the step's first 32 tokens
+        constexpr int CHUNKS = P::TOKENS / 32;
         float most = -INFINITY;
 #pragma unroll 1
         for (int c = 0; c < CHUNKS; ++c) {
-            const uint32_t word = PART ? seen(tile, c0 + c) : ~0u;
+            const uint32_t word = PART ? seen(tile, c) : ~0u;
             uint32_t x[32];
             tmem_load32(s + 32 * c, x);
             tcgen05_wait_load();
@@ -1025,7 +1034,7 @@ struct TreeSoft {
         float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll 1
         for (int c = 0; c < CHUNKS; ++c) {
-            const uint32_t word = PART ? seen(tile, c0 + c) : ~0u;
+            const uint32_t word = PART ? seen(tile, c) : ~0u;
             uint32_t x[32], w[32];
             tmem_load32(s + 32 * c, x);
             tcgen05_wait_load();
@@ -1077,7 +1086,7 @@ struct TreeSoft {
             for (int i = 0; i < 32; ++i)
                 add[i] = 0.0f;
 #pragma unroll 1
-            for (int c = P::half_of(u) * (P::STEP_TOKENS / 32); c < (P::half_of(u) + 1) * (P::STEP_TOKENS / 32) && valid; ++c) {
+            for (int c = 0; c < P::TOKENS / 32 && valid; ++c) {
 #pragma unroll 1
                 for (uint32_t word = tile.valid[c] & sees.sees(tile.token0 + 32 * c); word != 0; word &= word - 1) {
                     const int token = tile.token0 + 32 * c + __ffs(word) - 1;
@@ -1232,9 +1241,8 @@ struct TreeSoft {
                 factor = a.scale2;
                 ++items;
             }
-#pragma unroll 1
-            for (int half = 0; half < P::HALVES && (!P::SPLIT || (t & 1) == m); ++half) {
-                const int u = P::NM == 2 ? 4 * t + 2 * half + m : t;
+            if (!P::SPLIT || (t & 1) == m) {
+                const int u = P::NM == 2 ? 2 * t + m : t;
                 if (!bar_wait(sm.s_full(P::buffer_of(u)), u / P::BUFFERS & 1, stop))
                     return false;
                 tcgen05_after_sync();

@@ -42,8 +42,7 @@ def run(NM, GROUPS, NS, QS, RS, TILES, items, seed, scaled=False, boxes=False):
     hands = 2 if small else 4        # warps that finish a fill
     kv_full, kv_empty = [Bar(hands if boxes else 1) for _ in range(NS)], [Bar(1) for _ in range(NS)]
     q_full, q_empty = [Bar(4) for _ in range(QS)], [Bar(1) for _ in range(QS)]
-    H = 2 if NM == 2 else 1        # halves of a tile, a step each
-    B = 2 * H   # score buffers; scores are begun B / 2 steps before the weighted values
+    B = 2   # score buffers
     s_full, p_ready, o_done = [Bar(1) for _ in range(B)], [Bar(4) for _ in range(B)], [Bar(1) for _ in range(GROUPS)]
     p_used = [Bar(1) for _ in range(B)]
     tile_full, tile_empty = [Bar(1) for _ in range(TILES)], [Bar(warps + 1 + (4 if boxes else 0)) for _ in range(TILES)]
@@ -180,7 +179,7 @@ def run(NM, GROUPS, NS, QS, RS, TILES, items, seed, scaled=False, boxes=False):
                 filled += 1
             yield None
 
-    S = NM * H   # steps of a tile
+    S = NM   # steps of a tile
     group_of, phase_of = ((lambda u: u & 1), (lambda u: u >> 1)) if GROUPS == 2 else ((lambda u: 0), (lambda u: u))
 
     def scores():
@@ -208,7 +207,7 @@ def run(NM, GROUPS, NS, QS, RS, TILES, items, seed, scaled=False, boxes=False):
                 tile_empty[t % TILES].arrive()
                 yield wait(kv_full[slot(f)], turn(f), f"values of step {u}")
             yield wait(p_ready[u % B], u // B, f"weights {u}")
-            queues[1].append((f, u, [p_used[u % B], o_done[group_of(u)]] + ([kv_empty[slot(f)]] if u % S == S - 1 else [])))
+            queues[1].append((f, u, [o_done[group_of(u)], p_used[u % B]] + ([kv_empty[slot(f)]] if u % S == S - 1 else [])))
 
     def softmax(w):
         m, begun, joins, awaits, own = w // 4, 0, 0, False, -1
@@ -217,8 +216,7 @@ def run(NM, GROUPS, NS, QS, RS, TILES, items, seed, scaled=False, boxes=False):
             if tiles[t][0]:
                 own = -1
                 begun += 1
-            for half in range(H if not split or t & 1 == m else 0):
-                u = 4 * t + 2 * half + m if NM == 2 else t
+            for u in [S * t + (m if NM == 2 else 0)] if not split or t & 1 == m else []:
                 yield wait(s_full[u % B], u // B, f"scores {u}")
                 if scaled and own < 0:
                     assert powers[w % 4][(begun - 1) % POWERS] == begun - 1, "a row's power of two was written over"
