@@ -354,7 +354,9 @@ int ar_query_launch(int R, int hidden, int tokens, int dtype, int strategy, ar_l
  * ar_device_status -- whether any kernel of this library on the current
  * device gave up a bounded wait since the last call.  The one-shot fused
  * kernel that streams rows through a shared-memory ring waits on barriers
- * that its own copies complete; each such wait is limited to one second,
+ * that its own copies complete, and ar_tree_attention's kernel for 16-bit and
+ * 8-bit caches on such that its own copies, products and warps complete; each
+ * such wait is limited to one second,
  * after which the kernel stops early (its outputs are then incomplete),
  * records the event and returns instead of hanging.  No pages' counterpart:
  * the pages' kernels wait on peer GPUs through block_barrier /

@@ -63,22 +63,24 @@ constexpr int kTreeMaxDim = 256;
 constexpr int kTreeMaxBlocks = 304;
 
 // Rows of an item (drafted tokens times the query heads of a key-value head) and cached tokens of a tile.
-enum { kTreeFma16, kTreeFma64, kTreeMma128, kTreeMma256 };
 struct TreeShape {
-    int kind, rows, tile;
+    int rows, tile;
 };
 
 // Elements that a head of the matrix kernel has, those of a shorter one followed by zeros.
 inline int tree_dim(int head_dim) { return head_dim <= 64 ? 64 : head_dim <= 128 ? 128 : head_dim <= 192 ? 192 : 256; }
 
-// The rule, on what the host knows.  `rows`: of all sequences and one key-value head.
+// The rule, on what the host knows.  `rows`: of all sequences and one key-value head.  An item's cached tokens are read once for
+// each block of its rows, so blocks hold the mean item where there is a kernel of that size: 64 sequences of 256 rows over
+// 539 MB of bf16 take 220 us with blocks of 256 and 254 with 128; of 32 to 256 rows 267 and 312.  Heads over 128 leave shared
+// and tensor memory for 128 rows only, and tiles of 64 tokens.
 inline TreeShape tree_shape(int cache_esize, int head_dim, uint64_t rows, int batch)
 {
     if (cache_esize == 4)
-        return rows <= 16ull * batch ? TreeShape{kTreeFma16, 16, 32} : TreeShape{kTreeFma64, 64, 32};
+        return rows <= 16ull * batch ? TreeShape{16, 32} : TreeShape{64, 32};
     if (head_dim > 128)
-        return TreeShape{kTreeMma128, 128, 64};
-    return rows <= 128ull * batch ? TreeShape{kTreeMma128, 128, 128} : TreeShape{kTreeMma256, 256, 128};
+        return TreeShape{128, 64};
+    return rows <= 128ull * batch ? TreeShape{128, 128} : TreeShape{256, 128};
 }
 
 // At most `most` blocks of the attention kernel, and no more than `sms` SMs hold at once; then the join kernel.
