@@ -587,16 +587,22 @@ struct TreeFeed {
         bool bad = false;
         constexpr int HALF = BLOCKS * CH / 2, ONCE = 4;  // steps of the warp, and at once
         static_assert(HALF % ONCE == 0, "whole groups of steps");
-        const int which = warp & 1;
+        const uint32_t which = warp & 1;
+        // Where the rows of a warp's step lie alike in the permutation, in every step, a lane's places are two and a stride.
+        constexpr bool ALIKE = 64 % (8 * CH) == 0;
+        const uint32_t row0 = (which * 32 + lane) / CH, c0 = (which * 32 + lane) % CH;
+        char* const place0 = to + place(row0, 2 * c0, P::TOKENS);
+        char* const place1 = to + place(row0, 2 * c0 + 1, P::TOKENS);
+        const char* const from = raw + (which * 32 + lane) * 16;
 #pragma unroll 1
-        for (int i0 = 0; i0 < HALF; i0 += ONCE) {
+        for (uint32_t i0 = 0; i0 < HALF; i0 += ONCE) {
             uint4 all[ONCE];
 #pragma unroll
             for (int i = 0; i < ONCE; ++i)
-                all[i] = *reinterpret_cast<const uint4*>(raw + (((i0 + i) * 2 + which) * 32 + lane) * 16);
+                all[i] = *reinterpret_cast<const uint4*>(from + (i0 + i) * 1024);
 #pragma unroll
             for (int i = 0; i < ONCE; ++i) {
-                const int at_chunk = ((i0 + i) * 2 + which) * 32 + lane, row = at_chunk / CH, c = at_chunk - row * CH;
+                const uint32_t at_chunk = ((i0 + i) * 2 + which) * 32 + lane, row = at_chunk / CH, c = at_chunk - row * CH;
                 const uint4 w = all[i];
                 uint32_t y[8] = {half2_of_e4m3(w.x), half2_of_e4m3(w.x >> 16), half2_of_e4m3(w.y), half2_of_e4m3(w.y >> 16),
                                  half2_of_e4m3(w.z), half2_of_e4m3(w.z >> 16), half2_of_e4m3(w.w), half2_of_e4m3(w.w >> 16)};
@@ -609,8 +615,10 @@ struct TreeFeed {
                         y[j] = there ? y[j] & ~z : 0u;
                     }
                 }
-                *reinterpret_cast<uint4*>(to + place(row, 2 * c, P::TOKENS)) = make_uint4(y[0], y[1], y[2], y[3]);
-                *reinterpret_cast<uint4*>(to + place(row, 2 * c + 1, P::TOKENS)) = make_uint4(y[4], y[5], y[6], y[7]);
+                char* const p0 = ALIKE ? place0 + (i0 + i) * (64 / CH * 128) : to + place(row, 2 * c, P::TOKENS);
+                char* const p1 = ALIKE ? place1 + (i0 + i) * (64 / CH * 128) : to + place(row, 2 * c + 1, P::TOKENS);
+                *reinterpret_cast<uint4*>(p0) = make_uint4(y[0], y[1], y[2], y[3]);
+                *reinterpret_cast<uint4*>(p1) = make_uint4(y[4], y[5], y[6], y[7]);
             }
         }
         if (bad)
