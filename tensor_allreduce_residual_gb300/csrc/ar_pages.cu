@@ -29,7 +29,7 @@ struct MoveUnit<1> { using type = uint8_t; };
 // keys or values: PER units a thread, all loads at once.  Whether the pair is
 // made it finds by one pass over all pairs, whose loads hide behind the other
 // blocks' copies.  Bound by HBM: 1.05 GB read and written take 145 us, 7.2 TB/s.
-// 16 pages of 4 KB in 8 layers are a launch, 4.5 us.
+// 8 pages of 4 KB in 16 layers are a launch, 4.5 us.
 // ---------------------------------------------------------------------------
 template <int BYTES, int PER>
 __global__ void __launch_bounds__(kMoveThreads)

@@ -1,5 +1,5 @@
 // ar_tree.h -- kernel arguments of the attention of drafted tokens over a paged
-// cache, and what its kernels share with their host side (ar_tree_api.cu).
+// cache, and what its kernels share with their host side (ar_cache_api.cu).
 #pragma once
 
 #include <cuda.h>  // types only: tensor maps are encoded by the driver's function, found at run time

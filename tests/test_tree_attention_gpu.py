@@ -320,3 +320,29 @@ def test_parts_of_ranks_join():
     part = half_step(a[0].double(), torch.float16) + half_step(b[0].double(), torch.float16)
     check(out, want[0], 4 * want[2] + part + half_step(want[0], torch.float16), "out")
     _compare(whole, whole_lse, want, "fp16")
+
+
+@pytest.mark.parametrize("dtype,cache,page", [("bf16", "bf16", 16), ("bf16", "bf16", 17), ("fp32", "fp32", 16), ("fp16", "e4m3", 16), ("fp16", "e4m3", 17)])
+def test_pages_gigabytes_apart(dtype, cache, page):
+    """Offsets in the cache that pass 32 bits: pages 1 GB apart, for the attention, compacting and copying."""
+    c = Cache([3 * page - 2, page + 1], 2, 64, page, cache, "NHD", 6, scales=(0.05, 0.02) if cache == "e4m3" else (1.0, 1.0))
+    q = _queries(4, 8, 64, dtype)
+    want = ar.ar_tree_attention(q, c.k, c.v, c.table, c.n, **c.kw)
+    pages = c.k.shape[0]
+    assert 5 <= pages <= 8
+    apart = (1 << 30) // c.k.element_size()
+    far = []
+    for x in (c.k, c.v):
+        y = torch.empty((pages - 1) * apart + x[0].numel(), dtype=x.dtype, device="cuda").as_strided(x.shape, (apart, *x.stride()[1:]))
+        y.view(torch.uint8)[:] = x.view(torch.uint8)
+        far.append(y)
+    assert torch.equal(ar.ar_tree_attention(q, *far, c.table, c.n, **c.kw), want)
+    kept = _ints([[1], [0]])
+    layout = c.kw["layout"]
+    news = ar.ar_kv_compact(c.k, c.v, c.table, c.n, kept, drafted=2, layout=layout)
+    assert torch.equal(ar.ar_kv_compact(*far, c.table, c.n, kept, drafted=2, layout=layout), news)
+    src, dst = _ints([int(c.table[0, 2])]), _ints([int(c.table[0, 0])])
+    ar.ar_kv_copy_pages(c.k, c.v, src, dst)
+    ar.ar_kv_copy_pages(*far, src, dst)
+    for x, y in zip((c.k, c.v), far):
+        assert torch.equal(x.view(torch.uint8), y.contiguous().view(torch.uint8))
