@@ -204,15 +204,19 @@ int token_dim(PyObject* layout)
     bad("layout must be 'NHD' ([pages, page_size, kv_heads, head_dim]) or 'HND' ([pages, kv_heads, page_size, head_dim])");
 }
 
-// The pages' tensors, checked, and their device.
+// The pages' tensors, checked, and their device.  tokens: the dimension that counts them; 0 where the call takes either for it:
+// then the longer one, as heads are 1024 at the most and a page's tokens any number.
 int fill_pages(ar_kv_cache* c, const Tensor& k, const Tensor& v, int tokens)
 {
-    const int heads = 3 - tokens, dev = cuda_index(k);
+    const int dev = cuda_index(k);
     if (dev < 0 || dev != c10::cuda::current_device())
         bad("k_pages must be a CUDA tensor of the current device");
     if (k.dim() != 4 || v.sizes() != k.sizes() || v.strides() != k.strides() || v.scalar_type() != k.scalar_type() ||
         cuda_index(v) != dev || (k.stride(3) != 1 && k.size(3) > 1))
         bad("k_pages and v_pages must be 4-d tensors of one shape, dtype, device and set of strides, with dense heads");
+    if (tokens == 0)
+        tokens = k.size(2) > k.size(1) ? 2 : 1;
+    const int heads = 3 - tokens;
     const at::ScalarType type = k.scalar_type();
     if (type != at::kFloat && type != at::kHalf && type != at::kBFloat16 && type != at::kFloat8_e4m3fn)
         bad(std::string("unsupported cache dtype ") + c10::toString(type) + "; expected float32, float16, bfloat16 or float8_e4m3fn");
@@ -489,7 +493,7 @@ PyObject* kv_compact(PyObject* const* a)
 PyObject* kv_copy_pages(PyObject* const* a)
 {
     ar_kv_cache cache{};
-    const LayerPages layers(&cache, a[0], a[1], 1);  // whole pages: which dimension counts tokens does not matter
+    const LayerPages layers(&cache, a[0], a[1], 0);  // whole pages: which dimension counts tokens does not matter
     const int dev = layers.dev;
     const Tensor& src = tensor(a[2], "src");
     const Tensor& dst = tensor(a[3], "dst");
