@@ -734,7 +734,9 @@ int ar_kv_append_axes(const ar_kv_cache* cache, const ar_append_params* p, int a
  *                table and the lengths, drafted tokens included; its k, v and
  *                scales are not read
  *   k, v         host arrays of `layers` (1 .. AR_MAX_LAYERS) device pointers:
- *                each layer's pages of keys and of values
+ *                each layer's pages of keys and of values.  Layers that share
+ *                a cache name the same one, whose tokens move once; otherwise
+ *                the layers share no element
  *   kept         device [batch, most_kept], rows kept_stride apart
  *   seq_start    device [batch + 1]: n = seq_start[b + 1] - seq_start[b], as
  *                ar_kv_append took the tokens; or NULL: n = drafted
@@ -765,7 +767,8 @@ int ar_kv_compact(const ar_kv_cache* cache, void* const* k, void* const* v, int 
  * pool that is put in order.
  *   cache   shape, dtype and strides that all layers share; its k, v, scales,
  *           page table and lengths are not read
- *   k, v    host arrays of `layers` (1 .. AR_MAX_LAYERS) device pointers
+ *   k, v    host arrays of `layers` (1 .. AR_MAX_LAYERS) device pointers, as
+ *           in ar_kv_compact
  *   src, dst  device [pairs]
  *   - A pair that names no page of [0, pages), or the same page twice, moves
  *     nothing and counts for nothing below.

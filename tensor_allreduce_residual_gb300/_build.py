@@ -43,7 +43,7 @@ SOURCES = ["ar_api.cu", "ar_kern_f32.cu", "ar_kern_f16.cu", "ar_kern_bf16.cu", "
            "ar_peer.cu", "ar_cache_api.cu", "ar_append.cu", "ar_pages.cu", "ar_attn_f32.cu", "ar_attn_f16.cu", "ar_attn_bf16.cu",
            "ar_tree_f32.cu", "ar_tree_f16.cu", "ar_tree_bf16.cu"]
 HEADERS = ["ar_internal.h", "ar_kernels.cuh", "ar_tma.cuh", "ar_lamport.cuh", "ar_launch.cuh", "ar_launch_k.cuh",
-           "ar_auto_table.h", "ar_cache.h", "ar_split.h", "ar_attn.cuh", "ar_tree.h", "ar_tree.cuh",
+           "ar_auto_table.h", "ar_cache.h", "ar_layers.h", "ar_split.h", "ar_attn.cuh", "ar_tree.h", "ar_tree.cuh",
            "ar_tcgen05.cuh", "ar_tree_mma.cuh"]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

@@ -8,6 +8,7 @@
 #include <stdint.h>
 
 #include "ar_internal.h"
+#include "ar_layers.h"
 
 namespace ar {
 
@@ -56,13 +57,6 @@ constexpr int kAppendThreads = 256;
 template <typename T, typename CT, typename Args>
 cudaError_t launch_append(const Args& a, bool vec, cudaStream_t s);
 
-// The layers of one model whose caches have the same shape, dtype and strides.
-constexpr int kMaxLayers = 128;
-struct Layers {
-    char* k[kMaxLayers];
-    char* v[kMaxLayers];
-};
-
 // A page's (copying) or a token's (compacting) units of 1 to 16 bytes: `inner` units side by side, `mid` of these
 // mid_stride bytes apart, as often as needed outer_stride bytes apart.
 struct CopyArgs {
@@ -87,11 +81,11 @@ struct CompactArgs {
     uint64_t capacity;
     int drafted, most_kept, batch, pages, page_size, table_stride;
     uint32_t inner;           // units of one head of a token
-    uint32_t head_units;      // units of all heads of a token in one layer's keys
-    uint32_t units;           // of a token in all layers, keys and values
+    uint32_t head_units;      // units of all heads of a token in one buffer
+    uint32_t units;           // of a token in all buffers
 };
 // unit: 1, 2, 4, 8 or 16 bytes, that pointers and strides are multiples of.
-cudaError_t launch_copy_pages(const CopyArgs& a, int layers, int unit, cudaStream_t s);
+cudaError_t launch_copy_pages(const CopyArgs& a, int buffers, int unit, cudaStream_t s);
 cudaError_t launch_compact(const CompactArgs& a, int unit, cudaStream_t s);
 
 // Strides of the cache in bytes.

@@ -371,19 +371,18 @@ int unit_of(std::initializer_list<uint64_t> all)
     return unit;
 }
 
-bool fill_layers(ar::Layers* to, void* const* k, void* const* v, int layers, size_t esize, uint64_t* together)
+// Lists the layers' buffers, each once, and returns how many they are; 0 where one is missing or misaligned.
+int fill_layers(ar::Layers* to, void* const* k, void* const* v, int layers, size_t esize, uint64_t* together)
 {
     *together = 0;
     if (k == nullptr || v == nullptr)
-        return false;
+        return 0;
     for (int i = 0; i < layers; ++i) {
         if (!element_ok(k[i], esize) || !element_ok(v[i], esize))
-            return false;
-        to->k[i] = static_cast<char*>(k[i]);
-        to->v[i] = static_cast<char*>(v[i]);
+            return 0;
         *together |= reinterpret_cast<uintptr_t>(k[i]) | reinterpret_cast<uintptr_t>(v[i]);
     }
-    return true;
+    return ar::distinct_buffers(to, k, v, layers);
 }
 
 // Whether [a, a + n) and [b, b + m) share an element; either may be NULL.
@@ -425,7 +424,8 @@ int ar_kv_compact(const ar_kv_cache* cache, void* const* k, void* const* v, int 
     const uint64_t e = static_cast<uint64_t>(cache_esize_of(c->dtype)), batch = static_cast<uint64_t>(c->batch);
     ar::CompactArgs a{};
     uint64_t pointers;
-    if (!fill_layers(&a.to, k, v, layers, e, &pointers) || !element_ok(c->page_table, 4) || !element_ok(c->lengths, 4) ||
+    const int buffers = fill_layers(&a.to, k, v, layers, e, &pointers);
+    if (buffers == 0 || !element_ok(c->page_table, 4) || !element_ok(c->lengths, 4) ||
         !aligned(seq_start, 4) || !element_ok(new_lengths, 4) || (most_kept > 0 && !element_ok(kept, 4)))
         return AR_ERR_INVALID_ARG;
     a.kept_stride = c->batch > 1 ? kept_stride : 0;
@@ -451,7 +451,7 @@ int ar_kv_compact(const ar_kv_cache* cache, void* const* k, void* const* v, int 
     const int unit = unit_of({pointers, a.page_stride, a.token_stride, a.head_stride, c->head_dim * e});
     a.inner = static_cast<uint32_t>(c->head_dim * e / unit);
     a.head_units = a.inner * static_cast<uint32_t>(c->kv_heads);
-    a.units = a.head_units * 2u * static_cast<uint32_t>(layers);
+    a.units = a.head_units * static_cast<uint32_t>(buffers);
     return status_of(ar::launch_compact(a, unit, reinterpret_cast<cudaStream_t>(stream)));
 }
 
@@ -469,7 +469,8 @@ int ar_kv_copy_pages(const ar_kv_cache* cache, void* const* k, void* const* v, i
     const uint64_t e = static_cast<uint64_t>(cache_esize_of(c->dtype));
     ar::CopyArgs a{};
     uint64_t pointers;
-    if (!fill_layers(&a.to, k, v, layers, e, &pointers) || !element_ok(src, 4) || !element_ok(dst, 4))
+    const int buffers = fill_layers(&a.to, k, v, layers, e, &pointers);
+    if (buffers == 0 || !element_ok(src, 4) || !element_ok(dst, 4))
         return AR_ERR_INVALID_ARG;
     a.src = src;
     a.dst = dst;
@@ -503,7 +504,7 @@ int ar_kv_copy_pages(const ar_kv_cache* cache, void* const* k, void* const* v, i
     a.mid_stride = near.stride;
     a.outer_stride = far.stride;
     a.units = static_cast<uint32_t>(run / unit * near.n * far.n);
-    return status_of(ar::launch_copy_pages(a, layers, unit, reinterpret_cast<cudaStream_t>(stream)));
+    return status_of(ar::launch_copy_pages(a, buffers, unit, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 size_t ar_paged_attention_workspace_size(const ar_kv_cache* cache, int q_heads)

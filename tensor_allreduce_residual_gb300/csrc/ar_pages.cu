@@ -25,8 +25,8 @@ template <>
 struct MoveUnit<1> { using type = uint8_t; };
 
 // ---------------------------------------------------------------------------
-// Copying pages.  A block takes one pair's segment of a page in one layer's
-// keys or values: PER units a thread, all loads at once.  Whether the pair is
+// Copying pages.  A block takes one pair's segment of a page in one buffer (a
+// layer's keys or values): PER units a thread, all loads at once.  Whether the pair is
 // made it finds by one pass over all pairs, whose loads hide behind the other
 // blocks' copies.  Bound by HBM: 1.05 GB read and written take 145 us, 7.2 TB/s.
 // 8 pages of 4 KB in 16 layers are a launch, 4.5 us.
@@ -53,7 +53,7 @@ k_kv_copy_pages(const CopyArgs a)
     }
     if (__syncthreads_or(clash))
         return;
-    char* const base = blockIdx.y & 1 ? a.to.v[blockIdx.y >> 1] : a.to.k[blockIdx.y >> 1];
+    char* const base = a.to.buffer[blockIdx.y];
     const char* const from = base + static_cast<uint64_t>(src) * a.page_stride;
     char* const to = base + static_cast<uint64_t>(dst) * a.page_stride;
     U v[PER];
@@ -78,29 +78,29 @@ k_kv_copy_pages(const CopyArgs a)
 }
 
 template <int BYTES>
-static cudaError_t launch_copy_unit(const CopyArgs& args, int layers, cudaStream_t s)
+static cudaError_t launch_copy_unit(const CopyArgs& args, int buffers, cudaStream_t s)
 {
     CopyArgs a = args;
     const auto segments_of = [&](int per) { return (a.units + static_cast<uint64_t>(kMoveThreads) * per - 1) / (static_cast<uint64_t>(kMoveThreads) * per); };
     // Eight units a thread where that still leaves every SM eight blocks, else one, for more blocks.
-    const bool many = segments_of(8) * a.pairs * (2 * layers) >= 152 * 8;
+    const bool many = segments_of(8) * a.pairs * buffers >= 152 * 8;
     const uint64_t segments = segments_of(many ? 8 : 1);
     if (segments * a.pairs > static_cast<uint64_t>(INT_MAX))
         return cudaErrorInvalidConfiguration;
     a.segments = static_cast<uint32_t>(segments);
-    const dim3 grid(static_cast<unsigned>(segments * a.pairs), 2 * layers);
+    const dim3 grid(static_cast<unsigned>(segments * a.pairs), buffers);
     return many ? launch_k(k_kv_copy_pages<BYTES, 8>, grid, dim3(kMoveThreads), 0, s, a)
                 : launch_k(k_kv_copy_pages<BYTES, 1>, grid, dim3(kMoveThreads), 0, s, a);
 }
 
-cudaError_t launch_copy_pages(const CopyArgs& a, int layers, int unit, cudaStream_t s)
+cudaError_t launch_copy_pages(const CopyArgs& a, int buffers, int unit, cudaStream_t s)
 {
     switch (unit) {
-    case 16: return launch_copy_unit<16>(a, layers, s);
-    case 8: return launch_copy_unit<8>(a, layers, s);
-    case 4: return launch_copy_unit<4>(a, layers, s);
-    case 2: return launch_copy_unit<2>(a, layers, s);
-    default: return launch_copy_unit<1>(a, layers, s);
+    case 16: return launch_copy_unit<16>(a, buffers, s);
+    case 8: return launch_copy_unit<8>(a, buffers, s);
+    case 4: return launch_copy_unit<4>(a, buffers, s);
+    case 2: return launch_copy_unit<2>(a, buffers, s);
+    default: return launch_copy_unit<1>(a, buffers, s);
     }
 }
 
@@ -110,8 +110,8 @@ cudaError_t launch_copy_pages(const CopyArgs& a, int layers, int unit, cudaStrea
 // so taking the tokens in order never overwrites one that is still to move.  A
 // thread owns one unit (16 bytes of one head, of one layer's keys or values)
 // of all of a sequence's tokens and takes them in order, AHEAD loads at once
-// before their stores: no two threads touch the same bytes, and no barrier is
-// needed between moves.  Bound by HBM for large batches, by the chain of loads
+// before their stores: no two threads touch the same bytes, as each buffer is
+// listed once, and no barrier is needed between moves.  Bound by HBM for large batches, by the chain of loads
 // list, length, page, token for small ones (12.9 and 5.7 us; the chain, with
 // its barriers, is 4 us of both).
 // ---------------------------------------------------------------------------
@@ -151,7 +151,7 @@ k_kv_compact(const CompactArgs a)
     char* base = nullptr;
     if (unit < a.units) {
         const uint32_t part = unit / a.head_units, in = unit - part * a.head_units, head = in / a.inner;
-        base = (part & 1 ? a.to.v[part >> 1] : a.to.k[part >> 1]) + head * a.head_stride + (in - head * a.inner) * static_cast<uint64_t>(BYTES);
+        base = a.to.buffer[part] + head * a.head_stride + (in - head * a.inner) * static_cast<uint64_t>(BYTES);
     }
     const int* const table = a.table + static_cast<uint64_t>(b) * a.table_stride;
     const auto place = [&](int64_t token) -> int64_t {

@@ -1,0 +1,81 @@
+"""The buffers that one call of ar_kv_compact or ar_kv_copy_pages moves in (csrc/ar_layers.h, compiled for the host): each once, however
+many layers name it, as two owners of the same bytes would move what has moved already."""
+import ctypes
+import os
+import random
+import subprocess
+
+import pytest
+
+from tensor_allreduce_residual_gb300 import _build
+
+SOURCE = """
+#include "ar_layers.h"
+extern "C" int distinct(void* const* k, void* const* v, int layers, void** out)
+{
+    ar::Layers to;
+    const int n = ar::distinct_buffers(&to, k, v, layers);
+    for (int i = 0; i < n; ++i)
+        out[i] = to.buffer[i];
+    return n;
+}
+"""
+
+
+@pytest.fixture(scope="module")
+def distinct(tmp_path_factory):
+    d = tmp_path_factory.mktemp("layers")
+    (d / "layers.cpp").write_text(SOURCE)
+    subprocess.run(["g++", "-std=c++17", "-Wall", "-Werror", "-shared", "-fPIC", f"-I{_build.CSRC}", str(d / "layers.cpp"), "-o", str(d / "layers.so")], check=True)
+    lib = ctypes.CDLL(os.path.join(d, "layers.so"))
+
+    def call(k, v):
+        out = (ctypes.c_void_p * (2 * len(k)))()
+        n = lib.distinct((ctypes.c_void_p * len(k))(*k), (ctypes.c_void_p * len(v))(*v), len(k), out)
+        return list(out[:n])
+
+    return call
+
+
+def _in_turn(k, v):
+    return list(dict.fromkeys(x for pair in zip(k, v) for x in pair))
+
+
+def test_layers_of_their_own_keep_their_order(distinct):
+    for layers in (1, 2, 37, 128):
+        k, v = [0x7f0000000000 + (i << 21) for i in range(layers)], [0x7f8000000000 + (i << 21) for i in range(layers)]
+        assert distinct(k, v) == _in_turn(k, v) and len(distinct(k, v)) == 2 * layers
+
+
+def test_a_buffer_that_several_layers_name_is_listed_once(distinct):
+    assert distinct([0x1000, 0x1000], [0x2000, 0x2000]) == [0x1000, 0x2000]
+    assert distinct([0x1000, 0x3000, 0x1000], [0x2000, 0x1000, 0x4000]) == [0x1000, 0x2000, 0x3000, 0x4000]
+    assert distinct([0x1000], [0x1000]) == [0x1000]
+    assert distinct([0x1000] * 128, [0x1000] * 128) == [0x1000]
+    r = random.Random(4)
+    for _ in range(300):
+        layers, pool = r.randint(1, 128), [r.randrange(1, 1 << 47) for _ in range(r.randint(1, 200))]
+        k, v = [r.choice(pool) for _ in range(layers)], [r.choice(pool) for _ in range(layers)]
+        assert distinct(k, v) == _in_turn(k, v)
+    for step in (1, 2, 16, 256, 1 << 10, 1 << 20, 1 << 30, 1 << 40):   # distances at which a hash may crowd
+        k, v = [(1 << 46) + 2 * i * step for i in range(128)], [(1 << 46) + (2 * i + 1) * step for i in range(128)]
+        assert distinct(k, v) == _in_turn(k, v)
+
+
+def test_two_owners_of_one_buffer_would_move_tokens_twice(distinct):
+    """The moves of one sequence by each owner of a buffer, whole or in part before the other's: only one owner gives the result."""
+    kept = [1, 2, 4]
+    want = [11, 12, 14, 13, 14]
+    r = random.Random(1)
+
+    def moved(owners):
+        tokens, at = [10, 11, 12, 13, 14], [0] * owners
+        while any(x < len(kept) for x in at):
+            o = r.choice([o for o in range(owners) if at[o] < len(kept)])
+            tokens[at[o]] = tokens[kept[at[o]]]
+            at[o] += 1
+        return tokens
+
+    k, v = [0x1000, 0x1000], [0x2000, 0x2000]
+    assert any(moved(k.count(0x1000)) != want for _ in range(100))
+    assert all(moved(distinct(k, v).count(x)) == want for x in (0x1000, 0x2000) for _ in range(100))
