@@ -156,8 +156,8 @@ _lib_path = LIB_PATH
 
 def use_test_library() -> None:
     """Load libar_test.so instead of libar.so in this process (tests and shape sweeps only: its launch
-    shapes and fault injection follow AR_ONESHOT_SHAPE, AR_TEST_STALL_STAGE, AR_TEST_LAMPORT_SKIP_RANK
-    and AR_PDL).  Must come before the first call into the library."""
+    shapes and fault injection follow AR_ONESHOT_SHAPE, AR_TEST_STALL_STAGE, AR_TEST_TREE_STALL,
+    AR_TEST_LAMPORT_SKIP_RANK and AR_PDL).  Must come before the first call into the library."""
     global _lib_path
     if _lib is not None and _lib_path != TEST_LIB_PATH:
         raise RuntimeError("libar.so is already loaded in this process")

@@ -7,8 +7,8 @@ A second library, libar_test.so, is the same code with the test hooks
 compiled in (AR_TEST_HOOKS: the launch-shape override, the fault injection
 of the bounded-wait tests and the programmatic-launch switch, each read from
 the environment, and a communicator over local buffers for the peer
-barrier's timeout test).  Only ar_api.cu and ar_peer.cu differ, so only
-they are compiled twice.
+barrier's timeout test).  Only ar_api.cu, ar_peer.cu and ar_cache_api.cu
+differ, so only they are compiled twice.
 _binding-*.so is the CPython extension that marshals the paged key-value cache
 calls from torch tensors (host code only, compiled by g++ against torch's
 headers; its name tells torch's and Python's versions).  Where it cannot be built the other calls, which do not need it, are
@@ -113,8 +113,8 @@ def _build_library(verbose: bool, ptxas_info: bool) -> None:
     procs = []
     objs = []
     units = [(src, os.path.join(BUILD, src.replace(".cu", ".o")), []) for src in SOURCES]
-    units.append(("ar_api.cu", os.path.join(BUILD, "ar_api_test.o"), ["-DAR_TEST_HOOKS"]))
-    units.append(("ar_peer.cu", os.path.join(BUILD, "ar_peer_test.o"), ["-DAR_TEST_HOOKS"]))
+    hooked = ["ar_api.cu", "ar_peer.cu", "ar_cache_api.cu"]
+    units += [(src, os.path.join(BUILD, src.replace(".cu", "_test.o")), ["-DAR_TEST_HOOKS"]) for src in hooked]
     for src, obj, defs in units:
         cmd = [cc, *ARCH, *FLAGS, *defs, "-c", os.path.join(CSRC, src), "-o", obj]
         if ptxas_info:
@@ -125,7 +125,7 @@ def _build_library(verbose: bool, ptxas_info: bool) -> None:
     if failed:
         raise RuntimeError(f"nvcc failed on {failed}")
     product = objs[:len(SOURCES)]
-    swap = {os.path.join(BUILD, "ar_api.o"): objs[-2], os.path.join(BUILD, "ar_peer.o"): objs[-1]}
+    swap = {os.path.join(BUILD, src.replace(".cu", ".o")): obj for src, obj in zip(hooked, objs[len(SOURCES):])}
     test = [swap.get(o, o) for o in product]
     for lib, lib_objs in ((LIB, product), (TEST_LIB, test)):
         tmp = f"{lib}.{os.getpid()}.tmp"

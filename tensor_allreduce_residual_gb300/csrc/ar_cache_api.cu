@@ -10,6 +10,7 @@
 #include <climits>
 #include <cmath>
 #include <cstdint>
+#include <cstdlib>
 #include <initializer_list>
 
 #include "ar.h"
@@ -236,6 +237,21 @@ int tree_maps(const ar_kv_cache* c, int tile, int dim, ar::TreeMaps* maps, int* 
                       CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
     };
     return map(&maps->k, c->k) && map(&maps->v, c->v) ? tokens : 0;
+}
+
+// Fault injection of the tests: the test build of the library (compiled with AR_TEST_HOOKS, libar_test.so) reads it once from
+// AR_TEST_TREE_STALL; the product library never reads the environment.
+int tree_stall()
+{
+#ifdef AR_TEST_HOOKS
+    static const int stall = [] {
+        const char* e = std::getenv("AR_TEST_TREE_STALL");
+        return e != nullptr ? std::atoi(e) : 0;
+    }();
+    return stall;
+#else
+    return 0;
+#endif
 }
 
 struct TreePlan {
@@ -665,6 +681,7 @@ int ar_tree_attention(const ar_kv_cache* cache, const ar_tree_params* p, void* w
     a.v_scale = c->v_scale;
     a.slot_rows = plan.slot_rows;
     a.slot_floats = plan.slot_floats;
+    a.stall = tree_stall();
     ar::TreeMaps maps{};
     a.boxes = tree_maps(c, plan.shape.tile, ar::tree_dim(c->head_dim), &maps, &a.token_first);
 

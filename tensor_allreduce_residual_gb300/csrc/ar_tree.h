@@ -41,6 +41,7 @@ struct TreeArgs {
     int token_first;          // whether the maps' second axis is a page's tokens, and not the heads
     int slot_rows;            // rows of a partial slot: [slot_rows][head_dim] sums, [slot_rows] references, [slot_rows] weights
     uint64_t slot_floats;
+    int stall;                // tests only: 1 + the step of k_tree_mma whose weights no warp hands over, so that its waits run out; 0: none
 };
 
 // An item that several blocks have parts of, written by the one that begins it; rows == 0: there is none.

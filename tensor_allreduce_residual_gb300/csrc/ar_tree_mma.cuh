@@ -33,7 +33,9 @@
 //
 // All hand-overs are mbarriers.  Waits are bounded: one that gave up is
 // counted, raises the block's stop flag, on which all others give up too, and
-// the block leaves.
+// the block leaves, once what it has under way has had time to land: copies
+// and products of warps that were done with their part as much as of those that
+// gave up, as the wait that runs out for a late copy is not its own warp's.
 #pragma once
 
 #include "ar_tcgen05.cuh"
@@ -1290,7 +1292,7 @@ struct TreeSoft {
                     return false;
                 tcgen05_before_sync();
                 __syncwarp();
-                if (lane == 0)
+                if (lane == 0 && u + 1 != a.stall)
                     bar_arrive(sm.p_ready(P::buffer_of(u)));
                 own = u;
                 if (bad && !poison(tile, u, valid))
@@ -1363,13 +1365,7 @@ k_tree_mma(const TreeArgs a, const __grid_constant__ TreeMaps maps)
         if (warp >= BOXES) {
             if (a.boxes) {
                 TreeBoxes<P> boxes(a, sm, maps, stop);
-                if (!boxes.run(cur, line, n)) {  // stopped: copies under way land, within microseconds, before the block leaves
-                    unsigned long long t0, t;
-                    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t0));
-                    do
-                        asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
-                    while (t - t0 < kTreeLandNs);
-                }
+                boxes.run(cur, line, n);
             }
             __syncwarp();
         } else if (warp >= ISSUE) {
@@ -1387,8 +1383,11 @@ k_tree_mma(const TreeArgs a, const __grid_constant__ TreeMaps maps)
             __syncwarp();
         } else if (warp >= COPY) {
             TreeFeed<P> feed(a, sm, stop, cur);
-            if (!(a.boxes ? feed.help(n) : feed.run(cur, line, n)))
-                asm volatile("cp.async.wait_all;" ::: "memory");
+            if (a.boxes)
+                feed.help(n);
+            else
+                feed.run(cur, line, n);
+            asm volatile("cp.async.wait_all;" ::: "memory");  // nothing is left to wait for unless the block stops
             __syncwarp();
         } else {
             TreeSoft<P> soft(a, sm, tmem, stop);
@@ -1398,6 +1397,14 @@ k_tree_mma(const TreeArgs a, const __grid_constant__ TreeMaps maps)
     }
     tcgen05_before_sync();
     __syncthreads();
+    if (*stop != 0) {  // tensor copies and products under way, whosever they are, land within microseconds
+        unsigned long long t0, t;
+        asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t0));
+        do
+            asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+        while (t - t0 < kTreeLandNs);
+    }
+    __syncwarp();
     tcgen05_after_sync();
     if (warp == ISSUE)
         tmem_free(tmem, 512);
