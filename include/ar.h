@@ -753,7 +753,9 @@ int ar_kv_append_axes(const ar_kv_cache* cache, const ar_append_params* p, int a
  * Errors: AR_ERR_INVALID_ARG (NULL or not element-aligned pointer, layers
  *         < 1, most_kept or drafted < 0, a size or stride that is too small,
  *         new_lengths over an input), AR_ERR_UNSUPPORTED (dtype, heads or
- *         head_dim over 1024, more than AR_MAX_LAYERS layers), AR_ERR_CUDA.
+ *         head_dim over 1024, more than AR_MAX_LAYERS layers, a token of more
+ *         than 2^24 - 256 units in all layers: of 16 bytes, or less where a
+ *         pointer, a stride or the head is no multiple of them), AR_ERR_CUDA.
  */
 #define AR_MAX_LAYERS 128
 int ar_kv_compact(const ar_kv_cache* cache, void* const* k, void* const* v, int layers, const int* kept,
@@ -780,7 +782,9 @@ int ar_kv_compact(const ar_kv_cache* cache, void* const* k, void* const* v, int 
  * Errors: AR_ERR_INVALID_ARG (NULL or not element-aligned pointer, layers
  *         < 1, pairs < 0, a size or stride that is too small),
  *         AR_ERR_UNSUPPORTED (dtype, heads or head_dim over 1024, more than
- *         AR_MAX_LAYERS layers), AR_ERR_CUDA.
+ *         AR_MAX_LAYERS layers, a page of 2^32 such units or more, or more
+ *         pairs of pages than a launch has blocks for: 2^31 - 1, of up to 2048
+ *         units each), AR_ERR_CUDA.
  */
 int ar_kv_copy_pages(const ar_kv_cache* cache, void* const* k, void* const* v, int layers, const int* src,
                      const int* dst, int pairs, ar_stream_t stream);

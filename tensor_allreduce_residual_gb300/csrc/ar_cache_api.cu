@@ -377,6 +377,9 @@ int append(const ar_kv_cache* cache, const ar_append_params* p, int axes, size_t
     }));
 }
 
+// More blocks than a launch can have are a call that is not supported, and no failure of CUDA's.
+int moved_status(cudaError_t e) { return e == cudaErrorInvalidConfiguration ? AR_ERR_UNSUPPORTED : status_of(e); }
+
 // The largest unit of 16 bytes or less that all of these are whole multiples of.
 int unit_of(std::initializer_list<uint64_t> all)
 {
@@ -468,7 +471,7 @@ int ar_kv_compact(const ar_kv_cache* cache, void* const* k, void* const* v, int 
     a.inner = static_cast<uint32_t>(c->head_dim * e / unit);
     a.head_units = a.inner * static_cast<uint32_t>(c->kv_heads);
     a.units = a.head_units * static_cast<uint32_t>(buffers);
-    return status_of(ar::launch_compact(a, unit, reinterpret_cast<cudaStream_t>(stream)));
+    return moved_status(ar::launch_compact(a, unit, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 int ar_kv_copy_pages(const ar_kv_cache* cache, void* const* k, void* const* v, int layers, const int* src, const int* dst,
@@ -520,7 +523,7 @@ int ar_kv_copy_pages(const ar_kv_cache* cache, void* const* k, void* const* v, i
     a.mid_stride = near.stride;
     a.outer_stride = far.stride;
     a.units = static_cast<uint32_t>(run / unit * near.n * far.n);
-    return status_of(ar::launch_copy_pages(a, buffers, unit, reinterpret_cast<cudaStream_t>(stream)));
+    return moved_status(ar::launch_copy_pages(a, buffers, unit, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 size_t ar_paged_attention_workspace_size(const ar_kv_cache* cache, int q_heads)

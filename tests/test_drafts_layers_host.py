@@ -7,6 +7,7 @@ import subprocess
 
 import pytest
 
+import tensor_allreduce_residual_gb300 as ar
 from tensor_allreduce_residual_gb300 import _build
 
 SOURCE = """
@@ -79,3 +80,29 @@ def test_two_owners_of_one_buffer_would_move_tokens_twice(distinct):
     k, v = [0x1000, 0x1000], [0x2000, 0x2000]
     assert any(moved(k.count(0x1000)) != want for _ in range(100))
     assert all(moved(distinct(k, v).count(x)) == want for x in (0x1000, 0x2000) for _ in range(100))
+
+
+FAKE = 0x10000   # never dereferenced: the calls are refused before a launch
+
+
+def _cache(**kw):
+    d = dict(k=None, v=None, dtype=ar.AR_FP8_E4M3, pages=8, page_size=1, kv_heads=1024, head_dim=1023, page_stride=1 << 40, token_stride=0,
+             head_stride=1023, k_scale=1.0, v_scale=1.0, page_table=FAKE, batch=3, max_pages=4, table_stride=4, lengths=FAKE)
+    d.update(kw)
+    return ar.ArKVCache(**d)
+
+
+def _pointers(layers, at):
+    return (ctypes.c_void_p * layers)(*[at + (i << 30) for i in range(layers)])
+
+
+def test_more_blocks_than_a_launch_has_are_refused_as_unsupported():
+    """A token of 128 layers of 1024 heads of 1023 bytes: 268 million units of one byte; 2^31 - 1 pairs of pages of 5115 units."""
+    _build.build()
+    L = ar.lib()
+    k, v = _pointers(128, 1 << 40), _pointers(128, 1 << 41)
+    assert L.ar_kv_compact(_cache(), k, v, 128, FAKE, 5, 5, None, 5, 0x90000, None) == ar.AR_ERR_UNSUPPORTED
+    small = _cache(kv_heads=1, page_size=5, token_stride=1023)
+    assert L.ar_kv_copy_pages(small, k, v, 128, FAKE, FAKE, 2 ** 31 - 1, None) == ar.AR_ERR_UNSUPPORTED
+    wide = _cache(kv_heads=1024, head_dim=1023, page_size=2 ** 20, token_stride=1 << 21, page_stride=1 << 50)
+    assert L.ar_kv_copy_pages(wide, k, v, 128, FAKE, FAKE, 1, None) == ar.AR_ERR_UNSUPPORTED
