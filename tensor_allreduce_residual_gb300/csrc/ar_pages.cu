@@ -27,9 +27,12 @@ struct MoveUnit<1> { using type = uint8_t; };
 // ---------------------------------------------------------------------------
 // Copying pages.  A block takes one pair's segment of a page in one buffer (a
 // layer's keys or values): PER units a thread, all loads at once.  Whether the pair is
-// made it finds by one pass over all pairs, whose loads hide behind the other
-// blocks' copies.  Bound by HBM: 1.05 GB read and written take 145 us, 7.2 TB/s.
-// 8 pages of 4 KB in 16 layers are a launch, 4.5 us.
+// made it finds by one pass over all pairs, 8 bytes each.  Large pages and few pairs
+// hide that behind the other blocks' copies and are bound by HBM: 2000 pages of 32 KB
+// in 4 layers, 1.05 GB read and written, take 145 us, 7.2 TB/s.  Thousands of small
+// pages are bound by the passes, whose bytes grow with the pairs squared: 4 KB in 8
+// layers take 309 us for 4000 pairs, four times their bytes' time, and 2.99 ms for
+// 16000, ten times.  8 pages of 4 KB in 16 layers are a launch, 4.7 us.
 // ---------------------------------------------------------------------------
 template <int BYTES, int PER>
 __global__ void __launch_bounds__(kMoveThreads)

@@ -71,12 +71,13 @@ struct TreeShape {
 // Elements that a head of the matrix kernel has, those of a shorter one followed by zeros.
 inline int tree_dim(int head_dim) { return head_dim <= 64 ? 64 : head_dim <= 128 ? 128 : head_dim <= 192 ? 192 : 256; }
 
-// The rule, on what the host knows.  `rows`: of all sequences and one key-value head.  An item's cached tokens are read once for
-// each block of its rows, so blocks hold the mean item where there is a kernel of that size: 64 sequences of 256 rows over
-// 539 MB of bf16 take 220 us with blocks of 256 and 254 with 128; of 32 to 256 rows 267 and 312.  Heads over 128 leave shared
-// and tensor memory for 128 rows only, and tiles of 64 tokens.
-// fp32, 16 sequences of 2048 tokens, heads of 96: 10 or 16 rows 140 us with blocks of 16 and 252 with 64, 32 rows 79 and 82,
-// 64 rows 140 and 84.
+// The rule, on what the host knows.  `rows`: of all sequences and one key-value head, padding among them.  An item's cached tokens
+// are read once for each block of its rows, so blocks hold the mean item where there is a kernel of that size.  64 sequences of 4096
+// tokens, 4 key-value heads of 128 (537 MB of bf16): 32, 64 and 128 rows 137, 141 and 150 us with blocks of 128 and 187, 190 and 204
+// with 256; 136 and 256 rows 258 and 265 us with 128 and 203 and 222 with 256.  Heads over 128 leave shared and tensor memory for
+// 128 rows only, and tiles of 64 tokens.
+// fp32, 16 sequences of 2048 tokens, 8 key-value heads of 96 (201 MB): 10 or 16 rows 140 us with blocks of 16 and 252 with 64, 32
+// rows 264 and 253, 64 rows 512 and 258.
 inline TreeShape tree_shape(int cache_esize, int head_dim, uint64_t rows, int batch)
 {
     if (cache_esize == 4)

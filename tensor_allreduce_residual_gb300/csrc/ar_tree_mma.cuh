@@ -28,8 +28,10 @@
 // O (5 us), and the join (10 us).  With 256 rows a group's way round, scores,
 // softmax (3500 cycles), weighted values, is longer than a tile's copy: 4 us a
 // tile.  8-bit caches wait for the warps that turn them into fp16, at 4500
-// cycles a tile of 128 tokens by 128: 268 MB take 157 us with fp16 queries, 174
-// with bf16 ones, whose scaling is on the way from one item to the next.
+// cycles a tile of 128 tokens by 128: 268 MB take 158 us with fp16 queries, 173
+// with bf16 ones, whose scaling is on the way from one item to the next.  Heads of
+// 192 and 256, 16 + 2 of them over 64 sequences of 4096 tokens, take 110 and 116
+// us in bf16 (403 and 537 MB), 156 and 172 us in e4m3.
 //
 // All hand-overs are mbarriers.  Waits are bounded: one that gave up is
 // counted, raises the block's stop flag, on which all others give up too, and
@@ -164,7 +166,8 @@ struct TreeMmaShape {
     static_assert(EXPONENTS >= QS + 3, "powers are read before they are written over");
     static constexpr int SMEM = QS * Q + NS * SLOT + RS * RAW + MISC;
     // Weights may pass their reference's by 2^AHEAD before it is moved, which costs a pass over O.  fp16 weights are 2^LIFT
-    // times as large, so that small ones keep their bits: the largest is 2^15.
+    // times as large, so that small ones keep their bits: the largest is 2^15, and the sum holds one of 2^LIFT, so that a weight
+    // is off by 2^-25, 2^-36 of that one, where its second number runs out of bits.
     static constexpr float AHEAD = BF16 ? 8.0f : 4.0f, LIFT = BF16 ? 0.0f : 11.0f;
     static constexpr int S_COLUMNS = TOKENS, O_COLUMN = 256;  // score buffers from column 0 on; O of group m at 256 + 128 m
     static_assert(BUFFERS * S_COLUMNS <= O_COLUMN && O_COLUMN + (DIM <= 128 ? GROUPS * 128 : 256) <= 512, "tensor memory");
@@ -243,8 +246,9 @@ __device__ __forceinline__ bool elected()
 // whose slot is free, a fill that has arrived and needs its hands) and waits
 // for none while another is possible.  The fence between these writes and the
 // tensor core's reads is the issuing warp's: here it would wait for all copies
-// on their way.  Pages of 17 tokens, which take this way, read 268 MB of e4m3 in
-// 205 us where pages of 64 took 191.
+// on their way.  Pages of 17 tokens, which take this way, are 233 us (bf16
+// queries; 238 with fp16 ones) on 268 MB of e4m3, where pages of 64 are 173 (158),
+// and 187 us on 537 MB of bf16, where pages of 64 are 125.
 // ---------------------------------------------------------------------------
 template <typename P>
 struct TreeFeed {
