@@ -215,7 +215,7 @@ int fill_pages(ar_kv_cache* c, const Tensor& k, const Tensor& v, int tokens)
         cuda_index(v) != dev || (k.stride(3) != 1 && k.size(3) > 1))
         bad("k_pages and v_pages must be 4-d tensors of one shape, dtype, device and set of strides, with dense heads");
     if (tokens == 0)
-        tokens = k.size(2) > k.size(1) ? 2 : 1;
+        tokens = k.sizes()[2] > k.sizes()[1] ? 2 : 1;
     const int heads = 3 - tokens;
     const at::ScalarType type = k.scalar_type();
     if (type != at::kFloat && type != at::kHalf && type != at::kBFloat16 && type != at::kFloat8_e4m3fn)

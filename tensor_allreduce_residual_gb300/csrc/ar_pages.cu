@@ -32,7 +32,7 @@ struct MoveUnit<1> { using type = uint8_t; };
 // in 4 layers, 1.05 GB read and written, take 145 us, 7.2 TB/s.  Thousands of small
 // pages are bound by the passes, whose bytes grow with the pairs squared: 4 KB in 8
 // layers take 309 us for 4000 pairs, four times their bytes' time, and 2.99 ms for
-// 16000, ten times.  8 pages of 4 KB in 16 layers are a launch, 4.7 us.
+// 16000, ten times.  8 pages of 4 KB in 16 layers are a launch, 4.5 us.
 // ---------------------------------------------------------------------------
 template <int BYTES, int PER>
 __global__ void __launch_bounds__(kMoveThreads)
@@ -56,7 +56,7 @@ k_kv_copy_pages(const CopyArgs a)
     }
     if (__syncthreads_or(clash))
         return;
-    char* const base = a.to.buffer[blockIdx.y];
+    char* const base = blockIdx.y & 1 ? a.to.odd[blockIdx.y >> 1] : a.to.even[blockIdx.y >> 1];
     const char* const from = base + static_cast<uint64_t>(src) * a.page_stride;
     char* const to = base + static_cast<uint64_t>(dst) * a.page_stride;
     U v[PER];
@@ -115,7 +115,7 @@ cudaError_t launch_copy_pages(const CopyArgs& a, int buffers, int unit, cudaStre
 // of all of a sequence's tokens and takes them in order, AHEAD loads at once
 // before their stores: no two threads touch the same bytes, as each buffer is
 // listed once, and no barrier is needed between moves.  Bound by HBM for large batches, by the chain of loads
-// list, length, page, token for small ones (12.9 and 5.7 us; the chain, with
+// list, length, page, token for small ones (13.1 and 5.1 us; the chain, with
 // its barriers, is 4 us of both).
 // ---------------------------------------------------------------------------
 template <int BYTES>
@@ -154,7 +154,7 @@ k_kv_compact(const CompactArgs a)
     char* base = nullptr;
     if (unit < a.units) {
         const uint32_t part = unit / a.head_units, in = unit - part * a.head_units, head = in / a.inner;
-        base = a.to.buffer[part] + head * a.head_stride + (in - head * a.inner) * static_cast<uint64_t>(BYTES);
+        base = (part & 1 ? a.to.odd[part >> 1] : a.to.even[part >> 1]) + head * a.head_stride + (in - head * a.inner) * static_cast<uint64_t>(BYTES);
     }
     const int* const table = a.table + static_cast<uint64_t>(b) * a.table_stride;
     const auto place = [&](int64_t token) -> int64_t {

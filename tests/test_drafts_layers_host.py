@@ -17,7 +17,7 @@ extern "C" int distinct(void* const* k, void* const* v, int layers, void** out)
     ar::Layers to;
     const int n = ar::distinct_buffers(&to, k, v, layers);
     for (int i = 0; i < n; ++i)
-        out[i] = to.buffer[i];
+        out[i] = (i & 1 ? to.odd : to.even)[i >> 1];
     return n;
 }
 """
